@@ -680,3 +680,10 @@ __all__ = [
     "SBN_F32", "SBN_BF16", "SBN_I32_ACC", "SBN_OP_PACK", "SBN_OP_ACT_QUANT", "SBN_OP_GEMM",
     "SBN_OP_GEMV", "SBN_OP_BACKWARD", "SBN_OP_FORWARD", "sbn_profile_enable", "sbn_profile_reset", "sbn_profile_dump",
 ]
+
+
+# the operators around the layer (include/sbn_train.h); at the end, since it uses the helpers above
+from .training import (  # noqa: E402,F401
+    SBN_ADAMW_BLOCK, AdamWTable, sbn_adamw_decode_m, sbn_adamw_decode_v, sbn_adamw_encode_m, sbn_adamw_encode_v,
+    sbn_adamw_step, sbn_cross_entropy, sbn_cross_entropy_backward, sbn_cross_entropy_workspace_bytes, sbn_rmsnorm,
+    sbn_rmsnorm_backward, sbn_rmsnorm_quant, train_header_symbols)

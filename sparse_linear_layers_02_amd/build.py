@@ -19,7 +19,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build", "libsbn")
 LIB = os.path.join(PKG, "libsbn.so")
 
-SOURCES = ["api.cpp", "pack.hip", "act_quant.hip", "gemm.hip", "gemv.hip", "backward.hip", "finite.hip"]
+SOURCES = ["api.cpp", "pack.hip", "act_quant.hip", "gemm.hip", "gemv.hip", "backward.hip", "finite.hip",
+           "train_api.cpp", "rmsnorm.hip", "cross_entropy.hip", "adamw.hip"]
 ARCH = "gfx950"
 
 FLAGS = [

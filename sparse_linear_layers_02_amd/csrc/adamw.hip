@@ -1,0 +1,312 @@
+// AdamW over a table of tensors in one launch, states in 32 or in 8 bits.
+//
+//   m <- b1 m + (1-b1) g;  v <- b2 v + (1-b2) g^2
+//   p <- p (1 - lr wd) - (lr / (1-b1^t)) m / (sqrt(v) / sqrt(1-b2^t) + eps)
+//
+// A block takes one chunk of one tensor (the map says which), a thread 8
+// consecutive elements, so every stream moves in 8- and 16-byte accesses and
+// the 32 lanes of half a wave hold exactly one block of 256 elements of an
+// 8-bit state: its largest value is five lane exchanges away.
+//
+// 8-bit codes: m = s (c/127)|c/127|, v = s (c/255)^4 with s the block's largest
+// value.  The code is the rint of a root, taken with the one-ulp root
+// instruction; only estimates within 2^-12 of a half-integer are redone with
+// correctly rounded roots (the estimate's error is under 2^-14), so the codes
+// equal those of the correctly rounded formula.
+//
+// Products and sums are rounded one by one (no fused multiply-add): the result
+// is that of the same formula in elementary float32 operations.
+// Bound by memory traffic: 28 bytes an element with 32-bit parameters,
+// gradients and states, 12 with bf16 parameters and 8-bit states.
+#include "train_internal.h"
+
+#pragma clang fp contract(off)
+
+namespace sbn {
+namespace {
+
+constexpr int QB = SBN_ADAMW_BLOCK;
+constexpr float S_FLOOR = 0x1p-100f;                // a block whose largest value is smaller is all 0
+constexpr float INV127 = 1.0f / 127.0f, INV255 = 1.0f / 255.0f;
+
+__device__ inline float half_wave_max(float x) {
+#pragma unroll
+  for (int m = 16; m >= 1; m >>= 1) x = fmaxf(x, __shfl_xor(x, m));
+  return x;
+}
+
+__device__ inline float decode_m(int c, float s) {
+  const float t = (float)c * INV127;
+  return t * fabsf(t) * s;
+}
+__device__ inline float decode_v(int c, float s) {
+  float t = (float)c * INV255;
+  t = t * t;
+  return t * t * s;
+}
+__device__ inline bool near_half(float q) { return fabsf(q - rintf(q)) > 0.5f - 0x1p-12f; }
+
+__device__ inline int encode_m(float x, float inv) {
+  const float y = fabsf(x) * inv;
+  float q = 127.0f * __builtin_amdgcn_sqrtf(y);
+  if (near_half(q)) q = 127.0f * sqrtf(y);
+  const int c = (int)rintf(q);
+  return x < 0.0f ? -c : c;
+}
+__device__ inline int encode_v(float x, float inv) {
+  const float y = x * inv;
+  float q = 255.0f * __builtin_amdgcn_sqrtf(__builtin_amdgcn_sqrtf(y));
+  if (near_half(q)) q = 255.0f * sqrtf(sqrtf(y));
+  const int c = (int)rintf(q);
+  return y > 0.0f && c < 1 ? 1 : c;
+}
+
+// n (1..8) elements at p (16-byte aligned where n == 8); elements past n are 0
+template <bool F32>
+__device__ inline void load8(const void* p, int n, float* v) {
+  if (F32) {
+    const float* q = (const float*)p;
+    if (n == 8) {
+      *(v4f*)v = *(const v4f*)q;
+      *(v4f*)(v + 4) = *(const v4f*)(q + 4);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = i < n ? q[i] : 0.0f;
+    }
+  } else {
+    const uint16_t* q = (const uint16_t*)p;
+    if (n == 8) {
+      const uint4 u = *(const uint4*)q;
+      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[2 * i] = __uint_as_float(w[i] << 16);
+        v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = i < n ? bf16_to_f32(q[i]) : 0.0f;
+    }
+  }
+}
+template <bool F32>
+__device__ inline void store8(void* p, int n, const float* v) {
+  if (F32) {
+    float* q = (float*)p;
+    if (n == 8) {
+      *(v4f*)q = *(const v4f*)v;
+      *(v4f*)(q + 4) = *(const v4f*)(v + 4);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (i < n) q[i] = v[i];
+    }
+  } else {
+    uint16_t* q = (uint16_t*)p;
+    if (n == 8) {
+      *(uint4*)q = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                              pack_bf16x2(v[6], v[7]));
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (i < n) q[i] = f32_to_bf16_rne(v[i]);
+    }
+  }
+}
+
+// 8 codes of one byte
+__device__ inline uint2 load_codes(const uint8_t* p, int n) {
+  if (n == 8) return *(const uint2*)p;
+  uint32_t w[2] = {0u, 0u};
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (i < n) w[i >> 2] |= (uint32_t)p[i] << (8 * (i & 3));
+  return make_uint2(w[0], w[1]);
+}
+__device__ inline void store_codes(uint8_t* p, int n, const int* c) {
+  uint32_t w[2] = {0u, 0u};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) w[i >> 2] |= (uint32_t)(c[i] & 0xFF) << (8 * (i & 3));
+  if (n == 8) {
+    *(uint2*)p = make_uint2(w[0], w[1]);
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (i < n) p[i] = (uint8_t)(w[i >> 2] >> (8 * (i & 3)));
+}
+__device__ inline void unpack_codes(uint2 w, bool is_signed, int* c) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t b = ((i < 4 ? w.x : w.y) >> (8 * (i & 3))) & 0xFFu;
+    c[i] = is_signed ? (int)(int8_t)b : (int)b;
+  }
+}
+
+// scale and codes of the 8 elements v of each lane (half a wave: one block).
+// Lanes past the tensor hold zeros and take part in the maximum.
+template <bool SECOND>
+__device__ inline float encode8(const float* v, int* c) {
+  float s = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) s = fmaxf(s, fabsf(v[i]));
+  s = half_wave_max(s);
+  if (s < S_FLOOR) s = 0.0f;
+  const float inv = s > 0.0f ? 1.0f / s : 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) c[i] = SECOND ? encode_v(v[i], inv) : encode_m(v[i], inv);
+  return s;
+}
+
+template <bool PF, bool GF, bool S8>
+__global__ __launch_bounds__(256) void adamw_kernel(const sbn_adamw_entry* __restrict__ entries,
+                                                    const int2* __restrict__ map, AdamWScalars S,
+                                                    const float* __restrict__ dyn) {
+  const int2 mp = map[blockIdx.x];
+  const sbn_adamw_entry* E = entries + mp.x;
+  const int64_t e = (int64_t)mp.y * ADAMW_CHUNK + threadIdx.x * 8;
+  const int64_t left = E->n - e;
+  const int n = left >= 8 ? 8 : left > 0 ? (int)left : 0;
+  const float lr = dyn ? dyn[0] : S.lr, bias1 = dyn ? dyn[1] : S.bias1, bias2 = dyn ? dyn[2] : S.bias2;
+  const float gs = dyn ? dyn[3] : 1.0f;
+  const float keep = 1.0f - lr * E->weight_decay, rate = lr / bias1, rbias2 = 1.0f / sqrtf(bias2);
+
+  float p[8], g[8], m[8], v[8];
+  uint2 cm = make_uint2(0u, 0u), cv = cm;
+  float sm = 0.0f, sv = 0.0f;
+  if (n > 0) {
+    load8<GF>((const char*)E->grad + e * (GF ? 4 : 2), n, g);
+    load8<PF>((const char*)E->p + e * (PF ? 4 : 2), n, p);
+    if (S8) {
+      cm = load_codes((const uint8_t*)E->m + e, n);
+      cv = load_codes((const uint8_t*)E->v + e, n);
+      sm = E->m_scale[e / QB];
+      sv = E->v_scale[e / QB];
+    } else {
+      load8<true>((const float*)E->m + e, n, m);
+      load8<true>((const float*)E->v + e, n, v);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) p[i] = g[i] = m[i] = v[i] = 0.0f;
+  }
+  if (S8) {
+    int c[8];
+    unpack_codes(cm, true, c);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m[i] = decode_m(c[i], sm);
+    unpack_codes(cv, false, c);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = decode_v(c[i], sv);
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float gi = g[i] * gs;
+    m[i] = m[i] * S.beta1 + gi * S.one_minus_beta1;
+    v[i] = v[i] * S.beta2 + (gi * gi) * S.one_minus_beta2;
+    const float root = sqrtf(v[i]) * rbias2 + S.eps;
+    p[i] = p[i] * keep - (m[i] * rate) / root;
+  }
+  if (S8) {
+    int c[8];
+    sm = encode8<false>(m, c);
+    if (n > 0) store_codes((uint8_t*)E->m + e, n, c);
+    sv = encode8<true>(v, c);
+    if (n > 0) store_codes((uint8_t*)E->v + e, n, c);
+    if (n > 0 && (threadIdx.x & 31) == 0) {
+      E->m_scale[e / QB] = sm;
+      E->v_scale[e / QB] = sv;
+    }
+  }
+  if (n == 0) return;
+  store8<PF>((char*)E->p + e * (PF ? 4 : 2), n, p);
+  if (PF && E->shadow) store8<false>(E->shadow + e, n, p);
+  if (!S8) {
+    store8<true>((float*)E->m + e, n, m);
+    store8<true>((float*)E->v + e, n, v);
+  }
+}
+
+__global__ __launch_bounds__(256) void adamw_decode_kernel(const uint8_t* __restrict__ codes,
+                                                           const float* __restrict__ scale, int64_t n, bool second,
+                                                           float* __restrict__ out) {
+  for (int64_t e = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8; e < n; e += (int64_t)gridDim.x * ADAMW_CHUNK) {
+    const int k = n - e >= 8 ? 8 : (int)(n - e);
+    const float s = scale[e / QB];
+    int c[8];
+    unpack_codes(load_codes(codes + e, k), !second, c);
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = second ? decode_v(c[i], s) : decode_m(c[i], s);
+    store8<true>(out + e, k, v);
+  }
+}
+
+// rounds are the same for every lane of a wave: the maximum needs them all
+__global__ __launch_bounds__(256) void adamw_encode_kernel(const float* __restrict__ x, int64_t n, bool second,
+                                                           uint8_t* __restrict__ codes, float* __restrict__ scale) {
+  for (int64_t e0 = (int64_t)blockIdx.x * ADAMW_CHUNK; e0 < n; e0 += (int64_t)gridDim.x * ADAMW_CHUNK) {
+    const int64_t e = e0 + threadIdx.x * 8;
+    const int k = n - e >= 8 ? 8 : n > e ? (int)(n - e) : 0;
+    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (k > 0) load8<true>(x + e, k, v);
+    int c[8];
+    const float s = second ? encode8<true>(v, c) : encode8<false>(v, c);
+    if (k > 0) {
+      store_codes(codes + e, k, c);
+      if ((threadIdx.x & 31) == 0) scale[e / QB] = s;
+    }
+  }
+}
+
+dim3 stride_grid(int64_t n) {
+  const int64_t b = cdiv(n, ADAMW_CHUNK);
+  return dim3((unsigned)(b < (1 << 20) ? b : (1 << 20)));
+}
+
+template <bool PF, bool GF, bool S8>
+void run(const sbn_adamw_entry* entries, const int2* map, int64_t blocks, const AdamWScalars& s, const float* dyn,
+         hipStream_t st) {
+  SBN_LAUNCH(S8 ? "adamw_8bit" : "adamw", (adamw_kernel<PF, GF, S8>), dim3((unsigned)blocks), dim3(256), 0, st, entries,
+             map, s, dyn);
+}
+
+}  // namespace
+
+hipError_t launch_adamw(const sbn_adamw_entry* entries, const int32_t* map, int64_t blocks, bool p_f32, bool g_f32,
+                        bool state8, const AdamWScalars& s, const float* dyn, hipStream_t st) {
+  // grids are limited to 2^32 threads: long tables take several launches
+  constexpr int64_t PER = 1 << 23;
+  for (int64_t b = 0; b < blocks; b += PER) {
+    const int64_t nb = blocks - b < PER ? blocks - b : PER;
+    const int2* mp = (const int2*)map + b;
+    switch ((p_f32 ? 4 : 0) + (g_f32 ? 2 : 0) + (state8 ? 1 : 0)) {
+      case 0: run<false, false, false>(entries, mp, nb, s, dyn, st); break;
+      case 1: run<false, false, true>(entries, mp, nb, s, dyn, st); break;
+      case 2: run<false, true, false>(entries, mp, nb, s, dyn, st); break;
+      case 3: run<false, true, true>(entries, mp, nb, s, dyn, st); break;
+      case 4: run<true, false, false>(entries, mp, nb, s, dyn, st); break;
+      case 5: run<true, false, true>(entries, mp, nb, s, dyn, st); break;
+      case 6: run<true, true, false>(entries, mp, nb, s, dyn, st); break;
+      default: run<true, true, true>(entries, mp, nb, s, dyn, st); break;
+    }
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+hipError_t launch_adamw_decode(const void* codes, const float* scale, int64_t n, bool second, float* out,
+                               hipStream_t st) {
+  SBN_LAUNCH("adamw_decode", adamw_decode_kernel, stride_grid(n), dim3(256), 0, st, (const uint8_t*)codes, scale, n,
+             second, out);
+  return hipGetLastError();
+}
+
+hipError_t launch_adamw_encode(const float* x, int64_t n, bool second, void* codes, float* scale, hipStream_t st) {
+  SBN_LAUNCH("adamw_encode", adamw_encode_kernel, stride_grid(n), dim3(256), 0, st, x, n, second, (uint8_t*)codes,
+             scale);
+  return hipGetLastError();
+}
+
+}  // namespace sbn

@@ -13,13 +13,27 @@
 #include <string>
 #include <vector>
 
-#include "sbn_internal.h"
+#include "api_util.h"
 
 using namespace sbn;
 
 namespace {
 
 thread_local char g_last_error[512] = "";
+
+bool debug_sync() {
+  static const bool on = [] {
+    const char* e = std::getenv("SBN_DEBUG_SYNC");
+    return e && e[0] == '1';
+  }();
+  return on;
+}
+
+thread_local bool g_injected = false;
+
+}  // namespace
+
+namespace sbn {
 
 sbn_status fail(sbn_status s, const char* fmt, ...) {
   va_list ap;
@@ -32,14 +46,6 @@ sbn_status fail(sbn_status s, const char* fmt, ...) {
 sbn_status ok() {
   g_last_error[0] = '\0';
   return SBN_OK;
-}
-
-bool debug_sync() {
-  static const bool on = [] {
-    const char* e = std::getenv("SBN_DEBUG_SYNC");
-    return e && e[0] == '1';
-  }();
-  return on;
 }
 
 // SBN_CHECK_FINITE=1: entry points scan their floating-point inputs for
@@ -58,8 +64,6 @@ sbn_status check_finite(const char* fn, const char* what, const void* x, int64_t
   return SBN_OK;
 }
 
-thread_local bool g_injected = false;
-
 sbn_status hip_result(hipError_t e, hipStream_t st, const char* what) {
   if (g_injected) {
     g_injected = false;
@@ -70,64 +74,15 @@ sbn_status hip_result(hipError_t e, hipStream_t st, const char* what) {
   return ok();
 }
 
-bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
+}  // namespace sbn
 
-constexpr int64_t K_MAX = int64_t(1) << 18;
-constexpr int64_t NUMEL_MAX = int64_t(1) << 37;   // elements of W, Xq, dX, dW
-constexpr int64_t ROWS_MAX = int64_t(1) << 40;    // any T or R (so that R*K, T*K fit in int64)
-constexpr int64_t SPAN_MAX = int64_t(1) << 40;    // rows times a leading dimension (Y, X, W, dY)
-
-// a * b < limit for 1 <= a, b, decided without forming the product
-bool prod_below(int64_t a, int64_t b, int64_t limit) { return a <= (limit - 1) / b; }
+namespace {
 
 sbn_status check_nm(int n, int m) {
   if (!(m == 4 || m == 8) || n < 1 || n > m)
     return fail(SBN_ERR_UNSUPPORTED_NM, "unsupported N:M ratio %d:%d (m in {4,8}, 1 <= n <= m)", n, m);
   return SBN_OK;
 }
-
-sbn_status check_k(int64_t K) {
-  if (K < 64 || K % 64 != 0 || K > K_MAX)
-    return fail(SBN_ERR_SHAPE, "K = %lld must be a positive multiple of 64 and <= 2^18", (long long)K);
-  return SBN_OK;
-}
-
-sbn_status check_rows(const char* name, int64_t v) {
-  if (v < 1) return fail(SBN_ERR_SHAPE, "%s = %lld must be >= 1", name, (long long)v);
-  if (v > ROWS_MAX) return fail(SBN_ERR_SHAPE, "%s = %lld exceeds 2^40", name, (long long)v);
-  return SBN_OK;
-}
-
-// rows x K elements (rows and K already checked): below NUMEL_MAX
-sbn_status check_numel(const char* fn, const char* what, int64_t rows, int64_t K) {
-  if (!prod_below(rows, K, NUMEL_MAX)) return fail(SBN_ERR_SHAPE, "%s: %s has 2^37 elements or more", fn, what);
-  return SBN_OK;
-}
-
-// a leading dimension of `len` elements per row, for `rows` rows (rows already checked)
-sbn_status check_ld(const char* name, int64_t ld, int64_t len, int64_t rows = 1) {
-  if (ld < len) return fail(SBN_ERR_SHAPE, "%s = %lld is smaller than the row length %lld", name, (long long)ld, (long long)len);
-  if (ld % 8 != 0) return fail(SBN_ERR_ALIGN, "%s = %lld is not a multiple of 8", name, (long long)ld);
-  if (!prod_below(rows, ld, SPAN_MAX))
-    return fail(SBN_ERR_SHAPE, "%s = %lld times %lld rows reaches 2^40 elements", name, (long long)ld, (long long)rows);
-  return SBN_OK;
-}
-
-#define SBN_TRY(expr)                 \
-  do {                                \
-    const sbn_status s_ = (expr);     \
-    if (s_ != SBN_OK) return s_;      \
-  } while (0)
-
-#define SBN_NONNULL(p)                                                        \
-  do {                                                                        \
-    if (!(p)) return fail(SBN_ERR_NULL, "%s: argument '%s' is NULL", fn, #p); \
-  } while (0)
-
-#define SBN_ALIGNED(p)                                                                         \
-  do {                                                                                         \
-    if ((p) && !aligned16(p)) return fail(SBN_ERR_ALIGN, "%s: '%s' is not 16-byte aligned", fn, #p); \
-  } while (0)
 
 size_t packed_codes(int64_t R, int64_t K, int n, int m) {
   return (size_t)round_up(R * K * n / (4 * m), 16);

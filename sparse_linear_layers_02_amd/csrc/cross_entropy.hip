@@ -1,0 +1,596 @@
+// Softmax cross entropy of the output head without keeping the logits, and its
+// gradients, on gfx950 bf16 matrix cores.
+//
+//   l = X W^T;  lse_t = log sum_v exp l[t,v];  loss_t = lse_t - l[t, y_t]
+//   D[t,v] = g_t (exp(l[t,v] - lse_t) - [v = y_t]);  dX = D W;  dW = D^T X
+//
+// Forward: one product whose epilogue reduces each tile of logits, while it is
+// in registers, to the maximum and the sum of exponentials of each token over
+// the tile's vocabulary entries, plus the target's logit where it falls in the
+// tile; a second launch joins the tiles' pairs (m, s) in a fixed order.
+//
+// Gradients, per piece of the vocabulary: the same product with an epilogue
+// that writes D in bf16, as D [t][v] and as its transpose; dX and dW are then
+// two more products of the same kind on D and the transposes of W and X.  The
+// workspace holds one piece of D, of at most D_ELEMS elements.
+//
+// All three products are one kernel: C[a][b] = sum_k A[a][k] B[b][k] with both
+// operands contiguous along the contraction.
+#include "train_internal.h"
+
+namespace sbn {
+namespace {
+
+constexpr int BK = 64;                              // contraction entries of one stage: 128-byte rows, one cache line
+constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
+constexpr int64_t D_ELEMS = int64_t(1) << 27;       // elements of D in the workspace
+constexpr int CUS = 256;
+
+enum Epi { EPI_STATS, EPI_GRAD, EPI_OUT };
+
+struct GemmArgs {
+  const uint16_t *A, *B;               // [nA][lda], [nB][ldb], contraction along the row
+  int64_t lda, ldb;
+  int nA, nB;                          // rows; tiles past them read the last row
+  int tilesA, tilesB;
+  int steps, splits;                   // contraction stages in all, and parts they are split into
+  // EPI_STATS, EPI_GRAD: A rows are vocabulary entries, B rows tokens
+  const void* labels;
+  bool labels64;
+  int v0;                              // vocabulary entry of A row 0
+  int V;
+  float2* stats;                       // [2-wave column groups][nB]: maximum (times log2 e), sum
+  float* target;                       // [nB] logit of the label
+  const float *lse, *dloss;
+  uint16_t *D, *DT;                    // [t][ldd], [v][lddt]
+  int64_t ldd, lddt;
+  int tpad, vpad;                      // rows written of D^T's columns, D's columns
+  // EPI_OUT: C [nB][ldc], A rows along the row
+  void* C;
+  const float* Cin;                    // added first, or NULL
+  float* part;                         // splits > 1: [splits][nB][nA] float32 instead of C
+  int64_t ldc;
+  bool c_f32;
+};
+
+__device__ inline int64_t label_at(const void* labels, bool is64, int t) {
+  return is64 ? ((const int64_t*)labels)[t] : (int64_t)((const int32_t*)labels)[t];
+}
+
+// Tile order: the hardware deals consecutive blocks to the 8 XCDs in turn, so
+// block b belongs to XCD b % 8.  Each XCD takes a contiguous range of a list in
+// which 8 B tiles go together and A runs inside: the 32 blocks an XCD has in
+// flight then share 8 B and about 4 A row panels in its L2.
+__device__ inline void tile_of(int b, int blocks, int nta, int ntb, int& ta, int& tb) {
+  constexpr int XCDS = 8, GROUP = 8;
+  const int per = blocks / XCDS, rem = blocks % XCDS;
+  const int x = b % XCDS;
+  int i = x * per + (x < rem ? x : rem) + b / XCDS;
+  const int g = i / (nta * GROUP);
+  i -= g * nta * GROUP;
+  const int w = ntb - g * GROUP < GROUP ? ntb - g * GROUP : GROUP;
+  ta = i / w;
+  tb = g * GROUP + i % w;
+}
+
+// acc += a b^T, the accumulator held in the accumulation registers.  Written in
+// assembly because the builtin's accumulators of a 256 x 256 tile were moved
+// between the register files around every matrix instruction (some 500 moves a
+// stage against 128 products).  What the compiler then does not see: a result
+// may be read by other instructions only some cycles later.  settle() waits for
+// that, and fetch() is the only way the accumulators are read after it.
+__device__ inline void mfma_acc(v4f& acc, v8bf a, v8bf b) {
+  asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(acc) : "v"(a), "v"(b));
+}
+__device__ inline void settle() { asm volatile("s_nop 15\n\ts_nop 15" ::: "memory"); }
+__device__ inline v4f fetch(v4f& acc) {
+  asm volatile("" : "+a"(acc));
+  return acc;
+}
+
+// WA x WB waves, wave tile 16 MI x 16 MJ, NST stages of LDS.
+template <int WA, int WB, int MI, int MJ, int NST, int EPI>
+__global__ __launch_bounds__(256, 1) void ce_gemm_kernel(GemmArgs P) {
+  constexpr int TA = WA * MI * 16, TB = WB * MJ * 16;
+  constexpr int A_BYTES = TA * BK * 2, STAGE = (TA + TB) * BK * 2;
+  constexpr int LA = TA / 32, LB = TB / 32;          // 1 KB loads per wave and stage
+  constexpr int LPS = LA + LB;
+  extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
+  static_assert(WA * WB == 4, "four waves");
+
+  const int tid = threadIdx.x;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
+  const int wa = wave % WA, wb = wave / WA;
+  const int tiles = P.tilesA * P.tilesB;
+  const int part = (int)blockIdx.x / tiles;
+  int ta, tb;
+  tile_of((int)blockIdx.x % tiles, tiles, P.tilesA, P.tilesB, ta, tb);
+  const int a0 = ta * TA, b0 = tb * TB;
+  const int s_lo = (int)((int64_t)P.steps * part / P.splits), s_hi = (int)((int64_t)P.steps * (part + 1) / P.splits);
+  const int nsteps = s_hi - s_lo;
+
+  // Row r of a tile is 8 chunks of 16 bytes; chunk c lies at position c ^ (r & 7),
+  // so that the 16 rows of a fragment read spread over the banks.  One load moves
+  // 8 rows: lane l brings row l / 8, the chunk of position l % 8.
+  uint32_t offA[LA], offB[LB];
+  const int lrow = lane >> 3, lchunk = (lane & 7) ^ lrow;
+#pragma unroll
+  for (int q = 0; q < LA; ++q) {
+    const int r = 8 * (wave * LA + q) + lrow;
+    offA[q] = (uint32_t)((a0 + r < P.nA ? r : P.nA - 1 - a0) * P.lda * 2 + lchunk * 16);
+  }
+#pragma unroll
+  for (int q = 0; q < LB; ++q) {
+    const int r = 8 * (wave * LB + q) + lrow;
+    offB[q] = (uint32_t)((b0 + r < P.nB ? r : P.nB - 1 - b0) * P.ldb * 2 + lchunk * 16);
+  }
+  const uint8_t* gA = (const uint8_t*)(P.A + (int64_t)a0 * P.lda) + (int64_t)s_lo * (BK * 2);
+  const uint8_t* gB = (const uint8_t*)(P.B + (int64_t)b0 * P.ldb) + (int64_t)s_lo * (BK * 2);
+
+  auto load_one = [&](int q, int slot, int step) {   // load q of LPS of a stage
+    uint8_t* base = smem + slot * STAGE;
+    if (q < LA) g2lds16(gA + (int64_t)step * (BK * 2) + offA[q], base + (wave * LA + q) * 1024);
+    else g2lds16(gB + (int64_t)step * (BK * 2) + offB[q - LA], base + A_BYTES + (wave * LB + q - LA) * 1024);
+  };
+
+  v4f acc[MI][MJ];
+#pragma unroll
+  for (int i = 0; i < MI; ++i)
+#pragma unroll
+    for (int j = 0; j < MJ; ++j) {
+      acc[i][j] = (v4f){0.f, 0.f, 0.f, 0.f};
+      asm volatile("" : "+a"(acc[i][j]));
+    }
+  settle();
+
+  // fragment of 16 rows x 32 contraction entries: lane l holds row l % 16, entries 8 (l / 16) .. + 8
+  const int frow = (lane & 15) * 128;
+  const int fpos0 = ((lane >> 4) ^ (lane & 7)) * 16, fpos1 = ((4 + (lane >> 4)) ^ (lane & 7)) * 16;
+  v8bf fa[2][MI], fb[2][MJ];
+  auto read_a = [&](int slot, int sub, int i) {
+    const uint8_t* p = smem + slot * STAGE + (wa * MI + i) * 2048 + frow + (sub ? fpos1 : fpos0);
+    fa[sub][i] = __builtin_bit_cast(v8bf, *(const v4i*)p);
+  };
+  auto read_b = [&](int slot, int sub, int j) {
+    const uint8_t* p = smem + slot * STAGE + A_BYTES + (wb * MJ + j) * 2048 + frow + (sub ? fpos1 : fpos0);
+    fb[sub][j] = __builtin_bit_cast(v8bf, *(const v4i*)p);
+  };
+
+  // The loop has no branches: past the last stage it loads that stage again and
+  // reads LDS that no product uses.
+#pragma unroll
+  for (int s = 0; s < NST; ++s)
+#pragma unroll
+    for (int q = 0; q < LPS; ++q) load_one(q, s, s < nsteps ? s : nsteps - 1);
+  wait_vmcnt<(NST - 1) * LPS>();                     // stage 0 has landed; the later ones may still fly
+  lds_barrier();
+#pragma unroll
+  for (int j = 0; j < MJ; ++j) read_b(0, 0, j);
+#pragma unroll
+  for (int i = 0; i < MI; ++i) read_a(0, 0, i);
+
+  // One stage is two halves of 32 contraction entries.  While the matrix
+  // instructions of the first half run, the second half's fragments are read;
+  // then all waves meet (this stage's LDS is free, the next stage has landed),
+  // and while the second half runs, the next stage's first fragments are read
+  // and the loads of the stage NST further on are issued into the freed LDS.
+  int slot = 0;
+  for (int s = 0; s < nsteps; ++s) {
+    const int next = slot + 1 == NST ? 0 : slot + 1;
+    const int ahead = s + NST < nsteps ? s + NST : nsteps - 1;
+#pragma unroll
+    for (int i = 0; i < MI; ++i) {
+#pragma unroll
+      for (int j = 0; j < MJ; ++j)
+        if (j * MI / MJ == i) read_b(slot, 1, j);
+      read_a(slot, 1, i);
+#pragma unroll
+      for (int j = 0; j < MJ; ++j) mfma_acc(acc[i][j], fa[0][i], fb[0][j]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    wait_vmcnt<(NST - 2) * LPS>();
+    lds_barrier();
+#pragma unroll
+    for (int i = 0; i < MI; ++i) {
+#pragma unroll
+      for (int j = 0; j < MJ; ++j)
+        if (j * MI / MJ == i) read_b(next, 0, j);
+      read_a(next, 0, i);
+#pragma unroll
+      for (int q = 0; q < LPS; ++q)
+        if (q * MI / LPS == i) load_one(q, slot, ahead);
+#pragma unroll
+      for (int j = 0; j < MJ; ++j) mfma_acc(acc[i][j], fa[1][i], fb[1][j]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    slot = next;
+  }
+  settle();
+  wait_vmcnt<0>();
+
+  // acc[i][j]: A rows aw + 16 i + 4 (lane / 16) + 0..3, B row bw + 16 j + lane % 16
+  const int aw = a0 + wa * MI * 16, bw = b0 + wb * MJ * 16;
+  const int l4 = 4 * (lane >> 4), l15 = lane & 15;
+
+  if (EPI == EPI_STATS) {
+    const bool ragged = aw + MI * 16 > P.nA;
+#pragma unroll
+    for (int j = 0; j < MJ; ++j) {
+      const int t = bw + 16 * j + l15;
+      const int64_t y = t < P.nB ? label_at(P.labels, P.labels64, t) : -1;
+      const int want = y >= 0 && y < P.V ? (int)y - aw - l4 : -1;
+      float m = -INFINITY, hit = 0.0f;
+      v4f c[MI];
+#pragma unroll
+      for (int i = 0; i < MI; ++i) {
+        c[i] = fetch(acc[i][j]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if (ragged && aw + 16 * i + l4 + e >= P.nA) c[i][e] = -INFINITY;
+          m = fmaxf(m, c[i][e]);
+          if (want == 16 * i + e) hit = c[i][e];
+        }
+      }
+      if (want >= 0 && want < MI * 16 && (want & 12) == 0) P.target[t] = hit;
+      m = fmaxf(m, __shfl_xor(m, 16));
+      m = fmaxf(m, __shfl_xor(m, 32));
+      const float top = fmaxf(m, -1.0e38f) * LOG2E;  // finite where the group lies past the vocabulary
+      float sum = 0.0f;
+#pragma unroll
+      for (int i = 0; i < MI; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sum += __builtin_amdgcn_exp2f(c[i][e] * LOG2E - top);
+      sum += __shfl_xor(sum, 16);
+      sum += __shfl_xor(sum, 32);
+      if (lane < 16 && t < P.nB) P.stats[(int64_t)(ta * WA + wa) * P.nB + t] = make_float2(top, sum);
+    }
+  } else if (EPI == EPI_GRAD) {
+    // D through LDS, [t][v] with rows of 2 TA + 32 bytes and 8 more after every
+    // 8 rows: lanes that write 4 entries each of 16 rows, read whole rows, and
+    // read one column pair of 32 row groups all spread over the banks.
+    constexpr int PITCH = 2 * TA + 32;
+    auto at = [&](int t, int v) { return smem + t * PITCH + (t >> 3) * 8 + v * 2; };
+    lds_barrier();                                   // every wave has read its last fragments
+#pragma unroll
+    for (int j = 0; j < MJ; ++j) {
+      const int tl = wb * MJ * 16 + 16 * j + l15, t = b0 + tl;
+      const bool live = t < P.nB;
+      const int64_t y = live ? label_at(P.labels, P.labels64, t) : -1;
+      const bool kept = y >= 0 && y < P.V;
+      const float g = kept ? P.dloss[t] : 0.0f, ls = live ? P.lse[t] * LOG2E : 0.0f;
+      const int want = kept ? (int)y - P.v0 - aw - l4 : -1;
+#pragma unroll
+      for (int i = 0; i < MI; ++i) {
+        const v4f c = fetch(acc[i][j]);
+        float d[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float p = __builtin_amdgcn_exp2f(c[e] * LOG2E - ls);
+          if (want == 16 * i + e) p -= 1.0f;
+          d[e] = kept && aw + 16 * i + l4 + e < P.nA ? g * p : 0.0f;
+        }
+        *(uint2*)at(tl, wa * MI * 16 + 16 * i + l4) = make_uint2(pack_bf16x2(d[0], d[1]), pack_bf16x2(d[2], d[3]));
+      }
+    }
+    __syncthreads();
+    // D: 16 bytes of a row a thread
+    for (int q = tid; q < TB * (TA / 8); q += 256) {
+      const int tl = q / (TA / 8), c = q % (TA / 8);
+      if (b0 + tl < P.nB && a0 + 8 * c < P.vpad) {
+        const uint2* p = (const uint2*)at(tl, 8 * c);
+        const uint2 x = p[0], z = p[1];
+        *(uint4*)(P.D + (int64_t)(b0 + tl) * P.ldd + a0 + 8 * c) = make_uint4(x.x, x.y, z.x, z.y);
+      }
+    }
+    // D^T: a pair of columns of 8 rows a thread
+    for (int q = tid; q < (TB / 8) * (TA / 2); q += 256) {
+      const int tg = q % (TB / 8), vp = q / (TB / 8);
+      if (b0 + 8 * tg < P.tpad && a0 + 2 * vp < P.vpad) {
+        uint32_t x[8];
+#pragma unroll
+        for (int r = 0; r < 8; ++r) x[r] = *(const uint32_t*)at(8 * tg + r, 2 * vp);
+        uint4 lo, hi;
+        lo.x = (x[0] & 0xFFFFu) | (x[1] << 16), hi.x = (x[0] >> 16) | (x[1] & 0xFFFF0000u);
+        lo.y = (x[2] & 0xFFFFu) | (x[3] << 16), hi.y = (x[2] >> 16) | (x[3] & 0xFFFF0000u);
+        lo.z = (x[4] & 0xFFFFu) | (x[5] << 16), hi.z = (x[4] >> 16) | (x[5] & 0xFFFF0000u);
+        lo.w = (x[6] & 0xFFFFu) | (x[7] << 16), hi.w = (x[6] >> 16) | (x[7] & 0xFFFF0000u);
+        uint16_t* o = P.DT + (int64_t)(a0 + 2 * vp) * P.lddt + b0 + 8 * tg;
+        *(uint4*)o = lo;
+        *(uint4*)(o + P.lddt) = hi;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < MJ; ++j) {
+      const int b = bw + 16 * j + l15;
+      if (b >= P.nB) continue;
+#pragma unroll
+      for (int i = 0; i < MI; ++i) {
+        const int a = aw + 16 * i + l4;              // nA is a multiple of 64
+        v4f c = fetch(acc[i][j]);
+        if (a >= P.nA) continue;
+        if (P.part) {
+          *(v4f*)(P.part + ((int64_t)part * P.nB + b) * P.nA + a) = c;
+          continue;
+        }
+        if (P.Cin) c += *(const v4f*)(P.Cin + (int64_t)b * P.nA + a);
+        if (P.c_f32) *(v4f*)((float*)P.C + (int64_t)b * P.ldc + a) = c;
+        else *(uint2*)((uint16_t*)P.C + (int64_t)b * P.ldc + a) = make_uint2(pack_bf16x2(c[0], c[1]), pack_bf16x2(c[2], c[3]));
+      }
+    }
+  }
+}
+
+// lse and loss of a token from its groups' (maximum, sum): 64 tokens a block,
+// 16 waves take every 16th group each, then the 16 pairs are joined in order
+__global__ __launch_bounds__(1024) void ce_join_kernel(const float2* __restrict__ stats, int groups, int T,
+                                                       const void* __restrict__ labels, bool labels64, int V,
+                                                       const float* __restrict__ target, float* __restrict__ loss,
+                                                       float* __restrict__ lse) {
+  __shared__ float2 sm[16][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int t = blockIdx.x * 64 + lane;
+  float m = -INFINITY, s = 0.0f;
+  auto join = [&](float2 p) {
+    const float top = fmaxf(m, p.x);
+    s = s * __builtin_amdgcn_exp2f(m - top) + p.y * __builtin_amdgcn_exp2f(p.x - top);
+    m = top;
+  };
+  if (t < T)
+    for (int g = wave; g < groups; g += 16) join(stats[(int64_t)g * T + t]);
+  sm[wave][lane] = make_float2(m, s);
+  __syncthreads();
+  if (wave == 0 && t < T) {
+    for (int w = 1; w < 16 && w < groups; ++w) join(sm[w][lane]);
+    const float l = m * LN2 + logf(s);
+    const int64_t y = label_at(labels, labels64, t);
+    lse[t] = l;
+    loss[t] = y >= 0 && y < V ? l - target[t] : 0.0f;
+  }
+}
+
+// src [rows][ld] bf16 -> dst [cols][dld] (cols a multiple of 64), dst columns
+// rows .. dld - 1 set to 0; dld a multiple of 64
+__global__ __launch_bounds__(256) void ce_transpose_kernel(const uint16_t* __restrict__ src, int64_t ld, int rows,
+                                                           uint16_t* __restrict__ dst, int64_t dld) {
+  __shared__ uint32_t sm[64][33];                    // two rows of a column in a word
+  const int r0 = (int)blockIdx.x * 64, c0 = (int)blockIdx.y * 64;
+  const int tid = threadIdx.x;
+  {
+    const int rp = tid >> 3, c = (tid & 7) * 8;      // rows 2 rp, 2 rp + 1, columns c .. c + 7
+    uint4 x = make_uint4(0u, 0u, 0u, 0u), y = x;
+    if (r0 + 2 * rp < rows) x = *(const uint4*)(src + (int64_t)(r0 + 2 * rp) * ld + c0 + c);
+    if (r0 + 2 * rp + 1 < rows) y = *(const uint4*)(src + (int64_t)(r0 + 2 * rp + 1) * ld + c0 + c);
+    const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      sm[c + 2 * i][rp] = (xs[i] & 0xFFFFu) | (ys[i] << 16);
+      sm[c + 2 * i + 1][rp] = (xs[i] >> 16) | (ys[i] & 0xFFFF0000u);
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int q = tid + 256 * h, c = q >> 3, w = (q & 7) * 4;
+    *(uint4*)(dst + (int64_t)(c0 + c) * dld + r0 + 2 * w) = make_uint4(sm[c][w], sm[c][w + 1], sm[c][w + 2], sm[c][w + 3]);
+  }
+}
+
+// C[row][a] = Cin[row][a] (if any) + the sum over the parts, 4 columns a thread;
+// Cin [rows][cols] may be C itself
+__global__ __launch_bounds__(256) void ce_sum_kernel(const float* __restrict__ part, int splits, int64_t rows, int cols,
+                                                     const float* Cin, void* C, bool c_f32, int64_t ldc) {
+  const int64_t n = rows * (cols / 4);
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+    v4f c = ((const v4f*)part)[i];
+    for (int p = 1; p < splits; ++p) c += ((const v4f*)part)[p * n + i];
+    if (Cin) c += ((const v4f*)Cin)[i];
+    const int64_t r = i / (cols / 4), a = (i - r * (cols / 4)) * 4;
+    if (c_f32) *(v4f*)((float*)C + r * ldc + a) = c;
+    else *(uint2*)((uint16_t*)C + r * ldc + a) = make_uint2(pack_bf16x2(c[0], c[1]), pack_bf16x2(c[2], c[3]));
+  }
+}
+
+__global__ __launch_bounds__(256) void zero_rows_kernel(uint8_t* p, int64_t rows, int64_t len16, int64_t ld16) {
+  const int64_t n = rows * len16;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+    const int64_t r = i / len16;
+    ((uint4*)p)[r * ld16 + (i - r * len16)] = make_uint4(0u, 0u, 0u, 0u);
+  }
+}
+
+int grid_for(int64_t items) {
+  const int64_t b = cdiv(items, 256);
+  return (int)(b < 8192 ? b : 8192);
+}
+
+// ---------------------------------------------------------------- tile shapes
+// wide: 256 x 256, one block per compute unit; square: 128 x 128; flat: 128 A
+// rows x 64 B rows, for few tokens.
+enum Tile { WIDE, SQUARE, FLAT };
+struct TileShape {
+  int a, b;
+};
+constexpr TileShape SHAPE[] = {{256, 256}, {128, 128}, {128, 64}};
+
+template <int WA, int WB, int MI, int MJ, int NST, int EPI>
+hipError_t run_gemm(const char* name, const GemmArgs& P, hipStream_t st) {
+  constexpr int TA = WA * MI * 16, TB = WB * MJ * 16;
+  constexpr size_t stages = (size_t)NST * (TA + TB) * BK * 2;
+  constexpr size_t dtile = EPI == EPI_GRAD ? (size_t)TB * (2 * TA + 32) + TB : 0;
+  constexpr size_t lds = stages > dtile ? stages : dtile;
+  static const hipError_t e = hipFuncSetAttribute((const void*)ce_gemm_kernel<WA, WB, MI, MJ, NST, EPI>,
+                                                  hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+  if (e != hipSuccess) return e;
+  SBN_LAUNCH(name, (ce_gemm_kernel<WA, WB, MI, MJ, NST, EPI>), dim3((unsigned)(P.tilesA * P.tilesB * P.splits)),
+             dim3(256), lds, st, P);
+  return hipGetLastError();
+}
+
+template <int EPI>
+hipError_t gemm(const char* name, Tile tile, GemmArgs& P, hipStream_t st) {
+  P.tilesA = (int)cdiv(P.nA, SHAPE[tile].a);
+  P.tilesB = (int)cdiv(P.nB, SHAPE[tile].b);
+  switch (tile) {
+    case WIDE: return run_gemm<2, 2, 8, 8, 2, EPI>(name, P, st);
+    case SQUARE: return run_gemm<2, 2, 4, 4, 2, EPI>(name, P, st);
+    default: return run_gemm<4, 1, 2, 4, 4, EPI>(name, P, st);
+  }
+}
+
+int64_t tiles_of(Tile t, int64_t a, int64_t b) { return cdiv(a, SHAPE[t].a) * cdiv(b, SHAPE[t].b); }
+
+Tile pick_tile(int64_t a, int64_t b) {
+  if (b <= 64) return FLAT;
+  return tiles_of(WIDE, a, b) >= CUS ? WIDE : SQUARE;
+}
+
+// parts of a product with too few tiles for the machine
+int pick_splits(Tile t, int64_t a, int64_t b, int64_t steps) {
+  const int64_t n = tiles_of(t, a, b);
+  int64_t s = 2 * CUS / n;
+  if (s > steps / 8) s = steps / 8;                  // at least 8 stages a part
+  return (int)(s < 1 ? 1 : s > 16 ? 16 : s);
+}
+
+struct CePlan {
+  int64_t tpad;                        // tokens along a contraction
+  int64_t piece;                       // vocabulary entries of one piece, a multiple of 256
+  int64_t pieces;
+  Tile tile_x, tile_w;
+  int splits_x, splits_w;              // of dX over the piece, of dW over the tokens
+  size_t d, dt, wt, xt, acc, part, total;
+};
+
+CePlan ce_plan(int64_t T, int64_t V, int64_t K) {
+  CePlan L;
+  L.tpad = round_up(T, 64);
+  int64_t most = D_ELEMS / L.tpad / 256 * 256;
+  if (most < 256) most = 256;
+  const int64_t vpad = round_up(V, 256);
+  L.pieces = cdiv(vpad, most);
+  L.piece = round_up(cdiv(vpad, L.pieces), 256);
+  L.pieces = cdiv(V, L.piece);
+  L.tile_x = pick_tile(K, T);
+  L.splits_x = pick_splits(L.tile_x, K, T, L.piece / BK);
+  L.tile_w = pick_tile(K, L.piece);
+  L.splits_w = pick_splits(L.tile_w, K, L.piece, L.tpad / BK);
+  size_t o = 0;
+  auto take = [&](size_t bytes) {
+    const size_t at = o;
+    o += align256(bytes);
+    return at;
+  };
+  L.d = take((size_t)T * L.piece * 2);
+  L.dt = take((size_t)L.piece * L.tpad * 2);
+  L.wt = take((size_t)K * L.piece * 2);
+  L.xt = take((size_t)K * L.tpad * 2);
+  L.acc = take(L.pieces > 1 ? (size_t)T * K * 4 : 0);
+  const size_t px = L.splits_x > 1 ? (size_t)L.splits_x * T * K * 4 : 0;
+  const size_t pw = L.splits_w > 1 ? (size_t)L.splits_w * L.piece * K * 4 : 0;
+  L.part = take(px > pw ? px : pw);
+  L.total = o;
+  return L;
+}
+
+hipError_t transpose(const uint16_t* src, int64_t ld, int64_t rows, int64_t cols, uint16_t* dst, int64_t dld,
+                     hipStream_t st) {
+  SBN_LAUNCH("ce_transpose", ce_transpose_kernel, dim3((unsigned)(dld / 64), (unsigned)(cols / 64)), dim3(256), 0, st,
+             src, ld, (int)rows, dst, dld);
+  return hipGetLastError();
+}
+
+// C [nB][ldc] = A B^T with its sum over splits
+hipError_t product(const char* name, Tile tile, GemmArgs P, float* part, hipStream_t st) {
+  P.part = P.splits > 1 ? part : nullptr;
+  const hipError_t e = gemm<EPI_OUT>(name, tile, P, st);
+  if (e != hipSuccess || P.splits == 1) return e;
+  SBN_LAUNCH("ce_sum", ce_sum_kernel, dim3((unsigned)grid_for((int64_t)P.nB * (P.nA / 4))), dim3(256), 0, st, part,
+             P.splits, (int64_t)P.nB, P.nA, P.Cin, P.C, P.c_f32, P.ldc);
+  return hipGetLastError();
+}
+
+Tile stats_tile(int64_t T, int64_t V) { return pick_tile(V, T); }
+int64_t stats_groups(int64_t T, int64_t V) {
+  const Tile t = stats_tile(T, V);
+  return cdiv(V, SHAPE[t].a) * (t == FLAT ? 4 : 2);
+}
+
+}  // namespace
+
+size_t ce_ws_bytes(int64_t T, int64_t V, int64_t /*K*/) {
+  return align256((size_t)T * sizeof(float)) + align256((size_t)stats_groups(T, V) * T * sizeof(float2));
+}
+
+hipError_t launch_ce(const uint16_t* X, int64_t ldx, const uint16_t* W, int64_t ldw, const void* labels,
+                     bool labels64, int64_t T, int64_t V, int64_t K, float* loss, float* lse, void* ws,
+                     hipStream_t st) {
+  GemmArgs P{};
+  P.A = W, P.lda = ldw, P.nA = (int)V;
+  P.B = X, P.ldb = ldx, P.nB = (int)T;
+  P.steps = (int)(K / BK), P.splits = 1;
+  P.labels = labels, P.labels64 = labels64, P.V = (int)V;
+  P.target = (float*)ws;
+  P.stats = (float2*)((uint8_t*)ws + align256((size_t)T * sizeof(float)));
+  const hipError_t e = gemm<EPI_STATS>("ce_logits", stats_tile(T, V), P, st);
+  if (e != hipSuccess) return e;
+  SBN_LAUNCH("ce_join", ce_join_kernel, dim3((unsigned)cdiv(T, 64)), dim3(1024), 0, st, P.stats,
+             (int)stats_groups(T, V), (int)T, labels, labels64, (int)V, P.target, loss, lse);
+  return hipGetLastError();
+}
+
+size_t ce_bwd_ws_bytes(int64_t T, int64_t V, int64_t K) { return ce_plan(T, V, K).total; }
+
+hipError_t launch_ce_backward(const uint16_t* X, int64_t ldx, const uint16_t* W, int64_t ldw, const void* labels,
+                              bool labels64, const float* lse, const float* dloss, int64_t T, int64_t V, int64_t K,
+                              void* dX, bool dx_f32, int64_t lddx, void* dW, bool dw_f32, int64_t lddw, void* ws,
+                              hipStream_t st) {
+  const CePlan L = ce_plan(T, V, K);
+  uint8_t* w = (uint8_t*)ws;
+  uint16_t *D = (uint16_t*)(w + L.d), *DT = (uint16_t*)(w + L.dt), *WT = (uint16_t*)(w + L.wt),
+           *XT = (uint16_t*)(w + L.xt);
+  float *acc = (float*)(w + L.acc), *part = (float*)(w + L.part);
+  hipError_t e;
+  if (dW && (e = transpose(X, ldx, T, K, XT, L.tpad, st)) != hipSuccess) return e;
+  for (int64_t i = 0; i < L.pieces; ++i) {
+    const int64_t v0 = i * L.piece, nv = V - v0 < L.piece ? V - v0 : L.piece;
+    const int64_t vpad = round_up(nv, 64);           // contraction of dX over this piece
+    GemmArgs G{};
+    G.A = W + v0 * ldw, G.lda = ldw, G.nA = (int)nv;
+    G.B = X, G.ldb = ldx, G.nB = (int)T;
+    G.steps = (int)(K / BK), G.splits = 1;
+    G.labels = labels, G.labels64 = labels64, G.v0 = (int)v0, G.V = (int)V;
+    G.lse = lse, G.dloss = dloss;
+    G.D = D, G.DT = DT, G.ldd = L.piece, G.lddt = L.tpad, G.tpad = (int)L.tpad, G.vpad = (int)vpad;
+    if ((e = gemm<EPI_GRAD>("ce_dlogits", pick_tile(nv, T), G, st)) != hipSuccess) return e;
+    if (dX) {
+      if ((e = transpose(W + v0 * ldw, ldw, nv, K, WT, vpad, st)) != hipSuccess) return e;
+      GemmArgs P{};
+      P.A = WT, P.lda = vpad, P.nA = (int)K;
+      P.B = D, P.ldb = L.piece, P.nB = (int)T;
+      P.steps = (int)(vpad / BK), P.splits = L.splits_x <= P.steps ? L.splits_x : P.steps;
+      const bool last = i + 1 == L.pieces;
+      P.Cin = i > 0 ? acc : nullptr;
+      P.C = last ? dX : acc, P.c_f32 = last ? dx_f32 : true, P.ldc = last ? lddx : K;
+      if ((e = product("ce_dx", L.tile_x, P, part, st)) != hipSuccess) return e;
+    }
+    if (dW) {
+      GemmArgs P{};
+      P.A = XT, P.lda = L.tpad, P.nA = (int)K;
+      P.B = DT, P.ldb = L.tpad, P.nB = (int)nv;
+      P.steps = (int)(L.tpad / BK), P.splits = L.splits_w;
+      P.C = (uint8_t*)dW + v0 * lddw * (dw_f32 ? 4 : 2), P.c_f32 = dw_f32, P.ldc = lddw;
+      if ((e = product("ce_dw", L.tile_w, P, part, st)) != hipSuccess) return e;
+    }
+  }
+  return hipSuccess;
+}
+
+hipError_t launch_zero_rows(void* p, int64_t rows, int64_t len, int64_t ld, int elem_bytes, hipStream_t st) {
+  const int64_t l16 = len * elem_bytes / 16;
+  SBN_LAUNCH("zero_rows", zero_rows_kernel, dim3((unsigned)grid_for(rows * l16)), dim3(256), 0, st, (uint8_t*)p, rows,
+             l16, ld * elem_bytes / 16);
+  return hipGetLastError();
+}
+
+}  // namespace sbn

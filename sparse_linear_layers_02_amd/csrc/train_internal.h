@@ -1,0 +1,45 @@
+// Launchers of the operators declared in include/sbn_train.h.
+#pragma once
+
+#include "sbn_internal.h"
+#include "sbn_train.h"
+
+namespace sbn {
+
+// ----------------------------------------------------------------- RMS norm (T >= 1)
+// Xq != NULL: the 8-bit form (Y unused); otherwise Y.
+hipError_t launch_rmsnorm(const void* X, int64_t ldx, const void* res, int64_t ldr, bool f32, const void* gain,
+                          bool gain_f32, int64_t T, int64_t K, float eps, void* H, int64_t ldh, void* Y, int64_t ldy,
+                          int8_t* Xq, float* s_x, float* rstd, hipStream_t st);
+size_t rmsnorm_bwd_ws_bytes(int64_t T, int64_t K);
+hipError_t launch_rmsnorm_backward(const void* dY, int64_t lddy, const void* H, int64_t ldh, const void* dH,
+                                   int64_t lddh, bool f32, const void* gain, bool gain_f32, const float* rstd,
+                                   int64_t T, int64_t K, void* dX, int64_t lddx, float* dgain, void* ws,
+                                   hipStream_t st);
+
+// ----------------------------------------------------------------- cross entropy (T >= 1)
+size_t ce_ws_bytes(int64_t T, int64_t V, int64_t K);
+size_t ce_bwd_ws_bytes(int64_t T, int64_t V, int64_t K);
+hipError_t launch_ce(const uint16_t* X, int64_t ldx, const uint16_t* W, int64_t ldw, const void* labels,
+                     bool labels64, int64_t T, int64_t V, int64_t K, float* loss, float* lse, void* ws,
+                     hipStream_t st);
+hipError_t launch_ce_backward(const uint16_t* X, int64_t ldx, const uint16_t* W, int64_t ldw, const void* labels,
+                              bool labels64, const float* lse, const float* dloss, int64_t T, int64_t V, int64_t K,
+                              void* dX, bool dx_f32, int64_t lddx, void* dW, bool dw_f32, int64_t lddw, void* ws,
+                              hipStream_t st);
+// rows x len elements of `elem_bytes` at row stride ld, all set to 0
+hipError_t launch_zero_rows(void* p, int64_t rows, int64_t len, int64_t ld, int elem_bytes, hipStream_t st);
+
+// ----------------------------------------------------------------- AdamW
+constexpr int ADAMW_CHUNK = 2048;   // elements of one block: 8 per thread
+struct AdamWScalars {
+  float beta1, one_minus_beta1, beta2, one_minus_beta2, eps;
+  float lr, bias1, bias2;           // 1 - beta^step
+};
+hipError_t launch_adamw(const sbn_adamw_entry* entries, const int32_t* map, int64_t blocks, bool p_f32, bool g_f32,
+                        bool state8, const AdamWScalars& s, const float* dyn, hipStream_t st);
+hipError_t launch_adamw_decode(const void* codes, const float* scale, int64_t n, bool second, float* out,
+                               hipStream_t st);
+hipError_t launch_adamw_encode(const float* x, int64_t n, bool second, void* codes, float* scale, hipStream_t st);
+
+}  // namespace sbn

@@ -1,0 +1,209 @@
+"""The C ABI of include/sbn_train.h without a GPU: exported symbols, sizes, the
+AdamW launch plan, and refusals, which come before any launch (fake device
+addresses that nothing dereferences are enough)."""
+from __future__ import annotations
+
+import ctypes
+
+import pytest
+
+import sparse_linear_layers_02_amd as sbn
+
+OK, NULL, SHAPE, NM, ALIGN, WS, DTYPE, HIP, FLAGS, VALUE = range(10)
+P, P2, P3 = (ctypes.c_void_p(a) for a in (0x100000, 0x200000, 0x300000))
+MIS = ctypes.c_void_p(0x100004)
+F32, BF16 = sbn.SBN_F32, sbn.SBN_BF16
+
+
+@pytest.fixture(scope="module")
+def L():
+    return sbn.lib()
+
+
+def test_exports_every_header_symbol(L):
+    names = sbn.train_header_symbols()
+    assert len(names) == 12
+    for nm in names:
+        assert hasattr(L, nm), nm
+    assert not set(names) & set(sbn.header_symbols())
+
+
+@pytest.mark.parametrize("quant", [False, True])
+def test_rmsnorm_refusals(L, quant):
+    base = dict(X=P, ldx=64, res=P2, ldr=64, dt=BF16, gain=P3, gdt=F32, T=4, K=64, eps=1e-6, H=P2, ldh=64, Y=P, ldy=64,
+                s=P, rstd=P)
+
+    def call(**kw):
+        a = {**base, **kw}
+        head = (a["X"], a["ldx"], a["res"], a["ldr"], a["dt"], a["gain"], a["gdt"], a["T"], a["K"], a["eps"], a["H"],
+                a["ldh"])
+        if quant:
+            return L.sbn_rmsnorm_quant(*head, a["Y"], a["s"], a["rstd"], None)
+        return L.sbn_rmsnorm(*head, a["Y"], a["ldy"], a["rstd"], None)
+
+    assert call(T=0) == OK and call(T=0, X=None, gain=None, Y=None) == OK      # nothing to do
+    for kw, status in [(dict(X=None), NULL), (dict(gain=None), NULL), (dict(Y=None), NULL), (dict(H=None), NULL),
+                       (dict(T=-1), SHAPE), (dict(K=0), SHAPE), (dict(K=60), SHAPE), (dict(K=32776), SHAPE),
+                       (dict(T=1 << 41), SHAPE), (dict(T=1 << 36), SHAPE), (dict(ldx=56), SHAPE), (dict(ldx=68), ALIGN),
+                       (dict(ldr=56), SHAPE), (dict(ldh=68), ALIGN), (dict(dt=2), DTYPE), (dict(gdt=7), DTYPE),
+                       (dict(eps=-1.0), VALUE), (dict(eps=float("nan")), VALUE), (dict(eps=float("inf")), VALUE),
+                       (dict(X=MIS), ALIGN), (dict(gain=MIS), ALIGN), (dict(res=MIS), ALIGN), (dict(H=MIS), ALIGN),
+                       (dict(Y=MIS), ALIGN), (dict(rstd=MIS), ALIGN), (dict(H=P2, ldh=72), SHAPE)]:
+        assert call(**kw) == status, kw
+        assert sbn.lib().sbn_last_error() != b""
+    if quant:
+        assert call(s=None) == NULL and call(s=MIS) == ALIGN
+    else:
+        assert call(ldy=56) == SHAPE and call(ldy=68) == ALIGN
+
+
+def test_rmsnorm_backward_refusals(L):
+    base = dict(dY=P, lddy=64, H=P2, ldh=64, dH=P3, lddh=64, dt=F32, gain=P, gdt=BF16, rstd=P, T=4, K=64, dX=P2, lddx=64,
+                dg=P, ws=P3, wsb=1 << 20)
+
+    def call(**kw):
+        a = {**base, **kw}
+        return L.sbn_rmsnorm_backward(a["dY"], a["lddy"], a["H"], a["ldh"], a["dH"], a["lddh"], a["dt"], a["gain"],
+                                      a["gdt"], a["rstd"], a["T"], a["K"], a["dX"], a["lddx"], a["dg"], a["ws"],
+                                      a["wsb"], None)
+
+    for kw, status in [(dict(dY=None), NULL), (dict(H=None), NULL), (dict(gain=None), NULL), (dict(rstd=None), NULL),
+                       (dict(dX=None), NULL), (dict(dg=None), NULL), (dict(ws=None), NULL), (dict(wsb=256), WS),
+                       (dict(K=12), SHAPE), (dict(T=-2), SHAPE), (dict(lddy=32), SHAPE), (dict(lddh=66), ALIGN),
+                       (dict(lddx=66), ALIGN), (dict(dt=3), DTYPE), (dict(gdt=3), DTYPE), (dict(dH=MIS), ALIGN),
+                       (dict(dX=MIS), ALIGN), (dict(dX=P, lddx=128), SHAPE), (dict(dX=P3, lddx=128), SHAPE)]:
+        assert call(**kw) == status, kw
+    b = ctypes.c_size_t()
+    assert L.sbn_rmsnorm_backward_workspace_bytes(4, 64, ctypes.byref(b)) == OK and b.value == 1024
+    assert L.sbn_rmsnorm_backward_workspace_bytes(1 << 20, 4096, ctypes.byref(b)) == OK and b.value <= 1 << 24
+    assert L.sbn_rmsnorm_backward_workspace_bytes(4, 64, None) == NULL
+
+
+def test_cross_entropy_refusals(L):
+    big = 1 << 40
+    base = dict(X=P, ldx=128, W=P2, ldw=128, lab=P3, lb=8, T=5, V=1000, K=128, loss=P, lse=P2, ws=P3, wsb=big, dloss=P,
+                dX=P, dxdt=BF16, lddx=128, dW=P2, dwdt=F32, lddw=128)
+
+    def both(**kw):
+        a = {**base, **kw}
+        head = (a["X"], a["ldx"], a["W"], a["ldw"], a["lab"], a["lb"])
+        return (L.sbn_cross_entropy(*head, a["T"], a["V"], a["K"], a["loss"], a["lse"], a["ws"], a["wsb"], None),
+                L.sbn_cross_entropy_backward(*head, a["lse"], a["dloss"], a["T"], a["V"], a["K"], a["dX"], a["dxdt"],
+                                             a["lddx"], a["dW"], a["dwdt"], a["lddw"], a["ws"], a["wsb"], None))
+
+    for kw, status in [(dict(X=None), NULL), (dict(W=None), NULL), (dict(lab=None), NULL), (dict(lse=None), NULL),
+                       (dict(ws=None), NULL), (dict(wsb=16), WS), (dict(T=-1), SHAPE), (dict(V=0), SHAPE),
+                       (dict(V=1 << 31), SHAPE), (dict(K=96), SHAPE), (dict(K=0), SHAPE), (dict(ldx=120), SHAPE),
+                       (dict(ldw=132), ALIGN), (dict(ldx=(1 << 22) + 8), SHAPE), (dict(T=1 << 27), SHAPE),
+                       (dict(T=1 << 24, V=1 << 20), SHAPE), (dict(lb=2), DTYPE), (dict(X=MIS), ALIGN),
+                       (dict(W=MIS), ALIGN), (dict(lab=MIS), ALIGN), (dict(lse=MIS), ALIGN), (dict(ws=MIS), ALIGN)]:
+        assert both(**kw) == (status, status), kw
+    assert both(loss=None)[0] == NULL and both(loss=MIS)[0] == ALIGN
+    for kw, status in [(dict(dloss=None), NULL), (dict(dloss=MIS), ALIGN), (dict(dxdt=2), DTYPE), (dict(dwdt=9), DTYPE),
+                       (dict(lddx=64), SHAPE), (dict(lddw=132), ALIGN), (dict(dX=MIS), ALIGN), (dict(dW=MIS), ALIGN)]:
+        assert both(**kw)[1] == status, kw
+    assert both(T=0, X=None, W=None, dW=None) == (OK, OK)                      # nothing to do
+    assert both(dX=None, dW=None)[1] == OK                                     # no gradient asked for
+
+
+def test_cross_entropy_workspace_is_bounded():
+    """The backward's workspace holds a piece of D (and its transpose), not T x V."""
+    wsb = sbn.sbn_cross_entropy_workspace_bytes
+    T, V, K = 8192, 262144, 4096
+    assert wsb(T, V, K, True) < T * V * 2 * 2 / 4
+    assert wsb(T, V, K) < T * V * 2 / 16
+    assert wsb(0, V, K) == 0 and wsb(0, V, K, True) == 0
+
+
+def _entries(*rows):
+    from sparse_linear_layers_02_amd.training import _AdamWEntry
+    e = (_AdamWEntry * len(rows))()
+    for x, kw in zip(e, rows):
+        x.p, x.grad, x.m, x.v, x.m_scale, x.v_scale, x.shadow = 1 << 20, 1 << 21, 1 << 22, 1 << 23, 1 << 24, 1 << 25, None
+        x.n, x.weight_decay = 10, 0.1
+        for k, v in kw.items():
+            setattr(x, k, v)
+    return e
+
+
+def test_adamw_plan_and_refusals(L):
+    blocks = ctypes.c_int64(-1)
+
+    def plan(e, pdt=F32, gdt=F32, bits=32, mp=None, count=None):
+        return L.sbn_adamw_plan(e, len(e) if count is None else count, pdt, gdt, bits, mp, ctypes.byref(blocks))
+
+    e = _entries(dict(n=1), dict(n=0, p=None), dict(n=2048), dict(n=2049), dict(n=6000))
+    assert plan(e) == OK and blocks.value == 1 + 0 + 1 + 2 + 3
+    mp = (ctypes.c_int32 * (2 * blocks.value))()
+    assert plan(e, mp=mp) == OK
+    assert list(mp) == [0, 0, 2, 0, 3, 0, 3, 1, 4, 0, 4, 1, 4, 2]
+    for kw, status in [(dict(p=None), NULL), (dict(v=None), NULL), (dict(n=-1), SHAPE), (dict(n=1 << 37), SHAPE),
+                       (dict(grad=(1 << 21) + 4), ALIGN), (dict(weight_decay=float("nan")), VALUE)]:
+        assert plan(_entries({}, kw)) == status, kw
+        assert b"entry 1" in L.sbn_last_error()
+    assert plan(_entries(dict(m_scale=None)), bits=8) == NULL
+    assert plan(_entries(dict(m_scale=(1 << 24) + 2)), bits=8) == ALIGN
+    assert plan(_entries(dict(shadow=1 << 26)), pdt=BF16) == DTYPE
+    assert plan(_entries({}), bits=16) == DTYPE and plan(_entries({}), pdt=2) == DTYPE and plan(_entries({}), gdt=2) == DTYPE
+    assert plan(_entries({}), count=-1) == SHAPE
+    assert L.sbn_adamw_plan(None, 1, F32, F32, 32, None, ctypes.byref(blocks)) == NULL
+    assert L.sbn_adamw_plan(None, 0, F32, F32, 32, None, ctypes.byref(blocks)) == OK and blocks.value == 0
+    assert L.sbn_adamw_plan(e, 1, F32, F32, 32, None, None) == NULL
+
+
+def test_adamw_step_refusals(L):
+    base = dict(e=P, m=P2, blocks=3, pdt=F32, gdt=F32, bits=32, lr=1e-3, b1=0.9, b2=0.999, eps=1e-8, step=1, dyn=None)
+
+    def call(**kw):
+        a = {**base, **kw}
+        return L.sbn_adamw_step(a["e"], a["m"], a["blocks"], a["pdt"], a["gdt"], a["bits"], a["lr"], a["b1"], a["b2"],
+                                a["eps"], a["step"], a["dyn"], None)
+
+    assert call(blocks=0, e=None, m=None) == OK
+    for kw, status in [(dict(e=None), NULL), (dict(m=None), NULL), (dict(blocks=-1), SHAPE), (dict(blocks=1 << 37), SHAPE),
+                       (dict(pdt=2), DTYPE), (dict(bits=4), DTYPE), (dict(lr=float("inf")), VALUE), (dict(b1=1.0), VALUE),
+                       (dict(b2=-0.1), VALUE), (dict(b2=float("nan")), VALUE), (dict(eps=-1.0), VALUE),
+                       (dict(step=0), VALUE), (dict(dyn=MIS), ALIGN), (dict(e=MIS), ALIGN)]:
+        assert call(**kw) == status, kw
+    for f, head in ((L.sbn_adamw_decode_state, lambda c, s, n, o: (c, s, n, 0, o, None)),
+                    (L.sbn_adamw_encode_state, lambda c, s, n, o: (o, n, 1, c, s, None))):
+        assert f(*head(P, P2, 0, P3)) == OK
+        assert f(*head(P, P2, -1, P3)) == SHAPE and f(*head(None, P2, 5, P3)) == NULL
+        assert f(*head(P, None, 5, P3)) == NULL and f(*head(P, P2, 5, MIS)) == ALIGN
+
+
+def test_binding_refuses_layouts_the_abi_cannot_see():
+    import torch
+    bf, f32 = torch.bfloat16, torch.float32
+    z = lambda *s, dt=bf: torch.zeros(*s, dtype=dt)  # noqa: E731
+    bad = [
+        lambda: sbn.sbn_rmsnorm(z(4, 64, dt=torch.float16), z(64)),
+        lambda: sbn.sbn_rmsnorm(z(4, 64), z(32)),
+        lambda: sbn.sbn_rmsnorm(z(64, 4).t(), z(64)),
+        lambda: sbn.sbn_rmsnorm(z(4, 64), z(64), residual=z(4, 64, dt=f32)),
+        lambda: sbn.sbn_rmsnorm(z(4, 64), z(64), H=z(4, 64)),
+        lambda: sbn.sbn_rmsnorm_quant(z(4, 64), z(64), Xq=z(4, 64)),
+        lambda: sbn.sbn_rmsnorm_quant(z(4, 64), z(64), s_x=z(5, dt=f32)),
+        lambda: sbn.sbn_rmsnorm_backward(z(4, 64), z(4, 64), z(64), z(3, dt=f32)),
+        lambda: sbn.sbn_rmsnorm_backward(z(4, 64, dt=f32), z(4, 64), z(64), z(4, dt=f32)),
+        lambda: sbn.sbn_cross_entropy(z(4, 64), z(10, 128), z(4, dt=torch.int64)),
+        lambda: sbn.sbn_cross_entropy(z(4, 64, dt=f32), z(10, 64), z(4, dt=torch.int64)),
+        lambda: sbn.sbn_cross_entropy(z(4, 64), z(10, 64), z(4, dt=torch.int16)),
+        lambda: sbn.sbn_cross_entropy(z(4, 64), z(10, 64), z(8, dt=torch.int64)[::2]),
+        lambda: sbn.sbn_cross_entropy_backward(z(4, 64), z(10, 64), z(4, dt=torch.int64), z(4, dt=f32), z(4)),
+        lambda: sbn.sbn_cross_entropy_backward(z(4, 64), z(10, 64), z(4, dt=torch.int64), z(4, dt=f32), z(4, dt=f32),
+                                               dX=z(4, 64, dt=f32)),
+        lambda: sbn.AdamWTable([], [], [], []),
+        lambda: sbn.AdamWTable([z(8)], [z(9)], [z(8, dt=f32)], [z(8, dt=f32)]),
+        lambda: sbn.AdamWTable([z(8)], [z(8)], [z(8)], [z(8, dt=f32)]),
+        lambda: sbn.AdamWTable([z(8), z(8, dt=f32)], [z(8)] * 2, [z(8, dt=f32)] * 2, [z(8, dt=f32)] * 2),
+        lambda: sbn.AdamWTable([z(8)], [z(8)], [z(8, dt=torch.int8)], [z(8, dt=torch.uint8)], m_scales=[z(1, dt=f32)]),
+        lambda: sbn.AdamWTable([z(16)[::2]], [z(8)], [z(8, dt=f32)], [z(8, dt=f32)]),
+        lambda: sbn.sbn_adamw_step(None, lr=1e-3, step=1),
+        lambda: sbn.sbn_adamw_decode_m(z(8, dt=torch.uint8), z(1, dt=f32)),
+        lambda: sbn.sbn_adamw_encode_v(z(8)),
+    ]
+    for i, f in enumerate(bad):
+        with pytest.raises(sbn.SbnError):
+            f()
+            raise AssertionError(f"case {i} was accepted")
