@@ -93,15 +93,33 @@ __device__ inline v4f fetch(v4f& acc) {
   return acc;
 }
 
-// WA x WB waves, wave tile 16 MI x 16 MJ, NST stages of LDS.
-template <int WA, int WB, int MI, int MJ, int NST, int EPI>
-__global__ __launch_bounds__(256, 1) void ce_gemm_kernel(GemmArgs P) {
-  constexpr int TA = WA * MI * 16, TB = WB * MJ * 16;
-  constexpr int A_BYTES = TA * BK * 2, STAGE = (TA + TB) * BK * 2;
-  constexpr int LA = TA / 32, LB = TB / 32;          // 1 KB loads per wave and stage
-  constexpr int LPS = LA + LB;
+// All waves meet: each has its LDS reads and all but its latest N loads behind it.
+// By the builtin, so that the compiler knows the reads done and adds no wait.
+template <int N>
+__device__ inline void stage_barrier() {
+  static_assert(N >= 0 && N < 64, "vmcnt range");
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4));
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+// WA x WB waves, wave tile 16 MI x 16 MJ, RING half stages of LDS.
+//
+// A stage is 64 contraction entries of the tile's rows, so that a row of it is
+// one 128-byte line (half of that, with twice the stages in flight, measured
+// 10% slower).  It is loaded in two halves, the upper rows of A and of B and
+// then the lower ones, each into the next place of a ring of RING places: the
+// loads go out evenly over a stage instead of all after its barrier.
+template <int WA, int WB, int MI, int MJ, int RING, int EPI>
+__global__ __launch_bounds__(64 * WA * WB, 1) void ce_gemm_kernel(GemmArgs P) {
+  constexpr int TA = WA * MI * 16, TB = WB * MJ * 16, NW = WA * WB, NT = 64 * NW;
+  constexpr int ROW = BK * 2;
+  constexpr int A_BYTES = TA / 2 * ROW, HALF = (TA + TB) / 2 * ROW;
+  constexpr int LA = TA / (16 * NW), LB = TB / (16 * NW);    // 1 KB loads per wave and half stage
+  constexpr int LPH = LA + LB;
   extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
-  static_assert(WA * WB == 4, "four waves");
+  static_assert(RING >= 5 && (RING - 3) * LPH < 64, "places of a stage, the next one and a half in flight");
 
   const int tid = threadIdx.x;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
@@ -114,28 +132,31 @@ __global__ __launch_bounds__(256, 1) void ce_gemm_kernel(GemmArgs P) {
   const int s_lo = (int)((int64_t)P.steps * part / P.splits), s_hi = (int)((int64_t)P.steps * (part + 1) / P.splits);
   const int nsteps = s_hi - s_lo;
 
-  // Row r of a tile is 8 chunks of 16 bytes; chunk c lies at position c ^ (r & 7),
-  // so that the 16 rows of a fragment read spread over the banks.  One load moves
-  // 8 rows: lane l brings row l / 8, the chunk of position l % 8.
-  uint32_t offA[LA], offB[LB];
+  // Row r is 8 chunks of 16 bytes; chunk c lies at position c ^ (r & 7), so that
+  // the 16 rows of a fragment read spread over the banks.  One load moves 8 rows:
+  // lane l brings row l / 8, the chunk of position l % 8.
+  uint32_t offA[2][LA], offB[2][LB];
   const int lrow = lane >> 3, lchunk = (lane & 7) ^ lrow;
 #pragma unroll
-  for (int q = 0; q < LA; ++q) {
-    const int r = 8 * (wave * LA + q) + lrow;
-    offA[q] = (uint32_t)((a0 + r < P.nA ? r : P.nA - 1 - a0) * P.lda * 2 + lchunk * 16);
-  }
+  for (int h = 0; h < 2; ++h) {
 #pragma unroll
-  for (int q = 0; q < LB; ++q) {
-    const int r = 8 * (wave * LB + q) + lrow;
-    offB[q] = (uint32_t)((b0 + r < P.nB ? r : P.nB - 1 - b0) * P.ldb * 2 + lchunk * 16);
+    for (int q = 0; q < LA; ++q) {
+      const int r = h * (TA / 2) + 8 * (wave * LA + q) + lrow;
+      offA[h][q] = (uint32_t)((a0 + r < P.nA ? r : P.nA - 1 - a0) * P.lda * 2 + lchunk * 16);
+    }
+#pragma unroll
+    for (int q = 0; q < LB; ++q) {
+      const int r = h * (TB / 2) + 8 * (wave * LB + q) + lrow;
+      offB[h][q] = (uint32_t)((b0 + r < P.nB ? r : P.nB - 1 - b0) * P.ldb * 2 + lchunk * 16);
+    }
   }
-  const uint8_t* gA = (const uint8_t*)(P.A + (int64_t)a0 * P.lda) + (int64_t)s_lo * (BK * 2);
-  const uint8_t* gB = (const uint8_t*)(P.B + (int64_t)b0 * P.ldb) + (int64_t)s_lo * (BK * 2);
+  const uint8_t* gA = (const uint8_t*)(P.A + (int64_t)a0 * P.lda) + (int64_t)s_lo * ROW;
+  const uint8_t* gB = (const uint8_t*)(P.B + (int64_t)b0 * P.ldb) + (int64_t)s_lo * ROW;
 
-  auto load_one = [&](int q, int slot, int step) {   // load q of LPS of a stage
-    uint8_t* base = smem + slot * STAGE;
-    if (q < LA) g2lds16(gA + (int64_t)step * (BK * 2) + offA[q], base + (wave * LA + q) * 1024);
-    else g2lds16(gB + (int64_t)step * (BK * 2) + offB[q - LA], base + A_BYTES + (wave * LB + q - LA) * 1024);
+  auto load_one = [&](int q, int h, int place, int step) {   // load q of LPH of a half stage
+    uint8_t* base = smem + place * HALF;
+    if (q < LA) g2lds16(gA + (int64_t)step * ROW + offA[h][q], base + (wave * LA + q) * 1024);
+    else g2lds16(gB + (int64_t)step * ROW + offB[h][q - LA], base + A_BYTES + (wave * LB + q - LA) * 1024);
   };
 
   v4f acc[MI][MJ];
@@ -149,66 +170,75 @@ __global__ __launch_bounds__(256, 1) void ce_gemm_kernel(GemmArgs P) {
   settle();
 
   // fragment of 16 rows x 32 contraction entries: lane l holds row l % 16, entries 8 (l / 16) .. + 8
-  const int frow = (lane & 15) * 128;
+  const int frow = (lane & 15) * ROW;
   const int fpos0 = ((lane >> 4) ^ (lane & 7)) * 16, fpos1 = ((4 + (lane >> 4)) ^ (lane & 7)) * 16;
   v8bf fa[2][MI], fb[2][MJ];
-  auto read_a = [&](int slot, int sub, int i) {
-    const uint8_t* p = smem + slot * STAGE + (wa * MI + i) * 2048 + frow + (sub ? fpos1 : fpos0);
+  // fragment i of A (j of B) of the stage whose halves lie at places p0 and p1
+  auto read_a = [&](int p0, int p1, int sub, int i) {
+    const int f = WA > 1 ? wa % (WA / 2) * MI + i : i % (MI / 2);
+    const bool lower = WA > 1 ? wa >= WA / 2 : i >= MI / 2;
+    const uint8_t* p = smem + (lower ? p1 : p0) * HALF + f * (16 * ROW) + frow + (sub ? fpos1 : fpos0);
     fa[sub][i] = __builtin_bit_cast(v8bf, *(const v4i*)p);
   };
-  auto read_b = [&](int slot, int sub, int j) {
-    const uint8_t* p = smem + slot * STAGE + A_BYTES + (wb * MJ + j) * 2048 + frow + (sub ? fpos1 : fpos0);
+  auto read_b = [&](int p0, int p1, int sub, int j) {
+    const int f = WB > 1 ? wb % (WB / 2) * MJ + j : j % (MJ / 2);
+    const bool lower = WB > 1 ? wb >= WB / 2 : j >= MJ / 2;
+    const uint8_t* p = smem + (lower ? p1 : p0) * HALF + A_BYTES + f * (16 * ROW) + frow + (sub ? fpos1 : fpos0);
     fb[sub][j] = __builtin_bit_cast(v8bf, *(const v4i*)p);
   };
+  auto wrap = [](int p) { return p >= RING ? p - RING : p; };
+  auto clamp = [&](int s) { return s < nsteps ? s : nsteps - 1; };
 
-  // The loop has no branches: past the last stage it loads that stage again and
-  // reads LDS that no product uses.
+  // Half stage u (stage u / 2) lies at place u % RING.  Stage s: while the matrix
+  // instructions of its first 32 entries run, the fragments of the second 32 are
+  // read, and half stage 2 s + RING - 1 is loaded into the place of 2 s - 1; then
+  // all waves meet (stage s has been read, stage s + 1 has landed), and while
+  // the second 32 run, the next stage's first fragments are read, and half stage
+  // 2 s + RING is loaded into the place of 2 s.  The loop has no branches: past
+  // the last stage it loads that stage again and reads LDS that no product uses.
 #pragma unroll
-  for (int s = 0; s < NST; ++s)
+  for (int u = 0; u < RING - 1; ++u)
 #pragma unroll
-    for (int q = 0; q < LPS; ++q) load_one(q, s, s < nsteps ? s : nsteps - 1);
-  wait_vmcnt<(NST - 1) * LPS>();                     // stage 0 has landed; the later ones may still fly
-  lds_barrier();
+    for (int q = 0; q < LPH; ++q) load_one(q, u & 1, u, clamp(u / 2));
+  stage_barrier<(RING - 3) * LPH>();                 // half stages 0 and 1 have landed
 #pragma unroll
-  for (int j = 0; j < MJ; ++j) read_b(0, 0, j);
+  for (int j = 0; j < MJ; ++j) read_b(0, 1, 0, j);
 #pragma unroll
-  for (int i = 0; i < MI; ++i) read_a(0, 0, i);
+  for (int i = 0; i < MI; ++i) read_a(0, 1, 0, i);
 
-  // One stage is two halves of 32 contraction entries.  While the matrix
-  // instructions of the first half run, the second half's fragments are read;
-  // then all waves meet (this stage's LDS is free, the next stage has landed),
-  // and while the second half runs, the next stage's first fragments are read
-  // and the loads of the stage NST further on are issued into the freed LDS.
-  int slot = 0;
+  constexpr int H0 = (RING - 1) & 1, H1 = RING & 1;  // which halves the two phases load
+  int p0 = 0;                                        // place of half stage 2 s
   for (int s = 0; s < nsteps; ++s) {
-    const int next = slot + 1 == NST ? 0 : slot + 1;
-    const int ahead = s + NST < nsteps ? s + NST : nsteps - 1;
+    const int p1 = wrap(p0 + 1), n0 = wrap(p0 + 2), n1 = wrap(p0 + 3), free0 = wrap(p0 + RING - 1);
+    const int s0 = clamp(s + (RING - 1) / 2), s1 = clamp(s + RING / 2);
 #pragma unroll
     for (int i = 0; i < MI; ++i) {
 #pragma unroll
       for (int j = 0; j < MJ; ++j)
-        if (j * MI / MJ == i) read_b(slot, 1, j);
-      read_a(slot, 1, i);
+        if (j * MI / MJ == i) read_b(p0, p1, 1, j);
+      read_a(p0, p1, 1, i);
+#pragma unroll
+      for (int q = 0; q < LPH; ++q)
+        if (q * MI / LPH == i) load_one(q, H0, free0, s0);
 #pragma unroll
       for (int j = 0; j < MJ; ++j) mfma_acc(acc[i][j], fa[0][i], fb[0][j]);
       __builtin_amdgcn_sched_barrier(0);
     }
-    wait_vmcnt<(NST - 2) * LPS>();
-    lds_barrier();
+    stage_barrier<(RING - 4) * LPH>();
 #pragma unroll
     for (int i = 0; i < MI; ++i) {
 #pragma unroll
       for (int j = 0; j < MJ; ++j)
-        if (j * MI / MJ == i) read_b(next, 0, j);
-      read_a(next, 0, i);
+        if (j * MI / MJ == i) read_b(n0, n1, 0, j);
+      read_a(n0, n1, 0, i);
 #pragma unroll
-      for (int q = 0; q < LPS; ++q)
-        if (q * MI / LPS == i) load_one(q, slot, ahead);
+      for (int q = 0; q < LPH; ++q)
+        if (q * MI / LPH == i) load_one(q, H1, p0, s1);
 #pragma unroll
       for (int j = 0; j < MJ; ++j) mfma_acc(acc[i][j], fa[1][i], fb[1][j]);
       __builtin_amdgcn_sched_barrier(0);
     }
-    slot = next;
+    p0 = n0;
   }
   settle();
   wait_vmcnt<0>();
@@ -280,7 +310,7 @@ __global__ __launch_bounds__(256, 1) void ce_gemm_kernel(GemmArgs P) {
     }
     __syncthreads();
     // D: 16 bytes of a row a thread
-    for (int q = tid; q < TB * (TA / 8); q += 256) {
+    for (int q = tid; q < TB * (TA / 8); q += NT) {
       const int tl = q / (TA / 8), c = q % (TA / 8);
       if (b0 + tl < P.nB && a0 + 8 * c < P.vpad) {
         const uint2* p = (const uint2*)at(tl, 8 * c);
@@ -289,7 +319,7 @@ __global__ __launch_bounds__(256, 1) void ce_gemm_kernel(GemmArgs P) {
       }
     }
     // D^T: a pair of columns of 8 rows a thread
-    for (int q = tid; q < (TB / 8) * (TA / 2); q += 256) {
+    for (int q = tid; q < (TB / 8) * (TA / 2); q += NT) {
       const int tg = q % (TB / 8), vp = q / (TB / 8);
       if (b0 + 8 * tg < P.tpad && a0 + 2 * vp < P.vpad) {
         uint32_t x[8];
@@ -444,17 +474,17 @@ struct TileShape {
 };
 constexpr TileShape SHAPE[] = {{256, 256}, {128, 128}, {128, 64}};
 
-template <int WA, int WB, int MI, int MJ, int NST, int EPI>
+template <int WA, int WB, int MI, int MJ, int RING, int EPI>
 hipError_t run_gemm(const char* name, const GemmArgs& P, hipStream_t st) {
   constexpr int TA = WA * MI * 16, TB = WB * MJ * 16;
-  constexpr size_t stages = (size_t)NST * (TA + TB) * BK * 2;
+  constexpr size_t stages = (size_t)RING * (TA + TB) / 2 * BK * 2;
   constexpr size_t dtile = EPI == EPI_GRAD ? (size_t)TB * (2 * TA + 32) + TB : 0;
   constexpr size_t lds = stages > dtile ? stages : dtile;
-  static const hipError_t e = hipFuncSetAttribute((const void*)ce_gemm_kernel<WA, WB, MI, MJ, NST, EPI>,
+  static const hipError_t e = hipFuncSetAttribute((const void*)ce_gemm_kernel<WA, WB, MI, MJ, RING, EPI>,
                                                   hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
   if (e != hipSuccess) return e;
-  SBN_LAUNCH(name, (ce_gemm_kernel<WA, WB, MI, MJ, NST, EPI>), dim3((unsigned)(P.tilesA * P.tilesB * P.splits)),
-             dim3(256), lds, st, P);
+  SBN_LAUNCH(name, (ce_gemm_kernel<WA, WB, MI, MJ, RING, EPI>), dim3((unsigned)(P.tilesA * P.tilesB * P.splits)),
+             dim3(64 * WA * WB), lds, st, P);
   return hipGetLastError();
 }
 
@@ -463,9 +493,9 @@ hipError_t gemm(const char* name, Tile tile, GemmArgs& P, hipStream_t st) {
   P.tilesA = (int)cdiv(P.nA, SHAPE[tile].a);
   P.tilesB = (int)cdiv(P.nB, SHAPE[tile].b);
   switch (tile) {
-    case WIDE: return run_gemm<2, 2, 8, 8, 2, EPI>(name, P, st);
-    case SQUARE: return run_gemm<2, 2, 4, 4, 2, EPI>(name, P, st);
-    default: return run_gemm<4, 1, 2, 4, 4, EPI>(name, P, st);
+    case WIDE: return run_gemm<2, 4, 8, 4, 5, EPI>(name, P, st);
+    case SQUARE: return run_gemm<2, 2, 4, 4, 5, EPI>(name, P, st);
+    default: return run_gemm<4, 1, 2, 4, 8, EPI>(name, P, st);
   }
 }
 
