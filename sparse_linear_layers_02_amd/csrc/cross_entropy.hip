@@ -27,6 +27,7 @@ namespace {
 
 constexpr int BK = 64;                              // contraction entries of one stage: 128-byte rows, one cache line
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
+constexpr float NONE = -1.0e38f * LOG2E;            // the (scaled) maximum of no logits: finite, so that NONE - NONE is 0
 constexpr int64_t D_ELEMS = int64_t(1) << 27;       // elements of D in the workspace
 constexpr int CUS = 256;
 
@@ -64,10 +65,11 @@ __device__ inline int64_t label_at(const void* labels, bool is64, int t) {
 
 // Tile order: the hardware deals consecutive blocks to the 8 XCDs in turn, so
 // block b belongs to XCD b % 8.  Each XCD takes a contiguous range of a list in
-// which 8 B tiles go together and A runs inside: the 32 blocks an XCD has in
-// flight then share 8 B and about 4 A row panels in its L2.
+// which 4 B tiles go together and A runs inside: the 32 blocks an XCD has in
+// flight then share 4 B and 8 A row panels in its L2.  (T = 8192, V = 65536,
+// K = 4096, gradients included: 13.08 ms with 4, 13.23 with 8, 13.4 with 16.)
 __device__ inline void tile_of(int b, int blocks, int nta, int ntb, int& ta, int& tb) {
-  constexpr int XCDS = 8, GROUP = 8;
+  constexpr int XCDS = 8, GROUP = 4;
   const int per = blocks / XCDS, rem = blocks % XCDS;
   const int x = b % XCDS;
   int i = x * per + (x < rem ? x : rem) + b / XCDS;
@@ -103,6 +105,8 @@ __device__ inline void stage_barrier() {
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
 }
+
+__device__ inline void lds_reads_done() { __builtin_amdgcn_s_waitcnt(15 | (3 << 14) | (7 << 4)); }
 
 // WA x WB waves, wave tile 16 MI x 16 MJ, RING half stages of LDS.
 //
@@ -211,6 +215,7 @@ __global__ __launch_bounds__(64 * WA * WB, 1) void ce_gemm_kernel(GemmArgs P) {
   for (int s = 0; s < nsteps; ++s) {
     const int p1 = wrap(p0 + 1), n0 = wrap(p0 + 2), n1 = wrap(p0 + 3), free0 = wrap(p0 + RING - 1);
     const int s0 = clamp(s + (RING - 1) / 2), s1 = clamp(s + RING / 2);
+    lds_reads_done();                                // before new reads, which the first products need not wait for
 #pragma unroll
     for (int i = 0; i < MI; ++i) {
 #pragma unroll
@@ -269,7 +274,7 @@ __global__ __launch_bounds__(64 * WA * WB, 1) void ce_gemm_kernel(GemmArgs P) {
       if (want >= 0 && want < MI * 16 && (want & 12) == 0) P.target[t] = hit;
       m = fmaxf(m, __shfl_xor(m, 16));
       m = fmaxf(m, __shfl_xor(m, 32));
-      const float top = fmaxf(m, -1.0e38f) * LOG2E;  // finite where the group lies past the vocabulary
+      const float top = fmaxf(m * LOG2E, NONE);        // a group past the vocabulary has no logits
       float sum = 0.0f;
 #pragma unroll
       for (int i = 0; i < MI; ++i)
@@ -359,28 +364,43 @@ __global__ __launch_bounds__(64 * WA * WB, 1) void ce_gemm_kernel(GemmArgs P) {
   }
 }
 
-// lse and loss of a token from its groups' (maximum, sum): 64 tokens a block,
-// 16 waves take every 16th group each, then the 16 pairs are joined in order
+// lse and loss of a token from its groups' (maximum, sum): 16 tokens a block, 64
+// threads a token take every 64th group each, then the 64 pairs are joined in a
+// tree.  (64 tokens a block and 16 threads a token took 31 us for 17 tokens of
+// 50001 entries: one block, whose loads wait for each other.)
 __global__ __launch_bounds__(1024) void ce_join_kernel(const float2* __restrict__ stats, int groups, int T,
                                                        const void* __restrict__ labels, bool labels64, int V,
                                                        const float* __restrict__ target, float* __restrict__ loss,
                                                        float* __restrict__ lse) {
-  __shared__ float2 sm[16][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int t = blockIdx.x * 64 + lane;
-  float m = -INFINITY, s = 0.0f;
-  auto join = [&](float2 p) {
-    const float top = fmaxf(m, p.x);
-    s = s * __builtin_amdgcn_exp2f(m - top) + p.y * __builtin_amdgcn_exp2f(p.x - top);
-    m = top;
+  __shared__ float2 sm[64][17];
+  const int tl = threadIdx.x & 15, part = threadIdx.x >> 4;
+  const int t = blockIdx.x * 16 + tl;
+  auto join = [](float2 a, float2 b) {
+    const float top = fmaxf(a.x, b.x);
+    return make_float2(top, a.y * __builtin_amdgcn_exp2f(a.x - top) + b.y * __builtin_amdgcn_exp2f(b.x - top));
   };
-  if (t < T)
-    for (int g = wave; g < groups; g += 16) join(stats[(int64_t)g * T + t]);
-  sm[wave][lane] = make_float2(m, s);
+  float2 a = make_float2(NONE, 0.0f);
+  if (t < T) {
+    constexpr int AHEAD = 8;
+    for (int g = part; g < groups; g += 64 * AHEAD) {
+      float2 x[AHEAD];
+#pragma unroll
+      for (int k = 0; k < AHEAD; ++k)
+        x[k] = g + 64 * k < groups ? stats[(int64_t)(g + 64 * k) * T + t] : make_float2(NONE, 0.0f);
+#pragma unroll
+      for (int k = 0; k < AHEAD; ++k) a = join(a, x[k]);
+    }
+  }
+  sm[part][tl] = a;
   __syncthreads();
-  if (wave == 0 && t < T) {
-    for (int w = 1; w < 16 && w < groups; ++w) join(sm[w][lane]);
-    const float l = m * LN2 + logf(s);
+#pragma unroll
+  for (int d = 32; d >= 1; d >>= 1) {
+    if (part < d) sm[part][tl] = join(sm[part][tl], sm[part + d][tl]);
+    __syncthreads();
+  }
+  if (part == 0 && t < T) {
+    a = sm[0][tl];
+    const float l = a.x * LN2 + logf(a.y);
     const int64_t y = label_at(labels, labels64, t);
     lse[t] = l;
     loss[t] = y >= 0 && y < V ? l - target[t] : 0.0f;
@@ -495,31 +515,49 @@ hipError_t gemm(const char* name, Tile tile, GemmArgs& P, hipStream_t st) {
   switch (tile) {
     case WIDE: return run_gemm<2, 4, 8, 4, 5, EPI>(name, P, st);
     case SQUARE: return run_gemm<2, 2, 4, 4, 5, EPI>(name, P, st);
-    default: return run_gemm<4, 1, 2, 4, 8, EPI>(name, P, st);
+    default: return run_gemm<4, 1, 2, 4, 6, EPI>(name, P, st);
   }
 }
 
 int64_t tiles_of(Tile t, int64_t a, int64_t b) { return cdiv(a, SHAPE[t].a) * cdiv(b, SHAPE[t].b); }
 
-Tile pick_tile(int64_t a, int64_t b) {
-  if (b <= 64) return FLAT;
-  return tiles_of(WIDE, a, b) >= CUS ? WIDE : SQUARE;
+// parts of a product whose tiles are too few for the machine: as many as fill
+// `slots` blocks, of at least 16 stages each
+int pick_splits(int64_t tiles, int64_t steps, int slots) {
+  int64_t s = slots / tiles;
+  if (s > steps / 16) s = steps / 16;
+  return (int)(s < 1 ? 1 : s > 16 ? 16 : s);
 }
 
-// parts of a product with too few tiles for the machine
-int pick_splits(Tile t, int64_t a, int64_t b, int64_t steps) {
-  const int64_t n = tiles_of(t, a, b);
-  int64_t s = 2 * CUS / n;
-  if (s > steps / 8) s = steps / 8;                  // at least 8 stages a part
-  return (int)(s < 1 ? 1 : s > 16 ? 16 : s);
+// The tile shape of a product and the parts its contraction is split into
+// (splittable: 1 .. 16).  By the time of its rounds, in stages of a wide tile: a
+// compute unit runs one wide block, or two square ones, which take 0.7 stages
+// for a stage of each (measured 0.64 to 0.75 at the shapes below), and a block
+// costs 6 stages beside its contraction.
+struct Choice {
+  Tile tile;
+  int splits;
+};
+Choice pick(int64_t a, int64_t b, int64_t steps, bool splittable) {
+  if (b <= 64) return {FLAT, splittable ? pick_splits(tiles_of(FLAT, a, b), steps, 2 * CUS) : 1};
+  Choice best{WIDE, 1};
+  double least = 0;
+  for (const Tile t : {WIDE, SQUARE}) {
+    const int slots = t == WIDE ? CUS : 2 * CUS;
+    const int64_t n = tiles_of(t, a, b);
+    const int s = splittable ? pick_splits(n, steps, slots) : 1;
+    const double each = (double)cdiv(steps, s) * (t == WIDE ? 1.0 : 0.7) + 6.0 + (s > 1 ? 2.0 : 0.0);
+    const double time = (double)cdiv(n * s, slots) * each;
+    if (t == WIDE || time < least) best = {t, s}, least = time;
+  }
+  return best;
 }
 
 struct CePlan {
   int64_t tpad;                        // tokens along a contraction
   int64_t piece;                       // vocabulary entries of one piece, a multiple of 256
   int64_t pieces;
-  Tile tile_x, tile_w;
-  int splits_x, splits_w;              // of dX over the piece, of dW over the tokens
+  Choice x, w;                         // of dX, split over the piece, and dW, split over the tokens
   size_t gmax, d, dt, wt, xt, acc, part, total;
 };
 
@@ -532,10 +570,8 @@ CePlan ce_plan(int64_t T, int64_t V, int64_t K) {
   L.pieces = cdiv(vpad, most);
   L.piece = round_up(cdiv(vpad, L.pieces), 256);
   L.pieces = cdiv(V, L.piece);
-  L.tile_x = pick_tile(K, T);
-  L.splits_x = pick_splits(L.tile_x, K, T, L.piece / BK);
-  L.tile_w = pick_tile(K, L.piece);
-  L.splits_w = pick_splits(L.tile_w, K, L.piece, L.tpad / BK);
+  L.x = pick(K, T, L.piece / BK, true);
+  L.w = pick(K, L.piece, L.tpad / BK, true);
   size_t o = 0;
   auto take = [&](size_t bytes) {
     const size_t at = o;
@@ -548,8 +584,8 @@ CePlan ce_plan(int64_t T, int64_t V, int64_t K) {
   L.wt = take((size_t)K * L.piece * 2);
   L.xt = take((size_t)K * L.tpad * 2);
   L.acc = take(L.pieces > 1 ? (size_t)T * K * 4 : 0);
-  const size_t px = L.splits_x > 1 ? (size_t)L.splits_x * T * K * 4 : 0;
-  const size_t pw = L.splits_w > 1 ? (size_t)L.splits_w * L.piece * K * 4 : 0;
+  const size_t px = L.x.splits > 1 ? (size_t)L.x.splits * T * K * 4 : 0;
+  const size_t pw = L.w.splits > 1 ? (size_t)L.w.splits * L.piece * K * 4 : 0;
   L.part = take(px > pw ? px : pw);
   L.total = o;
   return L;
@@ -572,16 +608,16 @@ hipError_t product(const char* name, Tile tile, GemmArgs P, float* part, hipStre
   return hipGetLastError();
 }
 
-Tile stats_tile(int64_t T, int64_t V) { return pick_tile(V, T); }
-int64_t stats_groups(int64_t T, int64_t V) {
-  const Tile t = stats_tile(T, V);
+Tile stats_tile(int64_t T, int64_t V, int64_t K) { return pick(V, T, K / BK, false).tile; }
+int64_t stats_groups(int64_t T, int64_t V, int64_t K) {
+  const Tile t = stats_tile(T, V, K);
   return cdiv(V, SHAPE[t].a) * (t == FLAT ? 4 : 2);
 }
 
 }  // namespace
 
-size_t ce_ws_bytes(int64_t T, int64_t V, int64_t /*K*/) {
-  return align256((size_t)T * sizeof(float)) + align256((size_t)stats_groups(T, V) * T * sizeof(float2));
+size_t ce_ws_bytes(int64_t T, int64_t V, int64_t K) {
+  return align256((size_t)T * sizeof(float)) + align256((size_t)stats_groups(T, V, K) * T * sizeof(float2));
 }
 
 hipError_t launch_ce(const uint16_t* X, int64_t ldx, const uint16_t* W, int64_t ldw, const void* labels,
@@ -594,10 +630,10 @@ hipError_t launch_ce(const uint16_t* X, int64_t ldx, const uint16_t* W, int64_t 
   P.labels = labels, P.labels64 = labels64, P.V = (int)V;
   P.target = (float*)ws;
   P.stats = (float2*)((uint8_t*)ws + align256((size_t)T * sizeof(float)));
-  const hipError_t e = gemm<EPI_STATS>("ce_logits", stats_tile(T, V), P, st);
+  const hipError_t e = gemm<EPI_STATS>("ce_logits", stats_tile(T, V, K), P, st);
   if (e != hipSuccess) return e;
-  SBN_LAUNCH("ce_join", ce_join_kernel, dim3((unsigned)cdiv(T, 64)), dim3(1024), 0, st, P.stats,
-             (int)stats_groups(T, V), (int)T, labels, labels64, (int)V, P.target, loss, lse);
+  SBN_LAUNCH("ce_join", ce_join_kernel, dim3((unsigned)cdiv(T, 16)), dim3(1024), 0, st, P.stats,
+             (int)stats_groups(T, V, K), (int)T, labels, labels64, (int)V, P.target, loss, lse);
   return hipGetLastError();
 }
 
@@ -626,27 +662,27 @@ hipError_t launch_ce_backward(const uint16_t* X, int64_t ldx, const uint16_t* W,
     G.labels = labels, G.labels64 = labels64, G.v0 = (int)v0, G.V = (int)V;
     G.lse = lse, G.dloss = dloss, G.gmax = gmax;
     G.D = D, G.DT = DT, G.ldd = L.piece, G.lddt = L.tpad, G.tpad = (int)L.tpad, G.vpad = (int)vpad;
-    if ((e = gemm<EPI_GRAD>("ce_dlogits", pick_tile(nv, T), G, st)) != hipSuccess) return e;
+    if ((e = gemm<EPI_GRAD>("ce_dlogits", pick(nv, T, G.steps, false).tile, G, st)) != hipSuccess) return e;
     if (dX) {
       if ((e = transpose(W + v0 * ldw, ldw, nv, K, WT, vpad, st)) != hipSuccess) return e;
       GemmArgs P{};
       P.A = WT, P.lda = vpad, P.nA = (int)K;
       P.B = D, P.ldb = L.piece, P.nB = (int)T;
-      P.steps = (int)(vpad / BK), P.splits = L.splits_x <= P.steps ? L.splits_x : P.steps;
+      P.steps = (int)(vpad / BK), P.splits = L.x.splits <= P.steps ? L.x.splits : P.steps;
       const bool last = i + 1 == L.pieces;
       P.Cin = i > 0 ? acc : nullptr;
       P.gmax = last ? gmax : nullptr;
       P.C = last ? dX : acc, P.c_f32 = last ? dx_f32 : true, P.ldc = last ? lddx : K;
-      if ((e = product("ce_dx", L.tile_x, P, part, st)) != hipSuccess) return e;
+      if ((e = product("ce_dx", L.x.tile, P, part, st)) != hipSuccess) return e;
     }
     if (dW) {
       GemmArgs P{};
       P.A = XT, P.lda = L.tpad, P.nA = (int)K;
       P.B = DT, P.ldb = L.tpad, P.nB = (int)nv;
-      P.steps = (int)(L.tpad / BK), P.splits = L.splits_w;
+      P.steps = (int)(L.tpad / BK), P.splits = L.w.splits;
       P.C = (uint8_t*)dW + v0 * lddw * (dw_f32 ? 4 : 2), P.c_f32 = dw_f32, P.ldc = lddw;
       P.gmax = gmax;
-      if ((e = product("ce_dw", L.tile_w, P, part, st)) != hipSuccess) return e;
+      if ((e = product("ce_dw", L.w.tile, P, part, st)) != hipSuccess) return e;
     }
   }
   return hipSuccess;
