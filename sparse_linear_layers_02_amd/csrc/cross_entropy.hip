@@ -14,12 +14,15 @@
 // tile; a second launch joins the tiles' pairs (m, s) in a fixed order.
 //
 // Gradients, per piece of the vocabulary: the same product with an epilogue
-// that writes D in bf16, as D [t][v] and as its transpose; dX and dW are then
-// two more products of the same kind on D and the transposes of W and X.  The
-// workspace holds one piece of D, of at most D_ELEMS elements.
+// that writes D in bf16; dX and dW are then two more products, on D and W and on
+// D and X as they lie.  The workspace holds one piece of D, of at most D_ELEMS
+// elements.
 //
-// All three products are one kernel: C[a][b] = sum_k A[a][k] B[b][k] with both
-// operands contiguous along the contraction.
+// All three products are one kernel, C[a][b] = sum_k A[a][k] B[b][k], where an
+// operand's rows in memory are either its outputs (X and W of the logits, D of
+// dX) or the contraction (W of dX, D and X of dW): those go through the
+// transposing LDS reads.  (Transposed copies of D, W and X in memory instead
+// took 2% of the largest training step and a quarter of one of 64 tokens.)
 #include "train_internal.h"
 
 namespace sbn {
@@ -34,9 +37,11 @@ constexpr int CUS = 256;
 enum Epi { EPI_STATS, EPI_GRAD, EPI_OUT };
 
 struct GemmArgs {
-  const uint16_t *A, *B;               // [nA][lda], [nB][ldb], contraction along the row
+  const uint16_t *A, *B;               // rows of lda, ldb
   int64_t lda, ldb;
-  int nA, nB;                          // rows; tiles past them read the last row
+  int nA, nB;                          // outputs
+  int mA, mB;                          // outputs in memory: tiles past them read the last ones again
+  int kA, kB;                          // contraction rows in memory, where rows are the contraction: past them the last
   int tilesA, tilesB;
   int steps, splits;                   // contraction stages in all, and parts they are split into
   // EPI_STATS, EPI_GRAD: A rows are vocabulary entries, B rows tokens
@@ -48,9 +53,9 @@ struct GemmArgs {
   float* target;                       // [nB] logit of the label
   const float *lse, *dloss;
   const float* gmax;                   // max |dloss|; EPI_GRAD divides by it, EPI_OUT multiplies
-  uint16_t *D, *DT;                    // [t][ldd], [v][lddt]
-  int64_t ldd, lddt;
-  int tpad, vpad;                      // rows written of D^T's columns, D's columns
+  uint16_t* D;                         // [tpad][ldd]; 0 past the tokens, and in columns nA .. vpad - 1
+  int64_t ldd;
+  int tpad, vpad;
   // EPI_OUT: C [nB][ldc], A rows along the row
   void* C;
   const float* Cin;                    // added first, or NULL
@@ -89,6 +94,19 @@ __device__ inline void tile_of(int b, int blocks, int nta, int ntb, int& ta, int
 __device__ inline void mfma_acc(v4f& acc, v8bf a, v8bf b) {
   asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(acc) : "v"(a), "v"(b));
 }
+typedef short v4s __attribute__((ext_vector_type(4)));
+__device__ inline v4s read_transposed(const uint8_t* p) {
+  return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) v4s*)p);
+}
+// 16 bytes per lane from base + off into LDS at lds + 16 lane, like g2lds16 (no
+// register is written).  In assembly where fragments are read by transposing
+// reads: before each of those the compiler would wait for every load into LDS,
+// as it does not for plain reads.  The waits are stage_barrier()'s.
+__device__ inline void load_to_lds(const uint8_t* base, uint32_t off, const uint8_t* lds) {
+  const uint32_t at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const uint8_t*)lds;
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(at), "v"(off), "s"(base)
+               : "memory", "m0");
+}
 __device__ inline void settle() { asm volatile("s_nop 15\n\ts_nop 15" ::: "memory"); }
 __device__ inline v4f fetch(v4f& acc) {
   asm volatile("" : "+a"(acc));
@@ -108,18 +126,46 @@ __device__ inline void stage_barrier() {
 
 __device__ inline void lds_reads_done() { __builtin_amdgcn_s_waitcnt(15 | (3 << 14) | (7 << 4)); }
 
-// WA x WB waves, wave tile 16 MI x 16 MJ, RING half stages of LDS.
+// One operand's half stage in LDS: HR outputs x 64 contraction entries.
 //
-// A stage is 64 contraction entries of the tile's rows, so that a row of it is
-// one 128-byte line (half of that, with twice the stages in flight, measured
-// 10% slower).  It is loaded in two halves, the upper rows of A and of B and
-// then the lower ones, each into the next place of a ring of RING places: the
-// loads go out evenly over a stage instead of all after its barrier.
-template <int WA, int WB, int MI, int MJ, int RING, int EPI>
+// Rows are outputs (TR false): 128 bytes of 8 chunks of 16; chunk c of row r lies
+// at position c ^ (r & 7), so that the 16 rows of a fragment read spread over the
+// banks.
+// Rows are the contraction (TR true): 2 HR bytes, in groups of 32 (16 outputs);
+// group f of row c lies at f ^ swizzle(c).  A transposing read takes, for 16
+// lanes, 4 rows of one group; the four 16-lane parts of a wave read rows 8 apart.
+// The swizzle puts those 16 rows on all 8 groups of banks, two on each.
+template <bool TR, int HR>
+struct HalfStage {
+  static constexpr bool TRANSPOSED = TR;
+  static constexpr int OUTPUTS = HR;
+  static constexpr int ROW = TR ? 2 * HR : BK * 2, CHUNKS = ROW / 16, ROWS = 64 / CHUNKS;   // rows of a 1 KB load
+  static constexpr int BYTES = HR * BK * 2;
+  static constexpr int GROUPS = HR / 16, SPAN = 8 / GROUPS;    // SPAN rows lie side by side over the banks
+  static __device__ int swizzle(int k4, int g) { return k4 / SPAN + (g & 1) * (4 / SPAN); }   // row 8 g + k4 (+ 4)
+
+  // Of load `l` (of HR / 8) the row and the chunk's byte in its row in memory, for this lane
+  static __device__ int row_of(int l, int lane) { return l * ROWS + lane / CHUNKS; }
+  static __device__ int chunk_of(int row, int lane) {
+    const int at = lane % CHUNKS;
+    return TR ? at ^ (2 * swizzle(row & 3, row >> 3)) : at ^ (row & 7);
+  }
+};
+
+// WA x WB waves, wave tile 16 MI x 16 MJ, RING half stages of LDS; TRA, TRB: the
+// operand's rows in memory are the contraction.
+//
+// A stage is 64 contraction entries of the tile's outputs, so that a row of it is
+// at least one 128-byte line (half of that, with twice the stages in flight,
+// measured 10% slower).  It is loaded in two halves, the upper outputs of A and
+// of B and then the lower ones, each into the next place of a ring of RING
+// places: the loads go out evenly over a stage instead of all after its barrier.
+template <int WA, int WB, int MI, int MJ, int RING, int EPI, bool TRA, bool TRB>
 __global__ __launch_bounds__(64 * WA * WB, 1) void ce_gemm_kernel(GemmArgs P) {
   constexpr int TA = WA * MI * 16, TB = WB * MJ * 16, NW = WA * WB, NT = 64 * NW;
-  constexpr int ROW = BK * 2;
-  constexpr int A_BYTES = TA / 2 * ROW, HALF = (TA + TB) / 2 * ROW;
+  using HA = HalfStage<TRA, TA / 2>;
+  using HB = HalfStage<TRB, TB / 2>;
+  constexpr int HALF = HA::BYTES + HB::BYTES;
   constexpr int LA = TA / (16 * NW), LB = TB / (16 * NW);    // 1 KB loads per wave and half stage
   constexpr int LPH = LA + LB;
   extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
@@ -136,31 +182,49 @@ __global__ __launch_bounds__(64 * WA * WB, 1) void ce_gemm_kernel(GemmArgs P) {
   const int s_lo = (int)((int64_t)P.steps * part / P.splits), s_hi = (int)((int64_t)P.steps * (part + 1) / P.splits);
   const int nsteps = s_hi - s_lo;
 
-  // Row r is 8 chunks of 16 bytes; chunk c lies at position c ^ (r & 7), so that
-  // the 16 rows of a fragment read spread over the banks.  One load moves 8 rows:
-  // lane l brings row l / 8, the chunk of position l % 8.
-  uint32_t offA[2][LA], offB[2][LB];
-  const int lrow = lane >> 3, lchunk = (lane & 7) ^ lrow;
+  // Byte offsets of this lane's loads.  Outputs past the operand are clamped here;
+  // with contraction rows, offset() clamps the row in the stage that is loaded.
+  const uint32_t ldA = (uint32_t)P.lda * 2, ldB = (uint32_t)P.ldb * 2;
+  uint32_t offA[2][LA], offB[2][LB];                 // TR: of the chunk alone
+  int rowA[LA], rowB[LB];
+  auto offset = [&](auto half, int l, int h, int out0, int n, uint32_t ld, int& row) {
+    using H = decltype(half);
+    row = H::row_of(l, lane);
+    const int chunk = H::chunk_of(row, lane);
+    if constexpr (!H::TRANSPOSED) {
+      const int r = h * H::OUTPUTS + row;
+      return (uint32_t)(out0 + r < n ? r : n - 1 - out0) * ld + chunk * 16;
+    } else {
+      const int o = h * H::OUTPUTS + chunk * 8;
+      return (uint32_t)(out0 + o < n ? o : n - 8 - out0) * 2;
+    }
+  };
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
 #pragma unroll
-    for (int q = 0; q < LA; ++q) {
-      const int r = h * (TA / 2) + 8 * (wave * LA + q) + lrow;
-      offA[h][q] = (uint32_t)((a0 + r < P.nA ? r : P.nA - 1 - a0) * P.lda * 2 + lchunk * 16);
-    }
+    for (int q = 0; q < LA; ++q) offA[h][q] = offset(HA{}, wave * LA + q, h, a0, P.mA, ldA, rowA[q]);
 #pragma unroll
-    for (int q = 0; q < LB; ++q) {
-      const int r = h * (TB / 2) + 8 * (wave * LB + q) + lrow;
-      offB[h][q] = (uint32_t)((b0 + r < P.nB ? r : P.nB - 1 - b0) * P.ldb * 2 + lchunk * 16);
-    }
+    for (int q = 0; q < LB; ++q) offB[h][q] = offset(HB{}, wave * LB + q, h, b0, P.mB, ldB, rowB[q]);
   }
-  const uint8_t* gA = (const uint8_t*)(P.A + (int64_t)a0 * P.lda) + (int64_t)s_lo * ROW;
-  const uint8_t* gB = (const uint8_t*)(P.B + (int64_t)b0 * P.ldb) + (int64_t)s_lo * ROW;
+  const uint8_t* gA = (const uint8_t*)P.A + (TRA ? (int64_t)a0 * 2 : a0 * P.lda * 2);
+  const uint8_t* gB = (const uint8_t*)P.B + (TRB ? (int64_t)b0 * 2 : b0 * P.ldb * 2);
 
   auto load_one = [&](int q, int h, int place, int step) {   // load q of LPH of a half stage
     uint8_t* base = smem + place * HALF;
-    if (q < LA) g2lds16(gA + (int64_t)step * ROW + offA[h][q], base + (wave * LA + q) * 1024);
-    else g2lds16(gB + (int64_t)step * ROW + offB[h][q - LA], base + A_BYTES + (wave * LB + q - LA) * 1024);
+    const int64_t k0 = (int64_t)(s_lo + step) * BK;
+    auto load = [&](const uint8_t* from, uint32_t off, uint8_t* to) {
+      if constexpr (TRA || TRB) load_to_lds(from, off, to);
+      else g2lds16(from + off, to);
+    };
+    if (q < LA) {
+      uint32_t off = offA[h][q];
+      if (TRA) off += (uint32_t)min(rowA[q], (int)(P.kA - 1 - k0)) * ldA;
+      load(gA + k0 * (TRA ? P.lda * 2 : 2), off, base + (wave * LA + q) * 1024);
+    } else {
+      uint32_t off = offB[h][q - LA];
+      if (TRB) off += (uint32_t)min(rowB[q - LA], (int)(P.kB - 1 - k0)) * ldB;
+      load(gB + k0 * (TRB ? P.ldb * 2 : 2), off, base + HA::BYTES + (wave * LB + q - LA) * 1024);
+    }
   };
 
   v4f acc[MI][MJ];
@@ -174,21 +238,39 @@ __global__ __launch_bounds__(64 * WA * WB, 1) void ce_gemm_kernel(GemmArgs P) {
   settle();
 
   // fragment of 16 rows x 32 contraction entries: lane l holds row l % 16, entries 8 (l / 16) .. + 8
-  const int frow = (lane & 15) * ROW;
-  const int fpos0 = ((lane >> 4) ^ (lane & 7)) * 16, fpos1 = ((4 + (lane >> 4)) ^ (lane & 7)) * 16;
+  const int g16 = lane >> 4, l15 = lane & 15;
+  const int frow = l15 * (BK * 2);
+  const int fpos0 = (g16 ^ (lane & 7)) * 16, fpos1 = ((4 + g16) ^ (lane & 7)) * 16;
+  // Fragment f of a half stage, 32 contraction entries `sub`.  The transposing read
+  // gives lane l of 16 the 4 rows' entries of output l, where lane 4 k + q reads
+  // outputs 4 q .. + 3 of row k.
+  auto fragment = [&](auto half, const uint8_t* p, int f, int sub) {
+    using H = decltype(half);
+    if constexpr (H::TRANSPOSED) {
+      const int k4 = l15 >> 2;
+      p += (8 * g16 + k4) * H::ROW + ((f ^ H::swizzle(k4, g16)) * 32) + (l15 & 3) * 8 + sub * (32 * H::ROW);
+      union {
+        v4s h[2];
+        v8bf v;
+      } u;
+      u.h[0] = read_transposed(p);
+      u.h[1] = read_transposed(p + 4 * H::ROW);
+      return u.v;
+    } else {
+      return __builtin_bit_cast(v8bf, *(const v4i*)(p + f * (16 * BK * 2) + frow + (sub ? fpos1 : fpos0)));
+    }
+  };
   v8bf fa[2][MI], fb[2][MJ];
   // fragment i of A (j of B) of the stage whose halves lie at places p0 and p1
   auto read_a = [&](int p0, int p1, int sub, int i) {
     const int f = WA > 1 ? wa % (WA / 2) * MI + i : i % (MI / 2);
     const bool lower = WA > 1 ? wa >= WA / 2 : i >= MI / 2;
-    const uint8_t* p = smem + (lower ? p1 : p0) * HALF + f * (16 * ROW) + frow + (sub ? fpos1 : fpos0);
-    fa[sub][i] = __builtin_bit_cast(v8bf, *(const v4i*)p);
+    fa[sub][i] = fragment(HA{}, smem + (lower ? p1 : p0) * HALF, f, sub);
   };
   auto read_b = [&](int p0, int p1, int sub, int j) {
     const int f = WB > 1 ? wb % (WB / 2) * MJ + j : j % (MJ / 2);
     const bool lower = WB > 1 ? wb >= WB / 2 : j >= MJ / 2;
-    const uint8_t* p = smem + (lower ? p1 : p0) * HALF + A_BYTES + f * (16 * ROW) + frow + (sub ? fpos1 : fpos0);
-    fb[sub][j] = __builtin_bit_cast(v8bf, *(const v4i*)p);
+    fb[sub][j] = fragment(HB{}, smem + (lower ? p1 : p0) * HALF + HA::BYTES, f, sub);
   };
   auto wrap = [](int p) { return p >= RING ? p - RING : p; };
   auto clamp = [&](int s) { return s < nsteps ? s : nsteps - 1; };
@@ -250,7 +332,7 @@ __global__ __launch_bounds__(64 * WA * WB, 1) void ce_gemm_kernel(GemmArgs P) {
 
   // acc[i][j]: A rows aw + 16 i + 4 (lane / 16) + 0..3, B row bw + 16 j + lane % 16
   const int aw = a0 + wa * MI * 16, bw = b0 + wb * MJ * 16;
-  const int l4 = 4 * (lane >> 4), l15 = lane & 15;
+  const int l4 = 4 * g16;
 
   if (EPI == EPI_STATS) {
     const bool ragged = aw + MI * 16 > P.nA;
@@ -285,11 +367,10 @@ __global__ __launch_bounds__(64 * WA * WB, 1) void ce_gemm_kernel(GemmArgs P) {
       if (lane < 16 && t < P.nB) P.stats[(int64_t)(ta * WA + wa) * P.nB + t] = make_float2(top, sum);
     }
   } else if (EPI == EPI_GRAD) {
-    // D through LDS, [t][v] with rows of 2 TA + 32 bytes and 8 more after every
-    // 8 rows: lanes that write 4 entries each of 16 rows, read whole rows, and
-    // read one column pair of 32 row groups all spread over the banks.
+    // D through LDS, [t][v] with rows of 2 TA + 32 bytes: lanes that write 4 entries
+    // each of 16 rows spread over the banks, and rows leave in whole lines.
     constexpr int PITCH = 2 * TA + 32;
-    auto at = [&](int t, int v) { return smem + t * PITCH + (t >> 3) * 8 + v * 2; };
+    auto at = [&](int t, int v) { return smem + t * PITCH + v * 2; };
     const float gm = *P.gmax, ginv = gm > 0.0f ? 1.0f / gm : 0.0f;
     lds_barrier();                                   // every wave has read its last fragments
 #pragma unroll
@@ -314,31 +395,10 @@ __global__ __launch_bounds__(64 * WA * WB, 1) void ce_gemm_kernel(GemmArgs P) {
       }
     }
     __syncthreads();
-    // D: 16 bytes of a row a thread
     for (int q = tid; q < TB * (TA / 8); q += NT) {
       const int tl = q / (TA / 8), c = q % (TA / 8);
-      if (b0 + tl < P.nB && a0 + 8 * c < P.vpad) {
-        const uint2* p = (const uint2*)at(tl, 8 * c);
-        const uint2 x = p[0], z = p[1];
-        *(uint4*)(P.D + (int64_t)(b0 + tl) * P.ldd + a0 + 8 * c) = make_uint4(x.x, x.y, z.x, z.y);
-      }
-    }
-    // D^T: a pair of columns of 8 rows a thread
-    for (int q = tid; q < (TB / 8) * (TA / 2); q += NT) {
-      const int tg = q % (TB / 8), vp = q / (TB / 8);
-      if (b0 + 8 * tg < P.tpad && a0 + 2 * vp < P.vpad) {
-        uint32_t x[8];
-#pragma unroll
-        for (int r = 0; r < 8; ++r) x[r] = *(const uint32_t*)at(8 * tg + r, 2 * vp);
-        uint4 lo, hi;
-        lo.x = (x[0] & 0xFFFFu) | (x[1] << 16), hi.x = (x[0] >> 16) | (x[1] & 0xFFFF0000u);
-        lo.y = (x[2] & 0xFFFFu) | (x[3] << 16), hi.y = (x[2] >> 16) | (x[3] & 0xFFFF0000u);
-        lo.z = (x[4] & 0xFFFFu) | (x[5] << 16), hi.z = (x[4] >> 16) | (x[5] & 0xFFFF0000u);
-        lo.w = (x[6] & 0xFFFFu) | (x[7] << 16), hi.w = (x[6] >> 16) | (x[7] & 0xFFFF0000u);
-        uint16_t* o = P.DT + (int64_t)(a0 + 2 * vp) * P.lddt + b0 + 8 * tg;
-        *(uint4*)o = lo;
-        *(uint4*)(o + P.lddt) = hi;
-      }
+      if (b0 + tl < P.tpad && a0 + 8 * c < P.vpad)
+        *(uint4*)(P.D + (int64_t)(b0 + tl) * P.ldd + a0 + 8 * c) = *(const uint4*)at(tl, 8 * c);
     }
   } else {
     const float scale = P.gmax ? *P.gmax : 1.0f;
@@ -427,33 +487,6 @@ __global__ __launch_bounds__(1024) void ce_gmax_kernel(const float* __restrict__
   }
 }
 
-// src [rows][ld] bf16 -> dst [cols][dld] (cols a multiple of 64), dst columns
-// rows .. dld - 1 set to 0; dld a multiple of 64
-__global__ __launch_bounds__(256) void ce_transpose_kernel(const uint16_t* __restrict__ src, int64_t ld, int rows,
-                                                           uint16_t* __restrict__ dst, int64_t dld) {
-  __shared__ uint32_t sm[64][33];                    // two rows of a column in a word
-  const int r0 = (int)blockIdx.x * 64, c0 = (int)blockIdx.y * 64;
-  const int tid = threadIdx.x;
-  {
-    const int rp = tid >> 3, c = (tid & 7) * 8;      // rows 2 rp, 2 rp + 1, columns c .. c + 7
-    uint4 x = make_uint4(0u, 0u, 0u, 0u), y = x;
-    if (r0 + 2 * rp < rows) x = *(const uint4*)(src + (int64_t)(r0 + 2 * rp) * ld + c0 + c);
-    if (r0 + 2 * rp + 1 < rows) y = *(const uint4*)(src + (int64_t)(r0 + 2 * rp + 1) * ld + c0 + c);
-    const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      sm[c + 2 * i][rp] = (xs[i] & 0xFFFFu) | (ys[i] << 16);
-      sm[c + 2 * i + 1][rp] = (xs[i] >> 16) | (ys[i] & 0xFFFF0000u);
-    }
-  }
-  __syncthreads();
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int q = tid + 256 * h, c = q >> 3, w = (q & 7) * 4;
-    *(uint4*)(dst + (int64_t)(c0 + c) * dld + r0 + 2 * w) = make_uint4(sm[c][w], sm[c][w + 1], sm[c][w + 2], sm[c][w + 3]);
-  }
-}
-
 // C[row][a] = Cin[row][a] (if any) + the sum over the parts, 4 columns a thread;
 // Cin [rows][cols] may be C itself
 __global__ __launch_bounds__(256) void ce_sum_kernel(const float* __restrict__ part, int splits, int64_t rows, int cols,
@@ -494,28 +527,28 @@ struct TileShape {
 };
 constexpr TileShape SHAPE[] = {{256, 256}, {128, 128}, {128, 64}};
 
-template <int WA, int WB, int MI, int MJ, int RING, int EPI>
+template <int WA, int WB, int MI, int MJ, int RING, int EPI, bool TRA, bool TRB>
 hipError_t run_gemm(const char* name, const GemmArgs& P, hipStream_t st) {
   constexpr int TA = WA * MI * 16, TB = WB * MJ * 16;
   constexpr size_t stages = (size_t)RING * (TA + TB) / 2 * BK * 2;
-  constexpr size_t dtile = EPI == EPI_GRAD ? (size_t)TB * (2 * TA + 32) + TB : 0;
+  constexpr size_t dtile = EPI == EPI_GRAD ? (size_t)TB * (2 * TA + 32) : 0;
   constexpr size_t lds = stages > dtile ? stages : dtile;
-  static const hipError_t e = hipFuncSetAttribute((const void*)ce_gemm_kernel<WA, WB, MI, MJ, RING, EPI>,
+  static const hipError_t e = hipFuncSetAttribute((const void*)ce_gemm_kernel<WA, WB, MI, MJ, RING, EPI, TRA, TRB>,
                                                   hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
   if (e != hipSuccess) return e;
-  SBN_LAUNCH(name, (ce_gemm_kernel<WA, WB, MI, MJ, RING, EPI>), dim3((unsigned)(P.tilesA * P.tilesB * P.splits)),
+  SBN_LAUNCH(name, (ce_gemm_kernel<WA, WB, MI, MJ, RING, EPI, TRA, TRB>), dim3((unsigned)(P.tilesA * P.tilesB * P.splits)),
              dim3(64 * WA * WB), lds, st, P);
   return hipGetLastError();
 }
 
-template <int EPI>
+template <int EPI, bool TRA = false, bool TRB = false>
 hipError_t gemm(const char* name, Tile tile, GemmArgs& P, hipStream_t st) {
   P.tilesA = (int)cdiv(P.nA, SHAPE[tile].a);
   P.tilesB = (int)cdiv(P.nB, SHAPE[tile].b);
   switch (tile) {
-    case WIDE: return run_gemm<2, 4, 8, 4, 5, EPI>(name, P, st);
-    case SQUARE: return run_gemm<2, 2, 4, 4, 5, EPI>(name, P, st);
-    default: return run_gemm<4, 1, 2, 4, 6, EPI>(name, P, st);
+    case WIDE: return run_gemm<2, 4, 8, 4, 5, EPI, TRA, TRB>(name, P, st);
+    case SQUARE: return run_gemm<2, 2, 4, 4, 5, EPI, TRA, TRB>(name, P, st);
+    default: return run_gemm<4, 1, 2, 4, 6, EPI, TRA, TRB>(name, P, st);
   }
 }
 
@@ -558,7 +591,7 @@ struct CePlan {
   int64_t piece;                       // vocabulary entries of one piece, a multiple of 256
   int64_t pieces;
   Choice x, w;                         // of dX, split over the piece, and dW, split over the tokens
-  size_t gmax, d, dt, wt, xt, acc, part, total;
+  size_t gmax, d, acc, part, total;
 };
 
 CePlan ce_plan(int64_t T, int64_t V, int64_t K) {
@@ -579,10 +612,7 @@ CePlan ce_plan(int64_t T, int64_t V, int64_t K) {
     return at;
   };
   L.gmax = take(sizeof(float));
-  L.d = take((size_t)T * L.piece * 2);
-  L.dt = take((size_t)L.piece * L.tpad * 2);
-  L.wt = take((size_t)K * L.piece * 2);
-  L.xt = take((size_t)K * L.tpad * 2);
+  L.d = take((size_t)L.tpad * L.piece * 2);
   L.acc = take(L.pieces > 1 ? (size_t)T * K * 4 : 0);
   const size_t px = L.x.splits > 1 ? (size_t)L.x.splits * T * K * 4 : 0;
   const size_t pw = L.w.splits > 1 ? (size_t)L.w.splits * L.piece * K * 4 : 0;
@@ -591,17 +621,11 @@ CePlan ce_plan(int64_t T, int64_t V, int64_t K) {
   return L;
 }
 
-hipError_t transpose(const uint16_t* src, int64_t ld, int64_t rows, int64_t cols, uint16_t* dst, int64_t dld,
-                     hipStream_t st) {
-  SBN_LAUNCH("ce_transpose", ce_transpose_kernel, dim3((unsigned)(dld / 64), (unsigned)(cols / 64)), dim3(256), 0, st,
-             src, ld, (int)rows, dst, dld);
-  return hipGetLastError();
-}
-
-// C [nB][ldc] = A B^T with its sum over splits
+// C [nB][ldc] = A B^T, split as P says and summed
+template <bool TRB>
 hipError_t product(const char* name, Tile tile, GemmArgs P, float* part, hipStream_t st) {
   P.part = P.splits > 1 ? part : nullptr;
-  const hipError_t e = gemm<EPI_OUT>(name, tile, P, st);
+  const hipError_t e = gemm<EPI_OUT, true, TRB>(name, tile, P, st);
   if (e != hipSuccess || P.splits == 1) return e;
   SBN_LAUNCH("ce_sum", ce_sum_kernel, dim3((unsigned)grid_for((int64_t)P.nB * (P.nA / 4))), dim3(256), 0, st, part,
              P.splits, (int64_t)P.nB, P.nA, P.Cin, P.gmax, P.C, P.c_f32, P.ldc);
@@ -624,8 +648,8 @@ hipError_t launch_ce(const uint16_t* X, int64_t ldx, const uint16_t* W, int64_t 
                      bool labels64, int64_t T, int64_t V, int64_t K, float* loss, float* lse, void* ws,
                      hipStream_t st) {
   GemmArgs P{};
-  P.A = W, P.lda = ldw, P.nA = (int)V;
-  P.B = X, P.ldb = ldx, P.nB = (int)T;
+  P.A = W, P.lda = ldw, P.nA = P.mA = (int)V;
+  P.B = X, P.ldb = ldx, P.nB = P.mB = (int)T;
   P.steps = (int)(K / BK), P.splits = 1;
   P.labels = labels, P.labels64 = labels64, P.V = (int)V;
   P.target = (float*)ws;
@@ -645,44 +669,41 @@ hipError_t launch_ce_backward(const uint16_t* X, int64_t ldx, const uint16_t* W,
                               hipStream_t st) {
   const CePlan L = ce_plan(T, V, K);
   uint8_t* w = (uint8_t*)ws;
-  uint16_t *D = (uint16_t*)(w + L.d), *DT = (uint16_t*)(w + L.dt), *WT = (uint16_t*)(w + L.wt),
-           *XT = (uint16_t*)(w + L.xt);
+  uint16_t* D = (uint16_t*)(w + L.d);
   float *acc = (float*)(w + L.acc), *part = (float*)(w + L.part), *gmax = (float*)(w + L.gmax);
   hipError_t e;
   SBN_LAUNCH("ce_gmax", ce_gmax_kernel, dim3(1), dim3(1024), 0, st, dloss, labels, labels64, (int)V, (int)T, gmax);
   if ((e = hipGetLastError()) != hipSuccess) return e;
-  if (dW && (e = transpose(X, ldx, T, K, XT, L.tpad, st)) != hipSuccess) return e;
   for (int64_t i = 0; i < L.pieces; ++i) {
     const int64_t v0 = i * L.piece, nv = V - v0 < L.piece ? V - v0 : L.piece;
     const int64_t vpad = round_up(nv, 64);           // contraction of dX over this piece
     GemmArgs G{};
-    G.A = W + v0 * ldw, G.lda = ldw, G.nA = (int)nv;
-    G.B = X, G.ldb = ldx, G.nB = (int)T;
+    G.A = W + v0 * ldw, G.lda = ldw, G.nA = G.mA = (int)nv;
+    G.B = X, G.ldb = ldx, G.nB = G.mB = (int)T;
     G.steps = (int)(K / BK), G.splits = 1;
     G.labels = labels, G.labels64 = labels64, G.v0 = (int)v0, G.V = (int)V;
     G.lse = lse, G.dloss = dloss, G.gmax = gmax;
-    G.D = D, G.DT = DT, G.ldd = L.piece, G.lddt = L.tpad, G.tpad = (int)L.tpad, G.vpad = (int)vpad;
+    G.D = D, G.ldd = L.piece, G.tpad = (int)L.tpad, G.vpad = (int)vpad;
     if ((e = gemm<EPI_GRAD>("ce_dlogits", pick(nv, T, G.steps, false).tile, G, st)) != hipSuccess) return e;
     if (dX) {
-      if ((e = transpose(W + v0 * ldw, ldw, nv, K, WT, vpad, st)) != hipSuccess) return e;
       GemmArgs P{};
-      P.A = WT, P.lda = vpad, P.nA = (int)K;
-      P.B = D, P.ldb = L.piece, P.nB = (int)T;
+      P.A = W + v0 * ldw, P.lda = ldw, P.nA = P.mA = (int)K, P.kA = (int)nv;
+      P.B = D, P.ldb = L.piece, P.nB = P.mB = (int)T;
       P.steps = (int)(vpad / BK), P.splits = L.x.splits <= P.steps ? L.x.splits : P.steps;
       const bool last = i + 1 == L.pieces;
       P.Cin = i > 0 ? acc : nullptr;
       P.gmax = last ? gmax : nullptr;
       P.C = last ? dX : acc, P.c_f32 = last ? dx_f32 : true, P.ldc = last ? lddx : K;
-      if ((e = product("ce_dx", L.x.tile, P, part, st)) != hipSuccess) return e;
+      if ((e = product<false>("ce_dx", L.x.tile, P, part, st)) != hipSuccess) return e;
     }
     if (dW) {
       GemmArgs P{};
-      P.A = XT, P.lda = L.tpad, P.nA = (int)K;
-      P.B = DT, P.ldb = L.tpad, P.nB = (int)nv;
+      P.A = X, P.lda = ldx, P.nA = P.mA = (int)K, P.kA = (int)T;
+      P.B = D, P.ldb = L.piece, P.nB = (int)nv, P.mB = (int)vpad, P.kB = (int)L.tpad;
       P.steps = (int)(L.tpad / BK), P.splits = L.w.splits;
       P.C = (uint8_t*)dW + v0 * lddw * (dw_f32 ? 4 : 2), P.c_f32 = dw_f32, P.ldc = lddw;
       P.gmax = gmax;
-      if ((e = product("ce_dw", L.w.tile, P, part, st)) != hipSuccess) return e;
+      if ((e = product<true>("ce_dw", L.w.tile, P, part, st)) != hipSuccess) return e;
     }
   }
   return hipSuccess;
