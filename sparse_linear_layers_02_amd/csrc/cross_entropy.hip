@@ -548,7 +548,7 @@ hipError_t gemm(const char* name, Tile tile, GemmArgs& P, hipStream_t st) {
   switch (tile) {
     case WIDE: return run_gemm<2, 4, 8, 4, 5, EPI, TRA, TRB>(name, P, st);
     case SQUARE: return run_gemm<2, 2, 4, 4, 5, EPI, TRA, TRB>(name, P, st);
-    default: return run_gemm<4, 1, 2, 4, 6, EPI, TRA, TRB>(name, P, st);
+    default: return run_gemm<4, 1, 2, 4, 5, EPI, TRA, TRB>(name, P, st);
   }
 }
 
