@@ -10,9 +10,10 @@
 //
 // 8-bit codes: m = s (c/127)|c/127|, v = s (c/255)^4 with s the block's largest
 // value.  The code is the rint of a root, taken with the one-ulp root
-// instruction; only estimates within 2^-12 of a half-integer are redone with
-// correctly rounded roots (the estimate's error is under 2^-14), so the codes
-// equal those of the correctly rounded formula.
+// instruction: the estimate is off by at most 2 ulp below 256, under 2^-15.  If
+// one of a thread's 8 estimates lies within 2^-14 of a half-integer, all 8 are
+// taken again with correctly rounded roots, so the codes equal those of the
+// correctly rounded formula.
 //
 // Products and sums are rounded one by one (no fused multiply-add): the result
 // is that of the same formula in elementary float32 operations.
@@ -44,40 +45,34 @@ __device__ inline float decode_v(int c, float s) {
   t = t * t;
   return t * t * s;
 }
-__device__ inline bool near_half(float q) { return fabsf(q - rintf(q)) > 0.5f - 0x1p-12f; }
 
-__device__ inline int encode_m(float x, float inv) {
-  const float y = fabsf(x) * inv;
-  float q = 127.0f * __builtin_amdgcn_sqrtf(y);
-  if (near_half(q)) q = 127.0f * sqrtf(y);
-  const int c = (int)rintf(q);
-  return x < 0.0f ? -c : c;
-}
-__device__ inline int encode_v(float x, float inv) {
-  const float y = x * inv;
-  float q = 255.0f * __builtin_amdgcn_sqrtf(__builtin_amdgcn_sqrtf(y));
-  if (near_half(q)) q = 255.0f * sqrtf(sqrtf(y));
-  const int c = (int)rintf(q);
-  return y > 0.0f && c < 1 ? 1 : c;
+// Table entries hold plain pointers: into global memory, said so that the
+// accesses are global ones (a flat access also waits in the LDS queue).
+#define SBN_GLOBAL __attribute__((address_space(1)))
+typedef SBN_GLOBAL const char gcchar;
+typedef SBN_GLOBAL char gchar;
+template <class T>
+__device__ inline SBN_GLOBAL T* as_global(T* p) {
+  return (SBN_GLOBAL T*)p;
 }
 
 // n (1..8) elements at p (16-byte aligned where n == 8); elements past n are 0
 template <bool F32>
-__device__ inline void load8(const void* p, int n, float* v) {
+__device__ inline void load8(gcchar* p, int n, float* v) {
   if (F32) {
-    const float* q = (const float*)p;
+    SBN_GLOBAL const float* q = (SBN_GLOBAL const float*)p;
     if (n == 8) {
-      *(v4f*)v = *(const v4f*)q;
-      *(v4f*)(v + 4) = *(const v4f*)(q + 4);
+      *(v4f*)v = *(SBN_GLOBAL const v4f*)q;
+      *(v4f*)(v + 4) = *(SBN_GLOBAL const v4f*)(q + 4);
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[i] = i < n ? q[i] : 0.0f;
     }
   } else {
-    const uint16_t* q = (const uint16_t*)p;
+    SBN_GLOBAL const uint16_t* q = (SBN_GLOBAL const uint16_t*)p;
     if (n == 8) {
-      const uint4 u = *(const uint4*)q;
-      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+      const v4i u = *(SBN_GLOBAL const v4i*)q;
+      const uint32_t w[4] = {(uint32_t)u[0], (uint32_t)u[1], (uint32_t)u[2], (uint32_t)u[3]};
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         v[2 * i] = __uint_as_float(w[i] << 16);
@@ -90,22 +85,22 @@ __device__ inline void load8(const void* p, int n, float* v) {
   }
 }
 template <bool F32>
-__device__ inline void store8(void* p, int n, const float* v) {
+__device__ inline void store8(gchar* p, int n, const float* v) {
   if (F32) {
-    float* q = (float*)p;
+    SBN_GLOBAL float* q = (SBN_GLOBAL float*)p;
     if (n == 8) {
-      *(v4f*)q = *(const v4f*)v;
-      *(v4f*)(q + 4) = *(const v4f*)(v + 4);
+      *(SBN_GLOBAL v4f*)q = *(const v4f*)v;
+      *(SBN_GLOBAL v4f*)(q + 4) = *(const v4f*)(v + 4);
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i)
         if (i < n) q[i] = v[i];
     }
   } else {
-    uint16_t* q = (uint16_t*)p;
+    SBN_GLOBAL uint16_t* q = (SBN_GLOBAL uint16_t*)p;
     if (n == 8) {
-      *(uint4*)q = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
-                              pack_bf16x2(v[6], v[7]));
+      *(SBN_GLOBAL v4i*)q = (v4i){(int)pack_bf16x2(v[0], v[1]), (int)pack_bf16x2(v[2], v[3]),
+                                  (int)pack_bf16x2(v[4], v[5]), (int)pack_bf16x2(v[6], v[7])};
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i)
@@ -115,20 +110,24 @@ __device__ inline void store8(void* p, int n, const float* v) {
 }
 
 // 8 codes of one byte
-__device__ inline uint2 load_codes(const uint8_t* p, int n) {
-  if (n == 8) return *(const uint2*)p;
+typedef int v2i __attribute__((ext_vector_type(2)));
+__device__ inline uint2 load_codes(SBN_GLOBAL const uint8_t* p, int n) {
+  if (n == 8) {
+    const v2i w = *(SBN_GLOBAL const v2i*)p;
+    return make_uint2((uint32_t)w[0], (uint32_t)w[1]);
+  }
   uint32_t w[2] = {0u, 0u};
 #pragma unroll
   for (int i = 0; i < 8; ++i)
     if (i < n) w[i >> 2] |= (uint32_t)p[i] << (8 * (i & 3));
   return make_uint2(w[0], w[1]);
 }
-__device__ inline void store_codes(uint8_t* p, int n, const int* c) {
+__device__ inline void store_codes(SBN_GLOBAL uint8_t* p, int n, const int* c) {
   uint32_t w[2] = {0u, 0u};
 #pragma unroll
   for (int i = 0; i < 8; ++i) w[i >> 2] |= (uint32_t)(c[i] & 0xFF) << (8 * (i & 3));
   if (n == 8) {
-    *(uint2*)p = make_uint2(w[0], w[1]);
+    *(SBN_GLOBAL v2i*)p = (v2i){(int)w[0], (int)w[1]};
     return;
   }
 #pragma unroll
@@ -153,8 +152,24 @@ __device__ inline float encode8(const float* v, int* c) {
   s = half_wave_max(s);
   if (s < S_FLOOR) s = 0.0f;
   const float inv = s > 0.0f ? 1.0f / s : 0.0f;
+  float y[8], q[8], half = 0.0f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) c[i] = SECOND ? encode_v(v[i], inv) : encode_m(v[i], inv);
+  for (int i = 0; i < 8; ++i) {
+    y[i] = fabsf(v[i]) * inv;
+    float r = __builtin_amdgcn_sqrtf(y[i]);
+    if (SECOND) r = __builtin_amdgcn_sqrtf(r);
+    q[i] = (SECOND ? 255.0f : 127.0f) * r;
+    half = fmaxf(half, fabsf(q[i] - rintf(q[i])));
+  }
+  if (half > 0.5f - 0x1p-14f) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) q[i] = SECOND ? 255.0f * sqrtf(sqrtf(y[i])) : 127.0f * sqrtf(y[i]);
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float r = rintf(q[i]);
+    c[i] = (int)(SECOND ? (y[i] > 0.0f ? fmaxf(r, 1.0f) : r) : copysignf(r, v[i]));
+  }
   return s;
 }
 
@@ -167,24 +182,29 @@ __global__ __launch_bounds__(256) void adamw_kernel(const sbn_adamw_entry* __res
   const int64_t e = (int64_t)mp.y * ADAMW_CHUNK + threadIdx.x * 8;
   const int64_t left = E->n - e;
   const int n = left >= 8 ? 8 : left > 0 ? (int)left : 0;
-  const float lr = dyn ? dyn[0] : S.lr, bias1 = dyn ? dyn[1] : S.bias1, bias2 = dyn ? dyn[2] : S.bias2;
-  const float gs = dyn ? dyn[3] : 1.0f;
-  const float keep = 1.0f - lr * E->weight_decay, rate = lr / bias1, rbias2 = 1.0f / sqrtf(bias2);
+  float lr = S.lr, rate = S.rate, rbias2 = S.rbias2, gs = 1.0f;
+  if (dyn) {
+    lr = dyn[0];
+    rate = lr / dyn[1];
+    rbias2 = 1.0f / sqrtf(dyn[2]);
+    gs = dyn[3];
+  }
+  const float keep = 1.0f - lr * E->weight_decay;
 
   float p[8], g[8], m[8], v[8];
   uint2 cm = make_uint2(0u, 0u), cv = cm;
   float sm = 0.0f, sv = 0.0f;
   if (n > 0) {
-    load8<GF>((const char*)E->grad + e * (GF ? 4 : 2), n, g);
-    load8<PF>((const char*)E->p + e * (PF ? 4 : 2), n, p);
+    load8<GF>(as_global((const char*)E->grad) + e * (GF ? 4 : 2), n, g);
+    load8<PF>(as_global((const char*)E->p) + e * (PF ? 4 : 2), n, p);
     if (S8) {
-      cm = load_codes((const uint8_t*)E->m + e, n);
-      cv = load_codes((const uint8_t*)E->v + e, n);
-      sm = E->m_scale[e / QB];
-      sv = E->v_scale[e / QB];
+      cm = load_codes(as_global((const uint8_t*)E->m) + e, n);
+      cv = load_codes(as_global((const uint8_t*)E->v) + e, n);
+      sm = as_global(E->m_scale)[e / QB];
+      sv = as_global(E->v_scale)[e / QB];
     } else {
-      load8<true>((const float*)E->m + e, n, m);
-      load8<true>((const float*)E->v + e, n, v);
+      load8<true>(as_global((const char*)E->m) + e * 4, n, m);
+      load8<true>(as_global((const char*)E->v) + e * 4, n, v);
     }
   } else {
 #pragma unroll
@@ -210,20 +230,20 @@ __global__ __launch_bounds__(256) void adamw_kernel(const sbn_adamw_entry* __res
   if (S8) {
     int c[8];
     sm = encode8<false>(m, c);
-    if (n > 0) store_codes((uint8_t*)E->m + e, n, c);
+    if (n > 0) store_codes(as_global((uint8_t*)E->m) + e, n, c);
     sv = encode8<true>(v, c);
-    if (n > 0) store_codes((uint8_t*)E->v + e, n, c);
+    if (n > 0) store_codes(as_global((uint8_t*)E->v) + e, n, c);
     if (n > 0 && (threadIdx.x & 31) == 0) {
-      E->m_scale[e / QB] = sm;
-      E->v_scale[e / QB] = sv;
+      as_global(E->m_scale)[e / QB] = sm;
+      as_global(E->v_scale)[e / QB] = sv;
     }
   }
   if (n == 0) return;
-  store8<PF>((char*)E->p + e * (PF ? 4 : 2), n, p);
-  if (PF && E->shadow) store8<false>(E->shadow + e, n, p);
+  store8<PF>(as_global((char*)E->p) + e * (PF ? 4 : 2), n, p);
+  if (PF && E->shadow) store8<false>(as_global((char*)E->shadow) + e * 2, n, p);
   if (!S8) {
-    store8<true>((float*)E->m + e, n, m);
-    store8<true>((float*)E->v + e, n, v);
+    store8<true>(as_global((char*)E->m) + e * 4, n, m);
+    store8<true>(as_global((char*)E->v) + e * 4, n, v);
   }
 }
 
@@ -234,11 +254,11 @@ __global__ __launch_bounds__(256) void adamw_decode_kernel(const uint8_t* __rest
     const int k = n - e >= 8 ? 8 : (int)(n - e);
     const float s = scale[e / QB];
     int c[8];
-    unpack_codes(load_codes(codes + e, k), !second, c);
+    unpack_codes(load_codes(as_global(codes) + e, k), !second, c);
     float v[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = second ? decode_v(c[i], s) : decode_m(c[i], s);
-    store8<true>(out + e, k, v);
+    store8<true>(as_global((char*)(out + e)), k, v);
   }
 }
 
@@ -249,11 +269,11 @@ __global__ __launch_bounds__(256) void adamw_encode_kernel(const float* __restri
     const int64_t e = e0 + threadIdx.x * 8;
     const int k = n - e >= 8 ? 8 : n > e ? (int)(n - e) : 0;
     float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (k > 0) load8<true>(x + e, k, v);
+    if (k > 0) load8<true>(as_global((const char*)(x + e)), k, v);
     int c[8];
     const float s = second ? encode8<true>(v, c) : encode8<false>(v, c);
     if (k > 0) {
-      store_codes(codes + e, k, c);
+      store_codes(as_global(codes) + e, k, c);
       if ((threadIdx.x & 31) == 0) scale[e / QB] = s;
     }
   }

@@ -336,8 +336,8 @@ sbn_status sbn_adamw_step(const sbn_adamw_entry* entries, const int32_t* map, in
   s.beta1 = (float)beta1, s.one_minus_beta1 = (float)(1.0 - beta1);
   s.beta2 = (float)beta2, s.one_minus_beta2 = (float)(1.0 - beta2);
   s.eps = (float)eps, s.lr = (float)lr;
-  s.bias1 = (float)(1.0 - std::pow(beta1, (double)step));
-  s.bias2 = (float)(1.0 - std::pow(beta2, (double)step));
+  s.rate = s.lr / (float)(1.0 - std::pow(beta1, (double)step));
+  s.rbias2 = 1.0f / std::sqrt((float)(1.0 - std::pow(beta2, (double)step)));
   hipStream_t st = (hipStream_t)stream;
   return hip_result(launch_adamw(entries, map, blocks, pdt == SBN_F32, gdt == SBN_F32, state_bits == 8, s, dyn, st),
                     st, fn);

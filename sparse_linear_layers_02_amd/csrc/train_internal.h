@@ -34,7 +34,7 @@ hipError_t launch_zero_rows(void* p, int64_t rows, int64_t len, int64_t ld, int 
 constexpr int ADAMW_CHUNK = 2048;   // elements of one block: 8 per thread
 struct AdamWScalars {
   float beta1, one_minus_beta1, beta2, one_minus_beta2, eps;
-  float lr, bias1, bias2;           // 1 - beta^step
+  float lr, rate, rbias2;           // rate = lr / (1 - beta1^step), rbias2 = 1 / sqrt(1 - beta2^step), in float32
 };
 hipError_t launch_adamw(const sbn_adamw_entry* entries, const int32_t* map, int64_t blocks, bool p_f32, bool g_f32,
                         bool state8, const AdamWScalars& s, const float* dyn, hipStream_t st);
