@@ -6,18 +6,16 @@
 //
 // rstd multiplies a whole row, so it cancels from the codes: the maximum of |u|
 // and the sum of h^2 come out of one pass over the row, which stays in
-// registers until it is written.  The rounding of u / a is act_quant's
-// (act_quant.h): bit-equal to the division's rint.
+// registers until it is written.
 //
 // The gradient, with n = h rstd and w = gain dy:
 //   dx = rstd (w - n mean(w n)) + dh;  dgain = sum_t dy n
-// TPR threads hold a row, each the same columns of every row it sees, so
-// dgain's partial sums stay in registers over the rows of a block; blocks
-// write them side by side and a second launch adds them in a fixed order.
+// A thread holds the same columns of every row that its block sees, so dgain's
+// partial sums stay in registers over the rows of a block; blocks write them side
+// by side and a second launch adds them in a fixed order.
 //
 // Both directions are bound by memory traffic: every row is read once and
 // written once.
-#include "act_quant.h"
 #include "train_internal.h"
 
 namespace sbn {
@@ -91,6 +89,38 @@ __device__ inline float wave_max(float x) {
   return x;
 }
 
+// 8 codes rint((127 u) / a), rcp = fl(127 / a).  u * rcp is off by under 2^-15; if
+// one of the 8 lies within 2^-14 of a half-integer, all are divided again,
+// correctly rounded (about one wave in 17 does).
+__device__ inline uint2 codes8(const float* u, float rcp, float a) {
+  float q[8], half = 0.0f;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float x = u[j] * rcp;
+    q[j] = rintf(x);
+    half = fmaxf(half, fabsf(x - q[j]));
+  }
+  if (half > 0.5f - 0x1p-14f) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) q[j] = rintf((127.0f * u[j]) / a);
+  }
+  uint32_t o[2] = {0u, 0u};
+#pragma unroll
+  for (int j = 0; j < 8; ++j) o[j >> 2] |= (uint32_t)((int)q[j] & 0xFF) << (8 * (j & 3));
+  return make_uint2(o[0], o[1]);
+}
+
+__device__ inline float row16_sum(float x) {
+#pragma unroll
+  for (int m = 8; m >= 1; m >>= 1) x += __shfl_xor(x, m);
+  return x;
+}
+__device__ inline float row16_max(float x) {
+#pragma unroll
+  for (int m = 8; m >= 1; m >>= 1) x = fmaxf(x, __shfl_xor(x, m));
+  return x;
+}
+
 // ---------------------------------------------------------------- forward
 struct FwdArgs {
   const void *X, *res, *gain;
@@ -103,20 +133,15 @@ struct FwdArgs {
   bool gain_f32;
 };
 
-// TPR threads per row, BT / TPR rows per block, CH chunks of 8 elements per
-// thread (CH * TPR * 8 >= K).
-template <bool F32, bool Q, int BT, int TPR, int CH>
-__global__ __launch_bounds__(BT) void rmsnorm_kernel(FwdArgs A) {
-  constexpr int ROWS = BT / TPR, WPR = TPR / 64;
-  __shared__ float red[2][BT / 64];
-  const int g = threadIdx.x % TPR, wave = threadIdx.x >> 6;
-  const int kc = A.K / 8, es = F32 ? 4 : 2;
-  const int64_t step = (int64_t)gridDim.x * ROWS;
-  // every thread of a block makes the same number of rounds (barriers inside)
-  for (int64_t t0 = (int64_t)blockIdx.x * ROWS; t0 < A.T; t0 += step) {
-    const int64_t t = t0 + threadIdx.x / TPR;
-    const bool live = t < A.T;
-    const int n = live ? kc : 0;
+// A block holds one row at a time, CH chunks of 8 elements per thread
+// (CH * blockDim.x * 8 >= K); rows beyond the grid are taken in further rounds.
+template <bool F32, bool Q, int CH, int MAXT>
+__global__ __launch_bounds__(MAXT) void rmsnorm_kernel(FwdArgs A) {
+  __shared__ float red[2][2][MAXT / 64];
+  const int g = threadIdx.x, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+  const int n = A.K / 8, es = F32 ? 4 : 2, TPR = blockDim.x;
+  int turn = 0;
+  for (int64_t t = blockIdx.x; t < A.T; t += gridDim.x, turn ^= 1) {
     const char* xr = (const char*)A.X + t * A.ldx * es;
     const char* rr = (const char*)A.res + t * A.ldr * es;
     Vec8<F32> h[CH], r[CH];
@@ -160,25 +185,21 @@ __global__ __launch_bounds__(BT) void rmsnorm_kernel(FwdArgs A) {
     }
     ss = wave_sum(ss);
     if (Q) mx = wave_max(mx);
-    if (WPR > 1) {
-      __syncthreads();                              // the previous round's reads of red
+    if (waves > 1) {
+      // two sets of red in turn: one barrier a round keeps a fast wave's next
+      // write away from a slow wave's read
       if ((threadIdx.x & 63) == 0) {
-        red[0][wave] = ss;
-        red[1][wave] = mx;
+        red[turn][0][wave] = ss;
+        red[turn][1][wave] = mx;
       }
       __syncthreads();
-      const int w0 = wave / WPR * WPR;
-      ss = red[0][w0];
-      mx = red[1][w0];
-#pragma unroll
-      for (int w = 1; w < WPR; ++w) {
-        ss += red[0][w0 + w];
-        mx = fmaxf(mx, red[1][w0 + w]);
-      }
+      const int l = threadIdx.x & 15;               // at most 16 waves
+      ss = row16_sum(l < waves ? red[turn][0][l] : 0.0f);
+      if (Q) mx = row16_max(l < waves ? red[turn][1][l] : 0.0f);
     }
     const float rstd = 1.0f / sqrtf(ss / (float)A.K + A.eps);
     const float a = fmaxf(mx, U_FLOOR);
-    if (g == 0 && live) {
+    if (g == 0) {
       if (A.rstd) A.rstd[t] = rstd;
       if (Q) A.s_x[t] = (a * rstd) / 127.0f;
     }
@@ -191,11 +212,9 @@ __global__ __launch_bounds__(BT) void rmsnorm_kernel(FwdArgs A) {
         h[i].to(v);
         gain8(A.gain, A.gain_f32, c, w);
         if (Q) {
-          uint32_t o[2] = {0u, 0u};
 #pragma unroll
-          for (int j = 0; j < 8; ++j)
-            o[j >> 2] |= (uint32_t)(aq_quant_one(v[j] * w[j], rcp, a) & 0xFF) << (8 * (j & 3));
-          *(uint2*)(A.Xq + t * A.K + 8 * c) = make_uint2(o[0], o[1]);
+          for (int j = 0; j < 8; ++j) v[j] *= w[j];
+          *(uint2*)(A.Xq + t * A.K + 8 * c) = codes8(v, rcp, a);
         } else {
 #pragma unroll
           for (int j = 0; j < 8; ++j) v[j] = v[j] * rstd * w[j];
@@ -218,25 +237,19 @@ struct BwdArgs {
   bool gain_f32;
 };
 
-template <bool F32, int BT, int TPR, int CH>
-__global__ __launch_bounds__(BT) void rmsnorm_grad_kernel(BwdArgs A) {
-  constexpr int ROWS = BT / TPR, WPR = TPR / 64;
-  __shared__ float red[2][BT / 64];
-  extern __shared__ float gsum[];                   // [ROWS - 1][K]
-  const int g = threadIdx.x % TPR, wave = threadIdx.x >> 6, row = threadIdx.x / TPR;
-  const int kc = A.K / 8, es = F32 ? 4 : 2;
+template <bool F32, int CH, int MAXT>
+__global__ __launch_bounds__(MAXT) void rmsnorm_grad_kernel(BwdArgs A) {
+  __shared__ float red[2][MAXT / 64];
+  const int g = threadIdx.x, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+  const int n = A.K / 8, es = F32 ? 4 : 2, TPR = blockDim.x;
   float dg[CH][8];
 #pragma unroll
   for (int i = 0; i < CH; ++i)
 #pragma unroll
     for (int j = 0; j < 8; ++j) dg[i][j] = 0.0f;
-  const int64_t step = (int64_t)gridDim.x * ROWS;
   int turn = 0;
-  for (int64_t t0 = (int64_t)blockIdx.x * ROWS; t0 < A.T; t0 += step, turn ^= 1) {
-    const int64_t t = t0 + row;
-    const bool live = t < A.T;
-    const int n = live ? kc : 0;
-    const float rstd = live ? A.rstd[t] : 0.0f;
+  for (int64_t t = blockIdx.x; t < A.T; t += gridDim.x, turn ^= 1) {
+    const float rstd = A.rstd[t];
     const char* yr = (const char*)A.dY + t * A.lddy * es;
     const char* hr = (const char*)A.H + t * A.ldh * es;
     const char* dr = (const char*)A.dH + t * A.lddh * es;
@@ -270,15 +283,11 @@ __global__ __launch_bounds__(BT) void rmsnorm_grad_kernel(BwdArgs A) {
       }
     }
     s = wave_sum(s);
-    if (WPR > 1) {
-      // two rows of red in turn: one barrier a round keeps a fast wave's next
-      // write away from a slow wave's read
+    if (waves > 1) {
       if ((threadIdx.x & 63) == 0) red[turn][wave] = s;
-      __syncthreads();
-      const int w0 = wave / WPR * WPR;
-      s = red[turn][w0];
-#pragma unroll
-      for (int w = 1; w < WPR; ++w) s += red[turn][w0 + w];
+      __syncthreads();                              // and the other set of red for the next round
+      const int l = threadIdx.x & 15;
+      s = row16_sum(l < waves ? red[turn][l] : 0.0f);
     }
     const float mean = s / (float)A.K;
 #pragma unroll
@@ -301,28 +310,11 @@ __global__ __launch_bounds__(BT) void rmsnorm_grad_kernel(BwdArgs A) {
       }
     }
   }
-  // dgain of the block's ROWS groups, added in their order
-  if (ROWS > 1) {
-    if (row > 0) {
-#pragma unroll
-      for (int i = 0; i < CH; ++i) {
-        const int c = g + TPR * i;
-        if (c < kc)
-#pragma unroll
-          for (int j = 0; j < 8; ++j) gsum[(row - 1) * A.K + 8 * c + j] = dg[i][j];
-      }
-    }
-    __syncthreads();
-    if (row > 0) return;
-  }
   float* out = A.part + (int64_t)blockIdx.x * A.K;
 #pragma unroll
   for (int i = 0; i < CH; ++i) {
     const int c = g + TPR * i;
-    if (c < kc) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        for (int w = 1; w < ROWS; ++w) dg[i][j] += gsum[(w - 1) * A.K + 8 * c + j];
+    if (c < n) {
       Vec8<true> o;
       o.from(dg[i]);
       o.store(out, c);
@@ -330,73 +322,80 @@ __global__ __launch_bounds__(BT) void rmsnorm_grad_kernel(BwdArgs A) {
   }
 }
 
-// dgain[k] = sum over the blocks' partials: 64 columns a block, 16 waves take
-// every 16th partial each, then the 16 sums are added in order
-__global__ __launch_bounds__(1024) void rmsnorm_dgain_kernel(const float* __restrict__ part, int G, int K,
-                                                             float* __restrict__ dgain) {
-  __shared__ float sm[16][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int k = blockIdx.x * 64 + lane;
-  float s = 0.0f;
-  if (k < K)
-    for (int b = wave; b < G; b += 16) s += part[(int64_t)b * K + k];
-  sm[wave][lane] = s;
-  __syncthreads();
-  if (wave == 0 && k < K) {
-    for (int w = 1; w < 16; ++w) s += sm[w][lane];
-    dgain[k] = s;
+// dgain[k] = sum over the blocks' partials: 16 columns a block, 4 a thread, 64
+// threads a column take every 64th partial each, then the 64 sums are added in a
+// tree.  (64 columns a block and 16 threads a column: 9.4 us for 512 x 4096.)
+__global__ __launch_bounds__(256) void rmsnorm_dgain_kernel(const float* __restrict__ part, int G, int K,
+                                                            float* __restrict__ dgain) {
+  __shared__ v4f sm[64][4];
+  const int q = threadIdx.x & 3, r = threadIdx.x >> 2;
+  const int k = blockIdx.x * 16 + 4 * q;
+  v4f s = (v4f){0.f, 0.f, 0.f, 0.f};
+  if (k < K) {
+    int b = r;
+    for (; b + 192 < G; b += 256) {                 // four loads in flight
+      const v4f x0 = *(const v4f*)(part + (int64_t)b * K + k), x1 = *(const v4f*)(part + (int64_t)(b + 64) * K + k);
+      const v4f x2 = *(const v4f*)(part + (int64_t)(b + 128) * K + k), x3 = *(const v4f*)(part + (int64_t)(b + 192) * K + k);
+      s += (x0 + x1) + (x2 + x3);
+    }
+    for (; b < G; b += 64) s += *(const v4f*)(part + (int64_t)b * K + k);
   }
+  sm[r][q] = s;
+  __syncthreads();
+#pragma unroll
+  for (int d = 32; d >= 1; d >>= 1) {
+    if (r < d) sm[r][q] += sm[r + d][q];
+    __syncthreads();
+  }
+  if (r == 0 && k < K) *(v4f*)(dgain + k) = sm[0][q];
 }
 
-constexpr int BWD_BLOCKS = 512;                     // two blocks of 256 threads per compute unit
+// threads of a block for n chunks at CH a thread
+int threads_for(int n, int ch) { return (int)round_up(cdiv(n, ch), 64); }
+int chunks_for(int n) { return n <= 512 ? 1 : n <= 2048 ? 2 : 4; }
 
-int bwd_blocks(int64_t T) { return (int)(T < BWD_BLOCKS ? T : BWD_BLOCKS); }
+// Blocks of the gradient: 16 waves a compute unit, but a block's partial of dgain
+// costs as much traffic as two rows in 16 bits, so at least 8 rows a block where
+// that leaves one block a compute unit.  (bf16, microseconds at 256 / 512 / 1024
+// blocks: T = 8192, K = 4096: 76 / 64 / 68; T = 8192, K = 1024: 41 / 27 / 22;
+// T = 4096, K = 2560: 33 / 27 / 31; T = 1021, K = 4096: 16.3 / 17.3 / 23.)
+int bwd_blocks(int64_t T, int64_t K) {
+  const int n = (int)(K / 8), most = 256 * 16 / (threads_for(n, chunks_for(n)) / 64);
+  int64_t g = T / 8 < 256 ? 256 : T / 8;
+  if (g > most) g = most;
+  return (int)(g < T ? g : T);
+}
 
 constexpr int64_t GRID_MAX = 1 << 20;               // blocks; rows beyond are taken in further rounds
 
-template <bool F32, bool Q, int BT, int TPR, int CH>
+template <bool F32, bool Q, int CH, int MAXT>
 void run_fwd(const FwdArgs& A, hipStream_t st) {
-  constexpr int ROWS = BT / TPR;
-  int64_t blocks = cdiv(A.T, ROWS);
-  if (blocks > GRID_MAX) blocks = GRID_MAX;
-  SBN_LAUNCH(Q ? "rmsnorm_quant" : "rmsnorm", (rmsnorm_kernel<F32, Q, BT, TPR, CH>), dim3((unsigned)blocks), dim3(BT), 0,
-             st, A);
+  SBN_LAUNCH(Q ? "rmsnorm_quant" : "rmsnorm", (rmsnorm_kernel<F32, Q, CH, MAXT>),
+             dim3((unsigned)(A.T < GRID_MAX ? A.T : GRID_MAX)), dim3((unsigned)threads_for(A.K / 8, CH)), 0, st, A);
 }
 
 template <bool F32, bool Q>
 void pick_fwd(const FwdArgs& A, hipStream_t st) {
-  const int kc = A.K / 8;
-  if (kc <= 512 && A.T >= 1024) {
-    const int ch = (kc + 63) / 64;
-    if (ch <= 1) run_fwd<F32, Q, 256, 64, 1>(A, st);
-    else if (ch <= 2) run_fwd<F32, Q, 256, 64, 2>(A, st);
-    else if (ch <= 3) run_fwd<F32, Q, 256, 64, 3>(A, st);
-    else if (ch <= 4) run_fwd<F32, Q, 256, 64, 4>(A, st);
-    else if (ch <= 5) run_fwd<F32, Q, 256, 64, 5>(A, st);
-    else if (ch <= 6) run_fwd<F32, Q, 256, 64, 6>(A, st);
-    else run_fwd<F32, Q, 256, 64, 8>(A, st);
-  } else if (kc <= 256) run_fwd<F32, Q, 256, 256, 1>(A, st);
-  else if (kc <= 512) run_fwd<F32, Q, 256, 256, 2>(A, st);
-  else if (kc <= 1024) run_fwd<F32, Q, 256, 256, 4>(A, st);
-  else if (kc <= 2048) run_fwd<F32, Q, 1024, 1024, 2>(A, st);
-  else run_fwd<F32, Q, 1024, 1024, 4>(A, st);
+  const int n = A.K / 8;
+  if (n <= 512) run_fwd<F32, Q, 1, 512>(A, st);
+  else if (n <= 1024) run_fwd<F32, Q, 2, 512>(A, st);
+  else if (n <= 2048) run_fwd<F32, Q, 2, 1024>(A, st);
+  else run_fwd<F32, Q, 4, 1024>(A, st);
 }
 
-template <bool F32, int BT, int TPR, int CH>
+template <bool F32, int CH, int MAXT>
 void run_bwd(const BwdArgs& A, int blocks, hipStream_t st) {
-  constexpr int ROWS = BT / TPR;
-  SBN_LAUNCH("rmsnorm_grad", (rmsnorm_grad_kernel<F32, BT, TPR, CH>), dim3((unsigned)blocks), dim3(BT),
-             (size_t)(ROWS - 1) * A.K * sizeof(float), st, A);
+  SBN_LAUNCH("rmsnorm_grad", (rmsnorm_grad_kernel<F32, CH, MAXT>), dim3((unsigned)blocks),
+             dim3((unsigned)threads_for(A.K / 8, CH)), 0, st, A);
 }
 
 template <bool F32>
 void pick_bwd(const BwdArgs& A, int blocks, hipStream_t st) {
-  const int kc = A.K / 8;
-  if (kc <= 256) run_bwd<F32, 256, 256, 1>(A, blocks, st);
-  else if (kc <= 512) run_bwd<F32, 256, 256, 2>(A, blocks, st);
-  else if (kc <= 1024) run_bwd<F32, 256, 256, 4>(A, blocks, st);
-  else if (kc <= 2048) run_bwd<F32, 1024, 1024, 2>(A, blocks, st);
-  else run_bwd<F32, 1024, 1024, 4>(A, blocks, st);
+  const int n = A.K / 8;
+  if (n <= 512) run_bwd<F32, 1, 512>(A, blocks, st);
+  else if (n <= 1024) run_bwd<F32, 2, 512>(A, blocks, st);
+  else if (n <= 2048) run_bwd<F32, 2, 1024>(A, blocks, st);
+  else run_bwd<F32, 4, 1024>(A, blocks, st);
 }
 
 }  // namespace
@@ -415,13 +414,13 @@ hipError_t launch_rmsnorm(const void* X, int64_t ldx, const void* res, int64_t l
   return hipGetLastError();
 }
 
-size_t rmsnorm_bwd_ws_bytes(int64_t T, int64_t K) { return align256((size_t)bwd_blocks(T) * (size_t)K * sizeof(float)); }
+size_t rmsnorm_bwd_ws_bytes(int64_t T, int64_t K) { return align256((size_t)bwd_blocks(T, K) * (size_t)K * sizeof(float)); }
 
 hipError_t launch_rmsnorm_backward(const void* dY, int64_t lddy, const void* H, int64_t ldh, const void* dH,
                                    int64_t lddh, bool f32, const void* gain, bool gain_f32, const float* rstd,
                                    int64_t T, int64_t K, void* dX, int64_t lddx, float* dgain, void* ws,
                                    hipStream_t st) {
-  const int blocks = bwd_blocks(T);
+  const int blocks = bwd_blocks(T, K);
   if (T > 0) {
     const BwdArgs A{dY, H, dH, gain, rstd, dX, (float*)ws, lddy, ldh, lddh, lddx, T, (int)K, gain_f32};
     if (f32) pick_bwd<true>(A, blocks, st);
@@ -429,7 +428,7 @@ hipError_t launch_rmsnorm_backward(const void* dY, int64_t lddy, const void* H, 
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  SBN_LAUNCH("rmsnorm_dgain", rmsnorm_dgain_kernel, dim3((unsigned)cdiv(K, 64)), dim3(1024), 0, st, (const float*)ws,
+  SBN_LAUNCH("rmsnorm_dgain", rmsnorm_dgain_kernel, dim3((unsigned)cdiv(K, 16)), dim3(256), 0, st, (const float*)ws,
              blocks, (int)K, dgain);
   return hipGetLastError();
 }
