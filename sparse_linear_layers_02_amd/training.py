@@ -9,11 +9,11 @@ none, everything else happens in the HIP kernels.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import re
 
-from . import (SBN_BF16, SBN_F32, SbnError, _check, _ptr, _req, _stream, _torch, _workspace, PKG_DIR)
-from . import _SIGNATURES, lib
+from . import _SIGNATURES, _WS, SBN_BF16, SBN_F32, PKG_DIR, SbnError, _check, _req, _torch, lib
 
 TRAIN_HEADER_PATH = os.path.join(os.path.dirname(PKG_DIR), "include", "sbn_train.h")
 SBN_ADAMW_BLOCK = 256
@@ -45,28 +45,33 @@ def train_header_symbols() -> list[str]:
     return sorted(set(re.findall(r"^\s*sbn_status\s+(sbn_\w+)\s*\(", text, re.M)))
 
 
+# Small calls are bound by what happens here before the launch, so the checks
+# below cost one expression where all is well, and say what is wrong elsewhere.
 def _dtype(t, name: str, fn: str) -> int:
     torch = _torch()
-    if t.dtype == torch.bfloat16:
+    if t.dtype is torch.bfloat16:
         return SBN_BF16
-    if t.dtype == torch.float32:
+    if t.dtype is torch.float32:
         return SBN_F32
     raise SbnError(fn, 6, f"{name} must be bfloat16 or float32, got {t.dtype}")
 
 
 def _rows(t, name: str, like, fn: str):
     """`t` is a row-major tensor of `like`'s shape, type and device."""
+    if t.dtype is like.dtype and t.shape == like.shape and t.device == like.device and t.stride(1) == 1:
+        return
     if t.dtype != like.dtype:
         raise SbnError(fn, 6, f"{name} must be {like.dtype}, got {t.dtype}")
     if t.shape != like.shape or t.device != like.device:
         raise SbnError(fn, 2, f"{name} must be {tuple(like.shape)} on {like.device}, "
                               f"got {tuple(t.shape)} on {t.device}")
-    if t.shape[1] > 1 and t.stride(1) != 1:
-        raise SbnError(fn, 2, f"{name} must have unit column stride (row-major)")
+    _matrix(t, name, fn)
 
 
 def _vector(t, name: str, n: int, dtype, device, fn: str):
     """`t` is a contiguous vector of n `dtype` on `device`."""
+    if t.dtype is dtype and t.shape == (n,) and t.stride(0) == 1 and t.device == device:
+        return
     if t.dtype != dtype:
         raise SbnError(fn, 6, f"{name} must be {dtype}, got {t.dtype}")
     if t.dim() != 1 or t.shape[0] != n or t.device != device:
@@ -87,6 +92,31 @@ def _matrix(t, name: str, fn: str):
         raise SbnError(fn, 2, f"{name} must have unit column stride (row-major)")
 
 
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _raw_stream(stream, device) -> int:
+    """The HIP stream to launch on: `stream`, or the current one of the tensors' device."""
+    if device.index is None:
+        raise SbnError("stream", 2, f"the tensors must be on a GPU, not on {device}")
+    if stream is not None:
+        return stream.cuda_stream
+    return _torch()._C._cuda_getCurrentRawStream(device.index)   # torch.cuda.current_stream() without its Stream object
+
+
+def _scratch(kind: str, nbytes: int, device, stream, raw: int):
+    """The package's grow-only workspace of (kind, device, stream)."""
+    key = (kind, device, raw)
+    buf = _WS.get(key)
+    if buf is None or buf.numel() < nbytes:
+        torch = _torch()
+        with torch.cuda.stream(torch.cuda.current_stream(device) if stream is None else stream):
+            buf = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
+        _WS[key] = buf
+    return buf
+
+
 # ------------------------------------------------------------------ RMS norm
 def _norm_args(fn, X, gain, residual, H, rstd):
     torch = _torch()
@@ -98,13 +128,13 @@ def _norm_args(fn, X, gain, residual, H, rstd):
     if residual is not None:
         _rows(residual, "residual", X, fn)
         if H is None:
-            H = torch.empty((T, K), dtype=X.dtype, device=X.device)
+            H = X.new_empty((T, K))
         else:
             _rows(H, "H", X, fn)
     elif H is not None:
         raise SbnError(fn, 2, "H is written only with a residual (without one, h is X)")
     if rstd is None:
-        rstd = torch.empty(T, dtype=torch.float32, device=X.device)
+        rstd = X.new_empty(T, dtype=torch.float32)
     else:
         _vector(rstd, "rstd", T, torch.float32, X.device, fn)
     return dt, gdt, T, K, H, rstd
@@ -116,13 +146,13 @@ def sbn_rmsnorm(X, gain, *, residual=None, eps: float = 1e-6, H=None, Y=None, rs
     fn = "sbn_rmsnorm"
     dt, gdt, T, K, H, rstd = _norm_args(fn, X, gain, residual, H, rstd)
     if Y is None:
-        Y = _torch().empty((T, K), dtype=X.dtype, device=X.device)
+        Y = X.new_empty((T, K))
     else:
         _rows(Y, "Y", X, fn)
     if T:
-        _check(fn, lib().sbn_rmsnorm(X.data_ptr(), _ld(X), _ptr(residual), 0 if residual is None else _ld(residual), dt,
-                                     gain.data_ptr(), gdt, T, K, eps, _ptr(H), 0 if H is None else _ld(H),
-                                     Y.data_ptr(), _ld(Y), rstd.data_ptr(), _stream(stream)))
+        _check(fn, lib().sbn_rmsnorm(X.data_ptr(), _ld(X), _addr(residual), 0 if residual is None else _ld(residual),
+                                     dt, gain.data_ptr(), gdt, T, K, eps, _addr(H), 0 if H is None else _ld(H),
+                                     Y.data_ptr(), _ld(Y), rstd.data_ptr(), _raw_stream(stream, X.device)))
     return Y, X if H is None else H, rstd
 
 
@@ -134,21 +164,29 @@ def sbn_rmsnorm_quant(X, gain, *, residual=None, eps: float = 1e-6, H=None, Xq=N
     torch = _torch()
     dt, gdt, T, K, H, rstd = _norm_args(fn, X, gain, residual, H, rstd)
     if Xq is None:
-        Xq = torch.empty((T, K), dtype=torch.int8, device=X.device)
+        Xq = X.new_empty((T, K), dtype=torch.int8)
     else:
         _req(Xq, "Xq", "i8", True, fn)
         if Xq.shape != X.shape or Xq.device != X.device:
             raise SbnError(fn, 2, f"Xq must be {tuple(X.shape)} on {X.device}")
     if s_x is None:
-        s_x = torch.empty(T, dtype=torch.float32, device=X.device)
+        s_x = X.new_empty(T, dtype=torch.float32)
     else:
         _vector(s_x, "s_x", T, torch.float32, X.device, fn)
     if T:
-        _check(fn, lib().sbn_rmsnorm_quant(X.data_ptr(), _ld(X), _ptr(residual),
+        _check(fn, lib().sbn_rmsnorm_quant(X.data_ptr(), _ld(X), _addr(residual),
                                            0 if residual is None else _ld(residual), dt, gain.data_ptr(), gdt, T, K,
-                                           eps, _ptr(H), 0 if H is None else _ld(H), Xq.data_ptr(), s_x.data_ptr(),
-                                           rstd.data_ptr(), _stream(stream)))
+                                           eps, _addr(H), 0 if H is None else _ld(H), Xq.data_ptr(), s_x.data_ptr(),
+                                           rstd.data_ptr(), _raw_stream(stream, X.device)))
     return Xq, s_x, X if H is None else H, rstd
+
+
+@functools.lru_cache(maxsize=1024)
+def _norm_scratch_bytes(T: int, K: int) -> int:
+    b = _sz()
+    fn = "sbn_rmsnorm_backward_workspace_bytes"
+    _check(fn, lib().sbn_rmsnorm_backward_workspace_bytes(T, K, ctypes.byref(b)))
+    return b.value
 
 
 def sbn_rmsnorm_backward(dY, H, gain, rstd, *, dH=None, dX=None, dgain=None, ws=None, stream=None):
@@ -166,21 +204,19 @@ def sbn_rmsnorm_backward(dY, H, gain, rstd, *, dH=None, dX=None, dgain=None, ws=
     if dH is not None:
         _rows(dH, "dH", H, fn)
     if dX is None:
-        dX = torch.empty((T, K), dtype=H.dtype, device=H.device)
+        dX = H.new_empty((T, K))
     else:
         _rows(dX, "dX", H, fn)
     if dgain is None:
-        dgain = torch.empty(K, dtype=torch.float32, device=H.device)
+        dgain = H.new_empty(K, dtype=torch.float32)
     else:
         _vector(dgain, "dgain", K, torch.float32, H.device, fn)
+    raw = _raw_stream(stream, H.device)
     if ws is None:
-        b = _sz()
-        _check(fn, lib().sbn_rmsnorm_backward_workspace_bytes(T, K, ctypes.byref(b)))
-        ws = _workspace("rmsnorm_backward", b.value, H.device, stream)
-    _check(fn, lib().sbn_rmsnorm_backward(dY.data_ptr(), _ld(dY), H.data_ptr(), _ld(H), _ptr(dH),
+        ws = _scratch("rmsnorm_backward", _norm_scratch_bytes(T, K), H.device, stream, raw)
+    _check(fn, lib().sbn_rmsnorm_backward(dY.data_ptr(), _ld(dY), H.data_ptr(), _ld(H), _addr(dH),
                                           0 if dH is None else _ld(dH), dt, gain.data_ptr(), gdt, rstd.data_ptr(), T, K,
-                                          dX.data_ptr(), _ld(dX), dgain.data_ptr(), _ptr(ws),
-                                          0 if ws is None else ws.numel(), _stream(stream)))
+                                          dX.data_ptr(), _ld(dX), dgain.data_ptr(), ws.data_ptr(), ws.numel(), raw))
     return dX, dgain
 
 
@@ -201,6 +237,7 @@ def _head_args(fn, X, W, labels):
     return T, V, K, 8 if labels.dtype == torch.int64 else 4
 
 
+@functools.lru_cache(maxsize=1024)
 def sbn_cross_entropy_workspace_bytes(T: int, V: int, K: int, backward: bool = False) -> int:
     fn = "sbn_cross_entropy_backward_workspace_bytes" if backward else "sbn_cross_entropy_workspace_bytes"
     b = _sz()
@@ -216,18 +253,18 @@ def sbn_cross_entropy(X, W, labels, *, loss=None, lse=None, ws=None, stream=None
     torch = _torch()
     T, V, K, lb = _head_args(fn, X, W, labels)
     if loss is None:
-        loss = torch.empty(T, dtype=torch.float32, device=X.device)
+        loss = X.new_empty(T, dtype=torch.float32)
     else:
         _vector(loss, "loss", T, torch.float32, X.device, fn)
     if lse is None:
-        lse = torch.empty(T, dtype=torch.float32, device=X.device)
+        lse = X.new_empty(T, dtype=torch.float32)
     else:
         _vector(lse, "lse", T, torch.float32, X.device, fn)
+    raw = _raw_stream(stream, X.device)
     if ws is None:
-        ws = _workspace("cross_entropy", sbn_cross_entropy_workspace_bytes(T, V, K), X.device, stream)
+        ws = _scratch("cross_entropy", sbn_cross_entropy_workspace_bytes(T, V, K), X.device, stream, raw)
     _check(fn, lib().sbn_cross_entropy(X.data_ptr(), _ld(X), W.data_ptr(), _ld(W), labels.data_ptr(), lb, T, V, K,
-                                       loss.data_ptr(), lse.data_ptr(), _ptr(ws), 0 if ws is None else ws.numel(),
-                                       _stream(stream)))
+                                       loss.data_ptr(), lse.data_ptr(), ws.data_ptr(), ws.numel(), raw))
     return loss, lse
 
 
@@ -259,13 +296,13 @@ def sbn_cross_entropy_backward(X, W, labels, lse, dloss, *, dxdt: int = SBN_BF16
 
     dX = out(dX, "dX", need_dX, dxdt, X)
     dW = out(dW, "dW", need_dW, dwdt, W)
+    raw = _raw_stream(stream, X.device)
     if ws is None:
-        ws = _workspace("cross_entropy_backward", sbn_cross_entropy_workspace_bytes(T, V, K, True), X.device, stream)
+        ws = _scratch("cross_entropy_backward", sbn_cross_entropy_workspace_bytes(T, V, K, True), X.device, stream, raw)
     _check(fn, lib().sbn_cross_entropy_backward(X.data_ptr(), _ld(X), W.data_ptr(), _ld(W), labels.data_ptr(), lb,
-                                                lse.data_ptr(), dloss.data_ptr(), T, V, K, _ptr(dX), dxdt,
-                                                0 if dX is None else _ld(dX), _ptr(dW), dwdt,
-                                                0 if dW is None else _ld(dW), _ptr(ws), 0 if ws is None else ws.numel(),
-                                                _stream(stream)))
+                                                lse.data_ptr(), dloss.data_ptr(), T, V, K, _addr(dX), dxdt,
+                                                0 if dX is None else _ld(dX), _addr(dW), dwdt,
+                                                0 if dW is None else _ld(dW), ws.data_ptr(), ws.numel(), raw))
     return dX, dW
 
 
@@ -353,7 +390,8 @@ def sbn_adamw_step(table, *, lr: float, step: int, beta1: float = 0.9, beta2: fl
     if dyn is not None:
         _vector(dyn, "dyn", 4, _torch().float32, table.map.device, fn)
     _check(fn, lib().sbn_adamw_step(table.entries.data_ptr(), table.map.data_ptr(), table.blocks, table.pdt, table.gdt,
-                                    table.state_bits, lr, beta1, beta2, eps, step, _ptr(dyn), _stream(stream)))
+                                    table.state_bits, lr, beta1, beta2, eps, step, _addr(dyn),
+                                    _raw_stream(stream, table.map.device)))
 
 
 def _decode(codes, scale, second, out, stream):
@@ -369,7 +407,7 @@ def _decode(codes, scale, second, out, stream):
         if out.numel() != n or out.device != codes.device:
             raise SbnError(fn, 2, f"out must have {n} elements on {codes.device}")
     _check(fn, lib().sbn_adamw_decode_state(codes.data_ptr(), scale.data_ptr(), n, second, out.data_ptr(),
-                                            _stream(stream)))
+                                            _raw_stream(stream, codes.device)))
     return out
 
 
@@ -401,7 +439,7 @@ def _encode(x, second, codes, scale, stream):
     else:
         _vector(scale, "scale", ns, torch.float32, x.device, fn)
     _check(fn, lib().sbn_adamw_encode_state(x.data_ptr(), n, second, codes.data_ptr(), scale.data_ptr(),
-                                            _stream(stream)))
+                                            _raw_stream(stream, x.device)))
     return codes, scale
 
 

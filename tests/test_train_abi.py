@@ -207,3 +207,21 @@ def test_binding_refuses_layouts_the_abi_cannot_see():
         with pytest.raises(sbn.SbnError):
             f()
             raise AssertionError(f"case {i} was accepted")
+
+
+def test_binding_refuses_host_tensors():
+    """Layouts that are right, in host memory: refused before any pointer reaches a kernel."""
+    import torch
+    bf, f32 = torch.bfloat16, torch.float32
+    z = lambda *s, dt=bf: torch.zeros(*s, dtype=dt)  # noqa: E731
+    v = lambda n: z(n, dt=f32)  # noqa: E731
+    t = sbn.AdamWTable([v(8)], [v(8)], [v(8)], [v(8)])
+    for f in (lambda: sbn.sbn_rmsnorm(z(4, 64), z(64)), lambda: sbn.sbn_rmsnorm_quant(z(4, 64), z(64)),
+              lambda: sbn.sbn_rmsnorm_backward(z(4, 64), z(4, 64), z(64), v(4)),
+              lambda: sbn.sbn_cross_entropy(z(4, 64), z(10, 64), z(4, dt=torch.int64)),
+              lambda: sbn.sbn_cross_entropy_backward(z(4, 64), z(10, 64), z(4, dt=torch.int64), v(4), v(4)),
+              lambda: sbn.sbn_adamw_step(t, lr=1e-3, step=1), lambda: sbn.sbn_adamw_encode_m(v(8)),
+              lambda: sbn.sbn_adamw_decode_v(z(8, dt=torch.uint8), v(1))):
+        with pytest.raises(sbn.SbnError) as e:
+            f()
+        assert e.value.status == SHAPE and "GPU" in str(e.value)
