@@ -13,8 +13,9 @@
  *                   states in 32 or in 8 bits.
  *
  * The conventions of sbn.h hold: device pointers owned by the caller and
- * 16-byte aligned, row-major tensors with leading dimensions in elements and
- * multiples of 8, work enqueued on `stream`, arguments checked on the host
+ * 16-byte aligned (rstd, s_x, labels, loss, lse and dloss: aligned to their
+ * elements), row-major tensors with leading dimensions in elements and multiples
+ * of 8, work enqueued on `stream`, arguments checked on the host
  * before anything is launched, nothing launched on an error, messages from
  * sbn_last_error(), no allocation, no synchronisation, no exception across the
  * ABI.  Every call may be captured into a HIP graph.  Results do not depend on
@@ -101,7 +102,8 @@ sbn_status sbn_rmsnorm_backward(const void* dY, int64_t lddy, const void* H, int
  *   l[t,v]  = sum_k X[t,k] * W[v,k]                       (float32, not kept)
  *   lse[t]  = log sum_v exp(l[t,v])
  *   loss[t] = lse[t] - l[t, labels[t]], 0 where labels[t] is outside [0, V)
- * A label outside [0, V), such as -100, marks a token without a target.
+ * A label outside [0, V), such as -100, marks a token without a target.  What
+ * dloss and lse hold for it does not matter; its row of X has to be finite.
  *
  *   X      [T x K] bf16, row stride ldx >= K     hidden states
  *   W      [V x K] bf16, row stride ldw >= K     the head's weights

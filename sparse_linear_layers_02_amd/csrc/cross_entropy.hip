@@ -473,9 +473,19 @@ __global__ __launch_bounds__(1024) void ce_gmax_kernel(const float* __restrict__
                                                        float* __restrict__ gmax) {
   __shared__ float sm[16];
   float m = 0.0f;
-  for (int t = threadIdx.x; t < T; t += 1024) {
-    const int64_t y = label_at(labels, labels64, t);
-    if (y >= 0 && y < V) m = fmaxf(m, fabsf(dloss[t]));
+  constexpr int AHEAD = 8;                           // loads in flight
+  for (int t0 = threadIdx.x; t0 < T; t0 += 1024 * AHEAD) {
+    float g[AHEAD];
+    int64_t y[AHEAD];
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k) {
+      const int t = t0 + 1024 * k < T ? t0 + 1024 * k : t0;
+      g[k] = dloss[t];
+      y[k] = label_at(labels, labels64, t);
+    }
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k)
+      if (y[k] >= 0 && y[k] < V) m = fmaxf(m, fabsf(g[k]));
   }
 #pragma unroll
   for (int d = 32; d >= 1; d >>= 1) m = fmaxf(m, __shfl_xor(m, d));

@@ -22,6 +22,13 @@ sbn_status check_float_dtype(const char* fn, const char* name, sbn_dtype d) {
 
 int bytes_of(sbn_dtype d) { return d == SBN_F32 ? 4 : 2; }
 
+// vectors that are read and written one element at a time
+#define SBN_ELEM_ALIGNED(p, bytes)                                                                       \
+  do {                                                                                                   \
+    if ((uintptr_t)(p) & ((bytes) - 1))                                                                  \
+      return fail(SBN_ERR_ALIGN, "%s: '%s' is not aligned to its %d-byte elements", fn, #p, (int)(bytes)); \
+  } while (0)
+
 sbn_status check_t0(const char* fn, int64_t T) {
   if (T < 0) return fail(SBN_ERR_SHAPE, "%s: T = %lld is negative", fn, (long long)T);
   if (T > ROWS_MAX) return fail(SBN_ERR_SHAPE, "%s: T = %lld exceeds 2^40", fn, (long long)T);
@@ -51,7 +58,7 @@ sbn_status check_norm(const char* fn, const void* X, int64_t ldx, const void* re
   SBN_TRY(check_ld("ldx", ldx, K, T));
   SBN_ALIGNED(X);
   SBN_ALIGNED(gain);
-  SBN_ALIGNED(rstd);
+  SBN_ELEM_ALIGNED(rstd, 4);
   if (residual) {
     SBN_NONNULL(H);
     SBN_TRY(check_ld("ldres", ldres, K, T));
@@ -102,7 +109,7 @@ sbn_status check_ce(const char* fn, const uint16_t* X, int64_t ldx, const uint16
     return fail(SBN_ERR_SHAPE, "%s: ldx = %lld and ldw = %lld must be <= 2^22", fn, (long long)ldx, (long long)ldw);
   SBN_ALIGNED(X);
   SBN_ALIGNED(W);
-  SBN_ALIGNED(labels);
+  SBN_ELEM_ALIGNED(labels, label_bytes);
   return SBN_OK;
 }
 
@@ -140,7 +147,7 @@ sbn_status sbn_rmsnorm_quant(const void* X, int64_t ldx, const void* residual, i
   SBN_NONNULL(Xq);
   SBN_NONNULL(s_x);
   SBN_ALIGNED(Xq);
-  SBN_ALIGNED(s_x);
+  SBN_ELEM_ALIGNED(s_x, 4);
   hipStream_t st = (hipStream_t)stream;
   SBN_TRY(finite_norm(fn, X, ldx, residual, ldres, dt, gain, gaindt, T, K, st));
   return hip_result(launch_rmsnorm(X, ldx, residual, ldres, dt == SBN_F32, gain, gaindt == SBN_F32, T, K, eps, H, ldh,
@@ -182,7 +189,7 @@ sbn_status sbn_rmsnorm_backward(const void* dY, int64_t lddy, const void* H, int
     SBN_ALIGNED(H);
     SBN_ALIGNED(dH);
     SBN_ALIGNED(gain);
-    SBN_ALIGNED(rstd);
+    SBN_ELEM_ALIGNED(rstd, 4);
     SBN_ALIGNED(dX);
     SBN_ALIGNED(ws);
     if ((dX == dY && lddx != lddy) || (dX == dH && lddx != lddh))
@@ -217,8 +224,8 @@ sbn_status sbn_cross_entropy(const uint16_t* X, int64_t ldx, const uint16_t* W, 
   SBN_NONNULL(loss);
   SBN_NONNULL(lse);
   SBN_NONNULL(ws);
-  SBN_ALIGNED(loss);
-  SBN_ALIGNED(lse);
+  SBN_ELEM_ALIGNED(loss, 4);
+  SBN_ELEM_ALIGNED(lse, 4);
   SBN_ALIGNED(ws);
   const size_t need = ce_ws_bytes(T, V, K);
   if (ws_bytes < need) return fail(SBN_ERR_WORKSPACE, "%s: workspace %zu bytes, need %zu", fn, ws_bytes, need);
@@ -257,8 +264,8 @@ sbn_status sbn_cross_entropy_backward(const uint16_t* X, int64_t ldx, const uint
   SBN_NONNULL(lse);
   SBN_NONNULL(dloss);
   SBN_NONNULL(ws);
-  SBN_ALIGNED(lse);
-  SBN_ALIGNED(dloss);
+  SBN_ELEM_ALIGNED(lse, 4);
+  SBN_ELEM_ALIGNED(dloss, 4);
   SBN_ALIGNED(ws);
   const size_t need = ce_bwd_ws_bytes(T, V, K);
   if (ws_bytes < need) return fail(SBN_ERR_WORKSPACE, "%s: workspace %zu bytes, need %zu", fn, ws_bytes, need);

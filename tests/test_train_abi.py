@@ -12,6 +12,7 @@ import sparse_linear_layers_02_amd as sbn
 OK, NULL, SHAPE, NM, ALIGN, WS, DTYPE, HIP, FLAGS, VALUE = range(10)
 P, P2, P3 = (ctypes.c_void_p(a) for a in (0x100000, 0x200000, 0x300000))
 MIS = ctypes.c_void_p(0x100004)
+ODD = ctypes.c_void_p(0x100002)        # not aligned to a float either
 F32, BF16 = sbn.SBN_F32, sbn.SBN_BF16
 
 
@@ -48,11 +49,11 @@ def test_rmsnorm_refusals(L, quant):
                        (dict(ldr=56), SHAPE), (dict(ldh=68), ALIGN), (dict(dt=2), DTYPE), (dict(gdt=7), DTYPE),
                        (dict(eps=-1.0), VALUE), (dict(eps=float("nan")), VALUE), (dict(eps=float("inf")), VALUE),
                        (dict(X=MIS), ALIGN), (dict(gain=MIS), ALIGN), (dict(res=MIS), ALIGN), (dict(H=MIS), ALIGN),
-                       (dict(Y=MIS), ALIGN), (dict(rstd=MIS), ALIGN), (dict(H=P2, ldh=72), SHAPE)]:
+                       (dict(Y=MIS), ALIGN), (dict(rstd=ODD), ALIGN), (dict(H=P2, ldh=72), SHAPE)]:
         assert call(**kw) == status, kw
         assert sbn.lib().sbn_last_error() != b""
     if quant:
-        assert call(s=None) == NULL and call(s=MIS) == ALIGN
+        assert call(s=None) == NULL and call(s=ODD) == ALIGN
     else:
         assert call(ldy=56) == SHAPE and call(ldy=68) == ALIGN
 
@@ -96,10 +97,11 @@ def test_cross_entropy_refusals(L):
                        (dict(V=1 << 31), SHAPE), (dict(K=96), SHAPE), (dict(K=0), SHAPE), (dict(ldx=120), SHAPE),
                        (dict(ldw=132), ALIGN), (dict(ldx=(1 << 22) + 8), SHAPE), (dict(T=1 << 27), SHAPE),
                        (dict(T=1 << 24, V=1 << 20), SHAPE), (dict(lb=2), DTYPE), (dict(X=MIS), ALIGN),
-                       (dict(W=MIS), ALIGN), (dict(lab=MIS), ALIGN), (dict(lse=MIS), ALIGN), (dict(ws=MIS), ALIGN)]:
+                       (dict(W=MIS), ALIGN), (dict(lab=MIS), ALIGN), (dict(lb=4, lab=ODD), ALIGN), (dict(lse=ODD), ALIGN),
+                       (dict(ws=MIS), ALIGN)]:
         assert both(**kw) == (status, status), kw
-    assert both(loss=None)[0] == NULL and both(loss=MIS)[0] == ALIGN
-    for kw, status in [(dict(dloss=None), NULL), (dict(dloss=MIS), ALIGN), (dict(dxdt=2), DTYPE), (dict(dwdt=9), DTYPE),
+    assert both(loss=None)[0] == NULL and both(loss=ODD)[0] == ALIGN
+    for kw, status in [(dict(dloss=None), NULL), (dict(dloss=ODD), ALIGN), (dict(dxdt=2), DTYPE), (dict(dwdt=9), DTYPE),
                        (dict(lddx=64), SHAPE), (dict(lddw=132), ALIGN), (dict(dX=MIS), ALIGN), (dict(dW=MIS), ALIGN)]:
         assert both(**kw)[1] == status, kw
     assert both(T=0, X=None, W=None, dW=None) == (OK, OK)                      # nothing to do
