@@ -90,7 +90,9 @@ __device__ inline void tile_of(int b, int blocks, int nta, int ntb, int& ta, int
 // between the register files around every matrix instruction (some 500 moves a
 // stage against 128 products).  What the compiler then does not see: a result
 // may be read by other instructions only some cycles later.  settle() waits for
-// that, and fetch() is the only way the accumulators are read after it.
+// that, and fetch() is the only way the accumulators are read after it.  (The
+// fragments come from LDS reads, for which the compiler waits; a result is the
+// operand of a product again 8 products later at the soonest.)
 __device__ inline void mfma_acc(v4f& acc, v8bf a, v8bf b) {
   asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(acc) : "v"(a), "v"(b));
 }
@@ -182,8 +184,8 @@ __global__ __launch_bounds__(64 * WA * WB, 1) void ce_gemm_kernel(GemmArgs P) {
   const int s_lo = (int)((int64_t)P.steps * part / P.splits), s_hi = (int)((int64_t)P.steps * (part + 1) / P.splits);
   const int nsteps = s_hi - s_lo;
 
-  // Byte offsets of this lane's loads.  Outputs past the operand are clamped here;
-  // with contraction rows, offset() clamps the row in the stage that is loaded.
+  // Byte offsets of this lane's loads.  Outputs past the operand are clamped here,
+  // contraction rows past it (in the last stage) by load_one().
   const uint32_t ldA = (uint32_t)P.lda * 2, ldB = (uint32_t)P.ldb * 2;
   uint32_t offA[2][LA], offB[2][LB];                 // TR: of the chunk alone
   int rowA[LA], rowB[LB];
@@ -272,6 +274,8 @@ __global__ __launch_bounds__(64 * WA * WB, 1) void ce_gemm_kernel(GemmArgs P) {
     const bool lower = WB > 1 ? wb >= WB / 2 : j >= MJ / 2;
     fb[sub][j] = fragment(HB{}, smem + (lower ? p1 : p0) * HALF + HA::BYTES, f, sub);
   };
+  // taken in snake order: each product shares an operand with the one before (0.3% of a training step)
+  auto multiply = [&](int i, int j, int sub) { mfma_acc(acc[i][j], fa[sub][i], fb[sub][j]); };
   auto wrap = [](int p) { return p >= RING ? p - RING : p; };
   auto clamp = [&](int s) { return s < nsteps ? s : nsteps - 1; };
 
@@ -308,7 +312,7 @@ __global__ __launch_bounds__(64 * WA * WB, 1) void ce_gemm_kernel(GemmArgs P) {
       for (int q = 0; q < LPH; ++q)
         if (q * MI / LPH == i) load_one(q, H0, free0, s0);
 #pragma unroll
-      for (int j = 0; j < MJ; ++j) mfma_acc(acc[i][j], fa[0][i], fb[0][j]);
+      for (int j = 0; j < MJ; ++j) multiply(i, i & 1 ? MJ - 1 - j : j, 0);
       __builtin_amdgcn_sched_barrier(0);
     }
     stage_barrier<(RING - 4) * LPH>();
@@ -322,7 +326,7 @@ __global__ __launch_bounds__(64 * WA * WB, 1) void ce_gemm_kernel(GemmArgs P) {
       for (int q = 0; q < LPH; ++q)
         if (q * MI / LPH == i) load_one(q, H1, p0, s1);
 #pragma unroll
-      for (int j = 0; j < MJ; ++j) mfma_acc(acc[i][j], fa[1][i], fb[1][j]);
+      for (int j = 0; j < MJ; ++j) multiply(i, i & 1 ? MJ - 1 - j : j, 1);
       __builtin_amdgcn_sched_barrier(0);
     }
     p0 = n0;
@@ -371,7 +375,7 @@ __global__ __launch_bounds__(64 * WA * WB, 1) void ce_gemm_kernel(GemmArgs P) {
     // each of 16 rows spread over the banks, and rows leave in whole lines.
     constexpr int PITCH = 2 * TA + 32;
     auto at = [&](int t, int v) { return smem + t * PITCH + v * 2; };
-    const float gm = *P.gmax, ginv = gm > 0.0f ? 1.0f / gm : 0.0f;
+    const float gm = *P.gmax, ginv = gm >= 0x1p-126f ? 1.0f / gm : 0.0f;   // smaller ones have no quotient: gradients 0
     lds_barrier();                                   // every wave has read its last fragments
 #pragma unroll
     for (int j = 0; j < MJ; ++j) {
