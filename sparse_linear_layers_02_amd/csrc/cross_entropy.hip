@@ -32,6 +32,7 @@ constexpr int BK = 64;                              // contraction entries of on
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 constexpr float NONE = -1.0e38f * LOG2E;            // the (scaled) maximum of no logits: finite, so that NONE - NONE is 0
 constexpr int64_t D_ELEMS = int64_t(1) << 27;       // elements of D in the workspace
+constexpr int GMAX_WAVE = 1024;                     // tokens whose largest |dloss| a wave finds in two rounds of loads
 constexpr int CUS = 256;
 
 enum Epi { EPI_STATS, EPI_GRAD, EPI_OUT };
@@ -52,7 +53,7 @@ struct GemmArgs {
   float2* stats;                       // [2-wave column groups][nB]: maximum (times log2 e), sum
   float* target;                       // [nB] logit of the label
   const float *lse, *dloss;
-  const float* gmax;                   // max |dloss|; EPI_GRAD divides by it, EPI_OUT multiplies
+  float* gmax;                         // max |dloss|; EPI_GRAD divides by it, EPI_OUT multiplies
   uint16_t* D;                         // [tpad][ldd]; 0 past the tokens, and in columns nA .. vpad - 1
   int64_t ldd;
   int tpad, vpad;
@@ -66,6 +67,28 @@ struct GemmArgs {
 
 __device__ inline int64_t label_at(const void* labels, bool is64, int t) {
   return is64 ? ((const int64_t*)labels)[t] : (int64_t)((const int32_t*)labels)[t];
+}
+
+// max |dloss| over the tokens first, first + step, ... with a target, of a wave
+__device__ inline float max_dloss(const float* dloss, const void* labels, bool is64, int V, int T, int first, int step) {
+  constexpr int AHEAD = 8;                           // loads in flight
+  float m = 0.0f;
+  for (int t0 = first; t0 < T; t0 += step * AHEAD) {
+    float g[AHEAD];
+    int64_t y[AHEAD];
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k) {
+      const int t = t0 + step * k < T ? t0 + step * k : t0;
+      g[k] = dloss[t];
+      y[k] = label_at(labels, is64, t);
+    }
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k)
+      if (y[k] >= 0 && y[k] < V) m = fmaxf(m, fabsf(g[k]));
+  }
+#pragma unroll
+  for (int d = 32; d >= 1; d >>= 1) m = fmaxf(m, __shfl_xor(m, d));
+  return m;
 }
 
 // Tile order: the hardware deals consecutive blocks to the 8 XCDs in turn, so
@@ -375,7 +398,16 @@ __global__ __launch_bounds__(64 * WA * WB, 1) void ce_gemm_kernel(GemmArgs P) {
     // each of 16 rows spread over the banks, and rows leave in whole lines.
     constexpr int PITCH = 2 * TA + 32;
     auto at = [&](int t, int v) { return smem + t * PITCH + v * 2; };
-    const float gm = *P.gmax, ginv = gm >= 0x1p-126f ? 1.0f / gm : 0.0f;   // smaller ones have no quotient: gradients 0
+    // of few tokens every wave finds the largest |dloss| itself, which a launch of
+    // its own would take longer for
+    float gm;
+    if (P.nB <= GMAX_WAVE) {
+      gm = max_dloss(P.dloss, P.labels, P.labels64, P.V, P.nB, lane, 64);
+      if (blockIdx.x == 0 && tid == 0) *P.gmax = gm;
+    } else {
+      gm = *P.gmax;
+    }
+    const float ginv = gm >= 0x1p-126f ? 1.0f / gm : 0.0f;   // smaller ones have no quotient: gradients 0
     lds_barrier();                                   // every wave has read its last fragments
 #pragma unroll
     for (int j = 0; j < MJ; ++j) {
@@ -471,28 +503,12 @@ __global__ __launch_bounds__(1024) void ce_join_kernel(const float2* __restrict_
   }
 }
 
-// max |dloss| over the tokens with a target
+// max |dloss| over the tokens with a target, for more than GMAX_WAVE tokens
 __global__ __launch_bounds__(1024) void ce_gmax_kernel(const float* __restrict__ dloss,
                                                        const void* __restrict__ labels, bool labels64, int V, int T,
                                                        float* __restrict__ gmax) {
   __shared__ float sm[16];
-  float m = 0.0f;
-  constexpr int AHEAD = 8;                           // loads in flight
-  for (int t0 = threadIdx.x; t0 < T; t0 += 1024 * AHEAD) {
-    float g[AHEAD];
-    int64_t y[AHEAD];
-#pragma unroll
-    for (int k = 0; k < AHEAD; ++k) {
-      const int t = t0 + 1024 * k < T ? t0 + 1024 * k : t0;
-      g[k] = dloss[t];
-      y[k] = label_at(labels, labels64, t);
-    }
-#pragma unroll
-    for (int k = 0; k < AHEAD; ++k)
-      if (y[k] >= 0 && y[k] < V) m = fmaxf(m, fabsf(g[k]));
-  }
-#pragma unroll
-  for (int d = 32; d >= 1; d >>= 1) m = fmaxf(m, __shfl_xor(m, d));
+  float m = max_dloss(dloss, labels, labels64, V, T, threadIdx.x, 1024);
   if ((threadIdx.x & 63) == 0) sm[threadIdx.x >> 6] = m;
   __syncthreads();
   if (threadIdx.x == 0) {
@@ -686,8 +702,10 @@ hipError_t launch_ce_backward(const uint16_t* X, int64_t ldx, const uint16_t* W,
   uint16_t* D = (uint16_t*)(w + L.d);
   float *acc = (float*)(w + L.acc), *part = (float*)(w + L.part), *gmax = (float*)(w + L.gmax);
   hipError_t e;
-  SBN_LAUNCH("ce_gmax", ce_gmax_kernel, dim3(1), dim3(1024), 0, st, dloss, labels, labels64, (int)V, (int)T, gmax);
-  if ((e = hipGetLastError()) != hipSuccess) return e;
+  if (T > GMAX_WAVE) {
+    SBN_LAUNCH("ce_gmax", ce_gmax_kernel, dim3(1), dim3(1024), 0, st, dloss, labels, labels64, (int)V, (int)T, gmax);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+  }
   for (int64_t i = 0; i < L.pieces; ++i) {
     const int64_t v0 = i * L.piece, nv = V - v0 < L.piece ? V - v0 : L.piece;
     const int64_t vpad = round_up(nv, 64);           // contraction of dX over this piece
