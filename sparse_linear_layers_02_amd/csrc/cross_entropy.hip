@@ -57,11 +57,11 @@ struct GemmArgs {
   uint16_t* D;                         // [tpad][ldd]; 0 past the tokens, and in columns nA .. vpad - 1
   int64_t ldd;
   int tpad, vpad;
-  // EPI_OUT: C [nB][ldc], A rows along the row
+  // EPI_OUT: C [nB][ldc], A outputs along the row
   void* C;
-  const float* Cin;                    // added first, or NULL
-  float* part;                         // splits > 1: [splits][nB][nA] float32 instead of C
+  const float* Cin;                    // [nB][nA], added first, or NULL
   int64_t ldc;
+  int64_t part_stride;                 // elements of C from one part of the contraction to the next
   bool c_f32;
 };
 
@@ -96,16 +96,19 @@ __device__ inline float max_dloss(const float* dloss, const void* labels, bool i
 // which 4 B tiles go together and A runs inside: the 32 blocks an XCD has in
 // flight then share 4 B and 8 A row panels in its L2.  (T = 8192, V = 65536,
 // K = 4096, gradients included: 13.08 ms with 4, 13.23 with 8, 13.4 with 16.)
+// (The quotients are made by the vector unit; scalar(), so that what follows from
+// them, the addresses and counters of the loops, is not computed there too.)
+__device__ inline int scalar(int x) { return __builtin_amdgcn_readfirstlane(x); }
 __device__ inline void tile_of(int b, int blocks, int nta, int ntb, int& ta, int& tb) {
   constexpr int XCDS = 8, GROUP = 4;
   const int per = blocks / XCDS, rem = blocks % XCDS;
   const int x = b % XCDS;
   int i = x * per + (x < rem ? x : rem) + b / XCDS;
-  const int g = i / (nta * GROUP);
+  const int g = scalar(i / (nta * GROUP));
   i -= g * nta * GROUP;
   const int w = ntb - g * GROUP < GROUP ? ntb - g * GROUP : GROUP;
-  ta = i / w;
-  tb = g * GROUP + i % w;
+  ta = scalar(i / w);
+  tb = g * GROUP + (i - ta * w);
 }
 
 // acc += a b^T, the accumulator held in the accumulation registers.  Written in
@@ -137,6 +140,10 @@ __device__ inline v4f fetch(v4f& acc) {
   asm volatile("" : "+a"(acc));
   return acc;
 }
+__device__ inline void clear(v4f& acc) {
+  acc = (v4f){0.f, 0.f, 0.f, 0.f};
+  asm volatile("" : "+a"(acc));
+}
 
 // All waves meet: each has its LDS reads and all but its latest N loads behind it.
 // By the builtin, so that the compiler knows the reads done and adds no wait.
@@ -149,6 +156,16 @@ __device__ inline void stage_barrier() {
   asm volatile("" ::: "memory");
 }
 
+// The kernel's arguments, read again where they are used: held over the loops,
+// those of the epilogue and of the next tile's start pushed the loops' own
+// addresses out of the scalar registers.
+typedef __attribute__((address_space(4))) const GemmArgs ArgsInMemory;
+__device__ inline ArgsInMemory& reread_args() {
+  ArgsInMemory* q = (ArgsInMemory*)__builtin_amdgcn_kernarg_segment_ptr();
+  asm volatile("" : "+s"(q));
+  return *q;
+}
+__device__ inline float uniform(float x) { return __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(x))); }
 __device__ inline void lds_reads_done() { __builtin_amdgcn_s_waitcnt(15 | (3 << 14) | (7 << 4)); }
 
 // One operand's half stage in LDS: HR outputs x 64 contraction entries.
@@ -185,37 +202,60 @@ struct HalfStage {
 // measured 10% slower).  It is loaded in two halves, the upper outputs of A and
 // of B and then the lower ones, each into the next place of a ring of RING
 // places: the loads go out evenly over a stage instead of all after its barrier.
+//
+// Blocks stay and take tiles in turn.  The loads run AHEAD stages before the
+// products and go on into the next tile, so only a block's first tile waits for
+// its first stages, and the loads of a tile's last stages are not wasted.
+// (Against one tile a block: 64 tokens' gradients 137 for 144 us, 1021 tokens 462
+// for 474, evaluation of 4096 tokens 975 for 989, 8192 tokens 12.64 for 12.69 ms;
+// 512 tokens of 8000 entries, one round of tiles, 54.9 for 53.3.)
+//
+// Bound by the matrix cores: at T = 8192, V = 65536, K = 4096 they are busy 70% of
+// the cycles, at the 1.7 to 2.0 GHz that the part's power allows under them; 1.4
+// PFLOP/s of the forward, the library's plain product 1.4 to 1.5.
 template <int WA, int WB, int MI, int MJ, int RING, int EPI, bool TRA, bool TRB>
 __global__ __launch_bounds__(64 * WA * WB, 1) void ce_gemm_kernel(GemmArgs P) {
-  constexpr int TA = WA * MI * 16, TB = WB * MJ * 16, NW = WA * WB, NT = 64 * NW;
+  constexpr int TA = WA * MI * 16, TB = WB * MJ * 16, NW = WA * WB;
   using HA = HalfStage<TRA, TA / 2>;
   using HB = HalfStage<TRB, TB / 2>;
   constexpr int HALF = HA::BYTES + HB::BYTES;
   constexpr int LA = TA / (16 * NW), LB = TB / (16 * NW);    // 1 KB loads per wave and half stage
   constexpr int LPH = LA + LB;
+  constexpr int AHEAD = RING / 2;
   extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
-  static_assert(RING >= 5 && (RING - 3) * LPH < 64, "places of a stage, the next one and a half in flight");
+  static_assert(RING >= 5 && RING % 2 == 1 && (RING - 3) * LPH < 64, "a stage, the next one and a half in flight");
 
   const int tid = threadIdx.x;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
   const int wa = wave % WA, wb = wave / WA;
-  const int tiles = P.tilesA * P.tilesB;
-  const int part = (int)blockIdx.x / tiles;
-  int ta, tb;
-  tile_of((int)blockIdx.x % tiles, tiles, P.tilesA, P.tilesB, ta, tb);
-  const int a0 = ta * TA, b0 = tb * TB;
-  const int s_lo = (int)((int64_t)P.steps * part / P.splits), s_hi = (int)((int64_t)P.steps * (part + 1) / P.splits);
-  const int nsteps = s_hi - s_lo;
+  const int work = P.tilesA * P.tilesB * P.splits;
+  struct Item {                                      // one tile, one part of its contraction
+    int a0, b0, part, s_lo, nsteps;
+  };
+  auto item = [&](int w, auto& P) {
+    const int tiles = P.tilesA * P.tilesB;
+    Item t;
+    t.part = P.splits > 1 ? scalar(w / tiles) : 0;
+    int ta, tb;
+    tile_of(w - t.part * tiles, tiles, P.tilesA, P.tilesB, ta, tb);
+    t.a0 = ta * TA, t.b0 = tb * TB;
+    const int each = P.splits > 1 ? scalar(P.steps / P.splits) : P.steps;
+    const int more = P.steps - each * P.splits;      // the first `more` parts have one stage more
+    t.s_lo = t.part * each + (t.part < more ? t.part : more);
+    t.nsteps = each + (t.part < more ? 1 : 0);
+    return t;
+  };
 
-  // Byte offsets of this lane's loads.  Outputs past the operand are clamped here,
-  // contraction rows past it (in the last stage) by load_one().
+  // ---- the loading side: the stage to load next
+  // Byte offsets of this lane's loads.  Outputs past the operand are clamped here;
+  // contraction rows, which only a tile's last stage can pass, when they are loaded.
   const uint32_t ldA = (uint32_t)P.lda * 2, ldB = (uint32_t)P.ldb * 2;
   uint32_t offA[2][LA], offB[2][LB];                 // TR: of the chunk alone
-  int rowA[LA], rowB[LB];
-  auto offset = [&](auto half, int l, int h, int out0, int n, uint32_t ld, int& row) {
+  int lw = blockIdx.x, lleft, k0;                    // item, stages of it left, first contraction entry
+  const uint8_t *gA, *gB;
+  auto offset = [&](auto half, int l, int h, int out0, int n, uint32_t ld) {
     using H = decltype(half);
-    row = H::row_of(l, lane);
-    const int chunk = H::chunk_of(row, lane);
+    const int row = H::row_of(l, lane), chunk = H::chunk_of(row, lane);
     if constexpr (!H::TRANSPOSED) {
       const int r = h * H::OUTPUTS + row;
       return (uint32_t)(out0 + r < n ? r : n - 1 - out0) * ld + chunk * 16;
@@ -224,46 +264,57 @@ __global__ __launch_bounds__(64 * WA * WB, 1) void ce_gemm_kernel(GemmArgs P) {
       return (uint32_t)(out0 + o < n ? o : n - 8 - out0) * 2;
     }
   };
+  auto start_item = [&](const Item& t, auto& P) {
+    lleft = t.nsteps;
+    k0 = t.s_lo * BK;
+    gA = (const uint8_t*)P.A + (TRA ? k0 * P.lda + t.a0 : t.a0 * P.lda + k0) * 2;
+    gB = (const uint8_t*)P.B + (TRB ? k0 * P.ldb + t.b0 : t.b0 * P.ldb + k0) * 2;
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
+    for (int h = 0; h < 2; ++h) {
 #pragma unroll
-    for (int q = 0; q < LA; ++q) offA[h][q] = offset(HA{}, wave * LA + q, h, a0, P.mA, ldA, rowA[q]);
+      for (int q = 0; q < LA; ++q) offA[h][q] = offset(HA{}, wave * LA + q, h, t.a0, P.mA, ldA);
 #pragma unroll
-    for (int q = 0; q < LB; ++q) offB[h][q] = offset(HB{}, wave * LB + q, h, b0, P.mB, ldB, rowB[q]);
-  }
-  const uint8_t* gA = (const uint8_t*)P.A + (TRA ? (int64_t)a0 * 2 : a0 * P.lda * 2);
-  const uint8_t* gB = (const uint8_t*)P.B + (TRB ? (int64_t)b0 * 2 : b0 * P.ldb * 2);
-
-  auto load_one = [&](int q, int h, int place, int step) {   // load q of LPH of a half stage
+      for (int q = 0; q < LB; ++q) offB[h][q] = offset(HB{}, wave * LB + q, h, t.b0, P.mB, ldB);
+    }
+  };
+  auto next_stage = [&]() {                          // past the last item: its last stage again
+    if (lleft > 1) {
+      --lleft;
+      k0 += BK;
+      gA += TRA ? P.lda * (2 * BK) : 2 * BK;
+      gB += TRB ? P.ldb * (2 * BK) : 2 * BK;
+    } else if (lw + (int)gridDim.x < work) {
+      lw += (int)gridDim.x;
+      ArgsInMemory& Q = reread_args();               // (and keeps this a branch, taken once a tile)
+      start_item(item(lw, Q), Q);
+    }
+  };
+  auto load_one = [&](int q, int h, int place) {     // load q of LPH of a half stage
     uint8_t* base = smem + place * HALF;
-    const int64_t k0 = (int64_t)(s_lo + step) * BK;
     auto load = [&](const uint8_t* from, uint32_t off, uint8_t* to) {
       if constexpr (TRA || TRB) load_to_lds(from, off, to);
       else g2lds16(from + off, to);
     };
     if (q < LA) {
       uint32_t off = offA[h][q];
-      if (TRA) off += (uint32_t)min(rowA[q], (int)(P.kA - 1 - k0)) * ldA;
-      load(gA + k0 * (TRA ? P.lda * 2 : 2), off, base + (wave * LA + q) * 1024);
+      if (TRA) off += (uint32_t)min(HA::row_of(wave * LA + q, lane), P.kA - 1 - k0) * ldA;
+      load(gA, off, base + (wave * LA + q) * 1024);
     } else {
       uint32_t off = offB[h][q - LA];
-      if (TRB) off += (uint32_t)min(rowB[q - LA], (int)(P.kB - 1 - k0)) * ldB;
-      load(gB + k0 * (TRB ? P.ldb * 2 : 2), off, base + HA::BYTES + (wave * LB + q - LA) * 1024);
+      if (TRB) off += (uint32_t)min(HB::row_of(wave * LB + q - LA, lane), P.kB - 1 - k0) * ldB;
+      load(gB, off, base + HA::BYTES + (wave * LB + q - LA) * 1024);
     }
   };
 
+  // ---- the product side
   v4f acc[MI][MJ];
 #pragma unroll
   for (int i = 0; i < MI; ++i)
 #pragma unroll
-    for (int j = 0; j < MJ; ++j) {
-      acc[i][j] = (v4f){0.f, 0.f, 0.f, 0.f};
-      asm volatile("" : "+a"(acc[i][j]));
-    }
-  settle();
+    for (int j = 0; j < MJ; ++j) clear(acc[i][j]);
 
-  // fragment of 16 rows x 32 contraction entries: lane l holds row l % 16, entries 8 (l / 16) .. + 8
-  const int g16 = lane >> 4, l15 = lane & 15;
+  // fragment of 16 outputs x 32 contraction entries: lane l holds output l % 16, entries 8 (l / 16) .. + 8
+  const int g16 = lane >> 4, l15 = lane & 15, l4 = 4 * g16;
   const int frow = l15 * (BK * 2);
   const int fpos0 = (g16 ^ (lane & 7)) * 16, fpos1 = ((4 + g16) ^ (lane & 7)) * 16;
   // Fragment f of a half stage, 32 contraction entries `sub`.  The transposing read
@@ -285,12 +336,15 @@ __global__ __launch_bounds__(64 * WA * WB, 1) void ce_gemm_kernel(GemmArgs P) {
       return __builtin_bit_cast(v8bf, *(const v4i*)(p + f * (16 * BK * 2) + frow + (sub ? fpos1 : fpos0)));
     }
   };
-  v8bf fa[2][MI], fb[2][MJ];
+  // B's fragments of both halves of a stage, and A's of one: A's fragment i is read
+  // again, for the next half, once the products with it are under way; only its
+  // last one, which is needed latest, has two places
+  v8bf fa[MI - 1], fl[2], fb[2][MJ];
   // fragment i of A (j of B) of the stage whose halves lie at places p0 and p1
   auto read_a = [&](int p0, int p1, int sub, int i) {
     const int f = WA > 1 ? wa % (WA / 2) * MI + i : i % (MI / 2);
     const bool lower = WA > 1 ? wa >= WA / 2 : i >= MI / 2;
-    fa[sub][i] = fragment(HA{}, smem + (lower ? p1 : p0) * HALF, f, sub);
+    (i < MI - 1 ? fa[i] : fl[sub]) = fragment(HA{}, smem + (lower ? p1 : p0) * HALF, f, sub);
   };
   auto read_b = [&](int p0, int p1, int sub, int j) {
     const int f = WB > 1 ? wb % (WB / 2) * MJ + j : j % (MJ / 2);
@@ -298,166 +352,164 @@ __global__ __launch_bounds__(64 * WA * WB, 1) void ce_gemm_kernel(GemmArgs P) {
     fb[sub][j] = fragment(HB{}, smem + (lower ? p1 : p0) * HALF + HA::BYTES, f, sub);
   };
   // taken in snake order: each product shares an operand with the one before (0.3% of a training step)
-  auto multiply = [&](int i, int j, int sub) { mfma_acc(acc[i][j], fa[sub][i], fb[sub][j]); };
+  auto multiply = [&](int i, int j, int sub) { mfma_acc(acc[i][j], i < MI - 1 ? fa[i] : fl[sub], fb[sub][j]); };
   auto wrap = [](int p) { return p >= RING ? p - RING : p; };
-  auto clamp = [&](int s) { return s < nsteps ? s : nsteps - 1; };
 
-  // Half stage u (stage u / 2) lies at place u % RING.  Stage s: while the matrix
-  // instructions of its first 32 entries run, the fragments of the second 32 are
-  // read, and half stage 2 s + RING - 1 is loaded into the place of 2 s - 1; then
-  // all waves meet (stage s has been read, stage s + 1 has landed), and while
-  // the second 32 run, the next stage's first fragments are read, and half stage
-  // 2 s + RING is loaded into the place of 2 s.  The loop has no branches: past
-  // the last stage it loads that stage again and reads LDS that no product uses.
+  // Stages are numbered through all items of the block; half stage u (of stage
+  // u / 2) lies at place u % RING.  Stage n: while the matrix instructions of its
+  // first 32 entries run, the fragments of the second 32 are read, and the upper
+  // half of stage n + AHEAD is loaded into the place of half stage 2 n - 1; then all
+  // waves meet (stage n has been read, stage n + 1 has landed), and while the
+  // second 32 run, the next stage's first fragments are read, and the lower half of
+  // stage n + AHEAD is loaded into the place of half stage 2 n.
+  // EPI_GRAD: of few tokens every wave finds the largest |dloss| itself, which a
+  // launch of its own would take longer for
+  float gmax = 1.0f;
+  if (EPI == EPI_GRAD && P.nB <= GMAX_WAVE) {
+    gmax = uniform(max_dloss(P.dloss, P.labels, P.labels64, P.V, P.nB, lane, 64));
+    if (blockIdx.x == 0 && tid == 0) *P.gmax = gmax;
+  } else if (EPI != EPI_STATS && P.gmax) {
+    gmax = uniform(*P.gmax);
+  }
+  const float ginv = gmax >= 0x1p-126f ? 1.0f / gmax : 0.0f;   // smaller ones have no quotient: gradients 0
+  Item it = item(blockIdx.x, P);
+  start_item(it, P);
 #pragma unroll
-  for (int u = 0; u < RING - 1; ++u)
+  for (int n = 0; n < AHEAD; ++n) {
 #pragma unroll
-    for (int q = 0; q < LPH; ++q) load_one(q, u & 1, u, clamp(u / 2));
-  stage_barrier<(RING - 3) * LPH>();                 // half stages 0 and 1 have landed
+    for (int q = 0; q < 2 * LPH; ++q) load_one(q % LPH, q / LPH, 2 * n + q / LPH);
+    next_stage();
+  }
+  settle();
+  stage_barrier<(RING - 3) * LPH>();                 // stage 0 has landed
 #pragma unroll
   for (int j = 0; j < MJ; ++j) read_b(0, 1, 0, j);
 #pragma unroll
   for (int i = 0; i < MI; ++i) read_a(0, 1, 0, i);
 
-  constexpr int H0 = (RING - 1) & 1, H1 = RING & 1;  // which halves the two phases load
-  int p0 = 0;                                        // place of half stage 2 s
-  for (int s = 0; s < nsteps; ++s) {
-    const int p1 = wrap(p0 + 1), n0 = wrap(p0 + 2), n1 = wrap(p0 + 3), free0 = wrap(p0 + RING - 1);
-    const int s0 = clamp(s + (RING - 1) / 2), s1 = clamp(s + RING / 2);
-    lds_reads_done();                                // before new reads, which the first products need not wait for
-#pragma unroll
-    for (int i = 0; i < MI; ++i) {
-#pragma unroll
-      for (int j = 0; j < MJ; ++j)
-        if (j * MI / MJ == i) read_b(p0, p1, 1, j);
-      read_a(p0, p1, 1, i);
-#pragma unroll
-      for (int q = 0; q < LPH; ++q)
-        if (q * MI / LPH == i) load_one(q, H0, free0, s0);
-#pragma unroll
-      for (int j = 0; j < MJ; ++j) multiply(i, i & 1 ? MJ - 1 - j : j, 0);
-      __builtin_amdgcn_sched_barrier(0);
-    }
-    stage_barrier<(RING - 4) * LPH>();
-#pragma unroll
-    for (int i = 0; i < MI; ++i) {
-#pragma unroll
-      for (int j = 0; j < MJ; ++j)
-        if (j * MI / MJ == i) read_b(n0, n1, 0, j);
-      read_a(n0, n1, 0, i);
-#pragma unroll
-      for (int q = 0; q < LPH; ++q)
-        if (q * MI / LPH == i) load_one(q, H1, p0, s1);
-#pragma unroll
-      for (int j = 0; j < MJ; ++j) multiply(i, i & 1 ? MJ - 1 - j : j, 1);
-      __builtin_amdgcn_sched_barrier(0);
-    }
-    p0 = n0;
-  }
-  settle();
-  wait_vmcnt<0>();
-
-  // acc[i][j]: A rows aw + 16 i + 4 (lane / 16) + 0..3, B row bw + 16 j + lane % 16
-  const int aw = a0 + wa * MI * 16, bw = b0 + wb * MJ * 16;
-  const int l4 = 4 * g16;
-
-  if (EPI == EPI_STATS) {
-    const bool ragged = aw + MI * 16 > P.nA;
-#pragma unroll
-    for (int j = 0; j < MJ; ++j) {
-      const int t = bw + 16 * j + l15;
-      const int64_t y = t < P.nB ? label_at(P.labels, P.labels64, t) : -1;
-      const int want = y >= 0 && y < P.V ? (int)y - aw - l4 : -1;
-      float m = -INFINITY, hit = 0.0f;
-      v4f c[MI];
+  int p0 = 0;                                        // place of the stage's upper half
+  for (int w = blockIdx.x;; w += (int)gridDim.x) {
+    for (int left = it.nsteps; left > 0; --left) {
+      const int p1 = wrap(p0 + 1), n0 = wrap(p0 + 2), n1 = wrap(p0 + 3), free0 = wrap(p0 + RING - 1);
+      lds_reads_done();                              // before new reads, which the first products need not wait for
 #pragma unroll
       for (int i = 0; i < MI; ++i) {
-        c[i] = fetch(acc[i][j]);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          if (ragged && aw + 16 * i + l4 + e >= P.nA) c[i][e] = -INFINITY;
-          m = fmaxf(m, c[i][e]);
-          if (want == 16 * i + e) hit = c[i][e];
+        for (int j = 0; j < MJ; ++j)
+          if (j * MI / MJ == i) read_b(p0, p1, 1, j);
+        read_a(p0, p1, 1, i > 0 ? i - 1 : MI - 1);
+#pragma unroll
+        for (int q = 0; q < LPH; ++q)
+          if (q * MI / LPH == i) load_one(q, 0, free0);
+#pragma unroll
+        for (int j = 0; j < MJ; ++j) multiply(i, i & 1 ? MJ - 1 - j : j, 0);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      stage_barrier<(RING - 4) * LPH>();
+#pragma unroll
+      for (int i = 0; i < MI; ++i) {
+#pragma unroll
+        for (int j = 0; j < MJ; ++j)
+          if (j * MI / MJ == i) read_b(n0, n1, 0, j);
+        read_a(n0, n1, 0, i > 0 ? i - 1 : MI - 1);
+#pragma unroll
+        for (int q = 0; q < LPH; ++q)
+          if (q * MI / LPH == i) load_one(q, 1, p0);
+#pragma unroll
+        for (int j = 0; j < MJ; ++j) multiply(i, i & 1 ? MJ - 1 - j : j, 1);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      next_stage();
+      p0 = n0;
+    }
+    settle();
+
+    ArgsInMemory& P = reread_args();
+    // acc[i][j]: A outputs aw + 16 i + 4 (lane / 16) + 0..3, B output bw + 16 j + lane % 16
+    const int aw = it.a0 + wa * MI * 16, bw = it.b0 + wb * MJ * 16;
+    if (EPI == EPI_STATS) {
+      const bool ragged = aw + MI * 16 > P.nA;
+      const int group = it.a0 / (MI * 16) + wa;
+#pragma unroll
+      for (int j = 0; j < MJ; ++j) {
+        const int t = bw + 16 * j + l15;
+        const int64_t y = t < P.nB ? label_at(P.labels, P.labels64, t) : -1;
+        const int want = y >= 0 && y < P.V ? (int)y - aw - l4 : -1;
+        float m = -INFINITY, hit = 0.0f;
+        v4f c[MI];
+#pragma unroll
+        for (int i = 0; i < MI; ++i) {
+          c[i] = fetch(acc[i][j]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            if (ragged && aw + 16 * i + l4 + e >= P.nA) c[i][e] = -INFINITY;
+            m = fmaxf(m, c[i][e]);
+            if (want == 16 * i + e) hit = c[i][e];
+          }
+        }
+        if (want >= 0 && want < MI * 16 && (want & 12) == 0) P.target[t] = hit;
+        m = fmaxf(m, __shfl_xor(m, 16));
+        m = fmaxf(m, __shfl_xor(m, 32));
+        const float top = fmaxf(m * LOG2E, NONE);    // a group past the vocabulary has no logits
+        float sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < MI; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sum += __builtin_amdgcn_exp2f(c[i][e] * LOG2E - top);
+        sum += __shfl_xor(sum, 16);
+        sum += __shfl_xor(sum, 32);
+        if (lane < 16 && t < P.nB) P.stats[(int64_t)group * P.nB + t] = make_float2(top, sum);
+      }
+    } else if (EPI == EPI_GRAD) {
+#pragma unroll
+      for (int j = 0; j < MJ; ++j) {
+        const int t = bw + 16 * j + l15;
+        const bool live = t < P.nB;
+        const int64_t y = live ? label_at(P.labels, P.labels64, t) : -1;
+        const bool kept = y >= 0 && y < P.V;
+        const float g = kept ? P.dloss[t] * ginv : 0.0f, ls = live ? P.lse[t] * LOG2E : 0.0f;
+        const int want = kept ? (int)y - P.v0 - aw - l4 : -1;
+        uint16_t* row = P.D + (int64_t)t * P.ldd + aw + l4;
+#pragma unroll
+        for (int i = 0; i < MI; ++i) {
+          const v4f c = fetch(acc[i][j]);
+          float d[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float p = __builtin_amdgcn_exp2f(c[e] * LOG2E - ls);
+            if (want == 16 * i + e) p -= 1.0f;
+            d[e] = kept && aw + 16 * i + l4 + e < P.nA ? g * p : 0.0f;
+          }
+          if (t < P.tpad && aw + 16 * i + l4 < P.vpad)
+            *(uint2*)(row + 16 * i) = make_uint2(pack_bf16x2(d[0], d[1]), pack_bf16x2(d[2], d[3]));
         }
       }
-      if (want >= 0 && want < MI * 16 && (want & 12) == 0) P.target[t] = hit;
-      m = fmaxf(m, __shfl_xor(m, 16));
-      m = fmaxf(m, __shfl_xor(m, 32));
-      const float top = fmaxf(m * LOG2E, NONE);        // a group past the vocabulary has no logits
-      float sum = 0.0f;
-#pragma unroll
-      for (int i = 0; i < MI; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) sum += __builtin_amdgcn_exp2f(c[i][e] * LOG2E - top);
-      sum += __shfl_xor(sum, 16);
-      sum += __shfl_xor(sum, 32);
-      if (lane < 16 && t < P.nB) P.stats[(int64_t)(ta * WA + wa) * P.nB + t] = make_float2(top, sum);
-    }
-  } else if (EPI == EPI_GRAD) {
-    // D through LDS, [t][v] with rows of 2 TA + 32 bytes: lanes that write 4 entries
-    // each of 16 rows spread over the banks, and rows leave in whole lines.
-    constexpr int PITCH = 2 * TA + 32;
-    auto at = [&](int t, int v) { return smem + t * PITCH + v * 2; };
-    // of few tokens every wave finds the largest |dloss| itself, which a launch of
-    // its own would take longer for
-    float gm;
-    if (P.nB <= GMAX_WAVE) {
-      gm = max_dloss(P.dloss, P.labels, P.labels64, P.V, P.nB, lane, 64);
-      if (blockIdx.x == 0 && tid == 0) *P.gmax = gm;
     } else {
-      gm = *P.gmax;
-    }
-    const float ginv = gm >= 0x1p-126f ? 1.0f / gm : 0.0f;   // smaller ones have no quotient: gradients 0
-    lds_barrier();                                   // every wave has read its last fragments
+      const int64_t at = it.part * P.part_stride + (int64_t)bw * P.ldc;
 #pragma unroll
-    for (int j = 0; j < MJ; ++j) {
-      const int tl = wb * MJ * 16 + 16 * j + l15, t = b0 + tl;
-      const bool live = t < P.nB;
-      const int64_t y = live ? label_at(P.labels, P.labels64, t) : -1;
-      const bool kept = y >= 0 && y < P.V;
-      const float g = kept ? P.dloss[t] * ginv : 0.0f, ls = live ? P.lse[t] * LOG2E : 0.0f;
-      const int want = kept ? (int)y - P.v0 - aw - l4 : -1;
+      for (int j = 0; j < MJ; ++j) {
+        const int b = bw + 16 * j + l15;
+        const int64_t row = at + (int64_t)(16 * j + l15) * P.ldc;
 #pragma unroll
-      for (int i = 0; i < MI; ++i) {
-        const v4f c = fetch(acc[i][j]);
-        float d[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float p = __builtin_amdgcn_exp2f(c[e] * LOG2E - ls);
-          if (want == 16 * i + e) p -= 1.0f;
-          d[e] = kept && aw + 16 * i + l4 + e < P.nA ? g * p : 0.0f;
+        for (int i = 0; i < MI; ++i) {
+          const int a = aw + 16 * i + l4;            // nA is a multiple of 64
+          v4f c = fetch(acc[i][j]);
+          if (a >= P.nA || b >= P.nB) continue;
+          if (P.Cin) c += *(const v4f*)(P.Cin + (int64_t)b * P.nA + a);
+          c *= gmax;
+          if (P.c_f32) *(v4f*)((float*)P.C + row + a) = c;
+          else *(uint2*)((uint16_t*)P.C + row + a) = make_uint2(pack_bf16x2(c[0], c[1]), pack_bf16x2(c[2], c[3]));
         }
-        *(uint2*)at(tl, wa * MI * 16 + 16 * i + l4) = make_uint2(pack_bf16x2(d[0], d[1]), pack_bf16x2(d[2], d[3]));
       }
     }
-    __syncthreads();
-    for (int q = tid; q < TB * (TA / 8); q += NT) {
-      const int tl = q / (TA / 8), c = q % (TA / 8);
-      if (b0 + tl < P.tpad && a0 + 8 * c < P.vpad)
-        *(uint4*)(P.D + (int64_t)(b0 + tl) * P.ldd + a0 + 8 * c) = *(const uint4*)at(tl, 8 * c);
-    }
-  } else {
-    const float scale = P.gmax ? *P.gmax : 1.0f;
+    if (w + (int)gridDim.x >= work) break;
 #pragma unroll
-    for (int j = 0; j < MJ; ++j) {
-      const int b = bw + 16 * j + l15;
-      if (b >= P.nB) continue;
+    for (int i = 0; i < MI; ++i)
 #pragma unroll
-      for (int i = 0; i < MI; ++i) {
-        const int a = aw + 16 * i + l4;              // nA is a multiple of 64
-        v4f c = fetch(acc[i][j]);
-        if (a >= P.nA) continue;
-        if (P.part) {
-          *(v4f*)(P.part + ((int64_t)part * P.nB + b) * P.nA + a) = c;
-          continue;
-        }
-        if (P.Cin) c += *(const v4f*)(P.Cin + (int64_t)b * P.nA + a);
-        c *= scale;
-        if (P.c_f32) *(v4f*)((float*)P.C + (int64_t)b * P.ldc + a) = c;
-        else *(uint2*)((uint16_t*)P.C + (int64_t)b * P.ldc + a) = make_uint2(pack_bf16x2(c[0], c[1]), pack_bf16x2(c[2], c[3]));
-      }
-    }
+      for (int j = 0; j < MJ; ++j) clear(acc[i][j]);
+    it = item(w + (int)gridDim.x, P);
   }
+  wait_vmcnt<0>();                                   // no load into LDS outlives the block
 }
 
 // lse and loss of a token from its groups' (maximum, sum): 16 tokens a block, 64
@@ -560,13 +612,13 @@ constexpr TileShape SHAPE[] = {{256, 256}, {128, 128}, {128, 64}};
 template <int WA, int WB, int MI, int MJ, int RING, int EPI, bool TRA, bool TRB>
 hipError_t run_gemm(const char* name, const GemmArgs& P, hipStream_t st) {
   constexpr int TA = WA * MI * 16, TB = WB * MJ * 16;
-  constexpr size_t stages = (size_t)RING * (TA + TB) / 2 * BK * 2;
-  constexpr size_t dtile = EPI == EPI_GRAD ? (size_t)TB * (2 * TA + 32) : 0;
-  constexpr size_t lds = stages > dtile ? stages : dtile;
+  constexpr size_t lds = (size_t)RING * (TA + TB) / 2 * BK * 2;
+  constexpr int per_cu = (int)((160 << 10) / lds);
   static const hipError_t e = hipFuncSetAttribute((const void*)ce_gemm_kernel<WA, WB, MI, MJ, RING, EPI, TRA, TRB>,
                                                   hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
   if (e != hipSuccess) return e;
-  SBN_LAUNCH(name, (ce_gemm_kernel<WA, WB, MI, MJ, RING, EPI, TRA, TRB>), dim3((unsigned)(P.tilesA * P.tilesB * P.splits)),
+  const int64_t work = (int64_t)P.tilesA * P.tilesB * P.splits;
+  SBN_LAUNCH(name, (ce_gemm_kernel<WA, WB, MI, MJ, RING, EPI, TRA, TRB>), dim3((unsigned)(work < per_cu * CUS ? work : per_cu * CUS)),
              dim3(64 * WA * WB), lds, st, P);
   return hipGetLastError();
 }
@@ -654,9 +706,12 @@ CePlan ce_plan(int64_t T, int64_t V, int64_t K) {
 // C [nB][ldc] = A B^T, split as P says and summed
 template <bool TRB>
 hipError_t product(const char* name, Tile tile, GemmArgs P, float* part, hipStream_t st) {
-  P.part = P.splits > 1 ? part : nullptr;
-  const hipError_t e = gemm<EPI_OUT, true, TRB>(name, tile, P, st);
-  if (e != hipSuccess || P.splits == 1) return e;
+  if (P.splits == 1) return gemm<EPI_OUT, true, TRB>(name, tile, P, st);
+  GemmArgs Q = P;                                    // the parts' sums side by side
+  Q.C = part, Q.c_f32 = true, Q.ldc = P.nA, Q.part_stride = (int64_t)P.nB * P.nA;
+  Q.Cin = nullptr, Q.gmax = nullptr;
+  const hipError_t e = gemm<EPI_OUT, true, TRB>(name, tile, Q, st);
+  if (e != hipSuccess) return e;
   SBN_LAUNCH("ce_sum", ce_sum_kernel, dim3((unsigned)grid_for((int64_t)P.nB * (P.nA / 4))), dim3(256), 0, st, part,
              P.splits, (int64_t)P.nB, P.nA, P.Cin, P.gmax, P.C, P.c_f32, P.ldc);
   return hipGetLastError();
