@@ -18,7 +18,11 @@
 // Products and sums are rounded one by one (no fused multiply-add): the result
 // is that of the same formula in elementary float32 operations.
 // Bound by memory traffic: 28 bytes an element with 32-bit parameters,
-// gradients and states, 12 with bf16 parameters and 8-bit states.
+// gradients and states, 12 with bf16 parameters, float32 gradients and 8-bit
+// states.  75.8 M elements, float32 with bf16 gradients and a bf16 copy (28
+// bytes): 392 us, 5.4 TB/s; 135 M with 8-bit states (12 bytes): 318 to 360 us,
+// up to 5.2 TB/s (1.11 GB fetched, 0.55 GB written); a state read back: 117 us,
+// 5.8 TB/s.  A large copy reaches 4.9.
 #include "train_internal.h"
 
 #pragma clang fp contract(off)
