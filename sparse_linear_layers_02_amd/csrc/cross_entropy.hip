@@ -35,7 +35,7 @@ constexpr int64_t D_ELEMS = int64_t(1) << 27;       // elements of D in the work
 constexpr int GMAX_WAVE = 1024;                     // tokens whose largest |dloss| a wave finds in two rounds of loads
 constexpr int CUS = 256;
 
-enum Epi { EPI_STATS, EPI_GRAD, EPI_OUT };
+enum Epi { EPI_STATS, EPI_GRAD, EPI_OUT16, EPI_OUT32 };   // OUT: C in bf16, in float32
 
 struct GemmArgs {
   const uint16_t *A, *B;               // rows of lda, ldb
@@ -54,15 +54,14 @@ struct GemmArgs {
   float* target;                       // [nB] logit of the label
   const float *lse, *dloss;
   float* gmax;                         // max |dloss|; EPI_GRAD divides by it, EPI_OUT multiplies
-  uint16_t* D;                         // [tpad][ldd]; 0 past the tokens, and in columns nA .. vpad - 1
+  uint16_t* D;                         // [tpad][ldd], ldd a multiple of 256; 0 past the tokens and past nA
   int64_t ldd;
-  int tpad, vpad;
+  int tpad;                            // a multiple of 64
   // EPI_OUT: C [nB][ldc], A outputs along the row
   void* C;
-  const float* Cin;                    // [nB][nA], added first, or NULL
+  const float* Cin;                    // [nB][nA], added first, or NULL (only where TRB is false)
   int64_t ldc;
   int64_t part_stride;                 // elements of C from one part of the contraction to the next
-  bool c_f32;
 };
 
 __device__ inline int64_t label_at(const void* labels, bool is64, int t) {
@@ -140,11 +139,6 @@ __device__ inline v4f fetch(v4f& acc) {
   asm volatile("" : "+a"(acc));
   return acc;
 }
-__device__ inline void clear(v4f& acc) {
-  acc = (v4f){0.f, 0.f, 0.f, 0.f};
-  asm volatile("" : "+a"(acc));
-}
-
 // All waves meet: each has its LDS reads and all but its latest N loads behind it.
 // By the builtin, so that the compiler knows the reads done and adds no wait.
 template <int N>
@@ -154,6 +148,17 @@ __device__ inline void stage_barrier() {
   __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4));
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
+}
+
+// Two fragments of results, 4 consecutive outputs a lane each, as 8 consecutive
+// outputs in bf16: lane group g (of 16) holds outputs 16 (g % 2) + 8 (g / 2) .. + 7
+// of the pair's 32.  The 16-byte pieces of four lanes then make 64 bytes of a row:
+// 256 MB written so by 256 blocks take 54 us, in 8-byte pieces of one fragment
+// (32 bytes of a row) 68, one lane group after the other 51.
+__device__ inline uint4 pack_pair(const float* c, const float* d) {
+  const auto lo = __builtin_amdgcn_permlane16_swap(pack_bf16x2(c[0], c[1]), pack_bf16x2(d[0], d[1]), false, false);
+  const auto hi = __builtin_amdgcn_permlane16_swap(pack_bf16x2(c[2], c[3]), pack_bf16x2(d[2], d[3]), false, false);
+  return make_uint4(lo[0], hi[0], lo[1], hi[1]);
 }
 
 // The kernel's arguments, read again where they are used: held over the loops,
@@ -311,14 +316,31 @@ __global__ __launch_bounds__(64 * WA * WB, 1) void ce_gemm_kernel(GemmArgs P) {
   };
 
   // ---- the product side
+  const int g16 = lane >> 4, l15 = lane & 15, l4 = 4 * g16, l8 = (g16 & 1) * 16 + (g16 >> 1) * 8;
   v4f acc[MI][MJ];
+
+  // acc[i][j]: A outputs a0 + 16 (wa MI + i) + 4 (lane / 16) + 0..3, B output b0 + 16 (wb MJ + j) + lane % 16;
+  // a tile's sums start from Cin, loaded at once (added at the end, each load waited for the stores before it)
+  auto start_sums = [&](const Item& t, auto& P) {
+    const float* from = EPI == EPI_STATS || EPI == EPI_GRAD || TRB ? nullptr : P.Cin;
 #pragma unroll
-  for (int i = 0; i < MI; ++i)
+    for (int i = 0; i < MI; ++i)
 #pragma unroll
-    for (int j = 0; j < MJ; ++j) clear(acc[i][j]);
+      for (int j = 0; j < MJ; ++j) {
+        if (from) {
+          const int a = t.a0 + 16 * (wa * MI + i) + l4, b = t.b0 + 16 * (wb * MJ + j) + l15;
+          acc[i][j] = *(const v4f*)(from + (int64_t)(b < P.nB ? b : P.nB - 1) * P.nA + (a < P.nA ? a : 0));
+        } else {
+          acc[i][j] = (v4f){0.f, 0.f, 0.f, 0.f};
+        }
+      }
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+#pragma unroll
+      for (int j = 0; j < MJ; ++j) asm volatile("" : "+a"(acc[i][j]));
+  };
 
   // fragment of 16 outputs x 32 contraction entries: lane l holds output l % 16, entries 8 (l / 16) .. + 8
-  const int g16 = lane >> 4, l15 = lane & 15, l4 = 4 * g16;
   const int frow = l15 * (BK * 2);
   const int fpos0 = (g16 ^ (lane & 7)) * 16, fpos1 = ((4 + g16) ^ (lane & 7)) * 16;
   // Fragment f of a half stage, 32 contraction entries `sub`.  The transposing read
@@ -384,6 +406,7 @@ __global__ __launch_bounds__(64 * WA * WB, 1) void ce_gemm_kernel(GemmArgs P) {
     for (int q = 0; q < 2 * LPH; ++q) load_one(q % LPH, q / LPH, 2 * n + q / LPH);
     next_stage();
   }
+  start_sums(it, P);
   settle();
   stage_barrier<(RING - 3) * LPH>();                 // stage 0 has landed
 #pragma unroll
@@ -429,7 +452,6 @@ __global__ __launch_bounds__(64 * WA * WB, 1) void ce_gemm_kernel(GemmArgs P) {
     settle();
 
     ArgsInMemory& P = reread_args();
-    // acc[i][j]: A outputs aw + 16 i + 4 (lane / 16) + 0..3, B output bw + 16 j + lane % 16
     const int aw = it.a0 + wa * MI * 16, bw = it.b0 + wb * MJ * 16;
     if (EPI == EPI_STATS) {
       const bool ragged = aw + MI * 16 > P.nA;
@@ -465,53 +487,75 @@ __global__ __launch_bounds__(64 * WA * WB, 1) void ce_gemm_kernel(GemmArgs P) {
         if (lane < 16 && t < P.nB) P.stats[(int64_t)group * P.nB + t] = make_float2(top, sum);
       }
     } else if (EPI == EPI_GRAD) {
+      int want[MJ];
+      float g[MJ], ls[MJ];
+      uint32_t kept[MJ];                             // all ones, or 0: what a token without a target holds gives 0
 #pragma unroll
-      for (int j = 0; j < MJ; ++j) {
+      for (int j = 0; j < MJ; ++j) {                 // all loads before the first store: they would wait for it
         const int t = bw + 16 * j + l15;
         const bool live = t < P.nB;
         const int64_t y = live ? label_at(P.labels, P.labels64, t) : -1;
-        const bool kept = y >= 0 && y < P.V;
-        const float g = kept ? P.dloss[t] * ginv : 0.0f, ls = live ? P.lse[t] * LOG2E : 0.0f;
-        const int want = kept ? (int)y - P.v0 - aw - l4 : -1;
-        uint16_t* row = P.D + (int64_t)t * P.ldd + aw + l4;
+        kept[j] = y >= 0 && y < P.V ? ~0u : 0u;
+        g[j] = kept[j] ? P.dloss[t] * ginv : 0.0f, ls[j] = live ? P.lse[t] * LOG2E : 0.0f;
+        want[j] = kept[j] ? (int)y - P.v0 - aw - l4 : -1;
+      }
+      asm volatile("" ::: "memory");
+      const bool ragged = aw + MI * 16 > P.nA;
+      if (bw < P.tpad) {                             // a multiple of the wave's 64 tokens
 #pragma unroll
-        for (int i = 0; i < MI; ++i) {
-          const v4f c = fetch(acc[i][j]);
-          float d[4];
+        for (int j = 0; j < MJ; ++j) {
+          uint16_t* row = P.D + (int64_t)(bw + 16 * j + l15) * P.ldd + aw + l8;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            float p = __builtin_amdgcn_exp2f(c[e] * LOG2E - ls);
-            if (want == 16 * i + e) p -= 1.0f;
-            d[e] = kept && aw + 16 * i + l4 + e < P.nA ? g * p : 0.0f;
+          for (int i = 0; i < MI; i += 2) {
+            float d[2][4];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const v4f c = fetch(acc[i + h][j]);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const float p = __builtin_amdgcn_exp2f(c[e] * LOG2E - ls[j]);
+                const float q = g[j] * (p - (want[j] == 16 * (i + h) + e ? 1.0f : 0.0f));
+                d[h][e] = __uint_as_float(__float_as_uint(q) & kept[j]);   // (a select became a branch for each element)
+              }
+            }
+            if (ragged)
+#pragma unroll
+              for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  if (aw + 16 * (i + h) + l4 + e >= P.nA) d[h][e] = 0.0f;
+            *(uint4*)(row + 16 * i) = pack_pair(d[0], d[1]);
           }
-          if (t < P.tpad && aw + 16 * i + l4 < P.vpad)
-            *(uint2*)(row + 16 * i) = make_uint2(pack_bf16x2(d[0], d[1]), pack_bf16x2(d[2], d[3]));
         }
       }
     } else {
       const int64_t at = it.part * P.part_stride + (int64_t)bw * P.ldc;
 #pragma unroll
       for (int j = 0; j < MJ; ++j) {
-        const int b = bw + 16 * j + l15;
-        const int64_t row = at + (int64_t)(16 * j + l15) * P.ldc;
+        if (bw + 16 * j + l15 >= P.nB) continue;     // for all four groups of a column alike
+        const int64_t row = at + (int64_t)(16 * j + l15) * P.ldc + aw;
 #pragma unroll
-        for (int i = 0; i < MI; ++i) {
-          const int a = aw + 16 * i + l4;            // nA is a multiple of 64
-          v4f c = fetch(acc[i][j]);
-          if (a >= P.nA || b >= P.nB) continue;
-          if (P.Cin) c += *(const v4f*)(P.Cin + (int64_t)b * P.nA + a);
-          c *= gmax;
-          if (P.c_f32) *(v4f*)((float*)P.C + row + a) = c;
-          else *(uint2*)((uint16_t*)P.C + row + a) = make_uint2(pack_bf16x2(c[0], c[1]), pack_bf16x2(c[2], c[3]));
+        for (int i = 0; i < MI; i += 2) {
+          if (aw + 16 * i >= P.nA) break;            // nA is a multiple of 64
+          float c[2][4];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const v4f x = fetch(acc[i + h][j]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) c[h][e] = x[e] * gmax;
+          }
+          if (EPI == EPI_OUT32) {
+            float* to = (float*)P.C + row + 16 * i + l4;
+            *(v4f*)to = *(const v4f*)c[0], *(v4f*)(to + 16) = *(const v4f*)c[1];
+          } else {
+            *(uint4*)((uint16_t*)P.C + row + 16 * i + l8) = pack_pair(c[0], c[1]);
+          }
         }
       }
     }
     if (w + (int)gridDim.x >= work) break;
-#pragma unroll
-    for (int i = 0; i < MI; ++i)
-#pragma unroll
-      for (int j = 0; j < MJ; ++j) clear(acc[i][j]);
     it = item(w + (int)gridDim.x, P);
+    start_sums(it, P);
   }
   wait_vmcnt<0>();                                   // no load into LDS outlives the block
 }
@@ -709,15 +753,16 @@ CePlan ce_plan(int64_t T, int64_t V, int64_t K) {
 
 // C [nB][ldc] = A B^T, split as P says and summed
 template <bool TRB>
-hipError_t product(const char* name, Tile tile, GemmArgs P, float* part, hipStream_t st) {
-  if (P.splits == 1) return gemm<EPI_OUT, true, TRB>(name, tile, P, st);
+hipError_t product(const char* name, Tile tile, GemmArgs P, bool c_f32, float* part, hipStream_t st) {
+  if (P.splits == 1)
+    return c_f32 ? gemm<EPI_OUT32, true, TRB>(name, tile, P, st) : gemm<EPI_OUT16, true, TRB>(name, tile, P, st);
   GemmArgs Q = P;                                    // the parts' sums side by side
-  Q.C = part, Q.c_f32 = true, Q.ldc = P.nA, Q.part_stride = (int64_t)P.nB * P.nA;
+  Q.C = part, Q.ldc = P.nA, Q.part_stride = (int64_t)P.nB * P.nA;
   Q.Cin = nullptr, Q.gmax = nullptr;
-  const hipError_t e = gemm<EPI_OUT, true, TRB>(name, tile, Q, st);
+  const hipError_t e = gemm<EPI_OUT32, true, TRB>(name, tile, Q, st);
   if (e != hipSuccess) return e;
   SBN_LAUNCH("ce_sum", ce_sum_kernel, dim3((unsigned)grid_for((int64_t)P.nB * (P.nA / 4))), dim3(256), 0, st, part,
-             P.splits, (int64_t)P.nB, P.nA, P.Cin, P.gmax, P.C, P.c_f32, P.ldc);
+             P.splits, (int64_t)P.nB, P.nA, P.Cin, P.gmax, P.C, c_f32, P.ldc);
   return hipGetLastError();
 }
 
@@ -774,7 +819,7 @@ hipError_t launch_ce_backward(const uint16_t* X, int64_t ldx, const uint16_t* W,
     G.steps = (int)(K / BK), G.splits = 1;
     G.labels = labels, G.labels64 = labels64, G.v0 = (int)v0, G.V = (int)V;
     G.lse = lse, G.dloss = dloss, G.gmax = gmax;
-    G.D = D, G.ldd = L.piece, G.tpad = (int)L.tpad, G.vpad = (int)vpad;
+    G.D = D, G.ldd = L.piece, G.tpad = (int)L.tpad;
     if ((e = gemm<EPI_GRAD>("ce_dlogits", pick(nv, T, G.steps, false).tile, G, st)) != hipSuccess) return e;
     if (dX) {
       GemmArgs P{};
@@ -784,17 +829,17 @@ hipError_t launch_ce_backward(const uint16_t* X, int64_t ldx, const uint16_t* W,
       const bool last = i + 1 == L.pieces;
       P.Cin = i > 0 ? acc : nullptr;
       P.gmax = last ? gmax : nullptr;
-      P.C = last ? dX : acc, P.c_f32 = last ? dx_f32 : true, P.ldc = last ? lddx : K;
-      if ((e = product<false>("ce_dx", L.x.tile, P, part, st)) != hipSuccess) return e;
+      P.C = last ? dX : acc, P.ldc = last ? lddx : K;
+      if ((e = product<false>("ce_dx", L.x.tile, P, last ? dx_f32 : true, part, st)) != hipSuccess) return e;
     }
     if (dW) {
       GemmArgs P{};
       P.A = X, P.lda = ldx, P.nA = P.mA = (int)K, P.kA = (int)T;
       P.B = D, P.ldb = L.piece, P.nB = (int)nv, P.mB = (int)vpad, P.kB = (int)L.tpad;
       P.steps = (int)(L.tpad / BK), P.splits = L.w.splits;
-      P.C = (uint8_t*)dW + v0 * lddw * (dw_f32 ? 4 : 2), P.c_f32 = dw_f32, P.ldc = lddw;
+      P.C = (uint8_t*)dW + v0 * lddw * (dw_f32 ? 4 : 2), P.ldc = lddw;
       P.gmax = gmax;
-      if ((e = product<true>("ce_dw", L.w.tile, P, part, st)) != hipSuccess) return e;
+      if ((e = product<true>("ce_dw", L.w.tile, P, dw_f32, part, st)) != hipSuccess) return e;
     }
   }
   return hipSuccess;
