@@ -150,6 +150,12 @@ __device__ inline void stage_barrier() {
   asm volatile("" ::: "memory");
 }
 
+// x, in a branch that few waves take: what is computed from it stays in the branch
+__device__ inline int rarely(int x) {
+  asm volatile("" : "+v"(x));
+  return x;
+}
+
 // Two fragments of results, 4 consecutive outputs a lane each, as 8 consecutive
 // outputs in bf16: lane group g (of 16) holds outputs 16 (g % 2) + 8 (g / 2) .. + 7
 // of the pair's 32.  The 16-byte pieces of four lanes then make 64 bytes of a row:
@@ -453,27 +459,49 @@ __global__ __launch_bounds__(64 * WA * WB, 1) void ce_gemm_kernel(GemmArgs P) {
 
     ArgsInMemory& P = reread_args();
     const int aw = it.a0 + wa * MI * 16, bw = it.b0 + wb * MJ * 16;
+    // a label's place from the lane's first entry: is it one of the lane's?  (Few waves hold one of their tokens' labels.)
+    auto holds = [](int want) { return want >= 0 && want < MI * 16 && (want & 12) == 0; };
     if (EPI == EPI_STATS) {
       const bool ragged = aw + MI * 16 > P.nA;
       const int group = it.a0 / (MI * 16) + wa;
+      int wants[MJ];
 #pragma unroll
-      for (int j = 0; j < MJ; ++j) {
+      for (int j = 0; j < MJ; ++j) {                 // all loads before the first store: they would wait for it
         const int t = bw + 16 * j + l15;
         const int64_t y = t < P.nB ? label_at(P.labels, P.labels64, t) : -1;
-        const int want = y >= 0 && y < P.V ? (int)y - aw - l4 : -1;
-        float m = -INFINITY, hit = 0.0f;
+        wants[j] = y >= 0 && y < P.V ? (int)y - aw - l4 : -1;
+      }
+      asm volatile("" ::: "memory");
+#pragma unroll
+      for (int j = 0; j < MJ; ++j) {
+        const int t = bw + 16 * j + l15, want = wants[j];
+        float m = -INFINITY;
         v4f c[MI];
 #pragma unroll
-        for (int i = 0; i < MI; ++i) {
-          c[i] = fetch(acc[i][j]);
+        for (int i = 0; i < MI; ++i) c[i] = fetch(acc[i][j]);
+        if (ragged) {
+          const int left = rarely(P.nA - aw - l4);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            if (ragged && aw + 16 * i + l4 + e >= P.nA) c[i][e] = -INFINITY;
-            m = fmaxf(m, c[i][e]);
-            if (want == 16 * i + e) hit = c[i][e];
-          }
+          for (int i = 0; i < MI; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (16 * i + e >= left) c[i][e] = -INFINITY;
         }
-        if (want >= 0 && want < MI * 16 && (want & 12) == 0) P.target[t] = hit;
+        const bool has = holds(want);
+        if (__any(has)) {
+          const int at = rarely(want);
+          float hit = 0.0f;
+#pragma unroll
+          for (int i = 0; i < MI; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (at == 16 * i + e) hit = c[i][e];
+          if (has) P.target[t] = hit;
+        }
+#pragma unroll
+        for (int i = 0; i < MI; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) m = fmaxf(m, c[i][e]);
         m = fmaxf(m, __shfl_xor(m, 16));
         m = fmaxf(m, __shfl_xor(m, 32));
         const float top = fmaxf(m * LOG2E, NONE);    // a group past the vocabulary has no logits
@@ -505,6 +533,7 @@ __global__ __launch_bounds__(64 * WA * WB, 1) void ce_gemm_kernel(GemmArgs P) {
 #pragma unroll
         for (int j = 0; j < MJ; ++j) {
           uint16_t* row = P.D + (int64_t)(bw + 16 * j + l15) * P.ldd + aw + l8;
+          const bool hits = __any(holds(want[j]));
 #pragma unroll
           for (int i = 0; i < MI; i += 2) {
             float d[2][4];
@@ -512,18 +541,29 @@ __global__ __launch_bounds__(64 * WA * WB, 1) void ce_gemm_kernel(GemmArgs P) {
             for (int h = 0; h < 2; ++h) {
               const v4f c = fetch(acc[i + h][j]);
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const float p = __builtin_amdgcn_exp2f(c[e] * LOG2E - ls[j]);
-                const float q = g[j] * (p - (want[j] == 16 * (i + h) + e ? 1.0f : 0.0f));
-                d[h][e] = __uint_as_float(__float_as_uint(q) & kept[j]);   // (a select became a branch for each element)
-              }
+              for (int e = 0; e < 4; ++e) d[h][e] = __builtin_amdgcn_exp2f(c[e] * LOG2E - ls[j]);
             }
-            if (ragged)
+            if (hits) {
+              const int at = rarely(want[j]);
 #pragma unroll
               for (int h = 0; h < 2; ++h)
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                  if (aw + 16 * (i + h) + l4 + e >= P.nA) d[h][e] = 0.0f;
+                  if (at == 16 * (i + h) + e) d[h][e] -= 1.0f;
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+              for (int e = 0; e < 4; ++e)            // (a select became a branch for each element)
+                d[h][e] = __uint_as_float(__float_as_uint(g[j] * d[h][e]) & kept[j]);
+            if (ragged) {
+              const int left = rarely(P.nA - aw - l4);
+#pragma unroll
+              for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  if (16 * (i + h) + e >= left) d[h][e] = 0.0f;
+            }
             *(uint4*)(row + 16 * i) = pack_pair(d[0], d[1]);
           }
         }
