@@ -733,10 +733,14 @@ int pick_splits(int64_t tiles, int64_t steps, int slots) {
 }
 
 // The tile shape of a product and the parts its contraction is split into
-// (splittable: 1 .. 16).  By the time of its rounds, in stages of a wide tile: a
-// compute unit runs one wide block, or two square ones, which take 0.7 stages
-// for a stage of each (measured 0.64 to 0.75 at the shapes below), and a block
-// costs 6 stages beside its contraction.
+// (splittable: 1 .. 16), by their estimated time in stages of a wide tile:
+//   rounds (stages + 6, with parts + 8) + (2 parts + 1) a b 6.1e-7
+// A compute unit runs one wide block, or two square ones, which take 0.7 stages
+// for a stage of each; a stage is shorter while part of the machine is idle and
+// the clocks are higher; the last term is the parts' way through memory at 4.5
+// TB/s.  dX of 4096 tokens, 65536 entries, K = 2560 (160 tiles on 256 units) with
+// its D: estimated 2.38, 2.50, 2.19, 2.32 ms in 1, 2, 3, 4 parts, measured 2.40,
+// 2.48, 2.23, 2.31.
 struct Choice {
   Tile tile;
   int splits;
@@ -748,10 +752,13 @@ Choice pick(int64_t a, int64_t b, int64_t steps, bool splittable) {
   for (const Tile t : {WIDE, SQUARE}) {
     const int slots = t == WIDE ? CUS : 2 * CUS;
     const int64_t n = tiles_of(t, a, b);
-    const int s = splittable ? pick_splits(n, steps, slots) : 1;
-    const double each = (double)cdiv(steps, s) * (t == WIDE ? 1.0 : 0.7) + 6.0 + (s > 1 ? 2.0 : 0.0);
-    const double time = (double)cdiv(n * s, slots) * each;
-    if (t == WIDE || time < least) best = {t, s}, least = time;
+    for (int s = 1; s <= (splittable ? 16 : 1) && (s == 1 || steps / s >= 16); ++s) {
+      const double rounds = (double)cdiv(n * s, slots);
+      const double stage = (t == WIDE ? 1.0 : 0.7) * (0.75 + 0.25 * (double)(n * s) / (rounds * slots));
+      double time = rounds * ((double)cdiv(steps, s) * stage + (s > 1 ? 8.0 : 6.0));
+      if (s > 1) time += (2 * s + 1) * (double)a * (double)b * 6.1e-7;
+      if (least == 0 || time < least) best = {t, s}, least = time;
+    }
   }
   return best;
 }
