@@ -211,3 +211,17 @@ def test_finite_check(monkeypatch):
         with pytest.raises(sbn.SbnError) as e:
             f()
         assert e.value.status == sbn.SBN_ERR_VALUE
+
+
+@pytest.mark.parametrize("T,V,K", [(65400, 4500, 192), (65400, 4500, 64)])
+def test_several_pieces_with_a_tile_for_every_unit(T, V, K):
+    """dX's sums of one piece are where the next one starts (no parts are joined), at ragged edges of its tiles."""
+    import torch
+    X, W, y, d = make(T, V, K, 11)
+    r = reference(X, W, y, d)
+    _, lse = sbn.sbn_cross_entropy(X, W, y)
+    dX, _ = sbn.sbn_cross_entropy_backward(X, W, y, lse, d, dxdt=sbn.SBN_F32, need_dW=False)
+    close(dX, r["dX"], r["bX"], "dX f32")
+    dx16, dW = sbn.sbn_cross_entropy_backward(X, W, y, lse, d)
+    assert torch.equal(dx16, dX.to(torch.bfloat16))
+    close(dW, r["dW"], r["bW"] + B * r["dW"].abs(), "dW")
