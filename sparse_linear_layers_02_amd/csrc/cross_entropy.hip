@@ -690,7 +690,7 @@ int grid_for(int64_t items) {
 
 // ---------------------------------------------------------------- tile shapes
 // wide: 256 x 256, one block per compute unit; square: 128 x 128; flat: 128 A
-// rows x 64 B rows, for few tokens.
+// rows x 64 B rows, for few tokens or few tiles.
 enum Tile { WIDE, SQUARE, FLAT };
 struct TileShape {
   int a, b;
@@ -724,39 +724,37 @@ hipError_t gemm(const char* name, Tile tile, GemmArgs& P, hipStream_t st) {
 
 int64_t tiles_of(Tile t, int64_t a, int64_t b) { return cdiv(a, SHAPE[t].a) * cdiv(b, SHAPE[t].b); }
 
-// parts of a product whose tiles are too few for the machine: as many as fill
-// `slots` blocks, of at least 16 stages each
-int pick_splits(int64_t tiles, int64_t steps, int slots) {
-  int64_t s = slots / tiles;
-  if (s > steps / 16) s = steps / 16;
-  return (int)(s < 1 ? 1 : s > 16 ? 16 : s);
-}
-
 // The tile shape of a product and the parts its contraction is split into
-// (splittable: 1 .. 16), by their estimated time in stages of a wide tile:
-//   rounds (stages + 6, with parts + 8) + (2 parts + 1) a b 6.1e-7
-// A compute unit runs one wide block, or two square ones, which take 0.7 stages
-// for a stage of each; a stage is shorter while part of the machine is idle and
-// the clocks are higher; the last term is the parts' way through memory at 4.5
-// TB/s.  dX of 4096 tokens, 65536 entries, K = 2560 (160 tiles on 256 units) with
-// its D: estimated 2.38, 2.50, 2.19, 2.32 ms in 1, 2, 3, 4 parts, measured 2.40,
-// 2.48, 2.23, 2.31.
+// (splittable: 1 .. 16), by their estimated time in stages of a wide tile (1.45 us):
+//   sum of rounds (stages x stage + start, with parts + 1 or 2), with parts + 2 + (2 parts + 1) a b 6.1e-7
+// A compute unit runs one wide block or two of the others.  stage is that of a
+// round that fills the machine; where at most one block of two runs on each
+// unit, `alone`; of wide tiles it falls to 0.75 as units are idle and the clocks
+// higher; flat ones take longer with transposing reads.  The last terms are the
+// sum's launch and the parts' way through memory at 4.5 TB/s.
+// Both sides measured: dX of 4096 tokens, 65536 entries, K = 2560 (160 wide tiles
+// on 256 units) with its D in 1, 2, 3, 4 parts 2.40, 2.48, 2.23, 2.31 ms
+// (estimated 2.38, 2.48, 2.19, 2.32).  Loss of 128 tokens, 1000 entries, K = 4096:
+// square 34.3 us, flat 27.9; of 200, 32001, 2560: wide 54.5, square 44.4, flat
+// 57.3; of 600, 20000, 4096: wide 94, square 109.
 struct Choice {
   Tile tile;
   int splits;
 };
 Choice pick(int64_t a, int64_t b, int64_t steps, bool splittable) {
-  if (b <= 64) return {FLAT, splittable ? pick_splits(tiles_of(FLAT, a, b), steps, 2 * CUS) : 1};
+  const double STAGE[] = {1.0, 0.7, splittable ? 0.54 : 0.44}, ALONE[] = {1.0, 0.33, splittable ? 0.27 : 0.22};
+  constexpr double START[] = {6.0, 5.0, 4.0}, PARTS[] = {2.0, 1.0, 1.0};
   Choice best{WIDE, 1};
   double least = 0;
-  for (const Tile t : {WIDE, SQUARE}) {
+  for (const Tile t : {WIDE, SQUARE, FLAT}) {
     const int slots = t == WIDE ? CUS : 2 * CUS;
     const int64_t n = tiles_of(t, a, b);
     for (int s = 1; s <= (splittable ? 16 : 1) && (s == 1 || steps / s >= 16); ++s) {
-      const double rounds = (double)cdiv(n * s, slots);
-      const double stage = (t == WIDE ? 1.0 : 0.7) * (0.75 + 0.25 * (double)(n * s) / (rounds * slots));
-      double time = rounds * ((double)cdiv(steps, s) * stage + (s > 1 ? 8.0 : 6.0));
-      if (s > 1) time += (2 * s + 1) * (double)a * (double)b * 6.1e-7;
+      const int64_t full = n * s / slots, rest = n * s % slots;
+      double stage = (double)full * STAGE[t];
+      if (rest) stage += rest > CUS ? STAGE[t] : ALONE[t] * (t == WIDE ? 0.75 + 0.25 * (double)rest / CUS : 1.0);
+      double time = stage * (double)cdiv(steps, s) + (double)(full + (rest > 0)) * (START[t] + (s > 1 ? PARTS[t] : 0.0));
+      if (s > 1) time += 2.0 + (2 * s + 1) * (double)a * (double)b * 6.1e-7;
       if (least == 0 || time < least) best = {t, s}, least = time;
     }
   }
