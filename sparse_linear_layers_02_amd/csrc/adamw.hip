@@ -34,12 +34,6 @@ constexpr int QB = SBN_ADAMW_BLOCK;
 constexpr float S_FLOOR = 0x1p-100f;                // a block whose largest value is smaller is all 0
 constexpr float INV127 = 1.0f / 127.0f, INV255 = 1.0f / 255.0f;
 
-__device__ inline float half_wave_max(float x) {
-#pragma unroll
-  for (int m = 16; m >= 1; m >>= 1) x = fmaxf(x, __shfl_xor(x, m));
-  return x;
-}
-
 __device__ inline float decode_m(int c, float s) {
   const float t = (float)c * INV127;
   return t * fabsf(t) * s;
@@ -153,7 +147,7 @@ __device__ inline float encode8(const float* v, int* c) {
   float s = 0.0f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) s = fmaxf(s, fabsf(v[i]));
-  s = half_wave_max(s);
+  s = half_wave_all(s, Max{});
   if (s < S_FLOOR) s = 0.0f;
   const float inv = s > 0.0f ? 1.0f / s : 0.0f;
   float y[8], q[8], half = 0.0f;

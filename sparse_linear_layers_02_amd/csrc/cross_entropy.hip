@@ -85,9 +85,7 @@ __device__ inline float max_dloss(const float* dloss, const void* labels, bool i
     for (int k = 0; k < AHEAD; ++k)
       if (y[k] >= 0 && y[k] < V) m = fmaxf(m, fabsf(g[k]));
   }
-#pragma unroll
-  for (int d = 32; d >= 1; d >>= 1) m = fmaxf(m, __shfl_xor(m, d));
-  return m;
+  return wave_all(m, Max{});
 }
 
 // Tile order: the hardware deals consecutive blocks to the 8 XCDs in turn, so
@@ -502,16 +500,14 @@ __global__ __launch_bounds__(64 * WA * WB, 1) void ce_gemm_kernel(GemmArgs P) {
         for (int i = 0; i < MI; ++i)
 #pragma unroll
           for (int e = 0; e < 4; ++e) m = fmaxf(m, c[i][e]);
-        m = fmaxf(m, __shfl_xor(m, 16));
-        m = fmaxf(m, __shfl_xor(m, 32));
+        m = rows_all(m, Max{});
         const float top = fmaxf(m * LOG2E, NONE);    // a group past the vocabulary has no logits
         float sum = 0.0f;
 #pragma unroll
         for (int i = 0; i < MI; ++i)
 #pragma unroll
           for (int e = 0; e < 4; ++e) sum += __builtin_amdgcn_exp2f(c[i][e] * LOG2E - top);
-        sum += __shfl_xor(sum, 16);
-        sum += __shfl_xor(sum, 32);
+        sum = rows_all(sum, Add{});
         if (lane < 16 && t < P.nB) P.stats[(int64_t)group * P.nB + t] = make_float2(top, sum);
       }
     } else if (EPI == EPI_GRAD) {

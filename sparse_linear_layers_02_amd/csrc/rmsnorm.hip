@@ -81,47 +81,30 @@ __device__ inline void gain8(const void* gain, bool f32, int64_t i, float* v) {
   }
 }
 
-__device__ inline float wave_sum(float x) {
-#pragma unroll
-  for (int m = 32; m >= 1; m >>= 1) x += __shfl_xor(x, m);
-  return x;
-}
-__device__ inline float wave_max(float x) {
-#pragma unroll
-  for (int m = 32; m >= 1; m >>= 1) x = fmaxf(x, __shfl_xor(x, m));
-  return x;
-}
-
-// 8 codes rint((127 u) / a), rcp = fl(127 / a).  u * rcp is off by under 2^-15; if
-// one of the 8 lies within 2^-14 of a half-integer, all are divided again,
-// correctly rounded (about one wave in 17 does).
+// 8 codes rint((127 u) / a), rcp = 127 / a to two units in the last place.  Added
+// to 1.5 2^23, u rcp is rounded to an integer, whose byte the sum's lowest is; u
+// rcp is off by under 2^-15.  If one of the 8 lies within 2^-14 of a half-integer,
+// all are divided, correctly rounded (about one wave in 17 does).
 __device__ inline uint2 codes8(const float* u, float rcp, float a) {
+  constexpr float SHIFT = 12582912.0f;
   float q[8], half = 0.0f;
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    const float x = u[j] * rcp;
-    q[j] = rintf(x);
-    half = fmaxf(half, fabsf(x - q[j]));
+    q[j] = fmaf(u[j], rcp, SHIFT);
+    half = fmaxf(half, fabsf(fmaf(u[j], rcp, SHIFT - q[j])));
   }
   if (half > 0.5f - 0x1p-14f) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) q[j] = rintf((127.0f * u[j]) / a);
+    for (int j = 0; j < 8; ++j) q[j] = rintf((127.0f * u[j]) / a) + SHIFT;
   }
-  uint32_t o[2] = {0u, 0u};
+  uint32_t o[2];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) o[j >> 2] |= (uint32_t)((int)q[j] & 0xFF) << (8 * (j & 3));
+  for (int j = 0; j < 2; ++j) {                      // the four lowest bytes
+    const uint32_t lo = __builtin_amdgcn_perm(__float_as_uint(q[4 * j + 1]), __float_as_uint(q[4 * j]), 0x0c0c0400u);
+    const uint32_t hi = __builtin_amdgcn_perm(__float_as_uint(q[4 * j + 3]), __float_as_uint(q[4 * j + 2]), 0x0c0c0400u);
+    o[j] = __builtin_amdgcn_perm(hi, lo, 0x05040100u);
+  }
   return make_uint2(o[0], o[1]);
-}
-
-__device__ inline float row16_sum(float x) {
-#pragma unroll
-  for (int m = 8; m >= 1; m >>= 1) x += __shfl_xor(x, m);
-  return x;
-}
-__device__ inline float row16_max(float x) {
-#pragma unroll
-  for (int m = 8; m >= 1; m >>= 1) x = fmaxf(x, __shfl_xor(x, m));
-  return x;
 }
 
 // ---------------------------------------------------------------- forward
@@ -160,6 +143,12 @@ __global__ __launch_bounds__(MAXT) void rmsnorm_kernel(FwdArgs A) {
       for (int i = 0; i < CH; ++i)
         if (g + TPR * i < n) h[i].load(xr, g + TPR * i);
     }
+    // Of one chunk the gain is loaded before the first store, which a later load
+    // would wait for (8-bit output of 4096 x 2560 19.2 -> 18.5 us); more chunks of it
+    // leave room for half the blocks (1024 x 16384: 30 -> 34 us).
+    constexpr bool EARLY = CH == 1;
+    float gain[8];
+    if (EARLY && g < n) gain8(A.gain, A.gain_f32, g, gain);
     float ss = 0.0f, mx = 0.0f;
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
@@ -179,15 +168,14 @@ __global__ __launch_bounds__(MAXT) void rmsnorm_kernel(FwdArgs A) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) ss += v[j] * v[j];
         if (Q) {
-          float w[8];
-          gain8(A.gain, A.gain_f32, c, w);
+          if (!EARLY) gain8(A.gain, A.gain_f32, c, gain);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) mx = fmaxf(mx, fabsf(v[j] * w[j]));
+          for (int j = 0; j < 8; ++j) mx = fmaxf(mx, fabsf(v[j] * gain[j]));
         }
       }
     }
-    ss = wave_sum(ss);
-    if (Q) mx = wave_max(mx);
+    ss = wave_all(ss, Add{});
+    if (Q) mx = wave_all(mx, Max{});
     if (waves > 1) {
       // two sets of red in turn: one barrier a round keeps a fast wave's next
       // write away from a slow wave's read
@@ -197,8 +185,8 @@ __global__ __launch_bounds__(MAXT) void rmsnorm_kernel(FwdArgs A) {
       }
       __syncthreads();
       const int l = threadIdx.x & 15;               // at most 16 waves
-      ss = row16_sum(l < waves ? red[turn][0][l] : 0.0f);
-      if (Q) mx = row16_max(l < waves ? red[turn][1][l] : 0.0f);
+      ss = row16_all(l < waves ? red[turn][0][l] : 0.0f, Add{});
+      if (Q) mx = row16_all(l < waves ? red[turn][1][l] : 0.0f, Max{});
     }
     const float rstd = 1.0f / sqrtf(ss / (float)A.K + A.eps);
     const float a = fmaxf(mx, U_FLOOR);
@@ -206,21 +194,21 @@ __global__ __launch_bounds__(MAXT) void rmsnorm_kernel(FwdArgs A) {
       if (A.rstd) A.rstd[t] = rstd;
       if (Q) A.s_x[t] = (a * rstd) / 127.0f;
     }
-    const float rcp = 127.0f / a;
+    const float rcp = 127.0f * __builtin_amdgcn_rcpf(a);
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
       const int c = g + TPR * i;
       if (c < n) {
-        float v[8], w[8];
+        float v[8];
         h[i].to(v);
-        gain8(A.gain, A.gain_f32, c, w);
+        if (!EARLY) gain8(A.gain, A.gain_f32, c, gain);
         if (Q) {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) v[j] *= w[j];
+          for (int j = 0; j < 8; ++j) v[j] *= gain[j];
           *(uint2*)(A.Xq + t * A.K + 8 * c) = codes8(v, rcp, a);
         } else {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) v[j] = v[j] * rstd * w[j];
+          for (int j = 0; j < 8; ++j) v[j] = v[j] * rstd * gain[j];
           h[i].from(v);
           h[i].store((char*)A.Y + t * A.ldy * es, c);
         }
@@ -245,7 +233,12 @@ __global__ __launch_bounds__(MAXT) void rmsnorm_grad_kernel(BwdArgs A) {
   __shared__ float red[2][MAXT / 64];
   const int g = threadIdx.x, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
   const int n = A.K / 8, es = F32 ? 4 : 2, TPR = blockDim.x;
-  float dg[CH][8];
+  // up to two chunks of gain stay for all rows (8192 x 4096: 62.5 -> 56.8 us); four would not fit the registers
+  constexpr bool KEPT = CH <= 2;
+  float dg[CH][8], gain[KEPT ? CH : 1][8];
+#pragma unroll
+  for (int i = 0; i < CH; ++i)
+    if (KEPT && g + TPR * i < n) gain8(A.gain, A.gain_f32, g + TPR * i, gain[i]);
 #pragma unroll
   for (int i = 0; i < CH; ++i)
 #pragma unroll
@@ -273,10 +266,10 @@ __global__ __launch_bounds__(MAXT) void rmsnorm_grad_kernel(BwdArgs A) {
     for (int i = 0; i < CH; ++i) {
       const int c = g + TPR * i;
       if (c < n) {
-        float yv[8], hv[8], w[8];
+        float yv[8], hv[8], *w = gain[KEPT ? i : 0];
         y[i].to(yv);
         h[i].to(hv);
-        gain8(A.gain, A.gain_f32, c, w);
+        if (!KEPT) gain8(A.gain, A.gain_f32, c, w);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           const float yn = yv[j] * (hv[j] * rstd);
@@ -285,22 +278,22 @@ __global__ __launch_bounds__(MAXT) void rmsnorm_grad_kernel(BwdArgs A) {
         }
       }
     }
-    s = wave_sum(s);
+    s = wave_all(s, Add{});
     if (waves > 1) {
       if ((threadIdx.x & 63) == 0) red[turn][wave] = s;
       __syncthreads();                              // and the other set of red for the next round
       const int l = threadIdx.x & 15;
-      s = row16_sum(l < waves ? red[turn][l] : 0.0f);
+      s = row16_all(l < waves ? red[turn][l] : 0.0f, Add{});
     }
     const float mean = s / (float)A.K;
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
       const int c = g + TPR * i;
       if (c < n) {
-        float yv[8], hv[8], w[8], dv[8];
+        float yv[8], hv[8], dv[8], *w = gain[KEPT ? i : 0];
         y[i].to(yv);
         h[i].to(hv);
-        gain8(A.gain, A.gain_f32, c, w);
+        if (!KEPT) gain8(A.gain, A.gain_f32, c, w);
         if (A.dH) d[i].to(dv);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {

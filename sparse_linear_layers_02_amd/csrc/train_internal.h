@@ -6,6 +6,50 @@
 
 namespace sbn {
 
+#ifdef __HIPCC__
+// ----------------------------------------------------------------- sums and maxima over lanes
+// In the vector unit: within 16 lanes by quads, halves and mirrors of a row, then
+// by exchanging rows and halves.  (Through LDS each step waits some 60 cycles.)
+// Every lane gets the same value.
+struct Add {
+  __device__ float operator()(float a, float b) const { return a + b; }
+};
+struct Max {
+  __device__ float operator()(float a, float b) const { return fmaxf(a, b); }
+};
+template <int CTRL>
+__device__ inline float row_move(float x) {
+  return __uint_as_float((uint32_t)__builtin_amdgcn_mov_dpp((int)__float_as_uint(x), CTRL, 0xf, 0xf, true));
+}
+template <class Op>
+__device__ inline float row16_all(float x, Op op) {
+  x = op(x, row_move<0xB1>(x));                      // quad_perm 1 0 3 2
+  x = op(x, row_move<0x4E>(x));                      // quad_perm 2 3 0 1
+  x = op(x, row_move<0x141>(x));                     // row_half_mirror
+  return op(x, row_move<0x140>(x));                  // row_mirror
+}
+// lanes of equal place in the rows of 16: of the two rows of each half wave, of all four
+template <class Op>
+__device__ inline float row_pairs_all(float x, Op op) {
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return op(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+template <class Op>
+__device__ inline float rows_all(float x, Op op) {
+  x = row_pairs_all(x, op);
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return op(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+template <class Op>
+__device__ inline float half_wave_all(float x, Op op) {
+  return row_pairs_all(row16_all(x, op), op);
+}
+template <class Op>
+__device__ inline float wave_all(float x, Op op) {
+  return rows_all(row16_all(x, op), op);
+}
+#endif
+
 // ----------------------------------------------------------------- RMS norm (T >= 1)
 // Xq != NULL: the 8-bit form (Y unused); otherwise Y.
 hipError_t launch_rmsnorm(const void* X, int64_t ldx, const void* res, int64_t ldr, bool f32, const void* gain,
