@@ -144,9 +144,10 @@ __global__ __launch_bounds__(MAXT) void rmsnorm_kernel(FwdArgs A) {
         if (g + TPR * i < n) h[i].load(xr, g + TPR * i);
     }
     // Of one chunk the gain is loaded before the first store, which a later load
-    // would wait for (8-bit output of 4096 x 2560 19.2 -> 18.5 us); more chunks of it
-    // leave room for half the blocks (1024 x 16384: 30 -> 34 us).
-    constexpr bool EARLY = CH == 1;
+    // would wait for (8-bit output of 4096 x 2560 19.2 -> 18.5 us, bf16 of 1021 x 4096
+    // 8.85 -> 8.5, but float32 11.8 -> 12.4); more chunks of it leave room for half
+    // the blocks (1024 x 16384: 30 -> 34 us).
+    constexpr bool EARLY = CH == 1 && (Q || !F32);
     float gain[8];
     if (EARLY && g < n) gain8(A.gain, A.gain_f32, g, gain);
     float ss = 0.0f, mx = 0.0f;
