@@ -221,11 +221,12 @@ struct HalfStage {
 // 512 tokens of 8000 entries, one round of tiles, 54.9 for 53.3.)
 //
 // Bound by the matrix cores: at T = 8192, V = 65536, K = 4096 they are busy 74% of
-// the forward's cycles and 66 to 69% of the gradients', at the 1.7 to 2.0 GHz that
-// the part's power allows under them; 1.4 PFLOP/s of the forward and of D, dX and
-// dW in 808, 782 and 810 us for 16384 entries (1.36 to 1.41), the library's plain
-// product 1.4 to 1.5.  No LDS bank conflicts; 6.4 GB fetched from beyond L2 in the
-// forward's 3.05 ms.  At 17 tokens (FLAT) bound by reading W: a head of 50001 x
+// the forward's cycles and 67 to 69% of the gradients', at the 1.67 to 1.83 GHz
+// that the part's power allows under them.  The forward takes 3.01 ms (1.46
+// PFLOP/s; the library's bare product on the same card 2.88), D, dX and dW of half
+// the entries 1.61, 1.53 and 1.64 ms (1.37, 1.44, 1.34; the library's halves of dX
+// and dW 1.61 and 1.87); up to 8% more on cards of lower clocks.  No LDS bank
+// conflicts; 6.4 GB fetched from beyond L2 in the forward.  At 17 tokens (FLAT) bound by reading W: a head of 50001 x
 // 2560, 256 MB, in 50 us, 5.1 TB/s.
 template <int WA, int WB, int MI, int MJ, int RING, int EPI, bool TRA, bool TRB>
 __global__ __launch_bounds__(64 * WA * WB, 1) void ce_gemm_kernel(GemmArgs P) {

@@ -16,9 +16,10 @@
 //
 // Both directions are bound by memory traffic: every row is read once and
 // written once.  Kernel times in bf16: 8-bit output of 4096 x 2560 with the
-// residual 17.6 us (4.2 TB/s of 73 MB; a large copy reaches 4.9), gradient of
-// 8192 x 4096 with dh 49.4 us (5.4 TB/s of 268 MB; 202 MB fetched, 76 MB
-// written) and 4.8 us for dgain's sums.  One token of 2560: 3.1 us, latency.
+// residual 15.0 us (4.9 TB/s of 73 MB; a large copy reaches 4.7 to 4.9), gradient
+// of 8192 x 4096 with dh 40 us for one set of tensors again and again (6.6 TB/s of
+// 268 MB; 202 MB fetched, 76 MB written), 50 for three in turn, and 4.8 us for
+// dgain's sums.  One token of 2560: 2.8 us, latency.
 #include "train_internal.h"
 
 namespace sbn {
