@@ -85,7 +85,8 @@ __device__ inline void gain8(const void* gain, bool f32, int64_t i, float* v) {
 // 8 codes rint((127 u) / a), rcp = 127 / a to two units in the last place.  Added
 // to 1.5 2^23, u rcp is rounded to an integer, whose byte the sum's lowest is; u
 // rcp is off by under 2^-15.  If one of the 8 lies within 2^-14 of a half-integer,
-// all are divided, correctly rounded (about one wave in 17 does).
+// all are divided, correctly rounded, both sides scaled so that 127 u is finite
+// (about one wave in 17 does).
 __device__ inline uint2 codes8(const float* u, float rcp, float a) {
   constexpr float SHIFT = 12582912.0f;
   float q[8], half = 0.0f;
@@ -96,7 +97,7 @@ __device__ inline uint2 codes8(const float* u, float rcp, float a) {
   }
   if (half > 0.5f - 0x1p-14f) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) q[j] = rintf((127.0f * u[j]) / a) + SHIFT;
+    for (int j = 0; j < 8; ++j) q[j] = rintf((127.0f * (u[j] * 0x1p-8f)) / (a * 0x1p-8f)) + SHIFT;
   }
   uint32_t o[2];
 #pragma unroll
@@ -196,7 +197,7 @@ __global__ __launch_bounds__(MAXT) void rmsnorm_kernel(FwdArgs A) {
       if (A.rstd) A.rstd[t] = rstd;
       if (Q) A.s_x[t] = (a * rstd) / 127.0f;
     }
-    const float rcp = 127.0f * __builtin_amdgcn_rcpf(a);
+    const float rcp = __builtin_amdgcn_rcpf(a * (1.0f / 127.0f));   // (1 / a itself may be too small for a float)
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
       const int c = g + TPR * i;

@@ -267,3 +267,20 @@ def test_finite_check(monkeypatch):
         with pytest.raises(sbn.SbnError) as e:
             f()
         assert e.value.status == sbn.SBN_ERR_VALUE
+
+
+@pytest.mark.parametrize("K", [8, 2560, 4104])
+def test_rows_near_the_largest_float(K):
+    """h gain up to 3e38: neither 127 times a value nor the reciprocal of a row's maximum is a normal float."""
+    T = 40
+    x, xv = put((rnd([8, K], T, K) * 2e17).astype(np.float32), True)
+    gain = np.full(K, 1e20, np.float32)
+    g, gv = put(gain, True)
+    u = (xv * gv).astype(np.float32)
+    a = np.abs(u).max(1)
+    assert np.isfinite(a).all() and a.max() > 2.0 ** 125
+    q = np.rint((np.float32(127.0) * (u * np.float32(2.0 ** -8))) / (a * np.float32(2.0 ** -8))[:, None]).astype(np.int8)
+    Xq, s_x, _, rs = sbn.sbn_rmsnorm_quant(x, g, eps=EPS)
+    assert np.array_equal(host(Xq), q)
+    ref = a.astype(np.float64) / 127.0 / np.sqrt((xv.astype(np.float64) ** 2).mean(1) + EPS)
+    close(host(s_x), ref, 40 * U * ref, "s_x")
