@@ -356,8 +356,9 @@ int chunks_for(int n) { return n <= 512 ? 1 : n <= 2048 ? 2 : 4; }
 // Blocks of the gradient: 16 waves a compute unit, but a block's partial of dgain
 // costs as much traffic as two rows in 16 bits, so at least 8 rows a block where
 // that leaves one block a compute unit.  (bf16, microseconds at 256 / 512 / 1024
-// blocks: T = 8192, K = 4096: 76 / 64 / 68; T = 8192, K = 1024: 41 / 27 / 22;
-// T = 4096, K = 2560: 33 / 27 / 31; T = 1021, K = 4096: 16.3 / 17.3 / 23.)
+// blocks: T = 8192, K = 4096: 61.6 / 56.6 / 63.3; T = 8192, K = 1024: 32.5 / 22.5 /
+// 19.2; T = 4096, K = 2560: 24.6 / 21.3 / 23.1; T = 1021, K = 4096: 14.2 / 15.3 /
+// 21.6.)
 int bwd_blocks(int64_t T, int64_t K) {
   const int n = (int)(K / 8), most = 256 * 16 / (threads_for(n, chunks_for(n)) / 64);
   int64_t g = T / 8 < 256 ? 256 : T / 8;
