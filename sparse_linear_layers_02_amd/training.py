@@ -12,8 +12,9 @@ import ctypes
 import functools
 import os
 import re
+import sys
 
-from . import _SIGNATURES, _WS, SBN_BF16, SBN_F32, PKG_DIR, SbnError, _check, _req, _torch, lib
+from . import _SIGNATURES, _WS, SBN_BF16, SBN_F32, PKG_DIR, SbnError, _check, _req, lib
 
 TRAIN_HEADER_PATH = os.path.join(os.path.dirname(PKG_DIR), "include", "sbn_train.h")
 SBN_ADAMW_BLOCK = 256
@@ -46,7 +47,24 @@ def train_header_symbols() -> list[str]:
 
 
 # Small calls are bound by what happens here before the launch, so the checks
-# below cost one expression where all is well, and say what is wrong elsewhere.
+# below cost one expression where all is well, and say what is wrong elsewhere;
+# torch and the library are looked up without an import statement or a lock.
+_package = sys.modules[__package__]
+_torch_module = None
+
+
+def _torch():
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
+
+
+def _so():
+    return _package._lib or lib()
+
+
 def _dtype(t, name: str, fn: str) -> int:
     torch = _torch()
     if t.dtype is torch.bfloat16:
@@ -150,7 +168,7 @@ def sbn_rmsnorm(X, gain, *, residual=None, eps: float = 1e-6, H=None, Y=None, rs
     else:
         _rows(Y, "Y", X, fn)
     if T:
-        _check(fn, lib().sbn_rmsnorm(X.data_ptr(), _ld(X), _addr(residual), 0 if residual is None else _ld(residual),
+        _check(fn, _so().sbn_rmsnorm(X.data_ptr(), _ld(X), _addr(residual), 0 if residual is None else _ld(residual),
                                      dt, gain.data_ptr(), gdt, T, K, eps, _addr(H), 0 if H is None else _ld(H),
                                      Y.data_ptr(), _ld(Y), rstd.data_ptr(), _raw_stream(stream, X.device)))
     return Y, X if H is None else H, rstd
@@ -174,7 +192,7 @@ def sbn_rmsnorm_quant(X, gain, *, residual=None, eps: float = 1e-6, H=None, Xq=N
     else:
         _vector(s_x, "s_x", T, torch.float32, X.device, fn)
     if T:
-        _check(fn, lib().sbn_rmsnorm_quant(X.data_ptr(), _ld(X), _addr(residual),
+        _check(fn, _so().sbn_rmsnorm_quant(X.data_ptr(), _ld(X), _addr(residual),
                                            0 if residual is None else _ld(residual), dt, gain.data_ptr(), gdt, T, K,
                                            eps, _addr(H), 0 if H is None else _ld(H), Xq.data_ptr(), s_x.data_ptr(),
                                            rstd.data_ptr(), _raw_stream(stream, X.device)))
@@ -185,7 +203,7 @@ def sbn_rmsnorm_quant(X, gain, *, residual=None, eps: float = 1e-6, H=None, Xq=N
 def _norm_scratch_bytes(T: int, K: int) -> int:
     b = _sz()
     fn = "sbn_rmsnorm_backward_workspace_bytes"
-    _check(fn, lib().sbn_rmsnorm_backward_workspace_bytes(T, K, ctypes.byref(b)))
+    _check(fn, _so().sbn_rmsnorm_backward_workspace_bytes(T, K, ctypes.byref(b)))
     return b.value
 
 
@@ -214,7 +232,7 @@ def sbn_rmsnorm_backward(dY, H, gain, rstd, *, dH=None, dX=None, dgain=None, ws=
     raw = _raw_stream(stream, H.device)
     if ws is None:
         ws = _scratch("rmsnorm_backward", _norm_scratch_bytes(T, K), H.device, stream, raw)
-    _check(fn, lib().sbn_rmsnorm_backward(dY.data_ptr(), _ld(dY), H.data_ptr(), _ld(H), _addr(dH),
+    _check(fn, _so().sbn_rmsnorm_backward(dY.data_ptr(), _ld(dY), H.data_ptr(), _ld(H), _addr(dH),
                                           0 if dH is None else _ld(dH), dt, gain.data_ptr(), gdt, rstd.data_ptr(), T, K,
                                           dX.data_ptr(), _ld(dX), dgain.data_ptr(), ws.data_ptr(), ws.numel(), raw))
     return dX, dgain
@@ -241,7 +259,7 @@ def _head_args(fn, X, W, labels):
 def sbn_cross_entropy_workspace_bytes(T: int, V: int, K: int, backward: bool = False) -> int:
     fn = "sbn_cross_entropy_backward_workspace_bytes" if backward else "sbn_cross_entropy_workspace_bytes"
     b = _sz()
-    _check(fn, getattr(lib(), fn)(T, V, K, ctypes.byref(b)))
+    _check(fn, getattr(_so(), fn)(T, V, K, ctypes.byref(b)))
     return b.value
 
 
@@ -263,7 +281,7 @@ def sbn_cross_entropy(X, W, labels, *, loss=None, lse=None, ws=None, stream=None
     raw = _raw_stream(stream, X.device)
     if ws is None:
         ws = _scratch("cross_entropy", sbn_cross_entropy_workspace_bytes(T, V, K), X.device, stream, raw)
-    _check(fn, lib().sbn_cross_entropy(X.data_ptr(), _ld(X), W.data_ptr(), _ld(W), labels.data_ptr(), lb, T, V, K,
+    _check(fn, _so().sbn_cross_entropy(X.data_ptr(), _ld(X), W.data_ptr(), _ld(W), labels.data_ptr(), lb, T, V, K,
                                        loss.data_ptr(), lse.data_ptr(), ws.data_ptr(), ws.numel(), raw))
     return loss, lse
 
@@ -299,7 +317,7 @@ def sbn_cross_entropy_backward(X, W, labels, lse, dloss, *, dxdt: int = SBN_BF16
     raw = _raw_stream(stream, X.device)
     if ws is None:
         ws = _scratch("cross_entropy_backward", sbn_cross_entropy_workspace_bytes(T, V, K, True), X.device, stream, raw)
-    _check(fn, lib().sbn_cross_entropy_backward(X.data_ptr(), _ld(X), W.data_ptr(), _ld(W), labels.data_ptr(), lb,
+    _check(fn, _so().sbn_cross_entropy_backward(X.data_ptr(), _ld(X), W.data_ptr(), _ld(W), labels.data_ptr(), lb,
                                                 lse.data_ptr(), dloss.data_ptr(), T, V, K, _addr(dX), dxdt,
                                                 0 if dX is None else _ld(dX), _addr(dW), dwdt,
                                                 0 if dW is None else _ld(dW), ws.data_ptr(), ws.numel(), raw))
@@ -366,7 +384,7 @@ class AdamWTable:
             e.shadow = put(lists["shadows"][i], "shadows", i, torch.bfloat16, n)
             e.n, e.weight_decay = n, wds[i]
         blocks = _i64()
-        plan = lib().sbn_adamw_plan
+        plan = _so().sbn_adamw_plan
         _check("sbn_adamw_plan", plan(entries, count, self.pdt, self.gdt, self.state_bits, None, ctypes.byref(blocks)))
         self.blocks = blocks.value
         mp = torch.empty(max(2 * self.blocks, 2), dtype=torch.int32)
@@ -389,7 +407,7 @@ def sbn_adamw_step(table, *, lr: float, step: int, beta1: float = 0.9, beta2: fl
         raise SbnError(fn, 2, "table must be an AdamWTable")
     if dyn is not None:
         _vector(dyn, "dyn", 4, _torch().float32, table.map.device, fn)
-    _check(fn, lib().sbn_adamw_step(table.entries.data_ptr(), table.map.data_ptr(), table.blocks, table.pdt, table.gdt,
+    _check(fn, _so().sbn_adamw_step(table.entries.data_ptr(), table.map.data_ptr(), table.blocks, table.pdt, table.gdt,
                                     table.state_bits, lr, beta1, beta2, eps, step, _addr(dyn),
                                     _raw_stream(stream, table.map.device)))
 
@@ -406,7 +424,7 @@ def _decode(codes, scale, second, out, stream):
         _req(out, "out", "f32", True, fn)
         if out.numel() != n or out.device != codes.device:
             raise SbnError(fn, 2, f"out must have {n} elements on {codes.device}")
-    _check(fn, lib().sbn_adamw_decode_state(codes.data_ptr(), scale.data_ptr(), n, second, out.data_ptr(),
+    _check(fn, _so().sbn_adamw_decode_state(codes.data_ptr(), scale.data_ptr(), n, second, out.data_ptr(),
                                             _raw_stream(stream, codes.device)))
     return out
 
@@ -438,7 +456,7 @@ def _encode(x, second, codes, scale, stream):
         scale = torch.empty(ns, dtype=torch.float32, device=x.device)
     else:
         _vector(scale, "scale", ns, torch.float32, x.device, fn)
-    _check(fn, lib().sbn_adamw_encode_state(x.data_ptr(), n, second, codes.data_ptr(), scale.data_ptr(),
+    _check(fn, _so().sbn_adamw_encode_state(x.data_ptr(), n, second, codes.data_ptr(), scale.data_ptr(),
                                             _raw_stream(stream, x.device)))
     return codes, scale
 
