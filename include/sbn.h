@@ -79,7 +79,8 @@ typedef enum sbn_status {
 typedef enum sbn_dtype {
   SBN_F32 = 0,                 /* float32 */
   SBN_BF16 = 1,                /* bfloat16, round to nearest even from float32 */
-  SBN_I32_ACC = 2              /* raw int32 accumulator sum_k Xq*Wt, unscaled */
+  SBN_I32_ACC = 2,             /* raw int32 accumulator sum_k Xq*Wt, unscaled */
+  SBN_F32_FINE = 3             /* float32 gradients of sbn_cross_entropy_backward from 16-bit logit gradients (sbn_train.h) */
 } sbn_dtype;
 
 /*

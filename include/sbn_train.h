@@ -127,10 +127,13 @@ sbn_status sbn_cross_entropy(const uint16_t* X, int64_t ldx, const uint16_t* W, 
  * D exists for one piece of the vocabulary at a time, in the workspace: the
  * logits are computed again, piece by piece.  Rounding D to bf16 puts it
  * through the bf16 matrix cores; it costs each gradient a relative error of
- * about that of its own bf16 rounding.
+ * about that of its own bf16 rounding.  A gradient of type SBN_F32_FINE is
+ * float32 from a D of two bf16 numbers, a value and what its rounding left
+ * (at least 16 bits in all), each with a product of its own: that gradient's
+ * product takes twice the time, and its error falls to that of float32 sums.
  *
- *   dX [T x K] of dtype dxdt, dW [V x K] of dtype dwdt (SBN_BF16 or SBN_F32);
- *   either may be NULL.  With T = 0 dW is written as zeros.
+ *   dX [T x K] of dtype dxdt, dW [V x K] of dtype dwdt (SBN_BF16, SBN_F32 or
+ *   SBN_F32_FINE); either may be NULL.  With T = 0 dW is written as zeros.
  *   ws sbn_cross_entropy_backward_workspace_bytes(T, V, K) bytes
  */
 sbn_status sbn_cross_entropy_backward_workspace_bytes(int64_t T, int64_t V, int64_t K, size_t* bytes);

@@ -25,7 +25,7 @@ PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG_DIR, "libsbn.so")
 HEADER_PATH = os.path.join(os.path.dirname(PKG_DIR), "include", "sbn.h")
 
-SBN_F32, SBN_BF16, SBN_I32_ACC = 0, 1, 2
+SBN_F32, SBN_BF16, SBN_I32_ACC, SBN_F32_FINE = 0, 1, 2, 3
 SBN_FORM_PACKED, SBN_FORM_D2, SBN_FORM_J6 = 0, 1, 2     # the weight forms a GEMV table can hold
 SBN_OP_PACK, SBN_OP_ACT_QUANT, SBN_OP_GEMM, SBN_OP_GEMV, SBN_OP_BACKWARD, SBN_OP_FORWARD = 0, 1, 2, 3, 4, 5
 SBN_OP_GEMM_PREPARED = 6
@@ -677,7 +677,7 @@ __all__ = [
     "sbn_gemm_weight_bytes", "sbn_prepare_gemm_weight", "sbn_sparse_ternary_gemm_prepared", "SBN_OP_GEMM_PREPARED",
     "SBN_ERR_VALUE",
     "SBN_FLAGS_NONE", "SBN_MASK_FROM_TERNARY", "SBN_GRAD_W_MASKED",
-    "SBN_F32", "SBN_BF16", "SBN_I32_ACC", "SBN_OP_PACK", "SBN_OP_ACT_QUANT", "SBN_OP_GEMM",
+    "SBN_F32", "SBN_BF16", "SBN_I32_ACC", "SBN_F32_FINE", "SBN_OP_PACK", "SBN_OP_ACT_QUANT", "SBN_OP_GEMM",
     "SBN_OP_GEMV", "SBN_OP_BACKWARD", "SBN_OP_FORWARD", "sbn_profile_enable", "sbn_profile_reset", "sbn_profile_dump",
 ]
 

@@ -20,7 +20,13 @@ sbn_status check_float_dtype(const char* fn, const char* name, sbn_dtype d) {
   return SBN_OK;
 }
 
-int bytes_of(sbn_dtype d) { return d == SBN_F32 ? 4 : 2; }
+sbn_status check_head_grad_dtype(const char* fn, const char* name, sbn_dtype d) {
+  if (d != SBN_BF16 && d != SBN_F32 && d != SBN_F32_FINE)
+    return fail(SBN_ERR_DTYPE, "%s: %s = %d must be SBN_BF16, SBN_F32 or SBN_F32_FINE", fn, name, (int)d);
+  return SBN_OK;
+}
+
+int bytes_of(sbn_dtype d) { return d == SBN_BF16 ? 2 : 4; }
 
 // vectors that are read and written one element at a time
 #define SBN_ELEM_ALIGNED(p, bytes)                                                                       \
@@ -250,8 +256,8 @@ sbn_status sbn_cross_entropy_backward(const uint16_t* X, int64_t ldx, const uint
                                       void* stream) {
   const char* fn = "sbn_cross_entropy_backward";
   SBN_TRY(check_ce(fn, X, ldx, W, ldw, labels, label_bytes, T, V, K));
-  SBN_TRY(check_float_dtype(fn, "dxdt", dxdt));
-  SBN_TRY(check_float_dtype(fn, "dwdt", dwdt));
+  SBN_TRY(check_head_grad_dtype(fn, "dxdt", dxdt));
+  SBN_TRY(check_head_grad_dtype(fn, "dwdt", dwdt));
   if (dX && T > 0) SBN_TRY(check_ld("lddx", lddx, K, T));
   if (dW) SBN_TRY(check_ld("lddw", lddw, K, V));
   SBN_ALIGNED(dX);
@@ -274,7 +280,7 @@ sbn_status sbn_cross_entropy_backward(const uint16_t* X, int64_t ldx, const uint
   SBN_TRY(check_finite(fn, "W", W, V, K, ldw, 2, st));
   SBN_TRY(check_finite(fn, "dloss", dloss, 1, T, T, 4, st));
   return hip_result(launch_ce_backward(X, ldx, W, ldw, labels, label_bytes == 8, lse, dloss, T, V, K, dX,
-                                       dxdt == SBN_F32, lddx, dW, dwdt == SBN_F32, lddw, ws, st),
+                                       dxdt, lddx, dW, dwdt, lddw, ws, st),
                     st, fn);
 }
 

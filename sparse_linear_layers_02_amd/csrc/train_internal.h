@@ -69,8 +69,8 @@ hipError_t launch_ce(const uint16_t* X, int64_t ldx, const uint16_t* W, int64_t 
                      hipStream_t st);
 hipError_t launch_ce_backward(const uint16_t* X, int64_t ldx, const uint16_t* W, int64_t ldw, const void* labels,
                               bool labels64, const float* lse, const float* dloss, int64_t T, int64_t V, int64_t K,
-                              void* dX, bool dx_f32, int64_t lddx, void* dW, bool dw_f32, int64_t lddw, void* ws,
-                              hipStream_t st);
+                              void* dX, sbn_dtype dxdt, int64_t lddx, void* dW, sbn_dtype dwdt, int64_t lddw,
+                              void* ws, hipStream_t st);
 // rows x len elements of `elem_bytes` at row stride ld, all set to 0
 hipError_t launch_zero_rows(void* p, int64_t rows, int64_t len, int64_t ld, int elem_bytes, hipStream_t st);
 

@@ -14,7 +14,7 @@ import os
 import re
 import sys
 
-from . import _SIGNATURES, _WS, SBN_BF16, SBN_F32, PKG_DIR, SbnError, _check, _req, lib
+from . import _SIGNATURES, _WS, SBN_BF16, SBN_F32, SBN_F32_FINE, PKG_DIR, SbnError, _check, _req, lib
 
 TRAIN_HEADER_PATH = os.path.join(os.path.dirname(PKG_DIR), "include", "sbn_train.h")
 SBN_ADAMW_BLOCK = 256
@@ -290,17 +290,19 @@ def sbn_cross_entropy_backward(X, W, labels, lse, dloss, *, dxdt: int = SBN_BF16
                                dW=None, need_dX: bool = True, need_dW: bool = True, ws=None, stream=None):
     """Gradients of the hidden states and of the head's weights from the
     forward's lse and dloss [T], the gradient of each token's loss (float32).
+    SBN_F32_FINE: float32, from logit gradients of 16 bits instead of 8, at
+    twice the time of that gradient's product.
     Returns (dX, dW), each None where it is not needed."""
     fn = "sbn_cross_entropy_backward"
     torch = _torch()
     T, V, K, lb = _head_args(fn, X, W, labels)
     _vector(lse, "lse", T, torch.float32, X.device, fn)
     _vector(dloss, "dloss", T, torch.float32, X.device, fn)
-    types = {SBN_BF16: torch.bfloat16, SBN_F32: torch.float32}
+    types = {SBN_BF16: torch.bfloat16, SBN_F32: torch.float32, SBN_F32_FINE: torch.float32}
 
     def out(t, name, need, dt, like):
         if dt not in types:
-            raise SbnError(fn, 6, f"{name}'s type must be SBN_BF16 or SBN_F32, got {dt}")
+            raise SbnError(fn, 6, f"{name}'s type must be SBN_BF16, SBN_F32 or SBN_F32_FINE, got {dt}")
         if not need:
             return None
         if t is None:
