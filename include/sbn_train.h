@@ -22,7 +22,7 @@
  * launch geometry from run to run: there are no atomics, every sum has a fixed
  * order.  Inputs with NaN or Inf are outside the contract; with
  * SBN_CHECK_FINITE=1 the norm and cross entropy calls scan X, residual, gain,
- * W, dY, dH and dloss as sbn.h describes.
+ * W, dY, H, dH and dloss (of the tokens with a target) as sbn.h describes.
  */
 #ifndef SBN_TRAIN_H
 #define SBN_TRAIN_H

@@ -51,17 +51,29 @@ sbn_status ok() {
 // SBN_CHECK_FINITE=1: entry points scan their floating-point inputs for
 // NaN / Inf first (read on every call, so a process can switch it).  Skipped
 // while the stream is being captured: the scan reads a flag back to the host.
-sbn_status check_finite(const char* fn, const char* what, const void* x, int64_t rows, int64_t cols, int64_t ld,
-                        int elem_bytes, hipStream_t st) {
+template <class Scan>
+static sbn_status check_scan(const char* fn, const char* what, hipStream_t st, Scan scan) {
   const char* env = std::getenv("SBN_CHECK_FINITE");
   if (!(env && env[0] == '1')) return SBN_OK;
   hipStreamCaptureStatus cs = hipStreamCaptureStatusNone;
   if (hipStreamIsCapturing(st, &cs) != hipSuccess || cs != hipStreamCaptureStatusNone) return SBN_OK;
   bool found = false;
-  const hipError_t e = scan_nonfinite(x, rows, cols, ld, elem_bytes, st, &found);
+  const hipError_t e = scan(&found);
   if (e != hipSuccess) return fail(SBN_ERR_HIP, "%s: finite check of %s: %s", fn, what, hipGetErrorString(e));
   if (found) return fail(SBN_ERR_VALUE, "%s: %s holds a NaN or Inf (SBN_CHECK_FINITE)", fn, what);
   return SBN_OK;
+}
+
+sbn_status check_finite(const char* fn, const char* what, const void* x, int64_t rows, int64_t cols, int64_t ld,
+                        int elem_bytes, hipStream_t st) {
+  return check_scan(fn, what, st,
+                    [=](bool* found) { return scan_nonfinite(x, rows, cols, ld, elem_bytes, st, found); });
+}
+
+sbn_status check_finite_tokens(const char* fn, const char* what, const float* x, const void* labels, bool labels64,
+                               int64_t V, int64_t T, hipStream_t st) {
+  return check_scan(fn, what, st,
+                    [=](bool* found) { return scan_nonfinite_tokens(x, labels, labels64, V, T, st, found); });
 }
 
 sbn_status hip_result(hipError_t e, hipStream_t st, const char* what) {

@@ -14,6 +14,9 @@ sbn_status ok();
 // SBN_CHECK_FINITE=1: SBN_ERR_VALUE if `x` holds a NaN or Inf (see sbn.h).
 sbn_status check_finite(const char* fn, const char* what, const void* x, int64_t rows, int64_t cols, int64_t ld,
                         int elem_bytes, hipStream_t st);
+// The same for a value per token, of the tokens whose label is in [0, V).
+sbn_status check_finite_tokens(const char* fn, const char* what, const float* x, const void* labels, bool labels64,
+                               int64_t V, int64_t T, hipStream_t st);
 // The status of the launches of one entry point.
 sbn_status hip_result(hipError_t e, hipStream_t st, const char* what);
 
