@@ -15,8 +15,8 @@
 //
 // Gradients, per piece of the vocabulary: the same product with an epilogue
 // that writes D in bf16; dX and dW are then two more products, on D and W and on
-// D and X as they lie.  The workspace holds one piece of D, of at most D_ELEMS
-// elements.  For a gradient of type SBN_F32_FINE the epilogue also writes what
+// D and X as they lie.  The workspace holds one piece of D, of D_ELEMS elements
+// at most (of up to 2^20 tokens).  For a gradient of type SBN_F32_FINE the epilogue also writes what
 // the rounding to bf16 left of D, in bf16, and its product is added.  (Error
 // against 64 bits, 300 tokens of 2500 entries, K = 256: relative 1.4e-3
 // -> 2.0e-6; both gradients of 8192 tokens of 65536 entries, K = 4096: 9.6 -> 16.8 ms.)
@@ -35,6 +35,7 @@ constexpr int BK = 64;                              // contraction entries of on
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 constexpr float NONE = -1.0e38f * LOG2E;            // the (scaled) maximum of no logits: finite, so that NONE - NONE is 0
 // Elements of D in the workspace, 512 MB.  (Half: 1 to 3.5% slower at 4096 to 8192 tokens, dX summed over more pieces; twice: 1% either way.)
+// A piece has at least 256 entries: above 2^20 tokens D has 256 elements a token instead.
 constexpr int64_t D_ELEMS = int64_t(1) << 28;
 constexpr int GMAX_WAVE = 1024;                     // tokens whose largest |dloss| a wave finds in two rounds of loads
 constexpr int CUS = 256;
@@ -613,43 +614,47 @@ __global__ __launch_bounds__(64 * WA * WB, 1) void ce_gemm_kernel(GemmArgs P) {
 // lse and loss of a token from its groups' (maximum, sum): 16 tokens a block, 64
 // threads a token take every 64th group each, then the 64 pairs are joined in a
 // tree.  (64 tokens a block and 16 threads a token took 31 us for 17 tokens of
-// 50001 entries: one block, whose loads wait for each other.)
+// 50001 entries: one block, whose loads wait for each other.)  Tokens beyond the
+// grid are taken in further rounds: of 2^26 tokens, 64 threads each would be 2^32,
+// more than a launch runs.
 __global__ __launch_bounds__(1024) void ce_join_kernel(const float2* __restrict__ stats, int groups, int T,
                                                        const void* __restrict__ labels, bool labels64, int V,
                                                        const float* __restrict__ target, float* __restrict__ loss,
                                                        float* __restrict__ lse) {
   __shared__ float2 sm[64][17];
   const int tl = threadIdx.x & 15, part = threadIdx.x >> 4;
-  const int t = blockIdx.x * 16 + tl;
   auto join = [](float2 a, float2 b) {
     const float top = fmaxf(a.x, b.x);
     return make_float2(top, a.y * __builtin_amdgcn_exp2f(a.x - top) + b.y * __builtin_amdgcn_exp2f(b.x - top));
   };
-  float2 a = make_float2(NONE, 0.0f);
-  if (t < T) {
-    constexpr int AHEAD = 8;
-    for (int g = part; g < groups; g += 64 * AHEAD) {
-      float2 x[AHEAD];
+  for (int t0 = blockIdx.x * 16; t0 < T; t0 += gridDim.x * 16) {
+    const int t = t0 + tl;
+    float2 a = make_float2(NONE, 0.0f);
+    if (t < T) {
+      constexpr int AHEAD = 8;
+      for (int g = part; g < groups; g += 64 * AHEAD) {
+        float2 x[AHEAD];
 #pragma unroll
-      for (int k = 0; k < AHEAD; ++k)
-        x[k] = g + 64 * k < groups ? stats[(int64_t)(g + 64 * k) * T + t] : make_float2(NONE, 0.0f);
+        for (int k = 0; k < AHEAD; ++k)
+          x[k] = g + 64 * k < groups ? stats[(int64_t)(g + 64 * k) * T + t] : make_float2(NONE, 0.0f);
 #pragma unroll
-      for (int k = 0; k < AHEAD; ++k) a = join(a, x[k]);
+        for (int k = 0; k < AHEAD; ++k) a = join(a, x[k]);
+      }
     }
-  }
-  sm[part][tl] = a;
-  __syncthreads();
-#pragma unroll
-  for (int d = 32; d >= 1; d >>= 1) {
-    if (part < d) sm[part][tl] = join(sm[part][tl], sm[part + d][tl]);
+    sm[part][tl] = a;
     __syncthreads();
-  }
-  if (part == 0 && t < T) {
-    a = sm[0][tl];
-    const float l = a.x * LN2 + logf(a.y);
-    const int64_t y = label_at(labels, labels64, t);
-    lse[t] = l;
-    loss[t] = y >= 0 && y < V ? l - target[t] : 0.0f;
+#pragma unroll
+    for (int d = 32; d >= 1; d >>= 1) {
+      if (part < d) sm[part][tl] = join(sm[part][tl], sm[part + d][tl]);
+      __syncthreads();
+    }
+    if (part == 0 && t < T) {                        // the threads that write these places in the next round
+      a = sm[0][tl];
+      const float l = a.x * LN2 + logf(a.y);
+      const int64_t y = label_at(labels, labels64, t);
+      lse[t] = l;
+      loss[t] = y >= 0 && y < V ? l - target[t] : 0.0f;
+    }
   }
 }
 
@@ -848,7 +853,8 @@ hipError_t launch_ce(const uint16_t* X, int64_t ldx, const uint16_t* W, int64_t 
   P.stats = (float2*)((uint8_t*)ws + align256((size_t)T * sizeof(float)));
   const hipError_t e = gemm<EPI_STATS>("ce_logits", stats_tile(T, V, K), P, st);
   if (e != hipSuccess) return e;
-  SBN_LAUNCH("ce_join", ce_join_kernel, dim3((unsigned)cdiv(T, 16)), dim3(1024), 0, st, P.stats,
+  constexpr int64_t JOIN_BLOCKS = 1 << 20;
+  SBN_LAUNCH("ce_join", ce_join_kernel, dim3((unsigned)(T < 16 * JOIN_BLOCKS ? cdiv(T, 16) : JOIN_BLOCKS)), dim3(1024), 0, st, P.stats,
              (int)stats_groups(T, V, K), (int)T, labels, labels64, (int)V, P.target, loss, lse);
   return hipGetLastError();
 }
