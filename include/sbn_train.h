@@ -110,8 +110,8 @@ sbn_status sbn_rmsnorm_backward(const void* dY, int64_t lddy, const void* H, int
  *   labels [T] int64 (label_bytes = 8) or int32 (4)
  *   loss, lse  [T] float                                            (out)
  *   ws     sbn_cross_entropy_workspace_bytes(T, V, K) bytes, no initialisation
- * K is a multiple of 64 (as the layer's); 0 <= T < 2^27, 1 <= V < 2^31; T*K and
- * V*K < 2^37, ceil(T/64) * ceil(V/128) < 2^24; ldx, ldw <= 2^22.
+ * K is a multiple of 64 (as the layer's); 0 <= T < 2^27, 1 <= V <= 2^31 - 256;
+ * T*K and V*K < 2^37, ceil(T/64) * ceil(V/128) < 2^24; ldx, ldw <= 2^22.
  */
 sbn_status sbn_cross_entropy_workspace_bytes(int64_t T, int64_t V, int64_t K, size_t* bytes);
 sbn_status sbn_cross_entropy(const uint16_t* X, int64_t ldx, const uint16_t* W, int64_t ldw, const void* labels,

@@ -12,6 +12,7 @@ namespace {
 
 constexpr int64_t CE_LD_MAX = int64_t(1) << 22;   // row strides of X and W: 256 rows stay within 32-bit byte offsets
 constexpr int64_t CE_T_MAX = int64_t(1) << 27;
+constexpr int64_t CE_V_MAX = (int64_t(1) << 31) - 256;   // whole tiles of 256 entries end below 2^31
 constexpr int64_t I32_MAX = (int64_t(1) << 31) - 1;
 
 sbn_status check_float_dtype(const char* fn, const char* name, sbn_dtype d) {
@@ -88,7 +89,7 @@ sbn_status check_ce_shape(const char* fn, int64_t T, int64_t V, int64_t K) {
   SBN_TRY(check_t0(fn, T));
   SBN_TRY(check_rows("V", V));
   SBN_TRY(check_k(K));
-  if (V > I32_MAX) return fail(SBN_ERR_SHAPE, "%s: V = %lld must be < 2^31", fn, (long long)V);
+  if (V > CE_V_MAX) return fail(SBN_ERR_SHAPE, "%s: V = %lld must be <= 2^31 - 256", fn, (long long)V);
   SBN_TRY(check_numel(fn, "W (V*K)", V, K));
   if (T > 0) {
     SBN_TRY(check_numel(fn, "X (T*K)", T, K));
