@@ -4,7 +4,9 @@ head, and AdamW over many tensors.
 
 As in the package's own module: layouts that the C ABI cannot see are checked
 here, outputs and workspaces are allocated with PyTorch where the caller passed
-none, everything else happens in the HIP kernels.
+none, everything else happens in the HIP kernels.  A call that is given a
+`stream` runs as inside ``torch.cuda.stream(stream)``: outputs and workspaces
+that it allocates are that stream's.
 """
 from __future__ import annotations
 
@@ -114,22 +116,28 @@ def _addr(t):
     return None if t is None else t.data_ptr()
 
 
-def _raw_stream(stream, device) -> int:
-    """The HIP stream to launch on: `stream`, or the current one of the tensors' device."""
+def _on(stream, call, args):
+    """`call` with `args` (its parameters by name) while `stream` is current: what it
+    allocates then belongs to that stream, whose earlier work alone has to be done."""
+    args["stream"] = None
+    with _torch().cuda.stream(stream):
+        return call(**args)
+
+
+def _raw_stream(device) -> int:
+    """The HIP stream to launch on: the current one of the tensors' device."""
     if device.index is None:
         raise SbnError("stream", 2, f"the tensors must be on a GPU, not on {device}")
-    if stream is not None:
-        return stream.cuda_stream
     return _torch()._C._cuda_getCurrentRawStream(device.index)   # torch.cuda.current_stream() without its Stream object
 
 
-def _scratch(kind: str, nbytes: int, device, stream, raw: int):
-    """The package's grow-only workspace of (kind, device, stream)."""
+def _scratch(kind: str, nbytes: int, device, raw: int):
+    """The package's grow-only workspace of (kind, device, the device's current stream)."""
     key = (kind, device, raw)
     buf = _WS.get(key)
     if buf is None or buf.numel() < nbytes:
         torch = _torch()
-        with torch.cuda.stream(torch.cuda.current_stream(device) if stream is None else stream):
+        with torch.cuda.device(device):
             buf = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
         _WS[key] = buf
     return buf
@@ -161,6 +169,8 @@ def _norm_args(fn, X, gain, residual, H, rstd):
 def sbn_rmsnorm(X, gain, *, residual=None, eps: float = 1e-6, H=None, Y=None, rstd=None, stream=None):
     """h = X + residual and its RMS norm Y = h * rstd * gain, X [T, K] bf16 or
     float32.  Returns (Y, H, rstd); H is X itself without a residual."""
+    if stream is not None:
+        return _on(stream, sbn_rmsnorm, locals())
     fn = "sbn_rmsnorm"
     dt, gdt, T, K, H, rstd = _norm_args(fn, X, gain, residual, H, rstd)
     if Y is None:
@@ -170,7 +180,7 @@ def sbn_rmsnorm(X, gain, *, residual=None, eps: float = 1e-6, H=None, Y=None, rs
     if T:
         _check(fn, _so().sbn_rmsnorm(X.data_ptr(), _ld(X), _addr(residual), 0 if residual is None else _ld(residual),
                                      dt, gain.data_ptr(), gdt, T, K, eps, _addr(H), 0 if H is None else _ld(H),
-                                     Y.data_ptr(), _ld(Y), rstd.data_ptr(), _raw_stream(stream, X.device)))
+                                     Y.data_ptr(), _ld(Y), rstd.data_ptr(), _raw_stream(X.device)))
     return Y, X if H is None else H, rstd
 
 
@@ -178,6 +188,8 @@ def sbn_rmsnorm_quant(X, gain, *, residual=None, eps: float = 1e-6, H=None, Xq=N
     """The norm of h = X + residual as the layer's activations: per-token absmax
     int8 codes Xq and scales s_x.  Returns (Xq, s_x, H, rstd); H is X itself
     without a residual."""
+    if stream is not None:
+        return _on(stream, sbn_rmsnorm_quant, locals())
     fn = "sbn_rmsnorm_quant"
     torch = _torch()
     dt, gdt, T, K, H, rstd = _norm_args(fn, X, gain, residual, H, rstd)
@@ -195,7 +207,7 @@ def sbn_rmsnorm_quant(X, gain, *, residual=None, eps: float = 1e-6, H=None, Xq=N
         _check(fn, _so().sbn_rmsnorm_quant(X.data_ptr(), _ld(X), _addr(residual),
                                            0 if residual is None else _ld(residual), dt, gain.data_ptr(), gdt, T, K,
                                            eps, _addr(H), 0 if H is None else _ld(H), Xq.data_ptr(), s_x.data_ptr(),
-                                           rstd.data_ptr(), _raw_stream(stream, X.device)))
+                                           rstd.data_ptr(), _raw_stream(X.device)))
     return Xq, s_x, X if H is None else H, rstd
 
 
@@ -211,6 +223,8 @@ def sbn_rmsnorm_backward(dY, H, gain, rstd, *, dH=None, dX=None, dgain=None, ws=
     """Gradient of sbn_rmsnorm and sbn_rmsnorm_quant from the forward's H and
     rstd; dH is the gradient that reaches h along the residual stream.
     Returns (dX, dgain): dX is the gradient of X and of the residual alike."""
+    if stream is not None:
+        return _on(stream, sbn_rmsnorm_backward, locals())
     fn = "sbn_rmsnorm_backward"
     torch = _torch()
     _matrix(H, "H", fn)
@@ -229,9 +243,9 @@ def sbn_rmsnorm_backward(dY, H, gain, rstd, *, dH=None, dX=None, dgain=None, ws=
         dgain = H.new_empty(K, dtype=torch.float32)
     else:
         _vector(dgain, "dgain", K, torch.float32, H.device, fn)
-    raw = _raw_stream(stream, H.device)
+    raw = _raw_stream(H.device)
     if ws is None:
-        ws = _scratch("rmsnorm_backward", _norm_scratch_bytes(T, K), H.device, stream, raw)
+        ws = _scratch("rmsnorm_backward", _norm_scratch_bytes(T, K), H.device, raw)
     _check(fn, _so().sbn_rmsnorm_backward(dY.data_ptr(), _ld(dY), H.data_ptr(), _ld(H), _addr(dH),
                                           0 if dH is None else _ld(dH), dt, gain.data_ptr(), gdt, rstd.data_ptr(), T, K,
                                           dX.data_ptr(), _ld(dX), dgain.data_ptr(), ws.data_ptr(), ws.numel(), raw))
@@ -267,6 +281,8 @@ def sbn_cross_entropy(X, W, labels, *, loss=None, lse=None, ws=None, stream=None
     """Per-token softmax cross entropy of the logits X W^T, X [T, K] and W
     [V, K] bf16, labels [T] int64 or int32 (outside [0, V): no target, loss 0).
     Returns (loss, lse), float32 [T]; the mean over tokens is the caller's."""
+    if stream is not None:
+        return _on(stream, sbn_cross_entropy, locals())
     fn = "sbn_cross_entropy"
     torch = _torch()
     T, V, K, lb = _head_args(fn, X, W, labels)
@@ -278,9 +294,9 @@ def sbn_cross_entropy(X, W, labels, *, loss=None, lse=None, ws=None, stream=None
         lse = X.new_empty(T, dtype=torch.float32)
     else:
         _vector(lse, "lse", T, torch.float32, X.device, fn)
-    raw = _raw_stream(stream, X.device)
+    raw = _raw_stream(X.device)
     if ws is None:
-        ws = _scratch("cross_entropy", sbn_cross_entropy_workspace_bytes(T, V, K), X.device, stream, raw)
+        ws = _scratch("cross_entropy", sbn_cross_entropy_workspace_bytes(T, V, K), X.device, raw)
     _check(fn, _so().sbn_cross_entropy(X.data_ptr(), _ld(X), W.data_ptr(), _ld(W), labels.data_ptr(), lb, T, V, K,
                                        loss.data_ptr(), lse.data_ptr(), ws.data_ptr(), ws.numel(), raw))
     return loss, lse
@@ -293,6 +309,8 @@ def sbn_cross_entropy_backward(X, W, labels, lse, dloss, *, dxdt: int = SBN_BF16
     SBN_F32_FINE: float32, from logit gradients of 16 bits instead of 8, at
     twice the time of that gradient's product.
     Returns (dX, dW), each None where it is not needed."""
+    if stream is not None:
+        return _on(stream, sbn_cross_entropy_backward, locals())
     fn = "sbn_cross_entropy_backward"
     torch = _torch()
     T, V, K, lb = _head_args(fn, X, W, labels)
@@ -316,9 +334,9 @@ def sbn_cross_entropy_backward(X, W, labels, lse, dloss, *, dxdt: int = SBN_BF16
 
     dX = out(dX, "dX", need_dX, dxdt, X)
     dW = out(dW, "dW", need_dW, dwdt, W)
-    raw = _raw_stream(stream, X.device)
+    raw = _raw_stream(X.device)
     if ws is None:
-        ws = _scratch("cross_entropy_backward", sbn_cross_entropy_workspace_bytes(T, V, K, True), X.device, stream, raw)
+        ws = _scratch("cross_entropy_backward", sbn_cross_entropy_workspace_bytes(T, V, K, True), X.device, raw)
     _check(fn, _so().sbn_cross_entropy_backward(X.data_ptr(), _ld(X), W.data_ptr(), _ld(W), labels.data_ptr(), lb,
                                                 lse.data_ptr(), dloss.data_ptr(), T, V, K, _addr(dX), dxdt,
                                                 0 if dX is None else _ld(dX), _addr(dW), dwdt,
@@ -404,6 +422,8 @@ def sbn_adamw_step(table, *, lr: float, step: int, beta1: float = 0.9, beta2: fl
     4 floats in device memory in the place of lr, 1 - beta1^step,
     1 - beta2^step and the gradients' factor 1, for steps replayed from a graph
     (lr and step are then not used, but checked)."""
+    if stream is not None:
+        return _on(stream, sbn_adamw_step, locals())
     fn = "sbn_adamw_step"
     if not isinstance(table, AdamWTable):
         raise SbnError(fn, 2, "table must be an AdamWTable")
@@ -411,10 +431,12 @@ def sbn_adamw_step(table, *, lr: float, step: int, beta1: float = 0.9, beta2: fl
         _vector(dyn, "dyn", 4, _torch().float32, table.map.device, fn)
     _check(fn, _so().sbn_adamw_step(table.entries.data_ptr(), table.map.data_ptr(), table.blocks, table.pdt, table.gdt,
                                     table.state_bits, lr, beta1, beta2, eps, step, _addr(dyn),
-                                    _raw_stream(stream, table.map.device)))
+                                    _raw_stream(table.map.device)))
 
 
 def _decode(codes, scale, second, out, stream):
+    if stream is not None:
+        return _on(stream, _decode, locals())
     fn = "sbn_adamw_decode_state"
     torch = _torch()
     n = codes.numel()
@@ -427,7 +449,7 @@ def _decode(codes, scale, second, out, stream):
         if out.numel() != n or out.device != codes.device:
             raise SbnError(fn, 2, f"out must have {n} elements on {codes.device}")
     _check(fn, _so().sbn_adamw_decode_state(codes.data_ptr(), scale.data_ptr(), n, second, out.data_ptr(),
-                                            _raw_stream(stream, codes.device)))
+                                            _raw_stream(codes.device)))
     return out
 
 
@@ -442,6 +464,8 @@ def sbn_adamw_decode_v(codes, scale, *, out=None, stream=None):
 
 
 def _encode(x, second, codes, scale, stream):
+    if stream is not None:
+        return _on(stream, _encode, locals())
     fn = "sbn_adamw_encode_state"
     torch = _torch()
     _req(x, "x", "f32", True, fn)
@@ -459,7 +483,7 @@ def _encode(x, second, codes, scale, stream):
     else:
         _vector(scale, "scale", ns, torch.float32, x.device, fn)
     _check(fn, _so().sbn_adamw_encode_state(x.data_ptr(), n, second, codes.data_ptr(), scale.data_ptr(),
-                                            _raw_stream(stream, x.device)))
+                                            _raw_stream(x.device)))
     return codes, scale
 
 
