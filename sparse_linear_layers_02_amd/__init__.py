@@ -155,7 +155,9 @@ def _stream(stream):
 # Grow-only workspaces, one per (operation, device, stream): calls that share a
 # workspace must be ordered on one stream (the ABI's rule), and a buffer is
 # allocated while its stream is current, so the caching allocator hands its
-# memory to later work on that stream only once this work is done.
+# memory to later work on that stream only once this work is done.  A call under
+# capture gets a workspace of its own from the graph's memory: the graph keeps its
+# address, which a shared buffer would not survive being replaced by a larger one.
 _WS = {}
 
 
@@ -163,7 +165,12 @@ def _workspace(kind: str, nbytes: int, device, stream):
     torch = _torch()
     if nbytes == 0:
         return None
-    s = stream if stream is not None else torch.cuda.current_stream(device)
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return _workspace(kind, nbytes, device, None)
+    if torch.cuda.is_current_stream_capturing():
+        return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
+    s = torch.cuda.current_stream(device)
     key = (kind, str(device), s.cuda_stream)
     buf = _WS.get(key)
     if buf is None or buf.numel() < nbytes:

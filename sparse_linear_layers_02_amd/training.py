@@ -132,11 +132,14 @@ def _raw_stream(device) -> int:
 
 
 def _scratch(kind: str, nbytes: int, device, raw: int):
-    """The package's grow-only workspace of (kind, device, the device's current stream)."""
+    """The package's grow-only workspace of (kind, device, the device's current stream);
+    under capture one of its own, which belongs to the graph."""
+    torch = _torch()
+    if torch._C._cuda_isCurrentStreamCapturing():
+        return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
     key = (kind, device, raw)
     buf = _WS.get(key)
     if buf is None or buf.numel() < nbytes:
-        torch = _torch()
         with torch.cuda.device(device):
             buf = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
         _WS[key] = buf
