@@ -152,13 +152,20 @@ def _stream(stream):
     return ctypes.c_void_p(s.cuda_stream)
 
 
-# Grow-only workspaces, one per (operation, device, stream): calls that share a
-# workspace must be ordered on one stream (the ABI's rule), and a buffer is
+# Grow-only workspaces, one per (operation, device, stream) and thread: calls that
+# share a workspace must be ordered on one stream (the ABI's rule), and a buffer is
 # allocated while its stream is current, so the caching allocator hands its
-# memory to later work on that stream only once this work is done.  A call under
+# memory to later work on that stream only once this work is done.  Threads share
+# none: a call is several launches, between which another thread may enqueue its
+# own on the same stream.  A thread's buffers are released as it ends.  A call under
 # capture gets a workspace of its own from the graph's memory: the graph keeps its
 # address, which a shared buffer would not survive being replaced by a larger one.
-_WS = {}
+class _Workspaces(threading.local):
+    def __init__(self):
+        self.kept = {}
+
+
+_WS = _Workspaces()
 
 
 def _workspace(kind: str, nbytes: int, device, stream):
@@ -172,11 +179,11 @@ def _workspace(kind: str, nbytes: int, device, stream):
         return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
     s = torch.cuda.current_stream(device)
     key = (kind, str(device), s.cuda_stream)
-    buf = _WS.get(key)
+    buf = _WS.kept.get(key)
     if buf is None or buf.numel() < nbytes:
         with torch.cuda.stream(s):
             buf = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
-        _WS[key] = buf
+        _WS.kept[key] = buf
     return buf
 
 

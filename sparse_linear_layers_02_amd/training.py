@@ -132,17 +132,17 @@ def _raw_stream(device) -> int:
 
 
 def _scratch(kind: str, nbytes: int, device, raw: int):
-    """The package's grow-only workspace of (kind, device, the device's current stream);
-    under capture one of its own, which belongs to the graph."""
+    """The package's grow-only workspace of (kind, device, the device's current stream)
+    of the calling thread; under capture one of its own, which belongs to the graph."""
     torch = _torch()
     if torch._C._cuda_isCurrentStreamCapturing():
         return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
     key = (kind, device, raw)
-    buf = _WS.get(key)
+    buf = _WS.kept.get(key)
     if buf is None or buf.numel() < nbytes:
         with torch.cuda.device(device):
             buf = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
-        _WS[key] = buf
+        _WS.kept[key] = buf
     return buf
 
 

@@ -62,3 +62,26 @@ def test_the_kept_workspace_grows(scratch):
     a = get(300)
     b = get(4000)
     assert b is not a and b.numel() >= 4000 and get(4000) is b and get(20) is b
+
+
+def test_threads_do_not_share_a_workspace(scratch):
+    """A call is several launches, between which another thread may enqueue its own on the same stream."""
+    import gc
+    import threading
+    import weakref
+    _, get = scratch
+    mine, seen, gone = get(1000), [], []
+
+    def other():
+        buf = get(1000)
+        seen.append(buf is mine)
+        seen.append(get(800) is buf)
+        gone.append(weakref.ref(buf))
+
+    t = threading.Thread(target=other)
+    t.start()
+    t.join()
+    assert seen == [False, True] and get(1000) is mine
+    del t
+    gc.collect()
+    assert gone[0]() is None                                       # a thread's workspaces end with it
