@@ -146,6 +146,12 @@ def _scratch(kind: str, nbytes: int, device, raw: int):
     return buf
 
 
+def _given(ws, device, fn: str):
+    """A workspace of the caller's has no gaps and is on the tensors' device."""
+    if ws.device != device or not ws.is_contiguous():
+        raise SbnError(fn, 2, f"ws must be contiguous on {device}, got {ws.device}")
+
+
 # ------------------------------------------------------------------ RMS norm
 def _norm_args(fn, X, gain, residual, H, rstd):
     torch = _torch()
@@ -246,6 +252,8 @@ def sbn_rmsnorm_backward(dY, H, gain, rstd, *, dH=None, dX=None, dgain=None, ws=
         dgain = H.new_empty(K, dtype=torch.float32)
     else:
         _vector(dgain, "dgain", K, torch.float32, H.device, fn)
+    if ws is not None:
+        _given(ws, H.device, fn)
     raw = _raw_stream(H.device)
     if ws is None:
         ws = _scratch("rmsnorm_backward", _norm_scratch_bytes(T, K), H.device, raw)
@@ -297,6 +305,8 @@ def sbn_cross_entropy(X, W, labels, *, loss=None, lse=None, ws=None, stream=None
         lse = X.new_empty(T, dtype=torch.float32)
     else:
         _vector(lse, "lse", T, torch.float32, X.device, fn)
+    if ws is not None:
+        _given(ws, X.device, fn)
     raw = _raw_stream(X.device)
     if ws is None:
         ws = _scratch("cross_entropy", sbn_cross_entropy_workspace_bytes(T, V, K), X.device, raw)
@@ -337,6 +347,8 @@ def sbn_cross_entropy_backward(X, W, labels, lse, dloss, *, dxdt: int = SBN_BF16
 
     dX = out(dX, "dX", need_dX, dxdt, X)
     dW = out(dW, "dW", need_dW, dwdt, W)
+    if ws is not None:
+        _given(ws, X.device, fn)
     raw = _raw_stream(X.device)
     if ws is None:
         ws = _scratch("cross_entropy_backward", sbn_cross_entropy_workspace_bytes(T, V, K, True), X.device, raw)
