@@ -128,7 +128,10 @@ def _raw_stream(device) -> int:
     """The HIP stream to launch on: the current one of the tensors' device."""
     if device.index is None:
         raise SbnError("stream", 2, f"the tensors must be on a GPU, not on {device}")
-    return _torch()._C._cuda_getCurrentRawStream(device.index)   # torch.cuda.current_stream() without its Stream object
+    c = _torch()._C
+    if c._cuda_getDevice() != device.index:
+        raise SbnError("stream", 2, f"the tensors are on {device}, which is not the current device")
+    return c._cuda_getCurrentRawStream(device.index)   # torch.cuda.current_stream() without its Stream object
 
 
 def _scratch(kind: str, nbytes: int, device, raw: int):
@@ -140,9 +143,7 @@ def _scratch(kind: str, nbytes: int, device, raw: int):
     key = (kind, device, raw)
     buf = _WS.kept.get(key)
     if buf is None or buf.numel() < nbytes:
-        with torch.cuda.device(device):
-            buf = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
-        _WS.kept[key] = buf
+        buf = _WS.kept[key] = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
     return buf
 
 

@@ -29,3 +29,15 @@ def test_a_workspace_is_on_the_tensors_device_and_has_no_gaps(ws):
     refused(lambda: sbn.sbn_rmsnorm_backward(z(4, 64), z(4, 64), z(64), z(4, dt=f32), ws=ws), SHAPE, "ws must be")
     refused(lambda: sbn.sbn_cross_entropy(z(4, 64), z(10, 64), y, ws=ws), SHAPE, "ws must be")
     refused(lambda: sbn.sbn_cross_entropy_backward(z(4, 64), z(10, 64), y, z(4, dt=f32), z(4, dt=f32), ws=ws), SHAPE, "ws must be")
+
+
+def test_tensors_of_a_device_that_is_not_current(monkeypatch):
+    """A launch goes to the current device: on its default stream, with another device's addresses."""
+    import types
+
+    import torch
+    from sparse_linear_layers_02_amd import training
+    fake = types.SimpleNamespace(_C=types.SimpleNamespace(_cuda_getDevice=lambda: 0, _cuda_getCurrentRawStream=lambda i: 40 + i))
+    monkeypatch.setattr(training, "_torch_module", fake)
+    assert training._raw_stream(torch.device("cuda", 0)) == 40
+    refused(lambda: training._raw_stream(torch.device("cuda", 1)), SHAPE, "cuda:1")
