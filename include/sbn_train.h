@@ -145,7 +145,8 @@ sbn_status sbn_cross_entropy_backward(const uint16_t* X, int64_t ldx, const uint
 
 /* ------------------------------------------------------------------ AdamW
  *
- * One step on `count` tensors in one launch.  Per element, in float32 and in
+ * One step on `count` tensors in one launch, so no element may be in two of
+ * the tensors that it writes.  Per element, in float32 and in
  * this order (products and sums rounded one by one):
  *   g  = grad * grad_scale
  *   m <- m * beta1 + g * (1 - beta1)

@@ -373,7 +373,8 @@ class AdamWTable:
     the states, float32 or in 8 bits (m int8, v uint8, with float32 scales, one
     per SBN_ADAMW_BLOCK elements).  `shadows`: bf16 copies of float32
     parameters, written by the step.  `weight_decay`: one number, or one per
-    tensor.  The table refers to the tensors' memory and keeps them alive."""
+    tensor.  No element may be in two of the tensors that the step writes.  The
+    table refers to the tensors' memory and keeps them alive."""
 
     def __init__(self, params, grads, ms, vs, *, m_scales=None, v_scales=None, shadows=None, weight_decay=0.0):
         torch = _torch()
@@ -399,6 +400,7 @@ class AdamWTable:
         self.pdt, self.gdt = _dtype(params[0], "params[0]", fn), _dtype(grads[0], "grads[0]", fn)
         mt, vt = (torch.int8, torch.uint8) if self.state_bits == 8 else (torch.float32, torch.float32)
         entries = (_AdamWEntry * count)()
+        spans = []                                   # [first, past the last) byte, whether written, name
 
         def put(t, name, i, dtype, n, shape=None):
             if t is None:
@@ -407,6 +409,8 @@ class AdamWTable:
                 raise SbnError(fn, 6, f"{name}[{i}] must be {dtype}, got {t.dtype}")
             if t.numel() != n or t.device != dev or not t.is_contiguous():
                 raise SbnError(fn, 2, f"{name}[{i}] must be contiguous, with {n} elements on {dev}")
+            if n:
+                spans.append((t.data_ptr(), t.data_ptr() + n * t.element_size(), name != "grads", f"{name}[{i}]"))
             return t.data_ptr()
 
         for i in range(count):
@@ -419,6 +423,15 @@ class AdamWTable:
             e.v_scale = put(lists["v_scales"][i], "v_scales", i, torch.float32, ns)
             e.shadow = put(lists["shadows"][i], "shadows", i, torch.bfloat16, n)
             e.n, e.weight_decay = n, wds[i]
+        read = written = (0, 0, False, "")           # of the spans so far, the one that reaches furthest
+        for s in sorted(spans, key=lambda s: s[:2]):
+            with_ = written if s[0] < written[1] else read if s[2] and s[0] < read[1] else None
+            if with_:
+                raise SbnError(fn, 2, f"{with_[3]} and {s[3]} share memory that the step writes")
+            if s[2]:
+                written = max(written, s, key=lambda s: s[1])
+            else:
+                read = max(read, s, key=lambda s: s[1])
         blocks = _i64()
         plan = _so().sbn_adamw_plan
         _check("sbn_adamw_plan", plan(entries, count, self.pdt, self.gdt, self.state_bits, None, ctypes.byref(blocks)))

@@ -41,3 +41,26 @@ def test_tensors_of_a_device_that_is_not_current(monkeypatch):
     monkeypatch.setattr(training, "_torch_module", fake)
     assert training._raw_stream(torch.device("cuda", 0)) == 40
     refused(lambda: training._raw_stream(torch.device("cuda", 1)), SHAPE, "cuda:1")
+
+
+def test_a_table_writes_each_element_once():
+    """All tensors of a step are updated in one launch: memory that two of them share, such as a weight
+    listed twice, would be updated by blocks that race."""
+    import torch
+    v = lambda n: torch.zeros(n)  # noqa: E731
+    w, buf = v(1000), v(4000)
+    two = lambda p, g, m, s, **kw: (lambda: sbn.AdamWTable(p, g, m, s, **kw))  # noqa: E731
+    refused(two([w, w], [v(1000), v(1000)], [v(1000), v(1000)], [v(1000), v(1000)]), SHAPE, "params[1]")
+    refused(two([buf[:1000], buf[996:1996]], [v(1000), v(1000)], [v(1000), v(1000)], [v(1000), v(1000)]), SHAPE, "share")
+    refused(two([v(1000), v(1000)], [v(1000), v(1000)], [w, v(1000)], [v(1000), w]), SHAPE, "share")
+    refused(two([w], [v(1000)], [v(1000)], [w]), SHAPE, "share")
+    refused(two([buf[:2000], v(8)], [v(2000), buf[1000:1008]], [v(2000), v(8)], [v(2000), v(8)]), SHAPE, "grads[1]")
+    s = torch.zeros(4, dtype=torch.bfloat16)
+    refused(two([v(4), v(4)], [v(4), v(4)], [v(4), v(4)], [v(4), v(4)], shadows=[s, s]), SHAPE, "shadows[1]")
+    c, d = torch.zeros(8, dtype=torch.int8), torch.zeros(8, dtype=torch.uint8)
+    sc = v(1)
+    refused(two([v(8)], [v(8)], [c], [d], m_scales=[sc], v_scales=[sc]), SHAPE, "v_scales[0]")
+    # neighbours in one buffer, one gradient for two parameters, empty tensors anywhere
+    g, e = v(1000), buf[24:24]
+    t = sbn.AdamWTable([buf[:1000], buf[1000:2000], e], [g, g, e], [buf[2000:3000], v(1000), e], [buf[3000:], v(1000), e])
+    assert t.blocks == 2
