@@ -161,9 +161,11 @@ sbn_status sbn_cross_entropy_backward(const uint16_t* X, int64_t ldx, const uint
  * magnitude, 0 if that is under 2^-100.  A code c stands for
  *   m: s * (c/127) * |c/127|, int8 in [-127, 127]: c = rint(127 sqrt(|m|/s)), with m's sign
  *   v: s * (c/255)^4,         uint8:               c = rint(255 (v/s)^(1/4)), at least 1 where v > 0
- * both finer towards zero than at the block's largest value; v > 0 never
- * becomes 0, which its place under a quotient could not bear.  The step uses
- * the new m and v before they are rounded to codes.
+ * both finer towards zero than at the block's largest value.  In a block with
+ * a scale, v > 0 never becomes 0, which its place under a quotient could not
+ * bear; where v's scale is 0 (gradients under some 2^-50, whose squares are
+ * too small) the step takes the block's m as 0 as well, and so forgets its
+ * momentum.  The step uses the new m and v before they are rounded to codes.
  */
 #define SBN_ADAMW_BLOCK 256
 
@@ -192,8 +194,10 @@ sbn_status sbn_adamw_plan(const sbn_adamw_entry* entries, int64_t count, sbn_dty
 
 /*
  * The step, with `entries` and `map` in DEVICE memory as sbn_adamw_plan
- * accepted and wrote them (blocks = 0: nothing to do).  0 <= beta < 1, lr,
- * eps >= 0 finite, step >= 1.  `dyn`, if not NULL, is 4 floats in device
+ * accepted and wrote them (blocks = 0: nothing to do).  0 <= beta < 1, lr
+ * finite, eps >= 0 finite, and with 8-bit states > 0 (as float32), step >= 1.
+ * With eps = 0 an element whose v is 0 becomes the quotient by 0 that the
+ * formula says (Inf, or NaN where m is 0 too).  `dyn`, if not NULL, is 4 floats in device
  * memory that take the place of host values, for steps replayed from a graph:
  * lr, 1 - beta1^step, 1 - beta2^step, grad_scale (1 without dyn).
  */

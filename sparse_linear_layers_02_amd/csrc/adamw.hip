@@ -166,7 +166,8 @@ __device__ inline float encode8(const float* v, int* c) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const float r = rintf(q[i]);
-    c[i] = (int)(SECOND ? (y[i] > 0.0f ? fmaxf(r, 1.0f) : r) : copysignf(r, v[i]));
+    // v > 0, not y > 0: the quotient may underflow
+    c[i] = (int)(SECOND ? (v[i] > 0.0f && s > 0.0f ? fmaxf(r, 1.0f) : r) : copysignf(r, v[i]));
   }
   return s;
 }
@@ -211,6 +212,7 @@ __global__ __launch_bounds__(256) void adamw_kernel(const sbn_adamw_entry* __res
   if (S8) {
     int c[8];
     unpack_codes(cm, true, c);
+    if (sv == 0.0f) sm = 0.0f;                       // nothing to divide these m by
 #pragma unroll
     for (int i = 0; i < 8; ++i) m[i] = decode_m(c[i], sm);
     unpack_codes(cv, false, c);

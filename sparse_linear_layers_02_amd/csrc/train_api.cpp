@@ -337,6 +337,8 @@ sbn_status sbn_adamw_step(const sbn_adamw_entry* entries, const int32_t* map, in
   if (!(beta1 >= 0.0 && beta1 < 1.0) || !(beta2 >= 0.0 && beta2 < 1.0))
     return fail(SBN_ERR_VALUE, "%s: beta1 and beta2 must be in [0, 1)", fn);
   if (!(eps >= 0.0) || std::isinf(eps)) return fail(SBN_ERR_VALUE, "%s: eps must be finite and >= 0", fn);
+  if (state_bits == 8 && !((float)eps > 0.0f))
+    return fail(SBN_ERR_VALUE, "%s: eps must be > 0 in float32 with 8-bit states", fn);
   if (step < 1) return fail(SBN_ERR_VALUE, "%s: step = %lld must be >= 1", fn, (long long)step);
   if (blocks < 0 || blocks >= NUMEL_MAX)
     return fail(SBN_ERR_SHAPE, "%s: blocks = %lld must be in [0, 2^37)", fn, (long long)blocks);

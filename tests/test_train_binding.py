@@ -64,3 +64,13 @@ def test_a_table_writes_each_element_once():
     g, e = v(1000), buf[24:24]
     t = sbn.AdamWTable([buf[:1000], buf[1000:2000], e], [g, g, e], [buf[2000:3000], v(1000), e], [buf[3000:], v(1000), e])
     assert t.blocks == 2
+
+
+def test_eps_of_8_bit_states():
+    """A second moment that has become 0 leaves eps alone under the quotient."""
+    import ctypes
+    P, P2 = ctypes.c_void_p(0x100000), ctypes.c_void_p(0x200000)
+    for eps in (0.0, 1e-60):
+        st = sbn.lib().sbn_adamw_step(P, P2, 3, 0, 0, 8, 1e-3, 0.9, 0.999, eps, 1, None, None)
+        assert st == sbn.SBN_ERR_VALUE and b"eps" in sbn.lib().sbn_last_error()
+    assert sbn.lib().sbn_adamw_step(P, P2, 0, 0, 0, 8, 1e-3, 0.9, 0.999, 1e-30, 1, None, None) == 0
