@@ -140,20 +140,30 @@ __device__ inline void unpack_codes(uint2 w, bool is_signed, int* c) {
   }
 }
 
+// The larger of two magnitudes by their bits, where NaN is above Inf: a maximum
+// of floats would drop a NaN.
+struct MaxMagnitude {
+  __device__ float operator()(float a, float b) const {
+    const uint32_t x = __float_as_uint(a), y = __float_as_uint(b);
+    return __uint_as_float(x > y ? x : y);
+  }
+};
+
 // scale and codes of the 8 elements v of each lane (half a wave: one block).
-// Lanes past the tensor hold zeros and take part in the maximum.
+// Lanes past the tensor hold zeros and take part in the maximum.  A NaN or Inf
+// becomes the block's scale, and its values then decode to NaN or Inf.
 template <bool SECOND>
 __device__ inline float encode8(const float* v, int* c) {
   float s = 0.0f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) s = fmaxf(s, fabsf(v[i]));
-  s = half_wave_all(s, Max{});
+  for (int i = 0; i < 8; ++i) s = MaxMagnitude{}(s, fabsf(v[i]));
+  s = half_wave_all(s, MaxMagnitude{});
   if (s < S_FLOOR) s = 0.0f;
   const float inv = s > 0.0f ? 1.0f / s : 0.0f;
   float y[8], q[8], half = 0.0f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    y[i] = fabsf(v[i]) * inv;
+    y[i] = fminf(fabsf(v[i]) * inv, 1.0f);           // a number, also of Inf by Inf
     float r = __builtin_amdgcn_sqrtf(y[i]);
     if (SECOND) r = __builtin_amdgcn_sqrtf(r);
     q[i] = (SECOND ? 255.0f : 127.0f) * r;
