@@ -102,7 +102,7 @@ __device__ inline void store8(gchar* p, int n, const float* v) {
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        if (i < n) q[i] = f32_to_bf16_rne(v[i]);
+        if (i < n) q[i] = (uint16_t)pack_bf16x2(v[i], 0.0f);   // as above, so that NaN stays NaN
     }
   }
 }

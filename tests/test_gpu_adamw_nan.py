@@ -1,5 +1,6 @@
 """NaN and Inf in a gradient are outside the contract, but they show: with 8-bit states
-the block's moments stop being finite, as they do where the scale is the plain maximum."""
+the block's moments stop being finite, as they do where the scale is the plain maximum,
+and neither is a NaN of a parameter lost where it is rounded to bf16."""
 from __future__ import annotations
 
 import pytest
@@ -39,3 +40,16 @@ def test_step(bad):
     assert torch.isnan(p[at]) and torch.isfinite(p).sum() == n - 1
     for x in (sbn.sbn_adamw_decode_m(m, sm), sbn.sbn_adamw_decode_v(v, sv)):
         assert not torch.isfinite(x[256:512]).any() and torch.isfinite(x[:256]).all() and torch.isfinite(x[512:]).all()
+
+
+@pytest.mark.parametrize("pattern", [0x7FC00000, 0x7F800001, 0x7FFFFFFF, 0xFFFFFFFF - (1 << 32)])
+@pytest.mark.parametrize("at", [3, 10])                            # among eight that are stored together, and past them
+def test_bf16_copies(at, pattern):
+    import torch
+    n = 13
+    p = torch.ones(n, device="cuda")
+    p.view(torch.int32)[at] = pattern if pattern < 2 ** 31 else pattern - 2 ** 32
+    assert torch.isnan(p[at])
+    z, sh = torch.zeros(n, device="cuda"), torch.zeros(n, dtype=torch.bfloat16, device="cuda")
+    sbn.sbn_adamw_step(sbn.AdamWTable([p], [z], [z.clone()], [z.clone()], shadows=[sh]), lr=0.1, step=1)
+    assert torch.isnan(p[at]) and torch.isnan(sh[at]) and torch.isfinite(sh).sum() == n - 1
