@@ -26,6 +26,7 @@
 // dX) or the contraction (W of dX, D and X of dW): those go through the
 // transposing LDS reads.  (Transposed copies of D, W and X in memory instead
 // took 2% of the largest training step and a quarter of one of 64 tokens.)
+#include "once_per_device.h"
 #include "train_internal.h"
 
 namespace sbn {
@@ -717,8 +718,14 @@ hipError_t run_gemm(const char* name, const GemmArgs& P, hipStream_t st) {
   constexpr int TA = WA * MI * 16, TB = WB * MJ * 16;
   constexpr size_t lds = (size_t)RING * (TA + TB) / 2 * BK * 2;
   constexpr int per_cu = (int)((160 << 10) / lds);
-  static const hipError_t e = hipFuncSetAttribute((const void*)ce_gemm_kernel<WA, WB, MI, MJ, RING, EPI, TRA, TRB>,
-                                                  hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+  static OncePerDevice once;
+  int device = 0;
+  hipError_t e = hipGetDevice(&device);
+  if (e == hipSuccess)
+    e = once(device, [] {
+      return hipFuncSetAttribute((const void*)ce_gemm_kernel<WA, WB, MI, MJ, RING, EPI, TRA, TRB>,
+                                 hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+    });
   if (e != hipSuccess) return e;
   const int64_t work = (int64_t)P.tilesA * P.tilesB * P.splits;
   SBN_LAUNCH(name, (ce_gemm_kernel<WA, WB, MI, MJ, RING, EPI, TRA, TRB>), dim3((unsigned)(work < per_cu * CUS ? work : per_cu * CUS)),
