@@ -51,8 +51,10 @@ extern "C" {
  * residual may be NULL (then H is not written and may be NULL).  With a
  * residual H is required; it may be X or residual itself (same row stride).
  * K is a multiple of 8 and at most 32768; T >= 0 (T = 0: nothing to do, and
- * pointers may be NULL); T*K < 2^37.  eps >= 0 and finite.  |h| above 2^60 is
- * outside the contract (its square has to stay finite in a sum).
+ * pointers may be NULL); T*K < 2^37.  eps >= 0 and finite; with eps = 0 a row
+ * of zeros has no norm (rstd and s_x are Inf, y is NaN, codes are 0).  The sum
+ * of a row's squares has to stay below 2^128, which holds for all
+ * |h| <= 2^56 in a row of 32768; squares of |h| < 2^-75 count as 0.
  */
 #define SBN_RMSNORM_MAX_K 32768
 
