@@ -713,6 +713,13 @@ struct TileShape {
 };
 constexpr TileShape SHAPE[] = {{256, 256}, {128, 128}, {128, 64}};
 
+// a product's launches, named by what they compute and their tile shape
+using Names = const char* const[3];
+#define SBN_TILE_NAMES(what) {what "_wide", what "_square", what "_flat"}
+constexpr Names LOGITS = SBN_TILE_NAMES("ce_logits"), DLOGITS = SBN_TILE_NAMES("ce_dlogits"),
+                DX = SBN_TILE_NAMES("ce_dx"), DW = SBN_TILE_NAMES("ce_dw");
+#undef SBN_TILE_NAMES
+
 template <int WA, int WB, int MI, int MJ, int RING, int EPI, bool TRA, bool TRB>
 hipError_t run_gemm(const char* name, const GemmArgs& P, hipStream_t st) {
   constexpr int TA = WA * MI * 16, TB = WB * MJ * 16;
@@ -734,9 +741,10 @@ hipError_t run_gemm(const char* name, const GemmArgs& P, hipStream_t st) {
 }
 
 template <int EPI, bool TRA = false, bool TRB = false>
-hipError_t gemm(const char* name, Tile tile, GemmArgs& P, hipStream_t st) {
+hipError_t gemm(Names& names, Tile tile, GemmArgs& P, hipStream_t st) {
   P.tilesA = (int)cdiv(P.nA, SHAPE[tile].a);
   P.tilesB = (int)cdiv(P.nB, SHAPE[tile].b);
+  const char* name = names[tile];
   switch (tile) {
     case WIDE: return run_gemm<2, 4, 8, 4, 5, EPI, TRA, TRB>(name, P, st);
     case SQUARE: return run_gemm<2, 2, 4, 4, 5, EPI, TRA, TRB>(name, P, st);
@@ -821,15 +829,15 @@ CePlan ce_plan(int64_t T, int64_t V, int64_t K, bool pair) {
 
 // C [nB][ldc] = Cin + A B^T, split as P says and summed
 template <bool TRB>
-hipError_t product(const char* name, Tile tile, GemmArgs P, bool c_f32, float* part, hipStream_t st) {
+hipError_t product(Names& names, Tile tile, GemmArgs P, bool c_f32, float* part, hipStream_t st) {
   if (P.splits == 1) {
-    if (TRB && P.Cin) return gemm<EPI_ADD32, true, TRB>(name, tile, P, st);
-    return c_f32 ? gemm<EPI_OUT32, true, TRB>(name, tile, P, st) : gemm<EPI_OUT16, true, TRB>(name, tile, P, st);
+    if (TRB && P.Cin) return gemm<EPI_ADD32, true, TRB>(names, tile, P, st);
+    return c_f32 ? gemm<EPI_OUT32, true, TRB>(names, tile, P, st) : gemm<EPI_OUT16, true, TRB>(names, tile, P, st);
   }
   GemmArgs Q = P;                                    // the parts' sums side by side
   Q.C = part, Q.ldc = P.nA, Q.part_stride = (int64_t)P.nB * P.nA;
   Q.Cin = nullptr, Q.gmax = nullptr;
-  const hipError_t e = gemm<EPI_OUT32, true, TRB>(name, tile, Q, st);
+  const hipError_t e = gemm<EPI_OUT32, true, TRB>(names, tile, Q, st);
   if (e != hipSuccess) return e;
   SBN_LAUNCH("ce_sum", ce_sum_kernel, dim3((unsigned)grid_for((int64_t)P.nB * (P.nA / 4))), dim3(256), 0, st, part,
              P.splits, (int64_t)P.nB, P.nA, P.Cin, P.ldcin, P.gmax, P.C, c_f32, P.ldc);
@@ -858,7 +866,7 @@ hipError_t launch_ce(const uint16_t* X, int64_t ldx, const uint16_t* W, int64_t 
   P.labels = labels, P.labels64 = labels64, P.V = (int)V;
   P.target = (float*)ws;
   P.stats = (float2*)((uint8_t*)ws + align256((size_t)T * sizeof(float)));
-  const hipError_t e = gemm<EPI_STATS>("ce_logits", stats_tile(T, V, K), P, st);
+  const hipError_t e = gemm<EPI_STATS>(LOGITS, stats_tile(T, V, K), P, st);
   if (e != hipSuccess) return e;
   constexpr int64_t JOIN_BLOCKS = 1 << 20;
   SBN_LAUNCH("ce_join", ce_join_kernel, dim3((unsigned)(T < 16 * JOIN_BLOCKS ? cdiv(T, 16) : JOIN_BLOCKS)), dim3(1024), 0, st, P.stats,
@@ -898,7 +906,7 @@ hipError_t launch_ce_backward(const uint16_t* X, int64_t ldx, const uint16_t* W,
     G.lse = lse, G.dloss = dloss, G.gmax = gmax;
     G.D = D, G.ldd = L.piece, G.dlow = dlow, G.tpad = (int)L.tpad;
     const Tile tile = pick(nv, T, G.steps, false).tile;
-    e = pair ? gemm<EPI_GRAD_PAIR>("ce_dlogits", tile, G, st) : gemm<EPI_GRAD>("ce_dlogits", tile, G, st);
+    e = pair ? gemm<EPI_GRAD_PAIR>(DLOGITS, tile, G, st) : gemm<EPI_GRAD>(DLOGITS, tile, G, st);
     if (e != hipSuccess) return e;
     for (int low = 0; dX && low <= (int)dx_pair; ++low) {
       GemmArgs P{};
@@ -909,7 +917,7 @@ hipError_t launch_ce_backward(const uint16_t* X, int64_t ldx, const uint16_t* W,
       P.Cin = i > 0 || low > 0 ? acc : nullptr, P.ldcin = K;
       P.gmax = last ? gmax : nullptr;
       P.C = last ? dX : acc, P.ldc = last ? lddx : K;
-      if ((e = product<false>("ce_dx", L.x.tile, P, last ? dx_f32 : true, part, st)) != hipSuccess) return e;
+      if ((e = product<false>(DX, L.x.tile, P, last ? dx_f32 : true, part, st)) != hipSuccess) return e;
     }
     for (int low = 0; dW && low <= (int)dw_pair; ++low) {
       GemmArgs P{};
@@ -919,7 +927,7 @@ hipError_t launch_ce_backward(const uint16_t* X, int64_t ldx, const uint16_t* W,
       P.C = (uint8_t*)dW + v0 * lddw * (dw_f32 ? 4 : 2), P.ldc = lddw;
       P.Cin = low > 0 ? (const float*)P.C : nullptr, P.ldcin = lddw;
       P.gmax = low == (int)dw_pair ? gmax : nullptr;
-      if ((e = product<true>("ce_dw", L.w.tile, P, dw_f32, part, st)) != hipSuccess) return e;
+      if ((e = product<true>(DW, L.w.tile, P, dw_f32, part, st)) != hipSuccess) return e;
     }
   }
   return hipSuccess;
