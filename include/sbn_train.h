@@ -18,7 +18,8 @@
  * of 8, work enqueued on `stream`, arguments checked on the host
  * before anything is launched, nothing launched on an error, messages from
  * sbn_last_error(), no allocation, no synchronisation, no exception across the
- * ABI.  Every call may be captured into a HIP graph.  Results do not depend on
+ * ABI.  Tensors that a call writes overlap no other tensor of the call, except
+ * where it says that one may be in another's place.  Every call may be captured into a HIP graph.  Results do not depend on
  * launch geometry from run to run: there are no atomics, every sum has a fixed
  * order.  Inputs with NaN or Inf are outside the contract; with
  * SBN_CHECK_FINITE=1 the norm and cross entropy calls scan X, residual, gain,
@@ -49,7 +50,8 @@ extern "C" {
  *   rstd                [T] float, or NULL if the backward is not needed
  *
  * residual may be NULL (then H is not written and may be NULL).  With a
- * residual H is required; it may be X or residual itself (same row stride).
+ * residual H is required; it may be X or residual itself (same row stride),
+ * and so may Y, but not both in one place.
  * K is a multiple of 8 and at most 32768; T >= 0 (T = 0: nothing to do, and
  * pointers may be NULL); T*K < 2^37.  eps >= 0 and finite; with eps = 0 a row
  * of zeros has no norm (rstd and s_x are Inf, y is NaN, codes are 0).  The sum
@@ -88,7 +90,7 @@ sbn_status sbn_rmsnorm_quant(const void* X, int64_t ldx, const void* residual, i
  * dX is the gradient of x and of the residual alike.  dH (NULL for none) is
  * the gradient that reaches h along the residual stream.
  *
- *   dY, H, dH, dX  [T x K] of dtype dt; dX may be dY or dH itself (same stride)
+ *   dY, H, dH, dX  [T x K] of dtype dt; dX may be dY, H or dH itself (same stride)
  *   gain [K] of dtype gaindt, rstd [T] float
  *   dgain [K] float, always written (T = 0: zeros)
  *   ws    sbn_rmsnorm_backward_workspace_bytes(T, K) bytes, no initialisation

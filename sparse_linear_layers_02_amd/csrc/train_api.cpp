@@ -36,6 +36,19 @@ int bytes_of(sbn_dtype d) { return d == SBN_BF16 ? 2 : 4; }
       return fail(SBN_ERR_ALIGN, "%s: '%s' is not aligned to its %d-byte elements", fn, #p, (int)(bytes)); \
   } while (0)
 
+sbn_status in_place(const char* fn, const char* out, const char* of) {
+  return fail(SBN_ERR_SHAPE, "%s: %s cannot be in the place of %s", fn, out, of);
+}
+// an output in the place of an input that is read row by row before it is written: with the same rows only
+#define SBN_SAME_ROWS(out, ldout, in, ldin)                                                        \
+  do {                                                                                             \
+    if ((out) == (in) && (out) && (ldout) != (ldin)) return in_place(fn, #out, #in " with another row stride"); \
+  } while (0)
+#define SBN_NOT_IN_PLACE(out, other)                                                               \
+  do {                                                                                             \
+    if ((const void*)(out) == (const void*)(other) && (out)) return in_place(fn, #out, #other);    \
+  } while (0)
+
 sbn_status check_t0(const char* fn, int64_t T) {
   if (T < 0) return fail(SBN_ERR_SHAPE, "%s: T = %lld is negative", fn, (long long)T);
   if (T > ROWS_MAX) return fail(SBN_ERR_SHAPE, "%s: T = %lld exceeds 2^40", fn, (long long)T);
@@ -138,6 +151,9 @@ sbn_status sbn_rmsnorm(const void* X, int64_t ldx, const void* residual, int64_t
   SBN_NONNULL(Y);
   SBN_TRY(check_ld("ldy", ldy, K, T));
   SBN_ALIGNED(Y);
+  SBN_SAME_ROWS(Y, ldy, X, ldx);
+  SBN_SAME_ROWS(Y, ldy, residual, ldres);
+  if (residual) SBN_NOT_IN_PLACE(Y, H);
   hipStream_t st = (hipStream_t)stream;
   SBN_TRY(finite_norm(fn, X, ldx, residual, ldres, dt, gain, gaindt, T, K, st));
   return hip_result(launch_rmsnorm(X, ldx, residual, ldres, dt == SBN_F32, gain, gaindt == SBN_F32, T, K, eps, H, ldh,
@@ -155,6 +171,9 @@ sbn_status sbn_rmsnorm_quant(const void* X, int64_t ldx, const void* residual, i
   SBN_NONNULL(s_x);
   SBN_ALIGNED(Xq);
   SBN_ELEM_ALIGNED(s_x, 4);
+  SBN_NOT_IN_PLACE(Xq, X);
+  SBN_NOT_IN_PLACE(Xq, residual);
+  if (residual) SBN_NOT_IN_PLACE(Xq, H);
   hipStream_t st = (hipStream_t)stream;
   SBN_TRY(finite_norm(fn, X, ldx, residual, ldres, dt, gain, gaindt, T, K, st));
   return hip_result(launch_rmsnorm(X, ldx, residual, ldres, dt == SBN_F32, gain, gaindt == SBN_F32, T, K, eps, H, ldh,
@@ -199,8 +218,9 @@ sbn_status sbn_rmsnorm_backward(const void* dY, int64_t lddy, const void* H, int
     SBN_ELEM_ALIGNED(rstd, 4);
     SBN_ALIGNED(dX);
     SBN_ALIGNED(ws);
-    if ((dX == dY && lddx != lddy) || (dX == dH && lddx != lddh))
-      return fail(SBN_ERR_SHAPE, "%s: dX in the place of an input must have that input's row stride", fn);
+    SBN_SAME_ROWS(dX, lddx, dY, lddy);
+    SBN_SAME_ROWS(dX, lddx, H, ldh);
+    SBN_SAME_ROWS(dX, lddx, dH, lddh);
     const size_t need = rmsnorm_bwd_ws_bytes(T, K);
     if (ws_bytes < need)
       return fail(SBN_ERR_WORKSPACE, "%s: workspace %zu bytes, need %zu", fn, ws_bytes, need);
@@ -277,6 +297,11 @@ sbn_status sbn_cross_entropy_backward(const uint16_t* X, int64_t ldx, const uint
   const size_t need = ce_bwd_ws_bytes(T, V, K);
   if (ws_bytes < need) return fail(SBN_ERR_WORKSPACE, "%s: workspace %zu bytes, need %zu", fn, ws_bytes, need);
   if (!dX && !dW) return ok();
+  SBN_NOT_IN_PLACE(dX, X);                           // X and W are read again after dX, and after dW of a piece
+  SBN_NOT_IN_PLACE(dX, W);
+  SBN_NOT_IN_PLACE(dW, X);
+  SBN_NOT_IN_PLACE(dW, W);
+  SBN_NOT_IN_PLACE(dX, dW);
   SBN_TRY(check_finite(fn, "X", X, T, K, ldx, 2, st));
   SBN_TRY(check_finite(fn, "W", W, V, K, ldw, 2, st));
   SBN_TRY(check_finite_tokens(fn, "dloss", dloss, labels, label_bytes == 8, V, T, st));

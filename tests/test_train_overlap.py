@@ -1,0 +1,39 @@
+"""Outputs in the place of inputs: refused where a block would overwrite what another
+one, or a later launch of the same call, still reads.  Nothing is dereferenced."""
+from __future__ import annotations
+
+import ctypes
+
+import pytest
+
+import sparse_linear_layers_02_amd as sbn
+
+SHAPE = 2
+A, B, C, D, E, F, G = (ctypes.c_void_p(i << 20) for i in range(1, 8))
+BIG = 1 << 40
+F32, BF16 = sbn.SBN_F32, sbn.SBN_BF16
+
+
+@pytest.mark.parametrize("X,res,H,Y,ldy", [(A, None, None, A, 72), (A, B, C, A, 72), (A, B, C, B, 72), (A, B, C, C, 64),
+                                           (A, B, A, A, 64)])
+def test_norm(X, res, H, Y, ldy):
+    st = sbn.lib().sbn_rmsnorm(X, 64, res, 64, BF16, D, F32, 4, 64, 1e-6, H, 64, Y, ldy, E, None)
+    assert st == SHAPE and b"place" in sbn.lib().sbn_last_error()
+
+
+@pytest.mark.parametrize("Xq", [A, B, C])
+def test_norm_codes(Xq):
+    st = sbn.lib().sbn_rmsnorm_quant(A, 64, B, 64, BF16, D, F32, 4, 64, 1e-6, C, 64, Xq, F, E, None)
+    assert st == SHAPE and b"place" in sbn.lib().sbn_last_error()
+
+
+def test_norm_gradient():
+    st = sbn.lib().sbn_rmsnorm_backward(A, 64, B, 64, C, 64, BF16, D, F32, E, 4, 64, B, 72, F, G, BIG, None)
+    assert st == SHAPE and b"place" in sbn.lib().sbn_last_error()
+
+
+@pytest.mark.parametrize("dX,dW", [(A, D), (B, D), (D, A), (D, B), (A, B), (None, B), (A, None), (D, D)])
+def test_head_gradients(dX, dW):
+    """dX is written before dW's product reads X, and D of a later piece reads X and W again."""
+    st = sbn.lib().sbn_cross_entropy_backward(A, 64, B, 64, C, 8, E, F, 4, 100, 64, dX, BF16, 64, dW, BF16, 64, G, BIG, None)
+    assert st == SHAPE and b"place" in sbn.lib().sbn_last_error()
