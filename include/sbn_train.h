@@ -137,7 +137,8 @@ sbn_status sbn_cross_entropy(const uint16_t* X, int64_t ldx, const uint16_t* W, 
  * product takes twice the time, and its error falls to that of float32 sums.
  *
  *   dX [T x K] of dtype dxdt, dW [V x K] of dtype dwdt (SBN_BF16, SBN_F32 or
- *   SBN_F32_FINE); either may be NULL.  With T = 0 dW is written as zeros.
+ *   SBN_F32_FINE); either may be NULL.  With T = 0 dW is written as zeros.  dX
+ *   without dW may be in X's place, dW of bf16 in W's (same stride).
  *   ws sbn_cross_entropy_backward_workspace_bytes(T, V, K) bytes
  */
 sbn_status sbn_cross_entropy_backward_workspace_bytes(int64_t T, int64_t V, int64_t K, size_t* bytes);

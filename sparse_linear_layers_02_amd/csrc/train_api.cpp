@@ -297,10 +297,10 @@ sbn_status sbn_cross_entropy_backward(const uint16_t* X, int64_t ldx, const uint
   const size_t need = ce_bwd_ws_bytes(T, V, K);
   if (ws_bytes < need) return fail(SBN_ERR_WORKSPACE, "%s: workspace %zu bytes, need %zu", fn, ws_bytes, need);
   if (!dX && !dW) return ok();
-  SBN_NOT_IN_PLACE(dX, X);                           // X and W are read again after dX, and after dW of a piece
+  if (dW) SBN_NOT_IN_PLACE(dX, X);                   // which dW's product reads after dX's last
   SBN_NOT_IN_PLACE(dX, W);
   SBN_NOT_IN_PLACE(dW, X);
-  SBN_NOT_IN_PLACE(dW, W);
+  if (dwdt != SBN_BF16 || lddw != ldw) SBN_NOT_IN_PLACE(dW, W);   // the same rows: a piece's are read before they are written
   SBN_NOT_IN_PLACE(dX, dW);
   SBN_TRY(check_finite(fn, "X", X, T, K, ldx, 2, st));
   SBN_TRY(check_finite(fn, "W", W, V, K, ldw, 2, st));

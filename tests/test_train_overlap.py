@@ -32,8 +32,10 @@ def test_norm_gradient():
     assert st == SHAPE and b"place" in sbn.lib().sbn_last_error()
 
 
-@pytest.mark.parametrize("dX,dW", [(A, D), (B, D), (D, A), (D, B), (A, B), (None, B), (A, None), (D, D)])
-def test_head_gradients(dX, dW):
-    """dX is written before dW's product reads X, and D of a later piece reads X and W again."""
-    st = sbn.lib().sbn_cross_entropy_backward(A, 64, B, 64, C, 8, E, F, 4, 100, 64, dX, BF16, 64, dW, BF16, 64, G, BIG, None)
+@pytest.mark.parametrize("dX,dW,dwdt,lddw", [(A, D, BF16, 64), (B, D, BF16, 64), (B, None, BF16, 64), (D, A, BF16, 64),
+                                             (None, A, BF16, 64), (D, B, F32, 64), (None, B, BF16, 72), (A, B, BF16, 64),
+                                             (D, D, BF16, 64)])
+def test_head_gradients(dX, dW, dwdt, lddw):
+    """dX is written before dW's product reads X, and dX's product reads W as it writes."""
+    st = sbn.lib().sbn_cross_entropy_backward(A, 64, B, 64, C, 8, E, F, 4, 100, 64, dX, BF16, 64, dW, dwdt, lddw, G, BIG, None)
     assert st == SHAPE and b"place" in sbn.lib().sbn_last_error()
