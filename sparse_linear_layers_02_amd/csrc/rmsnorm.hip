@@ -19,7 +19,12 @@
 // residual 15.0 us (4.9 TB/s of 73 MB; a large copy reaches 4.7 to 4.9), gradient
 // of 8192 x 4096 with dh 40 us for one set of tensors again and again (6.6 TB/s of
 // 268 MB; 202 MB fetched, 76 MB written), 50 for three in turn, and 4.8 us for
-// dgain's sums.  One token of 2560: 2.8 us, latency.
+// dgain's sums.  One token of 2560: 2.8 us, latency.  Wider rows, 2048 with the
+// residual in bf16, 8-bit output / bf16 output / gradient: K = 6912 24.4 / 24.6 /
+// 30.7 us, 11008 39 / 40 / 45, 16384 53 / 52 / 63 (4.4, 5.2, 4.3 TB/s).  Above 16384
+// a thread holds four chunks, and of the six kernels four keep 76 to 216 bytes a
+// lane in scratch memory: K = 28672 104 / 99 / 140 us (4.0, 4.7, 3.4 TB/s), float32
+// 244 / 241 / 308 (3.1, 3.9, 3.1).
 #include "train_internal.h"
 
 namespace sbn {
@@ -146,9 +151,13 @@ __global__ __launch_bounds__(MAXT) void rmsnorm_kernel(FwdArgs A) {
         if (g + TPR * i < n) h[i].load(xr, g + TPR * i);
     }
     // Of one chunk the gain is loaded before the first store, which a later load
-    // would wait for (8-bit output of 4096 x 2560 19.2 -> 18.5 us, bf16 of 1021 x 4096
-    // 8.85 -> 8.5, but float32 11.8 -> 12.4); more chunks of it leave room for half
-    // the blocks (1024 x 16384: 30 -> 34 us).
+    // would wait for.  Microseconds late / early, with the residual: 8-bit output of
+    // bf16 4096 x 2560 16.3 / 15.6, 1021 x 4096 9.0 / 8.6, of float32 11.4 / 10.9; bf16
+    // output 1021 x 4096 7.5 / 7.0, 8192 x 4096 49.3 / 48.2; all of 333 x 2560 the same.
+    // Float32 output gains nothing by it: 12.1 / 12.7 at 1021 x 4096, 94.5 / 94.6 at
+    // 8192 x 4096, 4.4 / 4.4 at 333 x 2560 (without the residual 9.2 / 8.7, 50.1 / 49.7,
+    // 3.6 / 3.4).  More chunks leave room for fewer blocks: 1024 x 16384 30.1 / 33.2
+    // in 8 bits, 28.3 / 31.9 in bf16, 1024 x 6912 13.1 / 12.8 and 10.3 / 11.5.
     constexpr bool EARLY = CH == 1 && (Q || !F32);
     float gain[8];
     if (EARLY && g < n) gain8(A.gain, A.gain_f32, g, gain);
@@ -358,7 +367,10 @@ int chunks_for(int n) { return n <= 512 ? 1 : n <= 2048 ? 2 : 4; }
 // that leaves one block a compute unit.  (bf16, microseconds at 256 / 512 / 1024
 // blocks: T = 8192, K = 4096: 61.6 / 56.6 / 63.3; T = 8192, K = 1024: 32.5 / 22.5 /
 // 19.2; T = 4096, K = 2560: 24.6 / 21.3 / 23.1; T = 1021, K = 4096: 14.2 / 15.3 /
-// 21.6.)
+// 21.6.  With dgain's sums at 64 / 128 / 256 blocks, below the one a compute unit:
+// T = 1021, K = 4096 15.0 / 14.4 / 12.5, float32 17.0 / 16.4 / 14.4, K = 1024 10.1 / 9.8
+// / 7.9; T = 333, K = 2560 9.3 / 7.9 / 8.2, float32 9.8 / 8.3 / 8.6; 64 rows and fewer
+// one a block in any case.)
 int bwd_blocks(int64_t T, int64_t K) {
   const int n = (int)(K / 8), most = 256 * 16 / (threads_for(n, chunks_for(n)) / 64);
   int64_t g = T / 8 < 256 ? 256 : T / 8;
