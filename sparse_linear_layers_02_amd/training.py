@@ -67,13 +67,18 @@ def _so():
     return _package._lib or lib()
 
 
+_FLOATS = {}
+
+
 def _dtype(t, name: str, fn: str) -> int:
-    torch = _torch()
-    if t.dtype is torch.bfloat16:
-        return SBN_BF16
-    if t.dtype is torch.float32:
-        return SBN_F32
-    raise SbnError(fn, 6, f"{name} must be bfloat16 or float32, got {t.dtype}")
+    dt = _FLOATS.get(t.dtype)
+    if dt is None:
+        torch = _torch()
+        _FLOATS.update({torch.bfloat16: SBN_BF16, torch.float32: SBN_F32})
+        dt = _FLOATS.get(t.dtype)
+        if dt is None:
+            raise SbnError(fn, 6, f"{name} must be bfloat16 or float32, got {t.dtype}")
+    return dt
 
 
 def _rows(t, name: str, like, fn: str):
@@ -138,7 +143,7 @@ def _scratch(kind: str, nbytes: int, device, raw: int):
     """The package's grow-only workspace of (kind, device, the device's current stream)
     of the calling thread; under capture one of its own, which belongs to the graph."""
     torch = _torch()
-    if torch._C._cuda_isCurrentStreamCapturing():
+    if raw and torch._C._cuda_isCurrentStreamCapturing():   # the null stream cannot be captured
         return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
     key = (kind, device, raw)
     buf = _WS.kept.get(key)
