@@ -615,47 +615,44 @@ __global__ __launch_bounds__(64 * WA * WB, 1) void ce_gemm_kernel(GemmArgs P) {
 // lse and loss of a token from its groups' (maximum, sum): 16 tokens a block, 64
 // threads a token take every 64th group each, then the 64 pairs are joined in a
 // tree.  (64 tokens a block and 16 threads a token took 31 us for 17 tokens of
-// 50001 entries: one block, whose loads wait for each other.)  Tokens beyond the
-// grid are taken in further rounds: of 2^26 tokens, 64 threads each would be 2^32,
-// more than a launch runs.
-__global__ __launch_bounds__(1024) void ce_join_kernel(const float2* __restrict__ stats, int groups, int T,
+// 50001 entries: one block, whose loads wait for each other.)  2^26 tokens in one
+// launch would be 2^32 threads, more than it runs: `first` is a launch's first token.
+__global__ __launch_bounds__(1024) void ce_join_kernel(const float2* __restrict__ stats, int groups, int first, int T,
                                                        const void* __restrict__ labels, bool labels64, int V,
                                                        const float* __restrict__ target, float* __restrict__ loss,
                                                        float* __restrict__ lse) {
   __shared__ float2 sm[64][17];
   const int tl = threadIdx.x & 15, part = threadIdx.x >> 4;
+  const int t = first + blockIdx.x * 16 + tl;
   auto join = [](float2 a, float2 b) {
     const float top = fmaxf(a.x, b.x);
     return make_float2(top, a.y * __builtin_amdgcn_exp2f(a.x - top) + b.y * __builtin_amdgcn_exp2f(b.x - top));
   };
-  for (int t0 = blockIdx.x * 16; t0 < T; t0 += gridDim.x * 16) {
-    const int t = t0 + tl;
-    float2 a = make_float2(NONE, 0.0f);
-    if (t < T) {
-      constexpr int AHEAD = 8;
-      for (int g = part; g < groups; g += 64 * AHEAD) {
-        float2 x[AHEAD];
+  float2 a = make_float2(NONE, 0.0f);
+  if (t < T) {
+    constexpr int AHEAD = 8;
+    for (int g = part; g < groups; g += 64 * AHEAD) {
+      float2 x[AHEAD];
 #pragma unroll
-        for (int k = 0; k < AHEAD; ++k)
-          x[k] = g + 64 * k < groups ? stats[(int64_t)(g + 64 * k) * T + t] : make_float2(NONE, 0.0f);
+      for (int k = 0; k < AHEAD; ++k)
+        x[k] = g + 64 * k < groups ? stats[(int64_t)(g + 64 * k) * T + t] : make_float2(NONE, 0.0f);
 #pragma unroll
-        for (int k = 0; k < AHEAD; ++k) a = join(a, x[k]);
-      }
+      for (int k = 0; k < AHEAD; ++k) a = join(a, x[k]);
     }
-    sm[part][tl] = a;
+  }
+  sm[part][tl] = a;
+  __syncthreads();
+#pragma unroll
+  for (int d = 32; d >= 1; d >>= 1) {
+    if (part < d) sm[part][tl] = join(sm[part][tl], sm[part + d][tl]);
     __syncthreads();
-#pragma unroll
-    for (int d = 32; d >= 1; d >>= 1) {
-      if (part < d) sm[part][tl] = join(sm[part][tl], sm[part + d][tl]);
-      __syncthreads();
-    }
-    if (part == 0 && t < T) {                        // the threads that write these places in the next round
-      a = sm[0][tl];
-      const float l = a.x * LN2 + logf(a.y);
-      const int64_t y = label_at(labels, labels64, t);
-      lse[t] = l;
-      loss[t] = y >= 0 && y < V ? l - target[t] : 0.0f;
-    }
+  }
+  if (part == 0 && t < T) {
+    a = sm[0][tl];
+    const float l = a.x * LN2 + logf(a.y);
+    const int64_t y = label_at(labels, labels64, t);
+    lse[t] = l;
+    loss[t] = y >= 0 && y < V ? l - target[t] : 0.0f;
   }
 }
 
@@ -868,9 +865,11 @@ hipError_t launch_ce(const uint16_t* X, int64_t ldx, const uint16_t* W, int64_t 
   P.stats = (float2*)((uint8_t*)ws + align256((size_t)T * sizeof(float)));
   const hipError_t e = gemm<EPI_STATS>(LOGITS, stats_tile(T, V, K), P, st);
   if (e != hipSuccess) return e;
-  constexpr int64_t JOIN_BLOCKS = 1 << 20;
-  SBN_LAUNCH("ce_join", ce_join_kernel, dim3((unsigned)(T < 16 * JOIN_BLOCKS ? cdiv(T, 16) : JOIN_BLOCKS)), dim3(1024), 0, st, P.stats,
-             (int)stats_groups(T, V, K), (int)T, labels, labels64, (int)V, P.target, loss, lse);
+  constexpr int64_t JOIN_TOKENS = 1 << 24;           // of a launch
+  const int groups = (int)stats_groups(T, V, K);
+  for (int64_t t = 0; t < T; t += JOIN_TOKENS)
+    SBN_LAUNCH("ce_join", ce_join_kernel, dim3((unsigned)cdiv(T - t < JOIN_TOKENS ? T - t : JOIN_TOKENS, 16)), dim3(1024), 0,
+               st, P.stats, groups, (int)t, (int)T, labels, labels64, (int)V, P.target, loss, lse);
   return hipGetLastError();
 }
 

@@ -106,7 +106,7 @@ sbn_status check_ce_shape(const char* fn, int64_t T, int64_t V, int64_t K) {
   SBN_TRY(check_numel(fn, "W (V*K)", V, K));
   if (T > 0) {
     SBN_TRY(check_numel(fn, "X (T*K)", T, K));
-    // tiles are counted in 32 bits; a grid has at most the blocks that are resident, or takes rounds
+    // tiles are counted in 32 bits; the launches' grids stay below 2^32 threads
     if (T >= CE_T_MAX || !prod_below(cdiv(T, 64), cdiv(V, 128), int64_t(1) << 24))
       return fail(SBN_ERR_SHAPE, "%s: T = %lld with V = %lld exceeds the limits of one call", fn, (long long)T,
                   (long long)V);
