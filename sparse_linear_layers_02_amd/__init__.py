@@ -701,3 +701,9 @@ from .training import (  # noqa: E402,F401
     SBN_ADAMW_BLOCK, AdamWTable, sbn_adamw_decode_m, sbn_adamw_decode_v, sbn_adamw_encode_m, sbn_adamw_encode_v,
     sbn_adamw_step, sbn_cross_entropy, sbn_cross_entropy_backward, sbn_cross_entropy_workspace_bytes, sbn_rmsnorm,
     sbn_rmsnorm_backward, sbn_rmsnorm_quant, train_header_symbols)
+
+__all__ += [
+    "SBN_ADAMW_BLOCK", "AdamWTable", "sbn_adamw_decode_m", "sbn_adamw_decode_v", "sbn_adamw_encode_m", "sbn_adamw_encode_v",
+    "sbn_adamw_step", "sbn_cross_entropy", "sbn_cross_entropy_backward", "sbn_cross_entropy_workspace_bytes", "sbn_rmsnorm",
+    "sbn_rmsnorm_backward", "sbn_rmsnorm_quant", "train_header_symbols",
+]

@@ -74,3 +74,9 @@ def test_eps_of_8_bit_states():
         st = sbn.lib().sbn_adamw_step(P, P2, 3, 0, 0, 8, 1e-3, 0.9, 0.999, eps, 1, None, None)
         assert st == sbn.SBN_ERR_VALUE and b"eps" in sbn.lib().sbn_last_error()
     assert sbn.lib().sbn_adamw_step(P, P2, 0, 0, 0, 8, 1e-3, 0.9, 0.999, 1e-30, 1, None, None) == 0
+
+
+def test_the_operators_are_among_the_packages_names():
+    names = {n for n in dir(sbn.training) if n.startswith("sbn_") or n in ("AdamWTable", "SBN_ADAMW_BLOCK")}
+    assert names <= set(sbn.__all__), names - set(sbn.__all__)
+    assert all(getattr(sbn, n) is getattr(sbn.training, n) for n in names)
