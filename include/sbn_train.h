@@ -19,9 +19,9 @@
  * before anything is launched, nothing launched on an error, messages from
  * sbn_last_error(), no allocation, no synchronisation, no exception across the
  * ABI.  Tensors that a call writes overlap no other tensor of the call, except
- * where it says that one may be in another's place.  Every call may be captured into a HIP graph.  Results do not depend on
- * launch geometry from run to run: there are no atomics, every sum has a fixed
- * order.  Inputs with NaN or Inf are outside the contract; with
+ * where it says that one may be in another's place.  Every call may be captured
+ * into a HIP graph.  Results do not depend on launch geometry from run to run:
+ * there are no atomics, every sum has a fixed order.  Inputs with NaN or Inf are outside the contract; with
  * SBN_CHECK_FINITE=1 the norm and cross entropy calls scan X, residual, gain,
  * W, dY, H, dH and dloss (of the tokens with a target) as sbn.h describes.
  */
@@ -139,7 +139,7 @@ sbn_status sbn_cross_entropy(const uint16_t* X, int64_t ldx, const uint16_t* W, 
  *   dX [T x K] of dtype dxdt, dW [V x K] of dtype dwdt (SBN_BF16, SBN_F32 or
  *   SBN_F32_FINE); either may be NULL.  With T = 0 dW is written as zeros.  dX
  *   without dW may be in X's place, dW of bf16 in W's (same stride).
- *   ws sbn_cross_entropy_backward_workspace_bytes(T, V, K) bytes
+ *   ws sbn_cross_entropy_backward_workspace_bytes(T, V, K) bytes, for any types
  */
 sbn_status sbn_cross_entropy_backward_workspace_bytes(int64_t T, int64_t V, int64_t K, size_t* bytes);
 sbn_status sbn_cross_entropy_backward(const uint16_t* X, int64_t ldx, const uint16_t* W, int64_t ldw,
@@ -202,9 +202,9 @@ sbn_status sbn_adamw_plan(const sbn_adamw_entry* entries, int64_t count, sbn_dty
  * accepted and wrote them (blocks = 0: nothing to do).  0 <= beta < 1, lr
  * finite, eps >= 0 finite, and with 8-bit states > 0 (as float32), step >= 1.
  * With eps = 0 an element whose v is 0 becomes the quotient by 0 that the
- * formula says (Inf, or NaN where m is 0 too).  `dyn`, if not NULL, is 4 floats in device
- * memory that take the place of host values, for steps replayed from a graph:
- * lr, 1 - beta1^step, 1 - beta2^step, grad_scale (1 without dyn).
+ * formula says (Inf, or NaN where m is 0 too).  `dyn`, if not NULL, is 4 floats
+ * in device memory that take the place of host values, for steps replayed from
+ * a graph: lr, 1 - beta1^step, 1 - beta2^step, grad_scale (1 without dyn).
  */
 sbn_status sbn_adamw_step(const sbn_adamw_entry* entries, const int32_t* map, int64_t blocks, sbn_dtype pdt,
                           sbn_dtype gdt, int state_bits, double lr, double beta1, double beta2, double eps,

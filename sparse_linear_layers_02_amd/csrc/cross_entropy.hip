@@ -16,10 +16,11 @@
 // Gradients, per piece of the vocabulary: the same product with an epilogue
 // that writes D in bf16; dX and dW are then two more products, on D and W and on
 // D and X as they lie.  The workspace holds one piece of D, of D_ELEMS elements
-// at most (of up to 2^20 tokens).  For a gradient of type SBN_F32_FINE the epilogue also writes what
-// the rounding to bf16 left of D, in bf16, and its product is added.  (Error
-// against 64 bits, 300 tokens of 2500 entries, K = 256: relative 1.4e-3
-// -> 2.0e-6; both gradients of 8192 tokens of 65536 entries, K = 4096: 9.6 -> 16.8 ms.)
+// at most (of up to 2^20 tokens).  For a gradient of type SBN_F32_FINE the
+// epilogue also writes what the rounding to bf16 left of D, in bf16, and its
+// product is added.  (Relative error against 64 bits, 300 tokens of 2500 entries,
+// K = 256: 1.4e-3 -> 2.0e-6; both gradients of 8192 tokens of 65536 entries, K =
+// 4096: 9.6 -> 16.8 ms.)
 //
 // All three products are one kernel, C[a][b] = sum_k A[a][k] B[b][k], where an
 // operand's rows in memory are either its outputs (X and W of the logits, D of
@@ -41,7 +42,8 @@ constexpr int64_t D_ELEMS = int64_t(1) << 28;
 constexpr int GMAX_WAVE = 1024;                     // tokens whose largest |dloss| a wave finds in two rounds of loads
 constexpr int CUS = 256;
 
-enum Epi { EPI_STATS, EPI_GRAD, EPI_GRAD_PAIR, EPI_OUT16, EPI_OUT32, EPI_ADD32 };   // PAIR: D in two bf16 numbers; OUT, ADD: C in bf16, in float32
+// PAIR: D in two bf16 numbers; OUT, ADD: C in bf16 or float32, ADD on top of Cin
+enum Epi { EPI_STATS, EPI_GRAD, EPI_GRAD_PAIR, EPI_OUT16, EPI_OUT32, EPI_ADD32 };
 
 struct GemmArgs {
   const uint16_t *A, *B;               // rows of lda, ldb
@@ -873,10 +875,7 @@ hipError_t launch_ce(const uint16_t* X, int64_t ldx, const uint16_t* W, int64_t 
   return hipGetLastError();
 }
 
-size_t ce_bwd_ws_bytes(int64_t T, int64_t V, int64_t K) {
-  const size_t one = ce_plan(T, V, K, false).total, two = ce_plan(T, V, K, true).total;
-  return one > two ? one : two;
-}
+size_t ce_bwd_ws_bytes(int64_t T, int64_t V, int64_t K, bool pair) { return ce_plan(T, V, K, pair).total; }
 
 hipError_t launch_ce_backward(const uint16_t* X, int64_t ldx, const uint16_t* W, int64_t ldw, const void* labels,
                               bool labels64, const float* lse, const float* dloss, int64_t T, int64_t V, int64_t K,

@@ -266,7 +266,8 @@ sbn_status sbn_cross_entropy_backward_workspace_bytes(int64_t T, int64_t V, int6
   const char* fn = "sbn_cross_entropy_backward_workspace_bytes";
   SBN_NONNULL(bytes);
   SBN_TRY(check_ce_shape(fn, T, V, K));
-  *bytes = T > 0 ? ce_bwd_ws_bytes(T, V, K) : 0;
+  const size_t one = T > 0 ? ce_bwd_ws_bytes(T, V, K, false) : 0, two = T > 0 ? ce_bwd_ws_bytes(T, V, K, true) : 0;
+  *bytes = one > two ? one : two;
   return ok();
 }
 
@@ -294,7 +295,7 @@ sbn_status sbn_cross_entropy_backward(const uint16_t* X, int64_t ldx, const uint
   SBN_ELEM_ALIGNED(lse, 4);
   SBN_ELEM_ALIGNED(dloss, 4);
   SBN_ALIGNED(ws);
-  const size_t need = ce_bwd_ws_bytes(T, V, K);
+  const size_t need = ce_bwd_ws_bytes(T, V, K, (dX && dxdt == SBN_F32_FINE) || (dW && dwdt == SBN_F32_FINE));
   if (ws_bytes < need) return fail(SBN_ERR_WORKSPACE, "%s: workspace %zu bytes, need %zu", fn, ws_bytes, need);
   if (!dX && !dW) return ok();
   if (dW) SBN_NOT_IN_PLACE(dX, X);                   // which dW's product reads after dX's last

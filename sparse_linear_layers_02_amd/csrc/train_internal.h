@@ -63,7 +63,8 @@ hipError_t launch_rmsnorm_backward(const void* dY, int64_t lddy, const void* H, 
 
 // ----------------------------------------------------------------- cross entropy (T >= 1)
 size_t ce_ws_bytes(int64_t T, int64_t V, int64_t K);
-size_t ce_bwd_ws_bytes(int64_t T, int64_t V, int64_t K);
+// pair: a gradient of type SBN_F32_FINE is asked for
+size_t ce_bwd_ws_bytes(int64_t T, int64_t V, int64_t K, bool pair);
 hipError_t launch_ce(const uint16_t* X, int64_t ldx, const uint16_t* W, int64_t ldw, const void* labels,
                      bool labels64, int64_t T, int64_t V, int64_t K, float* loss, float* lse, void* ws,
                      hipStream_t st);

@@ -20,3 +20,19 @@ def test_tiles_of_the_largest_vocabulary_stay_in_32_bits():
     for V in (most + 1, 2 ** 31 - 128):
         assert L.sbn_cross_entropy(P, 64, P, 64, P, 8, 1, V, 64, P, P, P, big, None) == SHAPE
         assert L.sbn_cross_entropy_backward(P, 64, P, 64, P, 8, P, P, 1, V, 64, P, 0, 64, P, 0, 64, P, big, None) == SHAPE
+
+
+def test_a_gradients_type_alone_asks_for_its_workspace():
+    """The query's size holds for every type; a call of the other types asks for no more than it uses."""
+    L, b = sbn.lib(), ctypes.c_size_t()
+    P = [ctypes.c_void_p(i << 20) for i in range(1, 9)]
+    T, V, K = 1021, 32001, 2560
+    assert L.sbn_cross_entropy_backward_workspace_bytes(T, V, K, ctypes.byref(b)) == OK
+
+    def need(dt):
+        st = L.sbn_cross_entropy_backward(P[0], K, P[1], K, P[2], 8, P[3], P[4], T, V, K, P[5], dt, K, P[6], dt, K, P[7], 0, None)
+        assert st == 5
+        return int(L.sbn_last_error().split(b"need ")[1])
+
+    one, two = need(sbn.SBN_BF16), need(sbn.SBN_F32_FINE)
+    assert need(sbn.SBN_F32) == one and one < two <= b.value and max(one, two) == b.value
