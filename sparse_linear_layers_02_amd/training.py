@@ -405,7 +405,10 @@ class AdamWTable:
         self.pdt, self.gdt = _dtype(params[0], "params[0]", fn), _dtype(grads[0], "grads[0]", fn)
         mt, vt = (torch.int8, torch.uint8) if self.state_bits == 8 else (torch.float32, torch.float32)
         entries = (_AdamWEntry * count)()
-        spans = []                                   # [first, past the last) byte, whether written, name
+        state = 1 if self.state_bits == 8 else 4
+        sizes = {"params": params[0].element_size(), "grads": grads[0].element_size(), "ms": state, "vs": state,
+                 "m_scales": 4, "v_scales": 4, "shadows": 2}
+        spans = []                                   # first and past the last byte, whether written, name
 
         def put(t, name, i, dtype, n, shape=None):
             if t is None:
@@ -414,9 +417,10 @@ class AdamWTable:
                 raise SbnError(fn, 6, f"{name}[{i}] must be {dtype}, got {t.dtype}")
             if t.numel() != n or t.device != dev or not t.is_contiguous():
                 raise SbnError(fn, 2, f"{name}[{i}] must be contiguous, with {n} elements on {dev}")
+            at = t.data_ptr()
             if n:
-                spans.append((t.data_ptr(), t.data_ptr() + n * t.element_size(), name != "grads", f"{name}[{i}]"))
-            return t.data_ptr()
+                spans.append((at, at + n * sizes[name], name != "grads", name, i))
+            return at
 
         for i in range(count):
             n = params[i].numel()
@@ -428,15 +432,16 @@ class AdamWTable:
             e.v_scale = put(lists["v_scales"][i], "v_scales", i, torch.float32, ns)
             e.shadow = put(lists["shadows"][i], "shadows", i, torch.bfloat16, n)
             e.n, e.weight_decay = n, wds[i]
-        read = written = (0, 0, False, "")           # of the spans so far, the one that reaches furthest
-        for s in sorted(spans, key=lambda s: s[:2]):
-            with_ = written if s[0] < written[1] else read if s[2] and s[0] < read[1] else None
-            if with_:
-                raise SbnError(fn, 2, f"{with_[3]} and {s[3]} share memory that the step writes")
+        spans.sort()
+        read = written = (0, 0)                      # of the spans so far, the one that reaches furthest
+        for s in spans:
+            if s[0] < written[1] or (s[2] and s[0] < read[1]):
+                o = written if s[0] < written[1] else read
+                raise SbnError(fn, 2, f"{o[3]}[{o[4]}] and {s[3]}[{s[4]}] share memory that the step writes")
             if s[2]:
-                written = max(written, s, key=lambda s: s[1])
+                written = s if s[1] > written[1] else written
             else:
-                read = max(read, s, key=lambda s: s[1])
+                read = s if s[1] > read[1] else read
         blocks = _i64()
         plan = _so().sbn_adamw_plan
         _check("sbn_adamw_plan", plan(entries, count, self.pdt, self.gdt, self.state_bits, None, ctypes.byref(blocks)))
