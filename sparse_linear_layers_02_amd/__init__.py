@@ -707,3 +707,14 @@ __all__ += [
     "sbn_adamw_step", "sbn_cross_entropy", "sbn_cross_entropy_backward", "sbn_cross_entropy_workspace_bytes", "sbn_rmsnorm",
     "sbn_rmsnorm_backward", "sbn_rmsnorm_quant", "train_header_symbols",
 ]
+
+
+# what a training step keeps in 8 bits (include/sbn_keep.h)
+from .keeping import (  # noqa: E402,F401
+    SBN_KEEP_BLOCK, SBN_RELU2, SBN_SILU, Kept8, keep_header_symbols, sbn_activation_backward, sbn_activation_quant,
+    sbn_keep8_decode, sbn_keep8_encode, sbn_rmsnorm_backward_kept, sbn_rmsnorm_quant_keep)
+
+__all__ += [
+    "SBN_KEEP_BLOCK", "SBN_RELU2", "SBN_SILU", "Kept8", "keep_header_symbols", "sbn_activation_backward",
+    "sbn_activation_quant", "sbn_keep8_decode", "sbn_keep8_encode", "sbn_rmsnorm_backward_kept", "sbn_rmsnorm_quant_keep",
+]

@@ -20,7 +20,7 @@ BUILD = os.path.join(ROOT, "_build", "libsbn")
 LIB = os.path.join(PKG, "libsbn.so")
 
 SOURCES = ["api.cpp", "pack.hip", "act_quant.hip", "gemm.hip", "gemv.hip", "backward.hip", "finite.hip",
-           "train_api.cpp", "rmsnorm.hip", "cross_entropy.hip", "adamw.hip"]
+           "train_api.cpp", "rmsnorm.hip", "cross_entropy.hip", "adamw.hip", "keep_api.cpp", "kept_rows.hip"]
 ARCH = "gfx950"
 
 FLAGS = [

@@ -1,0 +1,469 @@
+// What lies between the sparse layers in a training step, kept for the backward
+// pass as int8 codes with a scale per 128 neighbours of a row: the RMS norm's
+// input and the factors of a feed-forward block's activation.
+//
+//   checkpoint   s = a / 127, a = max |x| of the block, q = rint(127 x / a)
+//   norm         u = x + residual, kept u; out: int8 codes of u gain, scale rstd max / 127
+//   activation   u = f(a) b, kept a and b; out: the same of u, with or without the norm
+//   gradient, from the kept values alone, with r = (mean u^2 + eps)^-1/2, w = gain dy:
+//     du = r (w - u r^2 mean(w u));  dgain = sum_t dy u r;  da = du b f'(a);  db = du f(a)
+//
+// Both directions hold a row in registers as the plain norm does: one pass over
+// memory.  A checkpoint's block is 16 threads of 8 elements, one row of lanes, so
+// that its maximum takes four lane exchanges and no memory.
+#include "keep_internal.h"
+#include "row_ops.h"
+
+namespace sbn {
+namespace {
+
+constexpr int LANES = SBN_KEEP_BLOCK / 8;            // threads of a checkpoint's block
+static_assert(LANES == 16, "a block is one row of lanes");
+
+template <int CTRL>
+__device__ inline uint32_t row_move_bits(uint32_t x) {
+  return (uint32_t)__builtin_amdgcn_mov_dpp((int)x, CTRL, 0xf, 0xf, true);
+}
+// max |x| of a block: as integers the bits of magnitudes order alike, NaN above all
+__device__ inline float block_max(const float* v) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(v[j]) & 0x7FFFFFFFu);
+  m = max(m, row_move_bits<0xB1>(m));                // as row16_all
+  m = max(m, row_move_bits<0x4E>(m));
+  m = max(m, row_move_bits<0x141>(m));
+  m = max(m, row_move_bits<0x140>(m));
+  return __uint_as_float(m);
+}
+
+// Chunk c of row t into a checkpoint of rows of K; all 16 lanes of a block come
+// here, with zeros past the row.  A maximum that is NaN or Inf makes the scale, and so
+// every value, NaN.
+__device__ inline void keep_chunk(const float* v, bool live, int64_t t, int c, int K, int nb, int8_t* codes,
+                                  float* scales) {
+  const float a = block_max(v);
+  const bool none = a < U_FLOOR;
+  const float rcp = none ? 0.0f : __builtin_amdgcn_rcpf(a * (1.0f / 127.0f));
+  if (live) {
+    *(uint2*)(codes + t * K + 8 * c) = codes8(v, rcp, a);
+    if ((c & (LANES - 1)) == 0) scales[t * nb + c / LANES] = none ? 0.0f : a / 127.0f + (a - a);   // Inf - Inf: NaN
+  }
+}
+
+__device__ inline void values8(uint2 q, float s, float* v) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    v[j] = (float)(int8_t)(q.x >> (8 * j)) * s;
+    v[4 + j] = (float)(int8_t)(q.y >> (8 * j)) * s;
+  }
+}
+
+// ---------------------------------------------------------------- checkpoints alone
+// Rows of `lanes` threads (a multiple of 16), one after the other; `rows` of a
+// launch keep their number of threads below 2^31.
+template <bool F32>
+__global__ __launch_bounds__(256) void keep8_encode_kernel(const char* __restrict__ X, int64_t ldx, uint32_t rows,
+                                                           int K, uint32_t lanes, int8_t* __restrict__ codes,
+                                                           float* __restrict__ scales) {
+  const uint32_t n = K / 8, nb = lanes / LANES, total = rows * lanes;
+  // whole rows of 16 lanes share a row of X, so all lanes of a block take the same rounds
+  for (uint32_t i = blockIdx.x * 256 + threadIdx.x; i < total; i += gridDim.x * 256) {
+    const uint32_t t = i / lanes, c = i - t * lanes;
+    float v[8] = {};
+    if (c < n) {
+      Vec8<F32> x;
+      x.load(X + (int64_t)t * ldx * (F32 ? 4 : 2), c);
+      x.to(v);
+    }
+    keep_chunk(v, c < n, t, (int)c, K, (int)nb, codes, scales);
+  }
+}
+
+template <bool F32>
+__global__ __launch_bounds__(256) void keep8_decode_kernel(const int8_t* __restrict__ codes,
+                                                           const float* __restrict__ scales, uint32_t rows, int K,
+                                                           char* __restrict__ Y, int64_t ldy) {
+  const uint32_t n = K / 8, nb = (n + LANES - 1) / LANES, total = rows * n;
+  for (uint32_t i = blockIdx.x * 256 + threadIdx.x; i < total; i += gridDim.x * 256) {
+    const uint32_t t = i / n, c = i - t * n;
+    float v[8];
+    values8(*(const uint2*)(codes + 8 * (int64_t)i), scales[(int64_t)t * nb + c / LANES], v);
+    Vec8<F32> y;
+    y.from(v);
+    y.store(Y + (int64_t)t * ldy * (F32 ? 4 : 2), c);
+  }
+}
+
+// ---------------------------------------------------------------- the functions
+enum RowOp { ROW_NORM, ROW_RELU2, ROW_SILU };        // ROW_NORM: u = x
+
+// f(a) and, if asked, f'(a)
+template <RowOp OP>
+__device__ inline float act(float a, float* slope = nullptr) {
+  if (OP == ROW_RELU2) {
+    const float r = fmaxf(a, 0.0f);
+    if (slope) *slope = 2.0f * r;
+    return r * r;
+  }
+  if (OP == ROW_SILU) {
+    const float g = 1.0f / (1.0f + expf(-a));        // exp overflows to Inf, of which g is 0
+    if (slope) *slope = g * (1.0f + a * (1.0f - g));
+    return a * g;
+  }
+  if (slope) *slope = 1.0f;
+  return a;
+}
+
+// sums or maxima of a row's waves, from LDS `red` of its own; all threads call it
+template <class Op>
+__device__ inline float across(const float* red, int waves, Op op) {
+  const int l = threadIdx.x & 15;                    // at most 16 waves
+  return row16_all(l < waves ? red[l] : 0.0f, op);
+}
+
+// ---------------------------------------------------------------- forward
+struct FwdArgs {
+  const void *A, *B, *gain;                          // B: the residual (ROW_NORM), the factor, or NULL
+  void* H;                                           // ROW_NORM with a residual
+  int8_t *Xq, *kA, *kB;
+  float *s_x, *sA, *sB;
+  int64_t lda, ldb, ldh, T;
+  int K;
+  float eps;
+  bool gain_f32;
+};
+
+// A block holds one row at a time, CH chunks of 8 elements per thread
+// (CH * blockDim.x * 8 >= K); rows beyond the grid are taken in further rounds.
+template <bool F32, RowOp OP, int CH, int MAXT>
+__global__ __launch_bounds__(MAXT) void kept_forward_kernel(FwdArgs P) {
+  __shared__ float red[2][2][MAXT / 64];
+  const int g = threadIdx.x, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+  const int n = P.K / 8, es = F32 ? 4 : 2, TPR = blockDim.x, nb = (n + LANES - 1) / LANES;
+  int turn = 0;
+  for (int64_t t = blockIdx.x; t < P.T; t += gridDim.x, turn ^= 1) {
+    const char* ar = (const char*)P.A + t * P.lda * es;
+    const char* br = (const char*)P.B + t * P.ldb * es;
+    Vec8<F32> a[CH], b[CH];
+#pragma unroll
+    for (int i = 0; i < CH; ++i)
+      if (g + TPR * i < n) {
+        a[i].load(ar, g + TPR * i);
+        if (P.B) b[i].load(br, g + TPR * i);
+      }
+    float v[CH][8];                                  // u, then u gain
+    float ss = 0.0f, mx = 0.0f;
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      const int c = g + TPR * i;
+      const bool live = c < n;
+      float x[8] = {}, y[8] = {}, gain[8];
+      if (live) {
+        a[i].to(x);
+        if (P.B) b[i].to(y);
+        if (P.gain) gain8(P.gain, P.gain_f32, c, gain);
+      }
+      if (OP == ROW_NORM) {
+        if (live && P.B) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) x[j] += y[j];
+          a[i].from(x);
+          a[i].store((char*)P.H + t * P.ldh * es, c);
+          if (!F32) a[i].to(x);                      // the stored h is what is normalised
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[i][j] = x[j];
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          v[i][j] = act<OP>(x[j]);
+          if (P.B) v[i][j] *= y[j];
+        }
+      }
+      if (P.kA) {
+        keep_chunk(x, live, t, c, P.K, nb, P.kA, P.sA);
+        if (OP != ROW_NORM && P.B) keep_chunk(y, live, t, c, P.K, nb, P.kB, P.sB);
+      }
+      if (live) {
+        if (P.gain) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            ss += v[i][j] * v[i][j];
+            v[i][j] *= gain[j];
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) mx = fmaxf(mx, fabsf(v[i][j]));
+      }
+    }
+    ss = wave_all(ss, Add{});
+    mx = wave_all(mx, Max{});
+    if (waves > 1) {
+      // two sets of red in turn: one barrier a round keeps a fast wave's next
+      // write away from a slow wave's read
+      if ((threadIdx.x & 63) == 0) red[turn][0][wave] = ss, red[turn][1][wave] = mx;
+      __syncthreads();
+      ss = across(red[turn][0], waves, Add{});
+      mx = across(red[turn][1], waves, Max{});
+    }
+    const float m = fmaxf(mx, U_FLOOR);
+    if (g == 0) {
+      const float rstd = P.gain ? 1.0f / sqrtf(ss / (float)P.K + P.eps) : 1.0f;
+      P.s_x[t] = (m * rstd) / 127.0f;
+    }
+    const float rcp = __builtin_amdgcn_rcpf(m * (1.0f / 127.0f));
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      const int c = g + TPR * i;
+      if (c < n) *(uint2*)(P.Xq + t * P.K + 8 * c) = codes8(v[i], rcp, m);
+    }
+  }
+}
+
+// ---------------------------------------------------------------- backward
+struct BwdArgs {
+  const void *dY, *dH, *gain;                        // dH: ROW_NORM, or NULL
+  const int8_t *kA, *kB;                             // kB NULL: no second factor
+  const float *sA, *sB;
+  void *dA, *dB;
+  float* part;                                       // [gridDim.x][K] partial sums of dgain
+  int64_t lddy, lddh, ldda, lddb, T;
+  int K;
+  float eps;
+  bool gain_f32;
+};
+
+template <bool F32, RowOp OP, int CH, int MAXT>
+__global__ __launch_bounds__(MAXT) void kept_backward_kernel(BwdArgs P) {
+  __shared__ float red[2][2][MAXT / 64];
+  const int g = threadIdx.x, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+  const int n = P.K / 8, es = F32 ? 4 : 2, TPR = blockDim.x, nb = (n + LANES - 1) / LANES;
+  float dg[CH][8];
+#pragma unroll
+  for (int i = 0; i < CH; ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) dg[i][j] = 0.0f;
+  int turn = 0;
+  for (int64_t t = blockIdx.x; t < P.T; t += gridDim.x, turn ^= 1) {
+    Vec8<F32> dy[CH], dh[CH];
+    uint2 qa[CH], qb[CH];
+    float sa[CH], sb[CH];
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      const int c = g + TPR * i;
+      if (c < n) {
+        dy[i].load((const char*)P.dY + t * P.lddy * es, c);
+        qa[i] = *(const uint2*)(P.kA + t * P.K + 8 * c);
+        sa[i] = P.sA[t * nb + c / LANES];
+        if (OP == ROW_NORM) {
+          if (P.dH) dh[i].load((const char*)P.dH + t * P.lddh * es, c);
+        } else if (P.kB) {
+          qb[i] = *(const uint2*)(P.kB + t * P.K + 8 * c);
+          sb[i] = P.sB[t * nb + c / LANES];
+        }
+      }
+    }
+    float r = 1.0f, back = 0.0f;                     // back: r^2 mean(w u)
+    if (P.gain) {
+      float uu = 0.0f, wu = 0.0f;
+#pragma unroll
+      for (int i = 0; i < CH; ++i) {
+        const int c = g + TPR * i;
+        if (c < n) {
+          float a[8], b[8], w[8], gain[8];
+          values8(qa[i], sa[i], a);
+          if (OP != ROW_NORM && P.kB) values8(qb[i], sb[i], b);
+          dy[i].to(w);
+          gain8(P.gain, P.gain_f32, c, gain);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            float u = act<OP>(a[j]);
+            if (OP != ROW_NORM && P.kB) u *= b[j];
+            uu += u * u;
+            wu += w[j] * gain[j] * u;
+          }
+        }
+      }
+      uu = wave_all(uu, Add{});
+      wu = wave_all(wu, Add{});
+      if (waves > 1) {
+        if ((threadIdx.x & 63) == 0) red[turn][0][wave] = uu, red[turn][1][wave] = wu;
+        __syncthreads();                             // and the other set of red for the next round
+        uu = across(red[turn][0], waves, Add{});
+        wu = across(red[turn][1], waves, Add{});
+      }
+      r = 1.0f / sqrtf(uu / (float)P.K + P.eps);
+      back = r * r * (wu / (float)P.K);
+    }
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      const int c = g + TPR * i;
+      if (c < n) {
+        float a[8], b[8], d[8], gain[8], da[8], db[8];
+        values8(qa[i], sa[i], a);
+        if (OP != ROW_NORM && P.kB) values8(qb[i], sb[i], b);
+        dy[i].to(d);
+        if (P.gain) gain8(P.gain, P.gain_f32, c, gain);
+        if (OP == ROW_NORM && P.dH) dh[i].to(db);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          float slope;
+          const float f = act<OP>(a[j], &slope);
+          float du = d[j];
+          if (P.gain) {
+            const float u = OP != ROW_NORM && P.kB ? f * b[j] : f;
+            dg[i][j] += d[j] * (u * r);
+            du = r * (d[j] * gain[j] - u * back);
+          }
+          if (OP == ROW_NORM) {
+            da[j] = P.dH ? du + db[j] : du;
+          } else {
+            da[j] = (P.kB ? du * b[j] : du) * slope;
+            db[j] = du * f;
+          }
+        }
+        Vec8<F32> o;
+        o.from(da);
+        o.store((char*)P.dA + t * P.ldda * es, c);
+        if (OP != ROW_NORM && P.kB) {
+          o.from(db);
+          o.store((char*)P.dB + t * P.lddb * es, c);
+        }
+      }
+    }
+  }
+  if (!P.gain) return;
+  float* out = P.part + (int64_t)blockIdx.x * P.K;
+#pragma unroll
+  for (int i = 0; i < CH; ++i) {
+    const int c = g + TPR * i;
+    if (c < n) {
+      Vec8<true> o;
+      o.from(dg[i]);
+      o.store(out, c);
+    }
+  }
+}
+
+constexpr int64_t GRID_MAX = 1 << 20;                // blocks; rows beyond are taken in further rounds
+
+template <bool F32, RowOp OP, int CH, int MAXT>
+void run_fwd(const char* name, const FwdArgs& P, hipStream_t st) {
+  SBN_LAUNCH(name, (kept_forward_kernel<F32, OP, CH, MAXT>), dim3((unsigned)(P.T < GRID_MAX ? P.T : GRID_MAX)),
+             dim3((unsigned)threads_for(P.K / 8, CH)), 0, st, P);
+}
+template <bool F32, RowOp OP>
+void pick_fwd(const char* name, const FwdArgs& P, hipStream_t st) {
+  const int n = P.K / 8;
+  if (n <= 512) run_fwd<F32, OP, 1, 512>(name, P, st);
+  else if (n <= 1024) run_fwd<F32, OP, 2, 512>(name, P, st);
+  else if (n <= 2048) run_fwd<F32, OP, 2, 1024>(name, P, st);
+  else run_fwd<F32, OP, 4, 1024>(name, P, st);
+}
+
+template <bool F32, RowOp OP, int CH, int MAXT>
+void run_bwd(const char* name, const BwdArgs& P, hipStream_t st) {
+  const int64_t blocks = P.gain ? norm_grad_blocks(P.T, P.K) : P.T < GRID_MAX ? P.T : GRID_MAX;
+  SBN_LAUNCH(name, (kept_backward_kernel<F32, OP, CH, MAXT>), dim3((unsigned)blocks),
+             dim3((unsigned)threads_for(P.K / 8, CH)), 0, st, P);
+}
+template <bool F32, RowOp OP>
+void pick_bwd(const char* name, const BwdArgs& P, hipStream_t st) {
+  const int n = P.K / 8;
+  if (n <= 512) run_bwd<F32, OP, 1, 512>(name, P, st);
+  else if (n <= 1024) run_bwd<F32, OP, 2, 512>(name, P, st);
+  else if (n <= 2048) run_bwd<F32, OP, 2, 1024>(name, P, st);
+  else run_bwd<F32, OP, 4, 1024>(name, P, st);
+}
+
+template <RowOp OP>
+hipError_t backward(const char* name, const BwdArgs& P, bool f32, float* dgain, hipStream_t st) {
+  if (P.T > 0) {
+    if (f32) pick_bwd<true, OP>(name, P, st);
+    else pick_bwd<false, OP>(name, P, st);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return dgain ? launch_norm_dgain(P.part, P.T, P.K, dgain, st) : hipSuccess;
+}
+
+// Rows of a launch of the checkpoints' own kernels: their threads stay below 2^31.
+int64_t slab_rows(int64_t lanes) { return ((int64_t(1) << 31) - (int64_t(1) << 24)) / lanes; }
+unsigned slab_grid(int64_t threads) {
+  const int64_t b = cdiv(threads, 256);
+  return (unsigned)(b < 16384 ? b : 16384);
+}
+
+}  // namespace
+
+hipError_t launch_keep8_encode(const void* X, int64_t ldx, bool f32, int64_t T, int64_t K, int8_t* codes, float* scales,
+                               hipStream_t st) {
+  const int64_t nb = cdiv(K, SBN_KEEP_BLOCK), lanes = nb * LANES, slab = slab_rows(lanes), es = f32 ? 4 : 2;
+  for (int64_t t = 0; t < T; t += slab) {
+    const int64_t rows = T - t < slab ? T - t : slab;
+    const char* x = (const char*)X + t * ldx * es;
+    const dim3 grid(slab_grid(rows * lanes));
+    if (f32) SBN_LAUNCH("keep8_encode", keep8_encode_kernel<true>, grid, dim3(256), 0, st, x, ldx, (uint32_t)rows, (int)K, (uint32_t)lanes, codes + t * K, scales + t * nb);
+    else SBN_LAUNCH("keep8_encode", keep8_encode_kernel<false>, grid, dim3(256), 0, st, x, ldx, (uint32_t)rows, (int)K, (uint32_t)lanes, codes + t * K, scales + t * nb);
+  }
+  return hipGetLastError();
+}
+
+hipError_t launch_keep8_decode(const int8_t* codes, const float* scales, int64_t T, int64_t K, void* Y, int64_t ldy,
+                               bool f32, hipStream_t st) {
+  const int64_t nb = cdiv(K, SBN_KEEP_BLOCK), slab = slab_rows(K / 8), es = f32 ? 4 : 2;
+  for (int64_t t = 0; t < T; t += slab) {
+    const int64_t rows = T - t < slab ? T - t : slab;
+    char* y = (char*)Y + t * ldy * es;
+    const dim3 grid(slab_grid(rows * (K / 8)));
+    if (f32) SBN_LAUNCH("keep8_decode", keep8_decode_kernel<true>, grid, dim3(256), 0, st, codes + t * K, scales + t * nb, (uint32_t)rows, (int)K, y, ldy);
+    else SBN_LAUNCH("keep8_decode", keep8_decode_kernel<false>, grid, dim3(256), 0, st, codes + t * K, scales + t * nb, (uint32_t)rows, (int)K, y, ldy);
+  }
+  return hipGetLastError();
+}
+
+hipError_t launch_rmsnorm_quant_keep(const void* X, int64_t ldx, const void* res, int64_t ldr, bool f32, const void* gain,
+                                     bool gain_f32, int64_t T, int64_t K, float eps, void* H, int64_t ldh, int8_t* Xq,
+                                     float* s_x, int8_t* codes, float* scales, hipStream_t st) {
+  const FwdArgs P{X, res, gain, H, Xq, codes, nullptr, s_x, scales, nullptr, ldx, ldr, ldh, T, (int)K, eps, gain_f32};
+  if (f32) pick_fwd<true, ROW_NORM>("rmsnorm_quant_keep", P, st);
+  else pick_fwd<false, ROW_NORM>("rmsnorm_quant_keep", P, st);
+  return hipGetLastError();
+}
+
+hipError_t launch_rmsnorm_backward_kept(const void* dY, int64_t lddy, const void* dH, int64_t lddh, bool f32,
+                                        const int8_t* codes, const float* scales, const void* gain, bool gain_f32,
+                                        int64_t T, int64_t K, float eps, void* dX, int64_t lddx, float* dgain, void* ws,
+                                        hipStream_t st) {
+  const BwdArgs P{dY, dH, gain, codes, nullptr, scales, nullptr, dX, nullptr, (float*)ws, lddy, lddh, lddx, 0, T, (int)K,
+                  eps, gain_f32};
+  return backward<ROW_NORM>("rmsnorm_grad_kept", P, f32, dgain, st);
+}
+
+hipError_t launch_activation_quant(const void* A, int64_t lda, const void* B, int64_t ldb, bool f32, sbn_act act,
+                                   const void* gain, bool gain_f32, int64_t T, int64_t K, float eps, int8_t* Xq,
+                                   float* s_x, int8_t* codes_a, float* scales_a, int8_t* codes_b, float* scales_b,
+                                   hipStream_t st) {
+  const FwdArgs P{A, B, gain, nullptr, Xq, codes_a, codes_b, s_x, scales_a, scales_b, lda, ldb, 0, T, (int)K, eps, gain_f32};
+  const char* name = "activation_quant";
+  if (act == SBN_RELU2) {
+    if (f32) pick_fwd<true, ROW_RELU2>(name, P, st);
+    else pick_fwd<false, ROW_RELU2>(name, P, st);
+  } else {
+    if (f32) pick_fwd<true, ROW_SILU>(name, P, st);
+    else pick_fwd<false, ROW_SILU>(name, P, st);
+  }
+  return hipGetLastError();
+}
+
+hipError_t launch_activation_backward(const void* dY, int64_t lddy, bool f32, const int8_t* codes_a,
+                                      const float* scales_a, const int8_t* codes_b, const float* scales_b, sbn_act act,
+                                      const void* gain, bool gain_f32, int64_t T, int64_t K, float eps, void* dA,
+                                      int64_t ldda, void* dB, int64_t lddb, float* dgain, void* ws, hipStream_t st) {
+  const BwdArgs P{dY, nullptr, gain, codes_a, codes_b, scales_a, scales_b, dA, dB, (float*)ws, lddy, 0, ldda, lddb, T,
+                  (int)K, eps, gain_f32};
+  const char* name = "activation_grad";
+  return act == SBN_RELU2 ? backward<ROW_RELU2>(name, P, f32, dgain, st) : backward<ROW_SILU>(name, P, f32, dgain, st);
+}
+
+}  // namespace sbn

@@ -25,94 +25,10 @@
 // a thread holds four chunks, and of the six kernels four keep 76 to 216 bytes a
 // lane in scratch memory: K = 28672 104 / 99 / 140 us (4.0, 4.7, 3.4 TB/s), float32
 // 244 / 241 / 308 (3.1, 3.9, 3.1).
-#include "train_internal.h"
+#include "row_ops.h"
 
 namespace sbn {
 namespace {
-
-constexpr float U_FLOOR = 0x1p-100f;   // least row maximum told from 0 (127 / a stays finite)
-
-// ---------------------------------------------------------------- 8 elements of a row
-template <bool F32>
-struct Vec8 {
-  uint4 a, b;                          // b: elements 4..7 of float32 rows
-  __device__ void load(const void* p, int64_t i) {
-    if (F32) {
-      a = ((const uint4*)p)[2 * i];
-      b = ((const uint4*)p)[2 * i + 1];
-    } else {
-      a = ((const uint4*)p)[i];
-    }
-  }
-  __device__ void to(float* v) const {
-    if (F32) {
-      v[0] = __uint_as_float(a.x), v[1] = __uint_as_float(a.y), v[2] = __uint_as_float(a.z), v[3] = __uint_as_float(a.w);
-      v[4] = __uint_as_float(b.x), v[5] = __uint_as_float(b.y), v[6] = __uint_as_float(b.z), v[7] = __uint_as_float(b.w);
-    } else {
-      const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        v[2 * i] = __uint_as_float(w[i] << 16);
-        v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-      }
-    }
-  }
-  __device__ void from(const float* v) {
-    if (F32) {
-      a = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
-      b = make_uint4(__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7]));
-    } else {
-      a = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
-    }
-  }
-  __device__ void store(void* p, int64_t i) const {
-    if (F32) {
-      ((uint4*)p)[2 * i] = a;
-      ((uint4*)p)[2 * i + 1] = b;
-    } else {
-      ((uint4*)p)[i] = a;
-    }
-  }
-};
-
-__device__ inline void gain8(const void* gain, bool f32, int64_t i, float* v) {
-  if (f32) {
-    Vec8<true> g;
-    g.load(gain, i);
-    g.to(v);
-  } else {
-    Vec8<false> g;
-    g.load(gain, i);
-    g.to(v);
-  }
-}
-
-// 8 codes rint((127 u) / a), rcp = 127 / a to two units in the last place.  Added
-// to 1.5 2^23, u rcp is rounded to an integer, whose byte the sum's lowest is; u
-// rcp is off by under 2^-15.  If one of the 8 lies within 2^-14 of a half-integer,
-// all are divided, correctly rounded, both sides scaled so that 127 u is finite
-// (about one wave in 17 does).
-__device__ inline uint2 codes8(const float* u, float rcp, float a) {
-  constexpr float SHIFT = 12582912.0f;
-  float q[8], half = 0.0f;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    q[j] = fmaf(u[j], rcp, SHIFT);
-    half = fmaxf(half, fabsf(fmaf(u[j], rcp, SHIFT - q[j])));
-  }
-  if (half > 0.5f - 0x1p-14f) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) q[j] = rintf((127.0f * (u[j] * 0x1p-8f)) / (a * 0x1p-8f)) + SHIFT;
-  }
-  uint32_t o[2];
-#pragma unroll
-  for (int j = 0; j < 2; ++j) {                      // the four lowest bytes
-    const uint32_t lo = __builtin_amdgcn_perm(__float_as_uint(q[4 * j + 1]), __float_as_uint(q[4 * j]), 0x0c0c0400u);
-    const uint32_t hi = __builtin_amdgcn_perm(__float_as_uint(q[4 * j + 3]), __float_as_uint(q[4 * j + 2]), 0x0c0c0400u);
-    o[j] = __builtin_amdgcn_perm(hi, lo, 0x05040100u);
-  }
-  return make_uint2(o[0], o[1]);
-}
 
 // ---------------------------------------------------------------- forward
 struct FwdArgs {
@@ -358,10 +274,6 @@ __global__ __launch_bounds__(256) void rmsnorm_dgain_kernel(const float* __restr
   if (r == 0 && k < K) *(v4f*)(dgain + k) = sm[0][q];
 }
 
-// threads of a block for n chunks at CH a thread
-int threads_for(int n, int ch) { return (int)round_up(cdiv(n, ch), 64); }
-int chunks_for(int n) { return n <= 512 ? 1 : n <= 2048 ? 2 : 4; }
-
 // Blocks of the gradient: 16 waves a compute unit, but a block's partial of dgain
 // costs as much traffic as two rows in 16 bits, so at least 8 rows a block where
 // that leaves one block a compute unit.  (bf16, microseconds at 256 / 512 / 1024
@@ -371,12 +283,15 @@ int chunks_for(int n) { return n <= 512 ? 1 : n <= 2048 ? 2 : 4; }
 // T = 1021, K = 4096 15.0 / 14.4 / 12.5, float32 17.0 / 16.4 / 14.4, K = 1024 10.1 / 9.8
 // / 7.9; T = 333, K = 2560 9.3 / 7.9 / 8.2, float32 9.8 / 8.3 / 8.6; 64 rows and fewer
 // one a block in any case.)
-int bwd_blocks(int64_t T, int64_t K) {
+// (in the namespace: the gradients from checkpoints go by the same rule)
+}  // namespace
+int norm_grad_blocks(int64_t T, int64_t K) {
   const int n = (int)(K / 8), most = 256 * 16 / (threads_for(n, chunks_for(n)) / 64);
   int64_t g = T / 8 < 256 ? 256 : T / 8;
   if (g > most) g = most;
   return (int)(g < T ? g : T);
 }
+namespace {
 
 constexpr int64_t GRID_MAX = 1 << 20;               // blocks; rows beyond are taken in further rounds
 
@@ -426,13 +341,19 @@ hipError_t launch_rmsnorm(const void* X, int64_t ldx, const void* res, int64_t l
   return hipGetLastError();
 }
 
-size_t rmsnorm_bwd_ws_bytes(int64_t T, int64_t K) { return align256((size_t)bwd_blocks(T, K) * (size_t)K * sizeof(float)); }
+size_t rmsnorm_bwd_ws_bytes(int64_t T, int64_t K) { return align256((size_t)norm_grad_blocks(T, K) * (size_t)K * sizeof(float)); }
+
+hipError_t launch_norm_dgain(const float* part, int64_t T, int64_t K, float* dgain, hipStream_t st) {
+  SBN_LAUNCH("rmsnorm_dgain", rmsnorm_dgain_kernel, dim3((unsigned)cdiv(K, 16)), dim3(256), 0, st, part,
+             norm_grad_blocks(T, K), (int)K, dgain);
+  return hipGetLastError();
+}
 
 hipError_t launch_rmsnorm_backward(const void* dY, int64_t lddy, const void* H, int64_t ldh, const void* dH,
                                    int64_t lddh, bool f32, const void* gain, bool gain_f32, const float* rstd,
                                    int64_t T, int64_t K, void* dX, int64_t lddx, float* dgain, void* ws,
                                    hipStream_t st) {
-  const int blocks = bwd_blocks(T, K);
+  const int blocks = norm_grad_blocks(T, K);
   if (T > 0) {
     const BwdArgs A{dY, H, dH, gain, rstd, dX, (float*)ws, lddy, ldh, lddh, lddx, T, (int)K, gain_f32};
     if (f32) pick_bwd<true>(A, blocks, st);
@@ -440,9 +361,7 @@ hipError_t launch_rmsnorm_backward(const void* dY, int64_t lddy, const void* H, 
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  SBN_LAUNCH("rmsnorm_dgain", rmsnorm_dgain_kernel, dim3((unsigned)cdiv(K, 16)), dim3(256), 0, st, (const float*)ws,
-             blocks, (int)K, dgain);
-  return hipGetLastError();
+  return launch_norm_dgain((const float*)ws, T, K, dgain, st);
 }
 
 }  // namespace sbn
