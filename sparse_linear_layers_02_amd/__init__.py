@@ -709,6 +709,15 @@ __all__ += [
 ]
 
 
+# the head as a distribution over tokens (include/sbn_score.h)
+from .scoring import (  # noqa: E402,F401
+    SBN_LOGPROBS_MAX_TOP, sbn_token_logprobs, sbn_token_logprobs_backward, sbn_token_logprobs_workspace_bytes,
+    score_header_symbols)
+
+__all__ += ["SBN_LOGPROBS_MAX_TOP", "sbn_token_logprobs", "sbn_token_logprobs_backward",
+            "sbn_token_logprobs_workspace_bytes", "score_header_symbols"]
+
+
 # what a training step keeps in 8 bits (include/sbn_keep.h)
 from .keeping import (  # noqa: E402,F401
     SBN_KEEP_BLOCK, SBN_RELU2, SBN_SILU, Kept8, keep_header_symbols, sbn_activation_backward, sbn_activation_quant,

@@ -20,7 +20,8 @@ BUILD = os.path.join(ROOT, "_build", "libsbn")
 LIB = os.path.join(PKG, "libsbn.so")
 
 SOURCES = ["api.cpp", "pack.hip", "act_quant.hip", "gemm.hip", "gemv.hip", "backward.hip", "finite.hip",
-           "train_api.cpp", "rmsnorm.hip", "cross_entropy.hip", "adamw.hip", "keep_api.cpp", "kept_rows.hip"]
+           "train_api.cpp", "rmsnorm.hip", "cross_entropy.hip", "adamw.hip", "keep_api.cpp", "kept_rows.hip",
+           "score_api.cpp", "logprobs.hip"]
 ARCH = "gfx950"
 
 FLAGS = [

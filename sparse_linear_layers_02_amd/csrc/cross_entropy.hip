@@ -28,7 +28,7 @@
 // transposing LDS reads.  (Transposed copies of D, W and X in memory instead
 // took 2% of the largest training step and a quarter of one of 64 tokens.)
 #include "once_per_device.h"
-#include "train_internal.h"
+#include "score_internal.h"
 
 namespace sbn {
 namespace {
@@ -42,8 +42,11 @@ constexpr int64_t D_ELEMS = int64_t(1) << 28;
 constexpr int GMAX_WAVE = 1024;                     // tokens whose largest |dloss| a wave finds in two rounds of loads
 constexpr int CUS = 256;
 
-// PAIR: D in two bf16 numbers; OUT, ADD: C in bf16 or float32, ADD on top of Cin
-enum Epi { EPI_STATS, EPI_GRAD, EPI_GRAD_PAIR, EPI_OUT16, EPI_OUT32, EPI_ADD32 };
+// PAIR: D in two bf16 numbers; OUT, ADD: C in bf16 or float32, ADD on top of Cin.
+// SCORE, POLICY: the statistics and D of log probabilities with entropies; TOPS: and
+// each lane's two largest logits.
+enum Epi { EPI_STATS, EPI_SCORE, EPI_SCORE_TOPS, EPI_GRAD, EPI_GRAD_PAIR, EPI_POLICY, EPI_POLICY_PAIR, EPI_OUT16, EPI_OUT32,
+           EPI_ADD32 };
 
 struct GemmArgs {
   const uint16_t *A, *B;               // rows of lda, ldb
@@ -62,6 +65,13 @@ struct GemmArgs {
   float* target;                       // [nB] logit of the label
   const float *lse, *dloss;
   float* gmax;                         // max |dloss|; EPI_GRAD divides by it, EPI_OUT multiplies
+  // EPI_SCORE, EPI_POLICY: logits are scale times the sums
+  float scale;
+  float none;                          // the sum that stands for no entry, -1e30 in scaled exponents
+  float* mean;                         // beside stats: sum of exponential times scaled exponent
+  float2* tops;                        // [nB][ldt] a lane's two largest sums, the first's place among its MI * 4 in its last bits
+  int64_t ldt;
+  const float *entropy, *dentropy;     // dloss: of the log probabilities; either gradient may be NULL
   uint16_t* D;                         // [tpad][ldd], ldd a multiple of 256; 0 past the tokens and past nA
   int64_t ldd;
   int64_t dlow;                        // EPI_GRAD_PAIR: elements from D to what its rounding left
@@ -93,6 +103,18 @@ __device__ inline float max_dloss(const float* dloss, const void* labels, bool i
 #pragma unroll
     for (int k = 0; k < AHEAD; ++k)
       if (y[k] >= 0 && y[k] < V) m = fmaxf(m, fabsf(g[k]));
+  }
+  return wave_all(m, Max{});
+}
+
+// The same of log probabilities and entropies; a token without a target has its entropy alone
+__device__ inline float max_policy(const float* dlogp, const float* dentropy, const void* labels, bool is64, int V, int T,
+                                   int first, int step) {
+  float m = 0.0f;
+  for (int t = first; t < T; t += step) {
+    const int64_t y = dlogp && labels ? label_at(labels, is64, t) : -1;
+    const float g = y >= 0 && y < V ? dlogp[t] : 0.0f;
+    m = fmaxf(m, fmaxf(fabsf(g), dentropy ? fabsf(dentropy[t]) : 0.0f));
   }
   return wave_all(m, Max{});
 }
@@ -244,7 +266,9 @@ __global__ __launch_bounds__(64 * WA * WB, 1) void ce_gemm_kernel(GemmArgs P) {
   constexpr int HALF = HA::BYTES + HB::BYTES;
   constexpr int LA = TA / (16 * NW), LB = TB / (16 * NW);    // 1 KB loads per wave and half stage
   constexpr int LPH = LA + LB;
-  constexpr bool GRAD = EPI == EPI_GRAD || EPI == EPI_GRAD_PAIR;
+  constexpr bool POLICY = EPI == EPI_POLICY || EPI == EPI_POLICY_PAIR, PAIR = EPI == EPI_GRAD_PAIR || EPI == EPI_POLICY_PAIR;
+  constexpr bool GRAD = EPI == EPI_GRAD || PAIR || POLICY;
+  constexpr bool TOPS = EPI == EPI_SCORE_TOPS, SCORE = EPI == EPI_SCORE || TOPS, STATS = EPI == EPI_STATS || SCORE;
   constexpr int AHEAD = RING / 2;
   extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
   static_assert(RING >= 5 && RING % 2 == 1 && (RING - 3) * LPH < 64, "a stage, the next one and a half in flight");
@@ -337,7 +361,7 @@ __global__ __launch_bounds__(64 * WA * WB, 1) void ce_gemm_kernel(GemmArgs P) {
   // acc[i][j]: A outputs a0 + 16 (wa MI + i) + 4 (lane / 16) + 0..3, B output b0 + 16 (wb MJ + j) + lane % 16;
   // a tile's sums start from Cin, loaded at once (added at the end, each load waited for the stores before it)
   auto start_sums = [&](const Item& t, auto& P) {
-    const float* from = EPI == EPI_STATS || GRAD || (TRB && EPI != EPI_ADD32) ? nullptr : P.Cin;
+    const float* from = STATS || GRAD || (TRB && EPI != EPI_ADD32) ? nullptr : P.Cin;
 #pragma unroll
     for (int i = 0; i < MI; ++i)
 #pragma unroll
@@ -407,9 +431,13 @@ __global__ __launch_bounds__(64 * WA * WB, 1) void ce_gemm_kernel(GemmArgs P) {
   // launch of its own would take longer for
   float gmax = 1.0f;
   if (GRAD && P.nB <= GMAX_WAVE) {
-    gmax = uniform(max_dloss(P.dloss, P.labels, P.labels64, P.V, P.nB, lane, 64));
-    if (blockIdx.x == 0 && tid == 0) *P.gmax = gmax;
-  } else if (EPI != EPI_STATS && P.gmax) {
+    gmax = uniform(POLICY ? max_policy(P.dloss, P.dentropy, P.labels, P.labels64, P.V, P.nB, lane, 64)
+                          : max_dloss(P.dloss, P.labels, P.labels64, P.V, P.nB, lane, 64));
+    if (blockIdx.x == 0 && tid == 0) {
+      P.gmax[0] = gmax;
+      if (POLICY) P.gmax[1] = gmax * P.scale;        // the products' factor
+    }
+  } else if (!STATS && P.gmax) {
     gmax = uniform(*P.gmax);
   }
   const float ginv = gmax >= 0x1p-126f ? 1.0f / gmax : 0.0f;   // smaller ones have no quotient: gradients 0
@@ -470,14 +498,15 @@ __global__ __launch_bounds__(64 * WA * WB, 1) void ce_gemm_kernel(GemmArgs P) {
     const int aw = it.a0 + wa * MI * 16, bw = it.b0 + wb * MJ * 16;
     // a label's place from the lane's first entry: is it one of the lane's?  (Few waves hold one of their tokens' labels.)
     auto holds = [](int want) { return want >= 0 && want < MI * 16 && (want & 12) == 0; };
-    if (EPI == EPI_STATS) {
+    if (STATS) {
+      const float factor = SCORE ? P.scale * LOG2E : LOG2E;
       const bool ragged = aw + MI * 16 > P.nA;
       const int group = it.a0 / (MI * 16) + wa;
       int wants[MJ];
 #pragma unroll
       for (int j = 0; j < MJ; ++j) {                 // all loads before the first store: they would wait for it
         const int t = bw + 16 * j + l15;
-        const int64_t y = t < P.nB ? label_at(P.labels, P.labels64, t) : -1;
+        const int64_t y = t < P.nB && (!SCORE || P.labels) ? label_at(P.labels, P.labels64, t) : -1;
         wants[j] = y >= 0 && y < P.V ? (int)y - aw - l4 : -1;
       }
       asm volatile("" ::: "memory");
@@ -494,7 +523,7 @@ __global__ __launch_bounds__(64 * WA * WB, 1) void ce_gemm_kernel(GemmArgs P) {
           for (int i = 0; i < MI; ++i)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              if (16 * i + e >= left) c[i][e] = -INFINITY;
+              if (16 * i + e >= left) c[i][e] = SCORE ? P.none : -INFINITY;
         }
         const bool has = holds(want);
         if (__any(has)) {
@@ -505,33 +534,62 @@ __global__ __launch_bounds__(64 * WA * WB, 1) void ce_gemm_kernel(GemmArgs P) {
 #pragma unroll
             for (int e = 0; e < 4; ++e)
               if (at == 16 * i + e) hit = c[i][e];
-          if (has) P.target[t] = hit;
+          if (has) P.target[t] = SCORE ? hit * P.scale : hit;
+        }
+        if (TOPS) {
+          // float order is kept but for the last bits, which hold the place; the middle of the
+          // two so far and the new one is the second (and, of a tie, the second is as large)
+          float first = -3.0e38f, second = -3.0e38f;
+#pragma unroll
+          for (int i = 0; i < MI; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float key = __uint_as_float((__float_as_uint(c[i][e]) & ~(uint32_t)(MI * 4 - 1)) | (4 * i + e));
+              second = __builtin_amdgcn_fmed3f(first, second, key);
+              first = fmaxf(first, key);
+            }
+          if (t < P.nB) P.tops[(int64_t)t * P.ldt + group * 4 + g16] = make_float2(first, second);
         }
 #pragma unroll
         for (int i = 0; i < MI; ++i)
 #pragma unroll
           for (int e = 0; e < 4; ++e) m = fmaxf(m, c[i][e]);
         m = rows_all(m, Max{});
-        const float top = fmaxf(m * LOG2E, NONE);    // a group past the vocabulary has no logits
-        float sum = 0.0f;
+        const float top = fmaxf(m * factor, NONE);   // a group past the vocabulary has no logits
+        float sum = 0.0f, mean = 0.0f;
 #pragma unroll
         for (int i = 0; i < MI; ++i)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) sum += __builtin_amdgcn_exp2f(c[i][e] * LOG2E - top);
+          for (int e = 0; e < 4; ++e) {
+            const float d = c[i][e] * factor - top, x = __builtin_amdgcn_exp2f(d);
+            sum += x;
+            if (SCORE) mean += x * d;
+          }
         sum = rows_all(sum, Add{});
-        if (lane < 16 && t < P.nB) P.stats[(int64_t)group * P.nB + t] = make_float2(top, sum);
+        if (SCORE) mean = rows_all(mean, Add{});
+        const bool empty = SCORE && aw >= P.nA;      // `none` less its own rounding is nothing to sum
+        if (lane < 16 && t < P.nB) {
+          P.stats[(int64_t)group * P.nB + t] = empty ? make_float2(NONE, 0.0f) : make_float2(top, sum);
+          if (SCORE) P.mean[(int64_t)group * P.nB + t] = empty ? 0.0f : mean;
+        }
       }
     } else if (GRAD) {
+      const float factor = POLICY ? P.scale * LOG2E : LOG2E;
       int want[MJ];
-      float g[MJ], ls[MJ];
-      uint32_t kept[MJ];                             // all ones, or 0: what a token without a target holds gives 0
+      float g[MJ], ls[MJ], c0[MJ], c1[MJ];           // POLICY: D = p (c0 + c1 log2 p), and g at the token
+      uint32_t kept[MJ], used[MJ];                   // all ones, or 0: what a token without a target (POLICY: a gradient) holds gives 0
 #pragma unroll
       for (int j = 0; j < MJ; ++j) {                 // all loads before the first store: they would wait for it
         const int t = bw + 16 * j + l15;
         const bool live = t < P.nB;
-        const int64_t y = live ? label_at(P.labels, P.labels64, t) : -1;
+        const int64_t y = live && (!POLICY || P.labels) ? label_at(P.labels, P.labels64, t) : -1;
         kept[j] = y >= 0 && y < P.V ? ~0u : 0u;
-        g[j] = kept[j] ? P.dloss[t] * ginv : 0.0f, ls[j] = live ? P.lse[t] * LOG2E : 0.0f;
+        g[j] = kept[j] && (!POLICY || P.dloss) ? P.dloss[t] * ginv : 0.0f, ls[j] = live ? P.lse[t] * LOG2E : 0.0f;
+        if (POLICY) {
+          const float h = live && P.dentropy ? P.dentropy[t] * ginv : 0.0f;
+          c0[j] = -(g[j] + (h != 0.0f ? h * P.entropy[t] : 0.0f)), c1[j] = -LN2 * h;
+          used[j] = g[j] != 0.0f || h != 0.0f ? ~0u : 0u;
+        }
         want[j] = kept[j] ? (int)y - P.v0 - aw - l4 : -1;
       }
       asm volatile("" ::: "memory");
@@ -548,7 +606,11 @@ __global__ __launch_bounds__(64 * WA * WB, 1) void ce_gemm_kernel(GemmArgs P) {
             for (int h = 0; h < 2; ++h) {
               const v4f c = fetch(acc[i + h][j]);
 #pragma unroll
-              for (int e = 0; e < 4; ++e) d[h][e] = __builtin_amdgcn_exp2f(c[e] * LOG2E - ls[j]);
+              for (int e = 0; e < 4; ++e) {
+                const float z = c[e] * factor - ls[j];
+                d[h][e] = __builtin_amdgcn_exp2f(z);
+                if (POLICY) d[h][e] *= fmaf(c1[j], z, c0[j]);
+              }
             }
             if (hits) {
               const int at = rarely(want[j]);
@@ -556,13 +618,13 @@ __global__ __launch_bounds__(64 * WA * WB, 1) void ce_gemm_kernel(GemmArgs P) {
               for (int h = 0; h < 2; ++h)
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                  if (at == 16 * (i + h) + e) d[h][e] -= 1.0f;
+                  if (at == 16 * (i + h) + e) d[h][e] += POLICY ? g[j] : -1.0f;
             }
 #pragma unroll
             for (int h = 0; h < 2; ++h)
 #pragma unroll
               for (int e = 0; e < 4; ++e)            // (a select became a branch for each element)
-                d[h][e] = __uint_as_float(__float_as_uint(g[j] * d[h][e]) & kept[j]);
+                d[h][e] = __uint_as_float(__float_as_uint(POLICY ? d[h][e] : g[j] * d[h][e]) & (POLICY ? used[j] : kept[j]));
             if (ragged) {
               const int left = rarely(P.nA - aw - l4);
 #pragma unroll
@@ -572,7 +634,7 @@ __global__ __launch_bounds__(64 * WA * WB, 1) void ce_gemm_kernel(GemmArgs P) {
                   if (16 * (i + h) + e >= left) d[h][e] = 0.0f;
             }
             *(uint4*)(row + 16 * i) = pack_pair(d[0], d[1]);
-            if (EPI == EPI_GRAD_PAIR) {
+            if (PAIR) {
 #pragma unroll
               for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -658,17 +720,21 @@ __global__ __launch_bounds__(1024) void ce_join_kernel(const float2* __restrict_
   }
 }
 
-// max |dloss| over the tokens with a target, for more than GMAX_WAVE tokens
-__global__ __launch_bounds__(1024) void ce_gmax_kernel(const float* __restrict__ dloss,
+// max |dloss| over the tokens with a target (POLICY: of both gradients, and that times
+// the logits' scale), for more than GMAX_WAVE tokens
+template <bool POLICY>
+__global__ __launch_bounds__(1024) void ce_gmax_kernel(const float* __restrict__ dloss, const float* __restrict__ dentropy,
                                                        const void* __restrict__ labels, bool labels64, int V, int T,
-                                                       float* __restrict__ gmax) {
+                                                       float scale, float* __restrict__ gmax) {
   __shared__ float sm[16];
-  float m = max_dloss(dloss, labels, labels64, V, T, threadIdx.x, 1024);
+  float m = POLICY ? max_policy(dloss, dentropy, labels, labels64, V, T, threadIdx.x, 1024)
+                   : max_dloss(dloss, labels, labels64, V, T, threadIdx.x, 1024);
   if ((threadIdx.x & 63) == 0) sm[threadIdx.x >> 6] = m;
   __syncthreads();
   if (threadIdx.x == 0) {
     for (int w = 1; w < 16; ++w) m = fmaxf(m, sm[w]);
-    *gmax = m;
+    gmax[0] = m;
+    if (POLICY) gmax[1] = m * scale;
   }
 }
 
@@ -716,7 +782,8 @@ constexpr TileShape SHAPE[] = {{256, 256}, {128, 128}, {128, 64}};
 using Names = const char* const[3];
 #define SBN_TILE_NAMES(what) {what "_wide", what "_square", what "_flat"}
 constexpr Names LOGITS = SBN_TILE_NAMES("ce_logits"), DLOGITS = SBN_TILE_NAMES("ce_dlogits"),
-                DX = SBN_TILE_NAMES("ce_dx"), DW = SBN_TILE_NAMES("ce_dw");
+                DX = SBN_TILE_NAMES("ce_dx"), DW = SBN_TILE_NAMES("ce_dw"), SCORES = SBN_TILE_NAMES("logprob_logits"),
+                DPOLICY = SBN_TILE_NAMES("logprob_dlogits");
 #undef SBN_TILE_NAMES
 
 template <int WA, int WB, int MI, int MJ, int RING, int EPI, bool TRA, bool TRB>
@@ -816,7 +883,7 @@ CePlan ce_plan(int64_t T, int64_t V, int64_t K, bool pair) {
     o += align256(bytes);
     return at;
   };
-  L.gmax = take(sizeof(float));
+  L.gmax = take(2 * sizeof(float));
   L.d = take((size_t)L.tpad * L.piece * 2 * (pair ? 2 : 1));
   L.acc = take(L.pieces > 1 || pair ? (size_t)T * K * 4 : 0);
   const size_t px = L.x.splits > 1 ? (size_t)L.x.splits * T * K * 4 : 0;
@@ -875,22 +942,49 @@ hipError_t launch_ce(const uint16_t* X, int64_t ldx, const uint16_t* W, int64_t 
   return hipGetLastError();
 }
 
+// Of a token's tops: the tile's entries that a lane holds, in groups by wave and lane.
+LogitTops logit_tops(int64_t T, int64_t V, int64_t K) {
+  const Tile t = stats_tile(T, V, K);
+  return {t == WIDE ? 8 : t == SQUARE ? 4 : 2, stats_groups(T, V, K) * 4};
+}
+
+hipError_t launch_logits(const uint16_t* X, int64_t ldx, const uint16_t* W, int64_t ldw, const void* tokens, bool tokens64,
+                         int64_t T, int64_t V, int64_t K, float scale, float* target, float2* stats, float* mean,
+                         float2* tops, hipStream_t st) {
+  GemmArgs P{};
+  P.A = W, P.lda = ldw, P.nA = P.mA = (int)V;
+  P.B = X, P.ldb = ldx, P.nB = P.mB = (int)T;
+  P.steps = (int)(K / BK), P.splits = 1;
+  P.labels = tokens, P.labels64 = tokens64, P.V = (int)V;
+  P.target = target, P.stats = stats, P.mean = mean, P.tops = tops;
+  P.ldt = logit_tops(T, V, K).groups;
+  P.scale = scale, P.none = -1e30f / (scale * LOG2E);
+  const Tile t = stats_tile(T, V, K);
+  return tops ? gemm<EPI_SCORE_TOPS>(SCORES, t, P, st) : gemm<EPI_SCORE>(SCORES, t, P, st);
+}
+int64_t logit_groups(int64_t T, int64_t V, int64_t K) { return stats_groups(T, V, K); }
+
 size_t ce_bwd_ws_bytes(int64_t T, int64_t V, int64_t K, bool pair) { return ce_plan(T, V, K, pair).total; }
 
-hipError_t launch_ce_backward(const uint16_t* X, int64_t ldx, const uint16_t* W, int64_t ldw, const void* labels,
-                              bool labels64, const float* lse, const float* dloss, int64_t T, int64_t V, int64_t K,
-                              void* dX, sbn_dtype dxdt, int64_t lddx, void* dW, sbn_dtype dwdt, int64_t lddw,
-                              void* ws, hipStream_t st) {
+hipError_t launch_ce_backward(const uint16_t* X, int64_t ldx, const uint16_t* W, int64_t ldw, const HeadGrad& H, int64_t T,
+                              int64_t V, int64_t K, void* dX, sbn_dtype dxdt, int64_t lddx, void* dW, sbn_dtype dwdt,
+                              int64_t lddw, void* ws, hipStream_t st) {
   const bool dx_f32 = dxdt != SBN_BF16, dw_f32 = dwdt != SBN_BF16;
   const bool dx_pair = dX && dxdt == SBN_F32_FINE, dw_pair = dW && dwdt == SBN_F32_FINE, pair = dx_pair || dw_pair;
   const CePlan L = ce_plan(T, V, K, pair);
   uint8_t* w = (uint8_t*)ws;
   uint16_t* D = (uint16_t*)(w + L.d);
   float *acc = (float*)(w + L.acc), *part = (float*)(w + L.part), *gmax = (float*)(w + L.gmax);
+  float* factor = H.policy ? gmax + 1 : gmax;        // of both products' sums
   const int64_t dlow = L.tpad * L.piece;
   hipError_t e;
   if (T > GMAX_WAVE) {
-    SBN_LAUNCH("ce_gmax", ce_gmax_kernel, dim3(1), dim3(1024), 0, st, dloss, labels, labels64, (int)V, (int)T, gmax);
+    if (H.policy)
+      SBN_LAUNCH("logprob_gmax", ce_gmax_kernel<true>, dim3(1), dim3(1024), 0, st, H.dloss, H.dentropy, H.labels, H.labels64,
+                 (int)V, (int)T, H.scale, gmax);
+    else
+      SBN_LAUNCH("ce_gmax", ce_gmax_kernel<false>, dim3(1), dim3(1024), 0, st, H.dloss, (const float*)nullptr, H.labels,
+                 H.labels64, (int)V, (int)T, 1.0f, gmax);
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
   for (int64_t i = 0; i < L.pieces; ++i) {
@@ -900,11 +994,13 @@ hipError_t launch_ce_backward(const uint16_t* X, int64_t ldx, const uint16_t* W,
     G.A = W + v0 * ldw, G.lda = ldw, G.nA = G.mA = (int)nv;
     G.B = X, G.ldb = ldx, G.nB = G.mB = (int)T;
     G.steps = (int)(K / BK), G.splits = 1;
-    G.labels = labels, G.labels64 = labels64, G.v0 = (int)v0, G.V = (int)V;
-    G.lse = lse, G.dloss = dloss, G.gmax = gmax;
+    G.labels = H.labels, G.labels64 = H.labels64, G.v0 = (int)v0, G.V = (int)V;
+    G.lse = H.lse, G.dloss = H.dloss, G.gmax = gmax;
+    G.scale = H.scale, G.entropy = H.entropy, G.dentropy = H.dentropy;
     G.D = D, G.ldd = L.piece, G.dlow = dlow, G.tpad = (int)L.tpad;
     const Tile tile = pick(nv, T, G.steps, false).tile;
-    e = pair ? gemm<EPI_GRAD_PAIR>(DLOGITS, tile, G, st) : gemm<EPI_GRAD>(DLOGITS, tile, G, st);
+    if (H.policy) e = pair ? gemm<EPI_POLICY_PAIR>(DPOLICY, tile, G, st) : gemm<EPI_POLICY>(DPOLICY, tile, G, st);
+    else e = pair ? gemm<EPI_GRAD_PAIR>(DLOGITS, tile, G, st) : gemm<EPI_GRAD>(DLOGITS, tile, G, st);
     if (e != hipSuccess) return e;
     for (int low = 0; dX && low <= (int)dx_pair; ++low) {
       GemmArgs P{};
@@ -913,7 +1009,7 @@ hipError_t launch_ce_backward(const uint16_t* X, int64_t ldx, const uint16_t* W,
       P.steps = (int)(vpad / BK), P.splits = L.x.splits <= P.steps ? L.x.splits : P.steps;
       const bool last = i + 1 == L.pieces && low == (int)dx_pair;
       P.Cin = i > 0 || low > 0 ? acc : nullptr, P.ldcin = K;
-      P.gmax = last ? gmax : nullptr;
+      P.gmax = last ? factor : nullptr;
       P.C = last ? dX : acc, P.ldc = last ? lddx : K;
       if ((e = product<false>(DX, L.x.tile, P, last ? dx_f32 : true, part, st)) != hipSuccess) return e;
     }
@@ -924,7 +1020,7 @@ hipError_t launch_ce_backward(const uint16_t* X, int64_t ldx, const uint16_t* W,
       P.steps = (int)(L.tpad / BK), P.splits = L.w.splits;
       P.C = (uint8_t*)dW + v0 * lddw * (dw_f32 ? 4 : 2), P.ldc = lddw;
       P.Cin = low > 0 ? (const float*)P.C : nullptr, P.ldcin = lddw;
-      P.gmax = low == (int)dw_pair ? gmax : nullptr;
+      P.gmax = low == (int)dw_pair ? factor : nullptr;
       if ((e = product<true>(DW, L.w.tile, P, dw_f32, part, st)) != hipSuccess) return e;
     }
   }

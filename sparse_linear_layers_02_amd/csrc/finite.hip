@@ -43,14 +43,14 @@ __global__ __launch_bounds__(256) void nonfinite_scan_kernel(const uint8_t* __re
   if (bad) flag[0] = 1;   // every writer stores the same value
 }
 
-// The tokens with a target among T: the vectors have the alignment of their
+// The tokens with a target among T (without labels: all of them): the vectors have the alignment of their
 // elements only, so one element a read.
 __global__ __launch_bounds__(256) void nonfinite_tokens_kernel(const float* __restrict__ x,
                                                                const void* __restrict__ labels, bool labels64,
                                                                int64_t V, int64_t T, int* flag) {
   bool bad = false;
   for (int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x; t < T; t += (int64_t)gridDim.x * 256) {
-    const int64_t y = labels64 ? ((const int64_t*)labels)[t] : (int64_t)((const int32_t*)labels)[t];
+    const int64_t y = !labels ? 0 : labels64 ? ((const int64_t*)labels)[t] : (int64_t)((const int32_t*)labels)[t];
     bad |= y >= 0 && y < V && (__float_as_uint(x[t]) & 0x7F800000u) == 0x7F800000u;
   }
   if (bad) flag[0] = 1;

@@ -95,7 +95,7 @@ bool gemm_uses_smfmac(int n, int m);
 // Synchronizes `st`.
 hipError_t scan_nonfinite(const void* x, int64_t rows, int64_t cols, int64_t ld, int elem_bytes, hipStream_t st,
                           bool* found);
-// The same among the T >= 1 values x[t] whose label is in [0, V).
+// The same among the T >= 1 values x[t] whose label is in [0, V) (labels NULL: all).
 hipError_t scan_nonfinite_tokens(const float* x, const void* labels, bool labels64, int64_t V, int64_t T,
                                  hipStream_t st, bool* found);
 size_t gemm_ws_bytes(int64_t T, int64_t R, int64_t K, int n, int m);

@@ -1,0 +1,33 @@
+// Launchers of the operators declared in include/sbn_score.h (T >= 1).
+#pragma once
+
+#include "sbn_score.h"
+#include "train_internal.h"
+
+namespace sbn {
+
+// ----------------------------------------------------------------- the logits' statistics (cross_entropy.hip)
+// Statistics come in logit_groups() groups of entries, [group][T]: (maximum, sum of
+// exponentials) and the sum of exponential times exponent, exponents times log2 e and
+// less the maximum.  `target` [T]: the token's logit.  tops (or NULL): per token
+// logit_tops().groups pairs of the largest and second largest of 4 * mi sums (logits
+// before their scale), the first's place in its last bits: place p of group g stands
+// for entry (g / 4) * 16 mi + 16 (p / 4) + 4 (g % 4) + p % 4.
+struct LogitTops {
+  int mi;
+  int64_t groups;
+};
+LogitTops logit_tops(int64_t T, int64_t V, int64_t K);
+int64_t logit_groups(int64_t T, int64_t V, int64_t K);
+hipError_t launch_logits(const uint16_t* X, int64_t ldx, const uint16_t* W, int64_t ldw, const void* tokens, bool tokens64,
+                         int64_t T, int64_t V, int64_t K, float scale, float* target, float2* stats, float* mean,
+                         float2* tops, hipStream_t st);
+
+// ----------------------------------------------------------------- logprobs.hip
+size_t logprobs_ws_bytes(int64_t T, int64_t V, int64_t K, int top);
+// tokens and logp may be NULL (both), entropy may be NULL
+hipError_t launch_logprobs(const uint16_t* X, int64_t ldx, const uint16_t* W, int64_t ldw, const void* tokens,
+                           bool tokens64, int64_t T, int64_t V, int64_t K, float scale, float* logp, float* entropy,
+                           float* lse, int top, int64_t* top_ids, float* top_logp, void* ws, hipStream_t st);
+
+}  // namespace sbn

@@ -183,8 +183,8 @@ sbn_status sbn_cross_entropy_backward(const uint16_t* X, int64_t ldx, const uint
   SBN_TRY(check_finite(fn, "X", X, T, K, ldx, 2, st));
   SBN_TRY(check_finite(fn, "W", W, V, K, ldw, 2, st));
   SBN_TRY(check_finite_tokens(fn, "dloss", dloss, labels, label_bytes == 8, V, T, st));
-  return hip_result(launch_ce_backward(X, ldx, W, ldw, labels, label_bytes == 8, lse, dloss, T, V, K, dX,
-                                       dxdt, lddx, dW, dwdt, lddw, ws, st),
+  return hip_result(launch_ce_backward(X, ldx, W, ldw, {labels, label_bytes == 8, lse, dloss}, T, V, K, dX, dxdt, lddx,
+                                       dW, dwdt, lddw, ws, st),
                     st, fn);
 }
 

@@ -71,10 +71,20 @@ size_t ce_bwd_ws_bytes(int64_t T, int64_t V, int64_t K, bool pair);
 hipError_t launch_ce(const uint16_t* X, int64_t ldx, const uint16_t* W, int64_t ldw, const void* labels,
                      bool labels64, int64_t T, int64_t V, int64_t K, float* loss, float* lse, void* ws,
                      hipStream_t st);
-hipError_t launch_ce_backward(const uint16_t* X, int64_t ldx, const uint16_t* W, int64_t ldw, const void* labels,
-                              bool labels64, const float* lse, const float* dloss, int64_t T, int64_t V, int64_t K,
-                              void* dX, sbn_dtype dxdt, int64_t lddx, void* dW, sbn_dtype dwdt, int64_t lddw,
-                              void* ws, hipStream_t st);
+// What the gradients of the logits come from: the losses' gradients, or, with `policy`,
+// those of log probabilities (dloss) and entropies, either of which may be NULL, of
+// logits times `scale`; labels may then be NULL too.
+struct HeadGrad {
+  const void* labels;
+  bool labels64;
+  const float *lse, *dloss;
+  bool policy = false;
+  float scale = 1.0f;
+  const float *entropy = nullptr, *dentropy = nullptr;
+};
+hipError_t launch_ce_backward(const uint16_t* X, int64_t ldx, const uint16_t* W, int64_t ldw, const HeadGrad& H, int64_t T,
+                              int64_t V, int64_t K, void* dX, sbn_dtype dxdt, int64_t lddx, void* dW, sbn_dtype dwdt,
+                              int64_t lddw, void* ws, hipStream_t st);
 // rows x len elements of `elem_bytes` at row stride ld, all set to 0
 hipError_t launch_zero_rows(void* p, int64_t rows, int64_t len, int64_t ld, int elem_bytes, hipStream_t st);
 

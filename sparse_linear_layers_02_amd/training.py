@@ -321,6 +321,24 @@ def sbn_cross_entropy(X, W, labels, *, loss=None, lse=None, ws=None, stream=None
     return loss, lse
 
 
+def _head_grad_out(t, name, need, dt, like, fn):
+    """A gradient of the head's, of type `dt` and the shape of `like`: `t`, checked, or a new one."""
+    torch = _torch()
+    types = {SBN_BF16: torch.bfloat16, SBN_F32: torch.float32, SBN_F32_FINE: torch.float32}
+    if dt not in types:
+        raise SbnError(fn, 6, f"{name}'s type must be SBN_BF16, SBN_F32 or SBN_F32_FINE, got {dt}")
+    if not need:
+        return None
+    if t is None:
+        return torch.empty(like.shape, dtype=types[dt], device=like.device)
+    if t.dtype != types[dt]:
+        raise SbnError(fn, 6, f"{name} must be {types[dt]}, got {t.dtype}")
+    if t.shape != like.shape or t.device != like.device:
+        raise SbnError(fn, 2, f"{name} must be {tuple(like.shape)} on {like.device}")
+    _matrix(t, name, fn)
+    return t
+
+
 def sbn_cross_entropy_backward(X, W, labels, lse, dloss, *, dxdt: int = SBN_BF16, dwdt: int = SBN_BF16, dX=None,
                                dW=None, need_dX: bool = True, need_dW: bool = True, ws=None, stream=None):
     """Gradients of the hidden states and of the head's weights from the
@@ -335,24 +353,8 @@ def sbn_cross_entropy_backward(X, W, labels, lse, dloss, *, dxdt: int = SBN_BF16
     T, V, K, lb = _head_args(fn, X, W, labels)
     _vector(lse, "lse", T, torch.float32, X.device, fn)
     _vector(dloss, "dloss", T, torch.float32, X.device, fn)
-    types = {SBN_BF16: torch.bfloat16, SBN_F32: torch.float32, SBN_F32_FINE: torch.float32}
-
-    def out(t, name, need, dt, like):
-        if dt not in types:
-            raise SbnError(fn, 6, f"{name}'s type must be SBN_BF16, SBN_F32 or SBN_F32_FINE, got {dt}")
-        if not need:
-            return None
-        if t is None:
-            return torch.empty(like.shape, dtype=types[dt], device=X.device)
-        if t.dtype != types[dt]:
-            raise SbnError(fn, 6, f"{name} must be {types[dt]}, got {t.dtype}")
-        if t.shape != like.shape or t.device != X.device:
-            raise SbnError(fn, 2, f"{name} must be {tuple(like.shape)} on {X.device}")
-        _matrix(t, name, fn)
-        return t
-
-    dX = out(dX, "dX", need_dX, dxdt, X)
-    dW = out(dW, "dW", need_dW, dwdt, W)
+    dX = _head_grad_out(dX, "dX", need_dX, dxdt, X, fn)
+    dW = _head_grad_out(dW, "dW", need_dW, dwdt, W, fn)
     if ws is not None:
         _given(ws, X.device, fn)
     raw = _raw_stream(X.device)

@@ -1,0 +1,114 @@
+"""The C ABI of include/sbn_score.h and its binding without a GPU: exported symbols, sizes and
+refusals, which come before any launch (fake device addresses that nothing dereferences)."""
+from __future__ import annotations
+
+import ctypes
+
+import pytest
+
+import sparse_linear_layers_02_amd as sbn
+from test_train_abi import ALIGN, BF16, DTYPE, F32, MIS, NULL, ODD, OK, P, P2, P3, SHAPE, VALUE, WS
+
+Q = [ctypes.c_void_p(0x400000 + 0x100000 * i) for i in range(8)]
+
+
+@pytest.fixture(scope="module")
+def L():
+    return sbn.lib()
+
+
+def test_exports_every_header_symbol(L):
+    names = sbn.score_header_symbols()
+    assert len(names) == 4 and all(hasattr(L, n) for n in names)
+    for other in (sbn.header_symbols, sbn.train_header_symbols, sbn.keep_header_symbols):
+        assert not set(names) & set(other())
+    ours = {n for n in dir(sbn.scoring) if n.startswith("sbn_") or n == "SBN_LOGPROBS_MAX_TOP"}
+    assert ours <= set(sbn.__all__) and all(getattr(sbn, n) is getattr(sbn.scoring, n) for n in ours)
+
+
+HEAD = [(dict(X=None), NULL), (dict(W=None), NULL), (dict(lse=None), NULL), (dict(ws=None), NULL), (dict(wsb=16), WS),
+        (dict(T=-1), SHAPE), (dict(V=0), SHAPE), (dict(V=1 << 31), SHAPE), (dict(K=96), SHAPE), (dict(ldx=120), SHAPE),
+        (dict(ldw=132), ALIGN), (dict(ldx=(1 << 22) + 8), SHAPE), (dict(T=1 << 27), SHAPE), (dict(T=1 << 24, V=1 << 20), SHAPE),
+        (dict(tb=2), DTYPE), (dict(X=MIS), ALIGN), (dict(W=MIS), ALIGN), (dict(tok=MIS), ALIGN), (dict(tb=4, tok=ODD), ALIGN),
+        (dict(lse=ODD), ALIGN), (dict(ws=MIS), ALIGN), (dict(scale=0.0), VALUE), (dict(scale=-1.0), VALUE),
+        (dict(scale=float("nan")), VALUE), (dict(scale=2.0 ** 21), VALUE), (dict(scale=float("inf")), VALUE)]
+
+
+def test_forward(L):
+    base = dict(X=P, ldx=128, W=P2, ldw=128, tok=P3, tb=8, T=5, V=1000, K=128, scale=1.0, logp=Q[0], ent=Q[1], lse=Q[2], top=3,
+                ids=Q[3], tlp=Q[4], ws=Q[5], wsb=1 << 40)
+
+    def call(**kw):
+        a = {**base, **kw}
+        return L.sbn_token_logprobs(*(a[k] for k in base), None)
+
+    assert call(T=0, X=None, W=None, tok=None, logp=None, lse=None) == OK
+    for kw, status in HEAD + [(dict(tok=None), NULL), (dict(logp=None), NULL), (dict(ids=None), NULL), (dict(tlp=None), NULL),
+                              (dict(top=-1), SHAPE), (dict(top=65), SHAPE), (dict(V=2), SHAPE), (dict(ids=MIS), ALIGN),
+                              (dict(tlp=ODD), ALIGN), (dict(ent=ODD), ALIGN), (dict(logp=Q[2]), SHAPE), (dict(ent=Q[2]), SHAPE),
+                              (dict(lse=P), SHAPE), (dict(tlp=P2), SHAPE), (dict(logp=P3), SHAPE)]:
+        assert call(**kw) == status, kw
+        assert L.sbn_last_error() != b""
+
+
+def test_backward(L):
+    base = dict(X=P, ldx=128, W=P2, ldw=128, tok=P3, tb=8, scale=1.0, lse=Q[0], ent=Q[1], dl=Q[2], dh=Q[3], T=5, V=1000, K=128,
+                dX=Q[4], dxdt=BF16, lddx=128, dW=Q[5], dwdt=F32, lddw=128, ws=Q[6], wsb=1 << 40)
+
+    def call(**kw):
+        a = {**base, **kw}
+        return L.sbn_token_logprobs_backward(*(a[k] for k in base), None)
+
+    assert call(T=0, X=None, W=None, tok=None, dl=None, dW=None) == OK and call(dX=None, dW=None) == OK
+    for kw, status in HEAD + [(dict(tok=None), NULL), (dict(ent=None), NULL), (dict(dl=ODD), ALIGN), (dict(dh=ODD), ALIGN),
+                              (dict(dxdt=2), DTYPE), (dict(dwdt=9), DTYPE), (dict(lddx=64), SHAPE), (dict(lddw=132), ALIGN),
+                              (dict(dX=MIS), ALIGN), (dict(dX=P), SHAPE), (dict(dW=P), SHAPE), (dict(dX=P2), SHAPE),
+                              (dict(dW=P2), SHAPE), (dict(dX=Q[5]), SHAPE)]:
+        assert call(**kw) == status, kw
+
+
+def test_workspaces():
+    wsb = sbn.sbn_token_logprobs_workspace_bytes
+    T, V, K = 8192, 262144, 4096
+    assert wsb(T, V, K) < T * V * 2 / 16 and wsb(T, V, K, 64) < T * V * 2 / 4 and wsb(T, V, K, 1) == wsb(T, V, K, 64)
+    assert wsb(T, V, K, 0, True) == sbn.sbn_cross_entropy_workspace_bytes(T, V, K, True)
+    assert wsb(0, V, K, 8) == 0 and wsb(0, V, K, 0, True) == 0
+    with pytest.raises(sbn.SbnError):
+        wsb(4, 20, 64, 21)
+
+
+def test_binding_refuses():
+    import torch
+    bf, f32, i64 = torch.bfloat16, torch.float32, torch.int64
+    z = lambda *s, dt=bf: torch.zeros(*s, dtype=dt)  # noqa: E731
+    v = lambda n: z(n, dt=f32)  # noqa: E731
+    X, W, y = z(4, 64), z(10, 64), z(4, dt=i64)
+    bad = [
+        lambda: sbn.sbn_token_logprobs(X, z(10, 128), y),
+        lambda: sbn.sbn_token_logprobs(X, z(10, 128)),
+        lambda: sbn.sbn_token_logprobs(z(4, 64, dt=f32), W),
+        lambda: sbn.sbn_token_logprobs(X, W, z(4, dt=torch.int16)),
+        lambda: sbn.sbn_token_logprobs(X, W, z(5, dt=i64)),
+        lambda: sbn.sbn_token_logprobs(X, W, logp=v(4)),
+        lambda: sbn.sbn_token_logprobs(X, W, y, top=11),
+        lambda: sbn.sbn_token_logprobs(X, z(100, 64), y, top=65),
+        lambda: sbn.sbn_token_logprobs(X, W, y, top=-1),
+        lambda: sbn.sbn_token_logprobs(X, W, y, top_ids=z(4, 3, dt=i64)),
+        lambda: sbn.sbn_token_logprobs(X, W, y, top=3, top_ids=z(4, 3, dt=torch.int32)),
+        lambda: sbn.sbn_token_logprobs(X, W, y, top=3, top_logp=z(4, 6, dt=f32)[:, ::2]),
+        lambda: sbn.sbn_token_logprobs(X, W, y, entropy=v(5)),
+        lambda: sbn.sbn_token_logprobs(X, W, y, ws=torch.zeros(1 << 20, dtype=torch.uint8)[::2]),
+        lambda: sbn.sbn_token_logprobs_backward(X, W, y, v(4), None, v(4), v(4)),
+        lambda: sbn.sbn_token_logprobs_backward(X, W, None, v(4), v(4), v(4)),
+        lambda: sbn.sbn_token_logprobs_backward(X, W, y, None, v(4), v(4)),
+        lambda: sbn.sbn_token_logprobs_backward(X, W, y, v(4), v(4), v(4), v(3)),
+        lambda: sbn.sbn_token_logprobs_backward(X, W, y, v(4), v(4), v(4), dX=z(4, 64, dt=f32)),
+        lambda: sbn.sbn_token_logprobs_backward(X, W, y, v(4), v(4), v(4), dxdt=2),
+        # right, but in host memory
+        lambda: sbn.sbn_token_logprobs(X, W, y),
+        lambda: sbn.sbn_token_logprobs_backward(X, W, y, v(4), v(4), v(4), v(4)),
+    ]
+    for i, f in enumerate(bad):
+        with pytest.raises(sbn.SbnError):
+            f()
+            raise AssertionError(f"case {i} was accepted")
