@@ -7,11 +7,10 @@
 // 2^(m - M) (q + (m - M) s).  Both terms of the entropy are of its own size, so a
 // distribution that is nearly certain loses nothing to a difference.
 //
-// Alternatives: of every 4 mi logits that a lane held, the two largest are kept in
-// float32.  The k-th largest of any partition's maxima is no larger than the k-th
+// Alternatives: of every 32 logits, the two largest are kept in float32.  The k-th largest of any partition's maxima is no larger than the k-th
 // largest logit, so a row's candidates are the firsts above such a bound, and, where
-// a second is above it as well, all of that lane's logits.  Candidates' sums are formed
-// again, in 64 bits, and ordered by them.
+// a second is above it as well, all 32.  Candidates' sums are formed again, in 64 bits,
+// and ordered by them.
 #include "score_internal.h"
 
 namespace sbn {
@@ -33,38 +32,63 @@ __device__ inline Stat join(Stat a, Stat b) {
   return {top, a.s * ea + b.s * eb, ea * (a.q + da * a.s) + eb * (b.q + db * b.s)};
 }
 
-struct JoinArgs {
+struct RowArgs {
   const float2* stats;
   const float *mean, *target;
   const void* tokens;
   bool tokens64;
-  int groups, first, T, V;             // first token of a launch
+  int groups, T, V;
   float *logp, *entropy, *lse;
+  // alternatives
+  const uint16_t *X, *W;
+  int64_t ldx, ldw;
+  int K, top;
+  LogitTops sets;
+  const float2* tops;
+  float scale;
+  int64_t* ids;
+  float* top_logp;
 };
+
+// a token's outputs from all its logits' statistics; returns lse
+__device__ inline float finish(const RowArgs& P, int64_t t, Stat a) {
+  const float ln = logf(a.s), l = a.m * LN2 + ln;
+  P.lse[t] = l;
+  if (P.entropy) P.entropy[t] = ln - (a.q / a.s) * LN2;
+  if (P.logp) {
+    const int64_t y = token_at(P.tokens, P.tokens64, t);
+    P.logp[t] = y >= 0 && y < P.V ? P.target[t] - l : 0.0f;
+  }
+  return l;
+}
+// every `step`-th group from `first` on, AHEAD loads in flight
+template <int AHEAD>
+__device__ inline Stat join_groups(const RowArgs& P, int64_t t, int first, int step) {
+  Stat a{NONE, 0.0f, 0.0f};
+  for (int g = first; g < P.groups; g += step * AHEAD) {
+    Stat x[AHEAD];
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k) {
+      const bool in = g + step * k < P.groups;
+      const int64_t at = (int64_t)(in ? g + step * k : g) * P.T + t;
+      const float2 ms = P.stats[at];
+      const float q = P.mean[at];
+      x[k] = in ? Stat{ms.x, ms.y, q} : Stat{NONE, 0.0f, 0.0f};
+    }
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k) a = join(a, x[k]);
+  }
+  return a;
+}
 
 // 16 tokens a block, 64 threads a token take every 64th group each, then the 64
 // triples are joined in a tree.
-__global__ __launch_bounds__(1024) void logprob_join_kernel(JoinArgs P) {
+__global__ __launch_bounds__(1024) void logprob_join_kernel(RowArgs P, int first) {
   __shared__ float sm[3][64][17];
   const int tl = threadIdx.x & 15, part = threadIdx.x >> 4;
-  const int t = P.first + blockIdx.x * 16 + tl;
+  const int t = first + blockIdx.x * 16 + tl;
   Stat a{NONE, 0.0f, 0.0f};
-  if (t < P.T) {
-    constexpr int AHEAD = 4;
-    for (int g = part; g < P.groups; g += 64 * AHEAD) {
-      Stat x[AHEAD];
-#pragma unroll
-      for (int k = 0; k < AHEAD; ++k) {
-        const bool in = g + 64 * k < P.groups;
-        const int64_t at = (int64_t)(in ? g + 64 * k : g) * P.T + t;
-        const float2 ms = P.stats[at];
-        const float q = P.mean[at];
-        x[k] = in ? Stat{ms.x, ms.y, q} : Stat{NONE, 0.0f, 0.0f};
-      }
-#pragma unroll
-      for (int k = 0; k < AHEAD; ++k) a = join(a, x[k]);
-    }
-  }
+  if (t < P.T) a = join_groups<4>(P, t, part, 64);
   auto put = [&](Stat x) { sm[0][part][tl] = x.m, sm[1][part][tl] = x.s, sm[2][part][tl] = x.q; };
   put(a);
   __syncthreads();
@@ -73,193 +97,235 @@ __global__ __launch_bounds__(1024) void logprob_join_kernel(JoinArgs P) {
     if (part < d) put(a = join(a, Stat{sm[0][part + d][tl], sm[1][part + d][tl], sm[2][part + d][tl]}));
     __syncthreads();
   }
-  if (part == 0 && t < P.T) {
-    const float ln = logf(a.s), l = a.m * LN2 + ln;
-    P.lse[t] = l;
-    if (P.entropy) P.entropy[t] = ln - (a.q / a.s) * LN2;
-    if (P.logp) {
-      const int64_t y = token_at(P.tokens, P.tokens64, t);
-      P.logp[t] = y >= 0 && y < P.V ? P.target[t] - l : 0.0f;
-    }
-  }
+  if (part == 0 && t < P.T) finish(P, t, a);
 }
 
 // ---------------------------------------------------------------- top alternatives
-struct TopArgs {
-  const uint16_t *X, *W;
-  int64_t ldx, ldw, groups;
-  int K, V, mi, T, top;
-  const float2* tops;
-  const float* lse;
-  float scale;
-  int64_t* ids;
-  float* logp;
-};
-
-// sum_k x w in 64 bits and sum_k |x w|, of a wave
+// sum_k x w in 64 bits and sum_k |x w|, of a wave; W's loads of 4096 entries at once
 __device__ inline double exact_sum(const uint16_t* x, const uint16_t* w, int K, float& size) {
-  const int lane = threadIdx.x & 63;
-  double s = 0.0;
+  constexpr int AHEAD = 8;
+  const int lane = threadIdx.x & 63, n = K / 8;
+  double s0 = 0.0, s1 = 0.0;
   float a = 0.0f;
-#pragma unroll 2
-  for (int c = lane; c < K / 8; c += 64) {
-    const uint4 xv = ((const uint4*)x)[c], wv = ((const uint4*)w)[c];
-    const uint32_t xs[4] = {xv.x, xv.y, xv.z, xv.w}, ws[4] = {wv.x, wv.y, wv.z, wv.w};
+#pragma unroll 1
+  for (int c0 = lane; c0 < n; c0 += 64 * AHEAD) {
+    v4i wv[AHEAD];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {                    // products of bf16 are exact in float32
-      const float lo = __uint_as_float(xs[j] << 16) * __uint_as_float(ws[j] << 16);
-      const float hi = __uint_as_float(xs[j] & 0xFFFF0000u) * __uint_as_float(ws[j] & 0xFFFF0000u);
-      s += (double)lo;
-      s += (double)hi;
-      a += fabsf(lo) + fabsf(hi);
+    for (int k = 0; k < AHEAD; ++k) {
+      wv[k] = (v4i){0, 0, 0, 0};
+      if (c0 + 64 * k < n) wv[k] = ((const v4i*)w)[c0 + 64 * k];
+    }
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k) {
+      const v4i xv = ((const v4i*)x)[c0 + 64 * k < n ? c0 + 64 * k : c0];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {                  // products of bf16 are exact in float32
+        const float lo = __uint_as_float((uint32_t)xv[j] << 16) * __uint_as_float((uint32_t)wv[k][j] << 16);
+        const float hi = __uint_as_float(xv[j] & 0xFFFF0000u) * __uint_as_float(wv[k][j] & 0xFFFF0000u);
+        s0 += (double)lo;
+        s1 += (double)hi;
+        a += fabsf(lo) + fabsf(hi);
+      }
     }
   }
+  double s = s0 + s1;
 #pragma unroll
   for (int d = 32; d >= 1; d >>= 1) s += __shfl_xor(s, d);
   size = wave_all(a, Add{});
   return s;
 }
 
-// NT threads take a token.  LDS atomics deal out places in a queue, whose order does
-// not matter: candidates are ordered by (sum, index) in the end.
-template <int NT>
-__global__ __launch_bounds__(NT) void logprob_top_kernel(TopArgs P) {
+// A float that at least k of 256 reach (-Inf if fewer than k are above it), within 2^-11 of
+// the k-th largest: the leading bits of the order-preserving integers, one at a time,
+// as long as k are no smaller.  Each wave for itself.  (Counting for each of the 256
+// how many are larger took 12.5 us of one token's 23.)
+__device__ inline float reached_by(const float* slot, int k) {
+  constexpr uint32_t LEAST = 0x00800000u;            // the integers of -Inf and below
+  const v4f o = *(const v4f*)(slot + 4 * (threadIdx.x & 63));
+  uint32_t key[4], found = 0;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const uint32_t u = __float_as_uint(o[e]);
+    key[e] = u & 0x80000000u ? ~u : u | 0x80000000u;
+  }
+#pragma unroll 1
+  for (uint32_t bit = 0x80000000u; bit >= 1u << 12; bit >>= 1) {
+    int n = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) n += (int)__popcll(__ballot(key[e] >= (found | bit)));
+    if (n >= k) found |= bit;
+  }
+  return found < LEAST ? -INFINITY : __uint_as_float(found & 0x80000000u ? found ^ 0x80000000u : ~found);
+}
+
+// NT threads take a token.  JOIN: they join its statistics as well (few tokens: a
+// launch less, and all of a block's threads on one token).  LDS atomics deal out
+// places in a queue, whose order does not matter: candidates are ordered by (sum,
+// index) in the end.  The code is kept short, without unrolling: one token's block
+// fetches each line of it for the first time.
+template <int NT, bool JOIN>
+__global__ __launch_bounds__(NT) void logprob_top_kernel(RowArgs P) {
   constexpr int WAVES = NT / 64, SLOTS = 256, QUEUE = 1024, BATCH = 256, MOST = SBN_LOGPROBS_MAX_TOP;
+  constexpr int HELD = 4;
   static_assert(NT % SLOTS == 0 && NT <= QUEUE, "threads");
-  __shared__ float slot[NT];
-  __shared__ float lower;
-  __shared__ uint32_t singles, wholes, largest;      // queued entries, queued groups, bits of the largest sum |x w|
+  __shared__ __attribute__((aligned(16))) float slot[NT];
+  __shared__ float log_sum;
+  __shared__ Stat stat[WAVES];
+  __shared__ uint32_t singles, wholes, largest;      // queued entries, queued sets, bits of the largest sum |x w|
   __shared__ int single[QUEUE], whole[QUEUE];
   __shared__ double value[MOST + BATCH];             // the best so far in order, then a batch
   __shared__ int index[MOST + BATCH];
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
-  const int per = 4 * P.mi, top = P.top;
+  const int top = P.top, n = P.sets.groups;
+  const LogitTops sets = P.sets;
 
-  for (int64_t t = blockIdx.x; t < P.T; t += gridDim.x) {
-    const float2* row = P.tops + t * P.groups;
+  for (int t = blockIdx.x; t < P.T; t += gridDim.x) {
+    const float2* row = P.tops + (int64_t)t * n;
     const uint16_t* x = P.X + t * P.ldx;
+    float firsts[HELD];                              // loaded before the statistics are waited for
+#pragma unroll
+    for (int k = 0; k < HELD; ++k) firsts[k] = top && tid + k * NT < n ? row[tid + k * NT].x : -INFINITY;
+    if (JOIN) {
+      Stat a = join_groups<2>(P, t, tid, NT);
+      auto over_lanes = [&](int d) {
+#pragma unroll 1
+        for (; d >= 1; d >>= 1) a = join(a, Stat{__shfl_xor(a.m, d), __shfl_xor(a.s, d), __shfl_xor(a.q, d)});
+      };
+      over_lanes(32);
+      if (lane == 0) stat[wave] = a;
+      __syncthreads();
+      if (wave == 0) {
+        a = stat[lane & (WAVES - 1)];
+        over_lanes(WAVES / 2);
+        if (tid == 0) log_sum = finish(P, t, a);
+      }
+      if (!top) {
+        __syncthreads();
+        continue;
+      }
+    } else if (tid == 0) {
+      log_sum = P.lse[t];
+    }
     // a bound that at least top + 2 firsts reach, if there are as many: the places past
     // the top itself leave room for the margin below, which then rarely asks for more
-    float m = -INFINITY;
-    for (int64_t g = tid; g < P.groups; g += NT) m = fmaxf(m, row[g].x);
-    bool any = false;                                // a row of zeros (padding) makes all logits equal: the first ones win
+    float m = firsts[0];
+#pragma unroll
+    for (int k = 1; k < HELD; ++k) m = fmaxf(m, firsts[k]);
+#pragma unroll 4
+    for (int g = tid + HELD * NT; g < n; g += NT) m = fmaxf(m, row[g].x);
+    bool any = false;
+#pragma unroll 1
     for (int c = tid; c < P.K / 8; c += NT) {
-      const uint4 v = ((const uint4*)x)[c];
-      any |= ((v.x | v.y | v.z | v.w) & 0x7FFF7FFFu) != 0;
-    }
-    if (!__syncthreads_or(any)) {
-      for (int i = tid; i < top; i += NT) P.ids[t * top + i] = i, P.logp[t * top + i] = -P.lse[t];
-      continue;
+      const v4i v = ((const v4i*)x)[c];
+      any |= ((v[0] | v[1] | v[2] | v[3]) & 0x7FFF7FFF) != 0;
     }
     slot[tid] = m;
-    if (tid == 0) lower = -INFINITY;
-    __syncthreads();
+    if (!__syncthreads_or(any)) {                    // a row of zeros (padding): all logits are equal, the first ones win
+      for (int i = tid; i < top; i += NT) P.ids[(int64_t)t * top + i] = i, P.top_logp[(int64_t)t * top + i] = -log_sum;
+      __syncthreads();
+      continue;
+    }
     if (NT > SLOTS) {
       if (tid < SLOTS)
+#pragma unroll
         for (int i = 1; i < NT / SLOTS; ++i) m = fmaxf(m, slot[tid + i * SLOTS]);
       __syncthreads();
       if (tid < SLOTS) slot[tid] = m;
       __syncthreads();
     }
-    if (tid < SLOTS) {
-      int better = 0;
-#pragma unroll 4
-      for (int i = 0; i < SLOTS; i += 4) {
-        const v4f o = *(const v4f*)(slot + i);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) better += o[e] > m || (o[e] == m && i + e < tid);
-      }
-      if (better == top + 1) lower = m;
-    }
-    __syncthreads();
-    float bound = lower;
-
-    auto entry = [&](int64_t g, int p) { return (int)((g >> 2) * (16 * P.mi) + 16 * (p >> 2) + 4 * (g & 3) + (p & 3)); };
-    auto put = [&](int64_t g, int limit) {           // a group's candidates into the queues
-      const float2 f = row[g];
-      if (f.y >= bound) {
-        const uint32_t at = atomicAdd(&wholes, 1u);
-        if (at < (uint32_t)limit) whole[at] = (int)g;
-      } else if (f.x >= bound) {
-        const uint32_t at = atomicAdd(&singles, 1u);
-        if (at < (uint32_t)limit) single[at] = entry(g, (int)(__float_as_uint(f.x) & (uint32_t)(per - 1)));
-      }
-    };
+    // candidates are those from bound to over
+    float bound = reached_by(slot, top + 2), over = INFINITY;
     int have = 0;
-    // n entries, the i-th by `name` (or none: < 0), into the best
-    auto take = [&](int n, auto name) {
-      for (int i = wave; i < n; i += WAVES) {
-        const int v = __builtin_amdgcn_readfirstlane(name(i));
-        float size = 0.0f;
-        double s = -INFINITY;
-        if (v >= 0) s = exact_sum(x, P.W + (int64_t)v * P.ldw, P.K, size);
-        if (lane == 0) {
-          value[have + i] = s, index[have + i] = v >= 0 ? v : 0x7FFFFFFF;
-          atomicMax(&largest, __float_as_uint(size));
+    if (tid == 0) largest = 0;
+    for (int round = 0; round < 16; ++round) {       // hardly ever a third
+      bool pieces = false;                           // as many equal logits that the queues do not hold all sets'
+      for (int b = 0; b < n;) {
+        if (tid == 0) singles = wholes = 0;
+        __syncthreads();
+        const int stop = pieces ? (n - b < NT ? n : b + NT) : n;
+#pragma unroll 1
+        for (int g = b + tid; g < stop; g += NT) {   // a set's candidates into the queues
+          const float2 f = row[g];
+          if (f.x < bound || f.y >= over) continue;  // none, or all of them before
+          if (f.y >= bound) {
+            const uint32_t at = atomicAdd(&wholes, 1u);
+            if (at < QUEUE) whole[at] = g;
+          } else if (f.x < over) {
+            const uint32_t at = atomicAdd(&singles, 1u);
+            if (at < QUEUE) single[at] = sets.entry(g, (int)(__float_as_uint(f.x) & (TOPS_OF - 1)));
+          }
         }
-      }
-      __syncthreads();
-      constexpr int EACH = (MOST + BATCH + NT - 1) / NT;
-      double s[EACH];
-      int v[EACH], rank[EACH];
-#pragma unroll
-      for (int k = 0; k < EACH; ++k) {
-        const int i = tid + k * NT;
-        rank[k] = MOST;
-        if (i < have + n) {
-          s[k] = value[i], v[k] = index[i];
-          rank[k] = 0;
-          for (int j = 0; j < have + n; ++j) rank[k] += value[j] > s[k] || (value[j] == s[k] && index[j] < v[k]);
+        __syncthreads();
+        const uint32_t ns = singles, nw = wholes;
+        __syncthreads();
+        if (!pieces && (ns > QUEUE || nw > QUEUE)) {
+          pieces = true;
+          continue;
         }
-      }
-      __syncthreads();
-      have = have + n < top ? have + n : top;
+        b = stop;
+        const int entries = (int)(ns + nw * TOPS_OF);
+#pragma unroll 1
+        for (int e = 0; e < entries; e += BATCH) {   // a batch of entries into the best so far
+          const int count = entries - e < BATCH ? entries - e : BATCH;
+#pragma unroll 1
+          for (int i = wave; i < count; i += WAVES) {
+            const int at = e + i - (int)ns;
+            int v;
+            if (at < 0) {
+              v = single[e + i];
+            } else {                                 // of a set whose first alone came before, without it
+              const int g = whole[at / TOPS_OF], p = at % TOPS_OF;
+              const float f = row[g].x;
+              v = f >= over && p == (int)(__float_as_uint(f) & (TOPS_OF - 1)) ? -1 : sets.entry(g, p);
+            }
+            v = __builtin_amdgcn_readfirstlane(v);
+            const bool real = (uint32_t)v < (uint32_t)P.V;   // and not past the vocabulary
+            float size = 0.0f;
+            double sum = -INFINITY;
+            if (real) sum = exact_sum(x, P.W + (int64_t)v * P.ldw, P.K, size);
+            if (!(sum == sum)) sum = -INFINITY;      // NaN (outside the contract): an order all the same
+            if (lane == 0) {
+              value[have + i] = sum, index[have + i] = real ? v : 0x7FFFFFFF;
+              atomicMax(&largest, __float_as_uint(size));
+            }
+          }
+          __syncthreads();
+          constexpr int EACH = (MOST + BATCH + NT - 1) / NT;
+          double sum[EACH];
+          int v[EACH], rank[EACH];
 #pragma unroll
-      for (int k = 0; k < EACH; ++k)
-        if (rank[k] < top) value[rank[k]] = s[k], index[rank[k]] = v[k];
-      __syncthreads();
-    };
-    auto empty_queues = [&](int ns, int nw) {
-      for (int b = 0; b < ns; b += BATCH) take(ns - b < BATCH ? ns - b : BATCH, [&](int i) { return single[b + i] < P.V ? single[b + i] : -1; });
-      const int groups = BATCH / per;                // of a batch
-      for (int b = 0; b < nw; b += groups)
-        take((nw - b < groups ? nw - b : groups) * per, [&](int i) {
-          const int v = entry(whole[b + i / per], i % per);
-          return v < P.V ? v : -1;
-        });
-    };
-    for (int round = 0; round < 4; ++round) {
-      have = 0;
-      if (tid == 0) singles = wholes = 0, largest = 0;
-      __syncthreads();
-      for (int64_t g = tid; g < P.groups; g += NT) put(g, QUEUE);
-      __syncthreads();
-      const uint32_t ns = singles, nw = wholes;
-      __syncthreads();
-      if (ns <= QUEUE && nw <= QUEUE) {
-        empty_queues((int)ns, (int)nw);
-      } else {                                       // as many equal logits: by pieces that fit
-        for (int64_t b = 0; b < P.groups; b += NT) {
-          if (tid == 0) singles = wholes = 0;
+          for (int k = 0; k < EACH; ++k) {
+            const int i = tid + k * NT;
+            rank[k] = MOST, sum[k] = 0.0, v[k] = 0;
+            if (i < have + count) {
+              sum[k] = value[i], v[k] = index[i];
+              rank[k] = 0;
+#pragma unroll 4
+              for (int j = 0; j < have + count; ++j)
+                rank[k] += (int)(value[j] > sum[k]) | ((int)(value[j] == sum[k]) & (int)(index[j] < v[k]));
+            }
+          }
           __syncthreads();
-          if (b + tid < P.groups) put(b + tid, QUEUE);
+          have = have + count < top ? have + count : top;
+#pragma unroll
+          for (int k = 0; k < EACH; ++k)
+            if (rank[k] < top) value[rank[k]] = sum[k], index[rank[k]] = v[k];
           __syncthreads();
-          const int n1 = (int)singles, n2 = (int)wholes;
-          __syncthreads();
-          empty_queues(n1, n2);
         }
       }
       // A logit that was left out is below `bound` in float32, so in 64 bits below it and a margin of
       // both sums' errors and of the last bits that hold its place.
+      if (have < top) break;                         // NaN again
       const double least = value[top - 1];
       const double margin = 2.0 * ((double)(P.K + 64) * 0x1p-24 * (double)__uint_as_float(largest) + 0x1p-17 * fabs(least));
-      if (bound == -INFINITY || (double)bound + margin <= least) break;
-      bound = __double2float_rd(least - 2.0 * margin);
+      if (bound == -INFINITY || !((double)bound + margin > least)) break;
+      over = bound, bound = __double2float_rd(least - margin);
       __syncthreads();                               // value and largest are read by all
     }
     for (int i = tid; i < top; i += NT) {
-      P.ids[t * top + i] = index[i];
-      P.logp[t * top + i] = (float)((double)P.scale * value[i] - (double)P.lse[t]);
+      const bool found = i < have && (uint32_t)index[i] < (uint32_t)P.V;   // always, of finite logits
+      P.ids[(int64_t)t * top + i] = found ? index[i] : 0;
+      P.top_logp[(int64_t)t * top + i] = found ? (float)((double)P.scale * value[i] - (double)log_sum) : NAN;
     }
     __syncthreads();
   }
@@ -280,10 +346,13 @@ Plan plan(int64_t T, int64_t V, int64_t K, int top) {
   L.target = take((size_t)T * sizeof(float));
   L.stats = take(n * sizeof(float2));
   L.mean = take(n * sizeof(float));
-  L.tops = take(top ? (size_t)logit_tops(T, V, K).groups * T * sizeof(float2) : 0);
+  L.tops = take(top ? (size_t)T * logit_tops(T, V, K).groups * sizeof(float2) : 0);
   L.total = o;
   return L;
 }
+
+// Tokens to whose statistics a block each is given: a round of blocks of 1024 threads.
+constexpr int64_t FEW_TOKENS = 256;
 
 }  // namespace
 
@@ -296,21 +365,21 @@ hipError_t launch_logprobs(const uint16_t* X, int64_t ldx, const uint16_t* W, in
   uint8_t* w = (uint8_t*)ws;
   float *target = (float*)(w + L.target), *mean = (float*)(w + L.mean);
   float2 *stats = (float2*)(w + L.stats), *tops = top ? (float2*)(w + L.tops) : nullptr;
-  hipError_t e = launch_logits(X, ldx, W, ldw, tokens, tokens64, T, V, K, scale, target, stats, mean, tops, st);
+  const hipError_t e = launch_logits(X, ldx, W, ldw, tokens, tokens64, T, V, K, scale, target, stats, mean, tops, st);
   if (e != hipSuccess) return e;
-  constexpr int64_t JOIN_TOKENS = 1 << 24;           // of a launch: fewer than 2^32 threads
-  for (int64_t t = 0; t < T; t += JOIN_TOKENS) {
-    const JoinArgs J{stats, mean, target, tokens, tokens64, (int)logit_groups(T, V, K), (int)t, (int)T, (int)V, logp, entropy,
-                     lse};
-    SBN_LAUNCH("logprob_join", logprob_join_kernel, dim3((unsigned)cdiv(T - t < JOIN_TOKENS ? T - t : JOIN_TOKENS, 16)),
-               dim3(1024), 0, st, J);
+  const RowArgs R{stats, mean, target, tokens, tokens64, (int)logit_groups(T, V, K), (int)T, (int)V, logp, entropy, lse, X, W,
+                  ldx, ldw, (int)K, top, logit_tops(T, V, K), tops, scale, top_ids, top_logp};
+  if (T <= FEW_TOKENS) {
+    SBN_LAUNCH("logprob_rows", (logprob_top_kernel<1024, true>), dim3((unsigned)T), dim3(1024), 0, st, R);
+    return hipGetLastError();
   }
-  if ((e = hipGetLastError()) != hipSuccess || !top) return e;
-  const LogitTops G = logit_tops(T, V, K);
-  const TopArgs A{X, W, ldx, ldw, G.groups, (int)K, (int)V, G.mi, (int)T, top, tops, lse, scale, top_ids, top_logp};
-  const unsigned blocks = (unsigned)(T < (1 << 20) ? T : (1 << 20));
-  if (T <= 256) SBN_LAUNCH("logprob_top", logprob_top_kernel<1024>, dim3(blocks), dim3(1024), 0, st, A);
-  else SBN_LAUNCH("logprob_top", logprob_top_kernel<256>, dim3(blocks), dim3(256), 0, st, A);
+  constexpr int64_t JOIN_TOKENS = 1 << 24;           // of a launch: fewer than 2^32 threads
+  for (int64_t t = 0; t < T; t += JOIN_TOKENS)
+    SBN_LAUNCH("logprob_join", logprob_join_kernel, dim3((unsigned)cdiv(T - t < JOIN_TOKENS ? T - t : JOIN_TOKENS, 16)),
+               dim3(1024), 0, st, R, (int)t);
+  if (top)
+    SBN_LAUNCH("logprob_top", (logprob_top_kernel<256, false>), dim3((unsigned)(T < (1 << 20) ? T : (1 << 20))), dim3(256), 0,
+               st, R);
   return hipGetLastError();
 }
 

@@ -10,13 +10,22 @@ namespace sbn {
 // Statistics come in logit_groups() groups of entries, [group][T]: (maximum, sum of
 // exponentials) and the sum of exponential times exponent, exponents times log2 e and
 // less the maximum.  `target` [T]: the token's logit.  tops (or NULL): per token
-// logit_tops().groups pairs of the largest and second largest of 4 * mi sums (logits
-// before their scale), the first's place in its last bits: place p of group g stands
-// for entry (g / 4) * 16 mi + 16 (p / 4) + 4 (g % 4) + p % 4.
+// logit_tops().groups pairs of the largest and second largest of TOPS_OF sums (logits
+// before their scale), the first's place in its last bits.  A set is what one lane
+// holds of a column, or two or four lanes where a lane holds less.
+constexpr int TOPS_OF = 32;
 struct LogitTops {
-  int mi;
-  int64_t groups;
+  int mi_log2;                         // a lane's 4 mi entries are 4 of each of mi fragments of 16
+  int groups;                          // of V / TOPS_OF, rounded up to whole tiles
+  // the vocabulary entry at place p of set g
+  __host__ __device__ int entry(int g, int p) const {
+    const int per = 2 + mi_log2;                                 // log2 of a lane's
+    const int lane = (g << (5 - per)) + (p >> per);              // counted through waves, 4 a column
+    p &= (1 << per) - 1;
+    return ((lane >> 2) << (4 + mi_log2)) + ((p >> 2) << 4) + ((lane & 3) << 2) + (p & 3);
+  }
 };
+static_assert(TOPS_OF == 32, "5 bits");
 LogitTops logit_tops(int64_t T, int64_t V, int64_t K);
 int64_t logit_groups(int64_t T, int64_t V, int64_t K);
 hipError_t launch_logits(const uint16_t* X, int64_t ldx, const uint16_t* W, int64_t ldw, const void* tokens, bool tokens64,

@@ -277,6 +277,11 @@ def test_ascending_and_descending_rows():
     assert torch.equal(sbn.sbn_token_logprobs(X, W, y, top=64)[3], want.expand(T, 64))
 
 
+def rows(T, top):
+    """The launches after the logits'."""
+    return {"logprob_rows": 1} if T <= 256 else {"logprob_join": 1, "logprob_top": 1} if top else {"logprob_join": 1}
+
+
 # tokens, entries, K: the tiles of the logits and of D
 @pytest.mark.parametrize("shape,tile", [((8100, 7000, 4096), "wide"), ((1285, 3664, 3136), "square"), ((65, 17007, 2112), "square"),
                                         ((16, 1796, 2112), "flat"), ((5000, 300, 320), "flat")])
@@ -286,9 +291,9 @@ def test_tiles(shape, tile):
     r = reference(X, W, y, 1.0, dl, dh)
     got, ran = launches(lambda: sbn.sbn_token_logprobs(X, W, y, top=10))
     check_forward(got, r, y, 10)
-    assert ran == {f"logprob_logits_{tile}": 1, "logprob_join": 1, "logprob_top": 1}
+    assert ran == {f"logprob_logits_{tile}": 1, **rows(T, True)}
     plain, ran = launches(lambda: sbn.sbn_token_logprobs(X, W, y))
-    assert ran == {f"logprob_logits_{tile}": 1, "logprob_join": 1}
+    assert ran == {f"logprob_logits_{tile}": 1, **rows(T, False)}
     assert all(bool((p == q).all()) for p, q in zip(got[:3], plain[:3]))
     (dX, dW), ran = launches(lambda: sbn.sbn_token_logprobs_backward(X, W, y, got[2], got[1], dl, dh))
     assert ran[f"logprob_dlogits_{tile}"] == 1
