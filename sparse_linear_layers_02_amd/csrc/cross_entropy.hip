@@ -44,7 +44,7 @@ constexpr int CUS = 256;
 
 // PAIR: D in two bf16 numbers; OUT, ADD: C in bf16 or float32, ADD on top of Cin.
 // SCORE, POLICY: the statistics and D of log probabilities with entropies; TOPS: and
-// the two largest logits of each TOPS_OF.
+// the two largest logits of each tops_of(MI).
 enum Epi { EPI_STATS, EPI_SCORE, EPI_SCORE_TOPS, EPI_GRAD, EPI_GRAD_PAIR, EPI_POLICY, EPI_POLICY_PAIR, EPI_OUT16, EPI_OUT32,
            EPI_ADD32 };
 
@@ -69,7 +69,7 @@ struct GemmArgs {
   float scale;
   float none;                          // the sum that stands for no entry, -1e30 in scaled exponents
   float* mean;                         // beside stats: sum of exponential times scaled exponent
-  float2* tops;                        // [nB][ldt] the two largest sums of each TOPS_OF, the first's place in its last bits
+  float2* tops;                        // [nB][ldt] the two largest sums of each set, the first's place in its last bits
   int64_t ldt;
   const float *entropy, *dentropy;     // dloss: of the log probabilities; either gradient may be NULL
   uint16_t* D;                         // [tpad][ldd], ldd a multiple of 256; 0 past the tokens and past nA
@@ -513,6 +513,41 @@ __global__ __launch_bounds__(64 * WA * WB, 1) void ce_gemm_kernel(GemmArgs P) {
 #pragma unroll
       for (int j = 0; j < MJ; ++j) {
         const int t = bw + 16 * j + l15, want = wants[j];
+        if (TOPS) {
+          // float order is kept but for the last bits, which hold the place; the middle of the
+          // two so far and the new one is the second (and, of a tie, the second is as large)
+          constexpr int LANES = tops_of(MI) / (MI * 4);   // lanes of a column that join
+          static_assert(LANES == 1 || LANES == 2, "a set is of one half of a column");
+          const uint32_t lane_bits = MI * 4 * (g16 & (LANES - 1));
+          float first = -3.0e38f, second = -3.0e38f;
+#pragma unroll
+          for (int i = 0; i < MI; ++i) {
+            v4f x = fetch(acc[i][j]);                // again below: held for both, 35 registers were spilled
+            if (ragged) {
+              const int left = rarely(P.nA - aw - l4);
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if (16 * i + e >= left) x[e] = P.none;
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float key = __uint_as_float((__float_as_uint(x[e]) & ~(uint32_t)(TOPS_MOST - 1)) | (4 * i + e));
+              second = __builtin_amdgcn_fmed3f(first, second, key);
+              first = fmaxf(first, key);
+            }
+          }
+          if (LANES > 1) {                           // in both, so that the first stays the larger
+            first = __uint_as_float(__float_as_uint(first) | lane_bits);
+            second = __uint_as_float(__float_as_uint(second) | lane_bits);
+            const auto f = __builtin_amdgcn_permlane16_swap(__float_as_uint(first), __float_as_uint(first), false, false);
+            const auto s = __builtin_amdgcn_permlane16_swap(__float_as_uint(second), __float_as_uint(second), false, false);
+            const float f0 = __uint_as_float(f[0]), f1 = __uint_as_float(f[1]);
+            second = fmaxf(fminf(f0, f1), fmaxf(__uint_as_float(s[0]), __uint_as_float(s[1])));
+            first = fmaxf(f0, f1);
+          }
+          if (t < P.nB && (g16 & (LANES - 1)) == 0)
+            P.tops[(int64_t)t * P.ldt + (group * 4 + g16) / LANES] = make_float2(first, second);
+        }
         float m = -INFINITY;
         v4f c[MI];
 #pragma unroll
@@ -535,44 +570,6 @@ __global__ __launch_bounds__(64 * WA * WB, 1) void ce_gemm_kernel(GemmArgs P) {
             for (int e = 0; e < 4; ++e)
               if (at == 16 * i + e) hit = c[i][e];
           if (has) P.target[t] = SCORE ? hit * P.scale : hit;
-        }
-        if (TOPS) {
-          // float order is kept but for the last bits, which hold the place; the middle of the
-          // two so far and the new one is the second (and, of a tie, the second is as large)
-          constexpr int LANES = TOPS_OF / (MI * 4);  // lanes of a column that join
-          static_assert(LANES == 1 || LANES == 2 || LANES == 4, "a set is of one column");
-          const uint32_t lane_bits = MI * 4 * (g16 & (LANES - 1));
-          float first = -3.0e38f, second = -3.0e38f;
-#pragma unroll
-          for (int i = 0; i < MI; ++i)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float key = __uint_as_float((__float_as_uint(c[i][e]) & ~(uint32_t)(TOPS_OF - 1)) | (4 * i + e));
-              second = __builtin_amdgcn_fmed3f(first, second, key);
-              first = fmaxf(first, key);
-            }
-          if (LANES > 1) {                           // in both, so that the first stays the larger
-            first = __uint_as_float(__float_as_uint(first) | lane_bits);
-            second = __uint_as_float(__float_as_uint(second) | lane_bits);
-          }
-          auto with = [&](float f, float s) {        // another lane's two
-            second = fmaxf(fminf(first, f), fmaxf(second, s));
-            first = fmaxf(first, f);
-          };
-          if (LANES > 1) {
-            const auto f = __builtin_amdgcn_permlane16_swap(__float_as_uint(first), __float_as_uint(first), false, false);
-            const auto s = __builtin_amdgcn_permlane16_swap(__float_as_uint(second), __float_as_uint(second), false, false);
-            first = __uint_as_float(f[0]), second = __uint_as_float(s[0]);
-            with(__uint_as_float(f[1]), __uint_as_float(s[1]));
-          }
-          if (LANES > 2) {
-            const auto f = __builtin_amdgcn_permlane32_swap(__float_as_uint(first), __float_as_uint(first), false, false);
-            const auto s = __builtin_amdgcn_permlane32_swap(__float_as_uint(second), __float_as_uint(second), false, false);
-            first = __uint_as_float(f[0]), second = __uint_as_float(s[0]);
-            with(__uint_as_float(f[1]), __uint_as_float(s[1]));
-          }
-          if (t < P.nB && (g16 & (LANES - 1)) == 0)
-            P.tops[(int64_t)t * P.ldt + (group * 4 + g16) / LANES] = make_float2(first, second);
         }
 #pragma unroll
         for (int i = 0; i < MI; ++i)
@@ -966,11 +963,12 @@ hipError_t launch_ce(const uint16_t* X, int64_t ldx, const uint16_t* W, int64_t 
   return hipGetLastError();
 }
 
-// Of a token's tops: the fragments of 16 entries that a wave holds, and the sets of TOPS_OF.
+// Of a token's tops: the fragments of 16 entries that a wave holds, and the sets.
 LogitTops logit_tops(int64_t T, int64_t V, int64_t K) {
   const Tile t = stats_tile(T, V, K);
   const int mi_log2 = t == WIDE ? 3 : t == SQUARE ? 2 : 1;
-  return {mi_log2, (int)((stats_groups(T, V, K) << (4 + mi_log2)) / TOPS_OF)};
+  const int of_log2 = tops_of(1 << mi_log2) == 32 ? 5 : 4;
+  return {mi_log2, of_log2, (int)((stats_groups(T, V, K) << (4 + mi_log2)) >> of_log2)};
 }
 
 hipError_t launch_logits(const uint16_t* X, int64_t ldx, const uint16_t* W, int64_t ldw, const void* tokens, bool tokens64,

@@ -7,9 +7,9 @@
 // 2^(m - M) (q + (m - M) s).  Both terms of the entropy are of its own size, so a
 // distribution that is nearly certain loses nothing to a difference.
 //
-// Alternatives: of every 32 logits, the two largest are kept in float32.  The k-th largest of any partition's maxima is no larger than the k-th
+// Alternatives: of every 32 or 16 logits, the two largest are kept in float32.  The k-th largest of any partition's maxima is no larger than the k-th
 // largest logit, so a row's candidates are the firsts above such a bound, and, where
-// a second is above it as well, all 32.  Candidates' sums are formed again, in 64 bits,
+// a second is above it as well, all of them.  Candidates' sums are formed again, in 64 bits,
 // and ordered by them.
 #include "score_internal.h"
 
@@ -101,9 +101,9 @@ __global__ __launch_bounds__(1024) void logprob_join_kernel(RowArgs P, int first
 }
 
 // ---------------------------------------------------------------- top alternatives
-// sum_k x w in 64 bits and sum_k |x w|, of a wave; W's loads of 4096 entries at once
+// sum_k x w in 64 bits and sum_k |x w|, of a wave; W's loads of 512 AHEAD entries at once
+template <int AHEAD>
 __device__ inline double exact_sum(const uint16_t* x, const uint16_t* w, int K, float& size) {
-  constexpr int AHEAD = 8;
   const int lane = threadIdx.x & 63, n = K / 8;
   double s0 = 0.0, s1 = 0.0;
   float a = 0.0f;
@@ -163,8 +163,10 @@ __device__ inline float reached_by(const float* slot, int k) {
 // places in a queue, whose order does not matter: candidates are ordered by (sum,
 // index) in the end.  The code is kept short, without unrolling: one token's block
 // fetches each line of it for the first time.
+// Many tokens: 5 loads ahead in 84 registers, 6 blocks a unit (4096 tokens of 65536
+// entries, K = 2560, 8 alternatives: 104 us; 8 ahead, 4 blocks: 113; 3, 8: 113).
 template <int NT, bool JOIN>
-__global__ __launch_bounds__(NT) void logprob_top_kernel(RowArgs P) {
+__global__ __launch_bounds__(NT, NT == 256 ? 6 : 4) void logprob_top_kernel(RowArgs P) {
   constexpr int WAVES = NT / 64, SLOTS = 256, QUEUE = 1024, BATCH = 256, MOST = SBN_LOGPROBS_MAX_TOP;
   constexpr int HELD = 4;
   static_assert(NT % SLOTS == 0 && NT <= QUEUE, "threads");
@@ -252,7 +254,7 @@ __global__ __launch_bounds__(NT) void logprob_top_kernel(RowArgs P) {
             if (at < QUEUE) whole[at] = g;
           } else if (f.x < over) {
             const uint32_t at = atomicAdd(&singles, 1u);
-            if (at < QUEUE) single[at] = sets.entry(g, (int)(__float_as_uint(f.x) & (TOPS_OF - 1)));
+            if (at < QUEUE) single[at] = sets.entry(g, (int)(__float_as_uint(f.x) & (TOPS_MOST - 1)));
           }
         }
         __syncthreads();
@@ -263,7 +265,7 @@ __global__ __launch_bounds__(NT) void logprob_top_kernel(RowArgs P) {
           continue;
         }
         b = stop;
-        const int entries = (int)(ns + nw * TOPS_OF);
+        const int entries = (int)(ns + (nw << sets.of_log2));
 #pragma unroll 1
         for (int e = 0; e < entries; e += BATCH) {   // a batch of entries into the best so far
           const int count = entries - e < BATCH ? entries - e : BATCH;
@@ -274,15 +276,15 @@ __global__ __launch_bounds__(NT) void logprob_top_kernel(RowArgs P) {
             if (at < 0) {
               v = single[e + i];
             } else {                                 // of a set whose first alone came before, without it
-              const int g = whole[at / TOPS_OF], p = at % TOPS_OF;
+              const int g = whole[at >> sets.of_log2], p = at & ((1 << sets.of_log2) - 1);
               const float f = row[g].x;
-              v = f >= over && p == (int)(__float_as_uint(f) & (TOPS_OF - 1)) ? -1 : sets.entry(g, p);
+              v = f >= over && p == (int)(__float_as_uint(f) & (TOPS_MOST - 1)) ? -1 : sets.entry(g, p);
             }
             v = __builtin_amdgcn_readfirstlane(v);
             const bool real = (uint32_t)v < (uint32_t)P.V;   // and not past the vocabulary
             float size = 0.0f;
             double sum = -INFINITY;
-            if (real) sum = exact_sum(x, P.W + (int64_t)v * P.ldw, P.K, size);
+            if (real) sum = exact_sum<JOIN ? 8 : 5>(x, P.W + (int64_t)v * P.ldw, P.K, size);
             if (!(sum == sum)) sum = -INFINITY;      // NaN (outside the contract): an order all the same
             if (lane == 0) {
               value[have + i] = sum, index[have + i] = real ? v : 0x7FFFFFFF;

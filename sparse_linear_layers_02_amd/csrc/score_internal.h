@@ -10,22 +10,26 @@ namespace sbn {
 // Statistics come in logit_groups() groups of entries, [group][T]: (maximum, sum of
 // exponentials) and the sum of exponential times exponent, exponents times log2 e and
 // less the maximum.  `target` [T]: the token's logit.  tops (or NULL): per token
-// logit_tops().groups pairs of the largest and second largest of TOPS_OF sums (logits
-// before their scale), the first's place in its last bits.  A set is what one lane
-// holds of a column, or two or four lanes where a lane holds less.
-constexpr int TOPS_OF = 32;
+// logit_tops().groups pairs of the largest and second largest of a set of 32 or 16
+// sums (logits before their scale), the first's place in its last 5 bits.  A set is
+// what one lane holds of a column; of lanes that hold 8, two.  (Few tokens: sets of 8
+// are 64 KB to read for each at 65536 entries, and of 32 twice as often one with two
+// candidates, all of which are then computed.)
+constexpr int TOPS_MOST = 32;
+constexpr int tops_of(int mi) { return 4 * mi >= 16 ? 4 * mi : 16; }
 struct LogitTops {
   int mi_log2;                         // a lane's 4 mi entries are 4 of each of mi fragments of 16
-  int groups;                          // of V / TOPS_OF, rounded up to whole tiles
+  int of_log2;                         // entries of a set
+  int groups;                          // sets, of V rounded up to whole tiles
   // the vocabulary entry at place p of set g
   __host__ __device__ int entry(int g, int p) const {
     const int per = 2 + mi_log2;                                 // log2 of a lane's
-    const int lane = (g << (5 - per)) + (p >> per);              // counted through waves, 4 a column
+    const int lane = (g << (of_log2 - per)) + (p >> per);        // counted through waves, 4 a column
     p &= (1 << per) - 1;
     return ((lane >> 2) << (4 + mi_log2)) + ((p >> 2) << 4) + ((lane & 3) << 2) + (p & 3);
   }
 };
-static_assert(TOPS_OF == 32, "5 bits");
+static_assert(tops_of(8) == TOPS_MOST && TOPS_MOST == 32, "5 bits");
 LogitTops logit_tops(int64_t T, int64_t V, int64_t K);
 int64_t logit_groups(int64_t T, int64_t V, int64_t K);
 hipError_t launch_logits(const uint16_t* X, int64_t ldx, const uint16_t* W, int64_t ldw, const void* tokens, bool tokens64,
