@@ -38,14 +38,15 @@ __device__ inline float block_max(const float* v) {
 
 // Chunk c of row t into a checkpoint of rows of K; all 16 lanes of a block come
 // here, with zeros past the row.  A maximum that is NaN or Inf makes the scale, and so
-// every value, NaN.
+// every value, NaN.  BF16: the values are.
+template <bool BF16>
 __device__ inline void keep_chunk(const float* v, bool live, int64_t t, int c, int K, int nb, int8_t* codes,
                                   float* scales) {
   const float a = block_max(v);
   const bool none = a < U_FLOOR;
   const float rcp = none ? 0.0f : __builtin_amdgcn_rcpf(a * (1.0f / 127.0f));
   if (live) {
-    *(uint2*)(codes + t * K + 8 * c) = codes8(v, rcp, a);
+    *(uint2*)(codes + t * K + 8 * c) = BF16 ? codes8_bf16(v, rcp) : codes8(v, rcp, a);
     if ((c & (LANES - 1)) == 0) scales[t * nb + c / LANES] = none ? 0.0f : a / 127.0f + (a - a);   // Inf - Inf: NaN
   }
 }
@@ -75,7 +76,7 @@ __global__ __launch_bounds__(256) void keep8_encode_kernel(const char* __restric
       x.load(X + (int64_t)t * ldx * (F32 ? 4 : 2), c);
       x.to(v);
     }
-    keep_chunk(v, c < n, t, (int)c, K, (int)nb, codes, scales);
+    keep_chunk<!F32>(v, c < n, t, (int)c, K, (int)nb, codes, scales);
   }
 }
 
@@ -106,7 +107,12 @@ __device__ inline float act(float a, float* slope = nullptr) {
     return r * r;
   }
   if (OP == ROW_SILU) {
-    const float g = 1.0f / (1.0f + expf(-a));        // exp overflows to Inf, of which g is 0
+    // exp(-a) by the base-2 instruction, with what the exponent's rounding left and the
+    // constant's: within 3 units of 2^-24; where it is Inf, g is 0
+    constexpr float L = -1.44269502f, LOW = -1.925963033e-8f;
+    const float z = a * L, low = fmaf(a, LOW, fmaf(a, L, -z));
+    const float e = __builtin_amdgcn_exp2f(z) * fmaf(low, 0.6931471806f, 1.0f);
+    const float g = __builtin_amdgcn_rcpf(1.0f + e);
     if (slope) *slope = g * (1.0f + a * (1.0f - g));
     return a * g;
   }
@@ -181,8 +187,8 @@ __global__ __launch_bounds__(MAXT) void kept_forward_kernel(FwdArgs P) {
         }
       }
       if (P.kA) {
-        keep_chunk(x, live, t, c, P.K, nb, P.kA, P.sA);
-        if (OP != ROW_NORM && P.B) keep_chunk(y, live, t, c, P.K, nb, P.kB, P.sB);
+        keep_chunk<!F32>(x, live, t, c, P.K, nb, P.kA, P.sA);
+        if (OP != ROW_NORM && P.B) keep_chunk<!F32>(y, live, t, c, P.K, nb, P.kB, P.sB);
       }
       if (live) {
         if (P.gain) {

@@ -110,6 +110,22 @@ def test_blocks_of_extremes():
             assert torch.isfinite(v[0]).all() and torch.isfinite(v[1, :BLOCK]).all() and torch.isfinite(v[1, 2 * BLOCK:]).all()
 
 
+def test_every_bf16_quotient():
+    """All mantissas against all mantissas of the block's maximum, down to 2^-9 of it: half-integers and
+    the quotients next to them."""
+    m = (128 + np.arange(128)).astype(np.float32) / 128
+    x = np.concatenate([m * np.float32(2.0 ** -e) for e in range(10)])
+    rows = []
+    for a in m:
+        v = np.where(x <= a, x, x / 2)
+        v = np.concatenate([v, np.zeros(-v.size % (BLOCK - 1), np.float32)]).reshape(-1, BLOCK - 1)
+        rows.append(np.concatenate([np.full((v.shape[0], 1), a, np.float32), v * np.where(np.arange(BLOCK - 1) % 2, 1, -1)], 1).ravel())
+    x = np.stack(rows).astype(np.float32)
+    for scale in (1.0, 2.0 ** 100, 2.0 ** -80):
+        t, v = put(x * np.float32(scale), False)
+        same_kept(sbn.sbn_keep8_encode(t), v, "quotients")
+
+
 @pytest.mark.parametrize("f32", [False, True])
 @pytest.mark.parametrize("T,K", SHAPES)
 def test_norm_forward(T, K, f32):
