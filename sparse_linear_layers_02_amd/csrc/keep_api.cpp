@@ -3,7 +3,6 @@
 // nothing and touches no output.
 #include "keep_internal.h"
 #include "train_checks.h"
-#include "train_internal.h"
 
 using namespace sbn;
 
@@ -95,7 +94,7 @@ sbn_status sbn_rmsnorm_backward_kept_workspace_bytes(int64_t T, int64_t K, size_
   const char* fn = "sbn_rmsnorm_backward_kept_workspace_bytes";
   SBN_NONNULL(bytes);
   SBN_TRY(check_norm_shape(fn, T, K));
-  *bytes = rmsnorm_bwd_ws_bytes(T, K);
+  *bytes = kept_bwd_ws_bytes(T, K);
   return ok();
 }
 
@@ -130,7 +129,7 @@ sbn_status sbn_rmsnorm_backward_kept(const void* dY, int64_t lddy, const void* d
     SBN_NOT_IN_PLACE(dX, codes);
     SBN_NOT_IN_PLACE(dX, scales);
     SBN_NOT_IN_PLACE(dX, gain);
-    const size_t need = rmsnorm_bwd_ws_bytes(T, K);
+    const size_t need = kept_bwd_ws_bytes(T, K);
     if (ws_bytes < need) return fail(SBN_ERR_WORKSPACE, "%s: workspace %zu bytes, need %zu", fn, ws_bytes, need);
     SBN_TRY(check_finite(fn, "dY", dY, T, K, lddy, bytes_of(dt), st));
     if (dH) SBN_TRY(check_finite(fn, "dH", dH, T, K, lddh, bytes_of(dt), st));
@@ -192,7 +191,7 @@ sbn_status sbn_activation_backward_workspace_bytes(int64_t T, int64_t K, size_t*
   const char* fn = "sbn_activation_backward_workspace_bytes";
   SBN_NONNULL(bytes);
   SBN_TRY(check_norm_shape(fn, T, K));
-  *bytes = rmsnorm_bwd_ws_bytes(T, K);
+  *bytes = kept_bwd_ws_bytes(T, K);
   return ok();
 }
 
@@ -240,7 +239,7 @@ sbn_status sbn_activation_backward(const void* dY, int64_t lddy, sbn_dtype dt, c
     if (gain) {
       SBN_NONNULL(ws);
       SBN_ALIGNED(ws);
-      const size_t need = rmsnorm_bwd_ws_bytes(T, K);
+      const size_t need = kept_bwd_ws_bytes(T, K);
       if (ws_bytes < need) return fail(SBN_ERR_WORKSPACE, "%s: workspace %zu bytes, need %zu", fn, ws_bytes, need);
     }
     SBN_TRY(check_finite(fn, "dY", dY, T, K, lddy, bytes_of(dt), st));

@@ -18,6 +18,8 @@ hipError_t launch_rmsnorm_backward_kept(const void* dY, int64_t lddy, const void
                                         const int8_t* codes, const float* scales, const void* gain, bool gain_f32,
                                         int64_t T, int64_t K, float eps, void* dX, int64_t lddx, float* dgain, void* ws,
                                         hipStream_t st);
+// workspace of both gradients with a gain
+size_t kept_bwd_ws_bytes(int64_t T, int64_t K);
 // B NULL: no second factor; codes_a NULL: nothing kept; gain and dgain NULL: no norm (and ws unused)
 hipError_t launch_activation_quant(const void* A, int64_t lda, const void* B, int64_t ldb, bool f32, sbn_act act,
                                    const void* gain, bool gain_f32, int64_t T, int64_t K, float eps, int8_t* Xq,

@@ -239,24 +239,17 @@ struct BwdArgs {
   bool gain_f32;
 };
 
-template <bool F32, RowOp OP, int CH, int MAXT>
-__global__ __launch_bounds__(MAXT) void kept_backward_kernel(BwdArgs P) {
-  __shared__ float red[2][2][MAXT / 64];
-  const int g = threadIdx.x, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
-  const int n = P.K / 8, es = F32 ? 4 : 2, TPR = blockDim.x, nb = (n + LANES - 1) / LANES;
-  float dg[CH][8];
-#pragma unroll
-  for (int i = 0; i < CH; ++i)
-#pragma unroll
-    for (int j = 0; j < 8; ++j) dg[i][j] = 0.0f;
-  int turn = 0;
-  for (int64_t t = blockIdx.x; t < P.T; t += gridDim.x, turn ^= 1) {
-    Vec8<F32> dy[CH], dh[CH];
-    uint2 qa[CH], qb[CH];
-    float sa[CH], sb[CH];
+// What the gradient reads of a row, CH chunks of a thread.
+template <bool F32, RowOp OP, int CH>
+struct KeptRow {
+  Vec8<F32> dy[CH], dh[OP == ROW_NORM ? CH : 1];
+  uint2 qa[CH], qb[CH];
+  float sa[CH], sb[CH];
+  __device__ void load(const BwdArgs& P, int64_t t, int nb) {
+    const int n = P.K / 8, es = F32 ? 4 : 2;
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
-      const int c = g + TPR * i;
+      const int c = threadIdx.x + blockDim.x * i;
       if (c < n) {
         dy[i].load((const char*)P.dY + t * P.lddy * es, c);
         qa[i] = *(const uint2*)(P.kA + t * P.K + 8 * c);
@@ -269,6 +262,35 @@ __global__ __launch_bounds__(MAXT) void kept_backward_kernel(BwdArgs P) {
         }
       }
     }
+  }
+};
+
+// AHEAD: a row is loaded while the one before it is worked on.
+template <bool F32, RowOp OP, int CH, int MAXT, bool AHEAD>
+__global__ __launch_bounds__(MAXT) void kept_backward_kernel(BwdArgs P) {
+  __shared__ float red[2][2][MAXT / 64];
+  const int g = threadIdx.x, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+  const int n = P.K / 8, es = F32 ? 4 : 2, TPR = blockDim.x, nb = (n + LANES - 1) / LANES;
+  float dg[CH][8], kept_gain[AHEAD ? CH : 1][8];
+#pragma unroll
+  for (int i = 0; i < CH; ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) dg[i][j] = 0.0f;
+  if (AHEAD && P.gain) {
+#pragma unroll
+    for (int i = 0; i < CH; ++i)
+      if (g + TPR * i < n) gain8(P.gain, P.gain_f32, g + TPR * i, kept_gain[i]);
+  }
+  int turn = 0;
+  KeptRow<F32, OP, CH> row, next;
+  if (AHEAD) next.load(P, blockIdx.x, nb);
+  for (int64_t t = blockIdx.x; t < P.T; t += gridDim.x, turn ^= 1) {
+    if (AHEAD) {
+      row = next;
+      next.load(P, t + gridDim.x < P.T ? t + gridDim.x : t, nb);
+    } else {
+      row.load(P, t, nb);
+    }
     float r = 1.0f, back = 0.0f;                     // back: r^2 mean(w u)
     if (P.gain) {
       float uu = 0.0f, wu = 0.0f;
@@ -276,11 +298,11 @@ __global__ __launch_bounds__(MAXT) void kept_backward_kernel(BwdArgs P) {
       for (int i = 0; i < CH; ++i) {
         const int c = g + TPR * i;
         if (c < n) {
-          float a[8], b[8], w[8], gain[8];
-          values8(qa[i], sa[i], a);
-          if (OP != ROW_NORM && P.kB) values8(qb[i], sb[i], b);
-          dy[i].to(w);
-          gain8(P.gain, P.gain_f32, c, gain);
+          float a[8], b[8], w[8], *gain = kept_gain[AHEAD ? i : 0];
+          values8(row.qa[i], row.sa[i], a);
+          if (OP != ROW_NORM && P.kB) values8(row.qb[i], row.sb[i], b);
+          row.dy[i].to(w);
+          if (!AHEAD) gain8(P.gain, P.gain_f32, c, gain);
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             float u = act<OP>(a[j]);
@@ -305,12 +327,12 @@ __global__ __launch_bounds__(MAXT) void kept_backward_kernel(BwdArgs P) {
     for (int i = 0; i < CH; ++i) {
       const int c = g + TPR * i;
       if (c < n) {
-        float a[8], b[8], d[8], gain[8], da[8], db[8];
-        values8(qa[i], sa[i], a);
-        if (OP != ROW_NORM && P.kB) values8(qb[i], sb[i], b);
-        dy[i].to(d);
-        if (P.gain) gain8(P.gain, P.gain_f32, c, gain);
-        if (OP == ROW_NORM && P.dH) dh[i].to(db);
+        float a[8], b[8], d[8], da[8], db[8], *gain = kept_gain[AHEAD ? i : 0];
+        values8(row.qa[i], row.sa[i], a);
+        if (OP != ROW_NORM && P.kB) values8(row.qb[i], row.sb[i], b);
+        row.dy[i].to(d);
+        if (!AHEAD && P.gain) gain8(P.gain, P.gain_f32, c, gain);
+        if (OP == ROW_NORM && P.dH) row.dh[i].to(db);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           float slope;
@@ -358,28 +380,47 @@ void run_fwd(const char* name, const FwdArgs& P, hipStream_t st) {
   SBN_LAUNCH(name, (kept_forward_kernel<F32, OP, CH, MAXT>), dim3((unsigned)(P.T < GRID_MAX ? P.T : GRID_MAX)),
              dim3((unsigned)threads_for(P.K / 8, CH)), 0, st, P);
 }
+// The norm goes by the plain norm's threads, so that its sums have the same order and its
+// scales the same bits.  The activation takes up to 512 threads and more chunks, of which
+// two blocks are on a unit (8192 x 11008, gated, normed and kept: 160 us; 704 threads, one
+// block: 193).
 template <bool F32, RowOp OP>
 void pick_fwd(const char* name, const FwdArgs& P, hipStream_t st) {
   const int n = P.K / 8;
   if (n <= 512) run_fwd<F32, OP, 1, 512>(name, P, st);
   else if (n <= 1024) run_fwd<F32, OP, 2, 512>(name, P, st);
-  else if (n <= 2048) run_fwd<F32, OP, 2, 1024>(name, P, st);
-  else run_fwd<F32, OP, 4, 1024>(name, P, st);
+  else if (n > 2048) run_fwd<F32, OP, 4, 1024>(name, P, st);
+  else if constexpr (OP == ROW_NORM) run_fwd<F32, OP, 2, 1024>(name, P, st);
+  else if (n <= 1536) run_fwd<F32, OP, 3, 512>(name, P, st);
+  else run_fwd<F32, OP, 4, 512>(name, P, st);
 }
 
-template <bool F32, RowOp OP, int CH, int MAXT>
+// Threads of a gradient's block, and blocks with a row of partial sums of dgain each: as
+// many as are on the machine at once (16 waves of a unit, one block of more than 8), but
+// at least 8 rows a block where that leaves one a unit, since a block's partial costs as
+// much traffic as two rows in 16 bits.
+int bwd_chunks(int n) { return n <= 512 ? 1 : n <= 2048 ? 2 : 4; }
+int bwd_blocks(int64_t T, int64_t K) {
+  const int waves = threads_for((int)(K / 8), bwd_chunks((int)(K / 8))) / 64, most = 256 * (16 / waves);
+  int64_t g = T / 8 < 256 ? 256 : T / 8;
+  if (g > most) g = most;
+  return (int)(g < T ? g : T);
+}
+
+template <bool F32, RowOp OP, int CH, int MAXT, bool AHEAD>
 void run_bwd(const char* name, const BwdArgs& P, hipStream_t st) {
-  const int64_t blocks = P.gain ? norm_grad_blocks(P.T, P.K) : P.T < GRID_MAX ? P.T : GRID_MAX;
-  SBN_LAUNCH(name, (kept_backward_kernel<F32, OP, CH, MAXT>), dim3((unsigned)blocks),
+  const int64_t blocks = P.gain ? bwd_blocks(P.T, P.K) : P.T < GRID_MAX ? P.T : GRID_MAX;
+  SBN_LAUNCH(name, (kept_backward_kernel<F32, OP, CH, MAXT, AHEAD>), dim3((unsigned)blocks),
              dim3((unsigned)threads_for(P.K / 8, CH)), 0, st, P);
 }
 template <bool F32, RowOp OP>
 void pick_bwd(const char* name, const BwdArgs& P, hipStream_t st) {
   const int n = P.K / 8;
-  if (n <= 512) run_bwd<F32, OP, 1, 512>(name, P, st);
-  else if (n <= 1024) run_bwd<F32, OP, 2, 512>(name, P, st);
-  else if (n <= 2048) run_bwd<F32, OP, 2, 1024>(name, P, st);
-  else run_bwd<F32, OP, 4, 1024>(name, P, st);
+  if (n <= 512) run_bwd<F32, OP, 1, 512, true>(name, P, st);
+  else if (n <= 1024) run_bwd<F32, OP, 2, 512, true>(name, P, st);
+  else if (n <= 1536) run_bwd<F32, OP, 2, 768, true>(name, P, st);
+  else if (n <= 2048) run_bwd<F32, OP, 2, 1024, false>(name, P, st);
+  else run_bwd<F32, OP, 4, 1024, false>(name, P, st);
 }
 
 template <RowOp OP>
@@ -390,7 +431,7 @@ hipError_t backward(const char* name, const BwdArgs& P, bool f32, float* dgain, 
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  return dgain ? launch_norm_dgain(P.part, P.T, P.K, dgain, st) : hipSuccess;
+  return dgain ? launch_norm_dgain(P.part, bwd_blocks(P.T, P.K), P.K, dgain, st) : hipSuccess;
 }
 
 // Rows of a launch of the checkpoints' own kernels: their threads stay below 2^31.
@@ -401,6 +442,8 @@ unsigned slab_grid(int64_t threads) {
 }
 
 }  // namespace
+
+size_t kept_bwd_ws_bytes(int64_t T, int64_t K) { return align256((size_t)bwd_blocks(T, K) * (size_t)K * sizeof(float)); }
 
 hipError_t launch_keep8_encode(const void* X, int64_t ldx, bool f32, int64_t T, int64_t K, int8_t* codes, float* scales,
                                hipStream_t st) {

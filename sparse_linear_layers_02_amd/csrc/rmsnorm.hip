@@ -283,15 +283,12 @@ __global__ __launch_bounds__(256) void rmsnorm_dgain_kernel(const float* __restr
 // T = 1021, K = 4096 15.0 / 14.4 / 12.5, float32 17.0 / 16.4 / 14.4, K = 1024 10.1 / 9.8
 // / 7.9; T = 333, K = 2560 9.3 / 7.9 / 8.2, float32 9.8 / 8.3 / 8.6; 64 rows and fewer
 // one a block in any case.)
-// (in the namespace: the gradients from checkpoints go by the same rule)
-}  // namespace
-int norm_grad_blocks(int64_t T, int64_t K) {
+int bwd_blocks(int64_t T, int64_t K) {
   const int n = (int)(K / 8), most = 256 * 16 / (threads_for(n, chunks_for(n)) / 64);
   int64_t g = T / 8 < 256 ? 256 : T / 8;
   if (g > most) g = most;
   return (int)(g < T ? g : T);
 }
-namespace {
 
 constexpr int64_t GRID_MAX = 1 << 20;               // blocks; rows beyond are taken in further rounds
 
@@ -341,11 +338,11 @@ hipError_t launch_rmsnorm(const void* X, int64_t ldx, const void* res, int64_t l
   return hipGetLastError();
 }
 
-size_t rmsnorm_bwd_ws_bytes(int64_t T, int64_t K) { return align256((size_t)norm_grad_blocks(T, K) * (size_t)K * sizeof(float)); }
+size_t rmsnorm_bwd_ws_bytes(int64_t T, int64_t K) { return align256((size_t)bwd_blocks(T, K) * (size_t)K * sizeof(float)); }
 
-hipError_t launch_norm_dgain(const float* part, int64_t T, int64_t K, float* dgain, hipStream_t st) {
-  SBN_LAUNCH("rmsnorm_dgain", rmsnorm_dgain_kernel, dim3((unsigned)cdiv(K, 16)), dim3(256), 0, st, part,
-             norm_grad_blocks(T, K), (int)K, dgain);
+hipError_t launch_norm_dgain(const float* part, int blocks, int64_t K, float* dgain, hipStream_t st) {
+  SBN_LAUNCH("rmsnorm_dgain", rmsnorm_dgain_kernel, dim3((unsigned)cdiv(K, 16)), dim3(256), 0, st, part, blocks, (int)K,
+             dgain);
   return hipGetLastError();
 }
 
@@ -353,7 +350,7 @@ hipError_t launch_rmsnorm_backward(const void* dY, int64_t lddy, const void* H, 
                                    int64_t lddh, bool f32, const void* gain, bool gain_f32, const float* rstd,
                                    int64_t T, int64_t K, void* dX, int64_t lddx, float* dgain, void* ws,
                                    hipStream_t st) {
-  const int blocks = norm_grad_blocks(T, K);
+  const int blocks = bwd_blocks(T, K);
   if (T > 0) {
     const BwdArgs A{dY, H, dH, gain, rstd, dX, (float*)ws, lddy, ldh, lddh, lddx, T, (int)K, gain_f32};
     if (f32) pick_bwd<true>(A, blocks, st);
@@ -361,7 +358,7 @@ hipError_t launch_rmsnorm_backward(const void* dY, int64_t lddy, const void* H, 
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  return launch_norm_dgain((const float*)ws, T, K, dgain, st);
+  return launch_norm_dgain((const float*)ws, blocks, K, dgain, st);
 }
 
 }  // namespace sbn

@@ -56,9 +56,8 @@ hipError_t launch_rmsnorm(const void* X, int64_t ldx, const void* res, int64_t l
                           bool gain_f32, int64_t T, int64_t K, float eps, void* H, int64_t ldh, void* Y, int64_t ldy,
                           int8_t* Xq, float* s_x, float* rstd, hipStream_t st);
 size_t rmsnorm_bwd_ws_bytes(int64_t T, int64_t K);
-// The gradients' blocks, each with a row of partial sums of dgain in the workspace, and the sum of those rows.
-int norm_grad_blocks(int64_t T, int64_t K);
-hipError_t launch_norm_dgain(const float* part, int64_t T, int64_t K, float* dgain, hipStream_t st);
+// dgain [K] from `blocks` rows of partial sums
+hipError_t launch_norm_dgain(const float* part, int blocks, int64_t K, float* dgain, hipStream_t st);
 hipError_t launch_rmsnorm_backward(const void* dY, int64_t lddy, const void* H, int64_t ldh, const void* dH,
                                    int64_t lddh, bool f32, const void* gain, bool gain_f32, const float* rstd,
                                    int64_t T, int64_t K, void* dX, int64_t lddx, float* dgain, void* ws,

@@ -207,7 +207,7 @@ def sbn_rmsnorm_backward_kept(dY, kept, gain, *, eps: float = 1e-6, dH=None, dX=
         _given(ws, dY.device, fn)
     raw = _raw_stream(dY.device)
     if ws is None:
-        ws = _scratch("rmsnorm_backward", _scratch_bytes(T, K, "sbn_rmsnorm_backward_kept_workspace_bytes"), dY.device,
+        ws = _scratch("kept_backward", _scratch_bytes(T, K, "sbn_rmsnorm_backward_kept_workspace_bytes"), dY.device,
                       raw)
     _check(fn, _so().sbn_rmsnorm_backward_kept(dY.data_ptr(), _ld(dY), _addr(dH), 0 if dH is None else _ld(dH), dt,
                                                codes.data_ptr(), scales.data_ptr(), gain.data_ptr(), gdt, T, K, eps,
@@ -284,7 +284,7 @@ def sbn_activation_backward(dY, kept_A, kept_B=None, *, act: int, gain=None, eps
         _given(ws, dY.device, fn)
     raw = _raw_stream(dY.device)
     if ws is None and gain is not None:
-        ws = _scratch("rmsnorm_backward", _scratch_bytes(T, K, "sbn_activation_backward_workspace_bytes"), dY.device, raw)
+        ws = _scratch("kept_backward", _scratch_bytes(T, K, "sbn_activation_backward_workspace_bytes"), dY.device, raw)
     _check(fn, _so().sbn_activation_backward(
         dY.data_ptr(), _ld(dY), dt, ca.data_ptr(), sa.data_ptr(), _addr(cb), _addr(sb), act, _addr(gain), gdt, T, K, eps,
         dA.data_ptr(), _ld(dA), _addr(dB), 0 if dB is None else _ld(dB), _addr(dgain), _addr(ws),
