@@ -12,6 +12,7 @@
 // memory.  A checkpoint's block is 16 threads of 8 elements, one row of lanes, so
 // that its maximum takes four lane exchanges and no memory.
 #include "keep_internal.h"
+#include "once_per_device.h"
 #include "row_ops.h"
 
 namespace sbn {
@@ -226,6 +227,96 @@ __global__ __launch_bounds__(MAXT) void kept_forward_kernel(FwdArgs P) {
   }
 }
 
+// Rows of more than 2048 chunks, which do not fit the registers: read twice, the second
+// time from the cache, chunk by chunk (holding four chunks a thread spilled up to half of
+// them: 4096 x 20480, gated, normed and kept, 289 us).  The same threads and order of sums
+// as the plain norm's.
+template <bool F32, RowOp OP>
+__global__ __launch_bounds__(1024) void kept_forward_wide_kernel(FwdArgs P) {
+  __shared__ float red[2][2][16];
+  const int g = threadIdx.x, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+  const int n = P.K / 8, es = F32 ? 4 : 2, TPR = blockDim.x, nb = (n + LANES - 1) / LANES;
+  const int all = (n + 63) / 64 * 64;                // whole waves take each round, for the blocks' maxima
+  int turn = 0;
+  for (int64_t t = blockIdx.x; t < P.T; t += gridDim.x, turn ^= 1) {
+    const char* ar = (const char*)P.A + t * P.lda * es;
+    const char* br = (const char*)P.B + t * P.ldb * es;
+    char* hr = (char*)P.H + t * P.ldh * es;
+    // what is normalised, of chunk c, from a and b
+    auto make = [&](const Vec8<F32>& a, const Vec8<F32>& b, float* x, float* y, float* v) {
+      a.to(x);
+      if (OP == ROW_NORM) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = x[j];
+        return;
+      }
+      if (P.B) b.to(y);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        v[j] = act<OP>(x[j]);
+        if (P.B) v[j] *= y[j];
+      }
+    };
+    float ss = 0.0f, mx = 0.0f;
+    for (int c = g; c < all; c += TPR) {
+      const bool live = c < n;
+      float x[8] = {}, y[8] = {}, v[8], gain[8];
+      if (live) {
+        Vec8<F32> a, b;
+        a.load(ar, c);
+        if (P.B) b.load(br, c);
+        if (P.gain) gain8(P.gain, P.gain_f32, c, gain);
+        if (OP == ROW_NORM && P.B) {
+          a.to(x), b.to(y);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) x[j] += y[j];
+          a.from(x);
+          a.store(hr, c);
+        }
+        make(a, b, x, y, v);
+        if (P.gain) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            ss += v[j] * v[j];
+            v[j] *= gain[j];
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) mx = fmaxf(mx, fabsf(v[j]));
+      }
+      if (P.kA) {
+        keep_chunk<!F32>(x, live, t, c, P.K, nb, P.kA, P.sA);
+        if (OP != ROW_NORM && P.B) keep_chunk<!F32>(y, live, t, c, P.K, nb, P.kB, P.sB);
+      }
+    }
+    ss = wave_all(ss, Add{});
+    mx = wave_all(mx, Max{});
+    if ((threadIdx.x & 63) == 0) red[turn][0][wave] = ss, red[turn][1][wave] = mx;
+    __syncthreads();                                 // and the other set of red for the next round
+    ss = across(red[turn][0], waves, Add{});
+    mx = across(red[turn][1], waves, Max{});
+    const float m = fmaxf(mx, U_FLOOR);
+    if (g == 0) {
+      const float rstd = P.gain ? 1.0f / sqrtf(ss / (float)P.K + P.eps) : 1.0f;
+      P.s_x[t] = (m * rstd) / 127.0f;
+    }
+    const float rcp = __builtin_amdgcn_rcpf(m * (1.0f / 127.0f));
+    for (int c = g; c < n; c += TPR) {
+      float x[8], y[8], v[8], gain[8];
+      Vec8<F32> a, b;
+      a.load(OP == ROW_NORM && P.B ? hr : ar, c);    // h by the thread that wrote it (it may be in an input's place)
+      if (OP != ROW_NORM && P.B) b.load(br, c);
+      make(a, b, x, y, v);
+      if (P.gain) {
+        gain8(P.gain, P.gain_f32, c, gain);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] *= gain[j];
+      }
+      *(uint2*)(P.Xq + t * P.K + 8 * c) = codes8(v, rcp, m);
+    }
+  }
+}
+
 // ---------------------------------------------------------------- backward
 struct BwdArgs {
   const void *dY, *dH, *gain;                        // dH: ROW_NORM, or NULL
@@ -265,32 +356,28 @@ struct KeptRow {
   }
 };
 
-// AHEAD: a row is loaded while the one before it is worked on.
-template <bool F32, RowOp OP, int CH, int MAXT, bool AHEAD>
+// A row is loaded while the one before it is worked on.
+template <bool F32, RowOp OP, int CH, int MAXT>
 __global__ __launch_bounds__(MAXT) void kept_backward_kernel(BwdArgs P) {
   __shared__ float red[2][2][MAXT / 64];
   const int g = threadIdx.x, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
   const int n = P.K / 8, es = F32 ? 4 : 2, TPR = blockDim.x, nb = (n + LANES - 1) / LANES;
-  float dg[CH][8], kept_gain[AHEAD ? CH : 1][8];
+  float dg[CH][8], kept_gain[CH][8];
 #pragma unroll
   for (int i = 0; i < CH; ++i)
 #pragma unroll
     for (int j = 0; j < 8; ++j) dg[i][j] = 0.0f;
-  if (AHEAD && P.gain) {
+  if (P.gain) {
 #pragma unroll
     for (int i = 0; i < CH; ++i)
       if (g + TPR * i < n) gain8(P.gain, P.gain_f32, g + TPR * i, kept_gain[i]);
   }
   int turn = 0;
   KeptRow<F32, OP, CH> row, next;
-  if (AHEAD) next.load(P, blockIdx.x, nb);
+  next.load(P, blockIdx.x, nb);
   for (int64_t t = blockIdx.x; t < P.T; t += gridDim.x, turn ^= 1) {
-    if (AHEAD) {
-      row = next;
-      next.load(P, t + gridDim.x < P.T ? t + gridDim.x : t, nb);
-    } else {
-      row.load(P, t, nb);
-    }
+    row = next;
+    next.load(P, t + gridDim.x < P.T ? t + gridDim.x : t, nb);
     float r = 1.0f, back = 0.0f;                     // back: r^2 mean(w u)
     if (P.gain) {
       float uu = 0.0f, wu = 0.0f;
@@ -298,11 +385,10 @@ __global__ __launch_bounds__(MAXT) void kept_backward_kernel(BwdArgs P) {
       for (int i = 0; i < CH; ++i) {
         const int c = g + TPR * i;
         if (c < n) {
-          float a[8], b[8], w[8], *gain = kept_gain[AHEAD ? i : 0];
+          float a[8], b[8], w[8], *gain = kept_gain[i];
           values8(row.qa[i], row.sa[i], a);
           if (OP != ROW_NORM && P.kB) values8(row.qb[i], row.sb[i], b);
           row.dy[i].to(w);
-          if (!AHEAD) gain8(P.gain, P.gain_f32, c, gain);
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             float u = act<OP>(a[j]);
@@ -327,11 +413,10 @@ __global__ __launch_bounds__(MAXT) void kept_backward_kernel(BwdArgs P) {
     for (int i = 0; i < CH; ++i) {
       const int c = g + TPR * i;
       if (c < n) {
-        float a[8], b[8], d[8], da[8], db[8], *gain = kept_gain[AHEAD ? i : 0];
+        float a[8], b[8], d[8], da[8], db[8], *gain = kept_gain[i];
         values8(row.qa[i], row.sa[i], a);
         if (OP != ROW_NORM && P.kB) values8(row.qb[i], row.sb[i], b);
         row.dy[i].to(d);
-        if (!AHEAD && P.gain) gain8(P.gain, P.gain_f32, c, gain);
         if (OP == ROW_NORM && P.dH) row.dh[i].to(db);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
@@ -373,6 +458,94 @@ __global__ __launch_bounds__(MAXT) void kept_backward_kernel(BwdArgs P) {
   }
 }
 
+// Rows of more than 2048 chunks: read twice, and dgain's sums in LDS.
+template <bool F32, RowOp OP>
+__global__ __launch_bounds__(1024) void kept_backward_wide_kernel(BwdArgs P) {
+  __shared__ float red[2][2][16];
+  extern __shared__ v4f sums[];                      // [2][n] with a gain: each thread its own columns
+  const int g = threadIdx.x, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+  const int n = P.K / 8, nb = (n + LANES - 1) / LANES, TPR = blockDim.x, es = F32 ? 4 : 2;
+  const bool two = OP != ROW_NORM && P.kB;
+  if (P.gain)
+    for (int c = g; c < n; c += TPR) sums[c] = sums[n + c] = (v4f){0.f, 0.f, 0.f, 0.f};
+  int turn = 0;
+  for (int64_t t = blockIdx.x; t < P.T; t += gridDim.x, turn ^= 1) {
+    auto load = [&](int c, float* a, float* b, float* d) {
+      Vec8<F32> dy;
+      dy.load((const char*)P.dY + t * P.lddy * es, c);
+      values8(*(const uint2*)(P.kA + t * P.K + 8 * c), P.sA[t * nb + c / LANES], a);
+      if (two) values8(*(const uint2*)(P.kB + t * P.K + 8 * c), P.sB[t * nb + c / LANES], b);
+      dy.to(d);
+    };
+    float r = 1.0f, back = 0.0f;                     // back: r^2 mean(w u)
+    if (P.gain) {
+      float uu = 0.0f, wu = 0.0f;
+      for (int c = g; c < n; c += TPR) {
+        float a[8], b[8], w[8], gain[8];
+        load(c, a, b, w);
+        gain8(P.gain, P.gain_f32, c, gain);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          float u = act<OP>(a[j]);
+          if (two) u *= b[j];
+          uu += u * u;
+          wu += w[j] * gain[j] * u;
+        }
+      }
+      uu = wave_all(uu, Add{});
+      wu = wave_all(wu, Add{});
+      if ((threadIdx.x & 63) == 0) red[turn][0][wave] = uu, red[turn][1][wave] = wu;
+      __syncthreads();                               // and the other set of red for the next round
+      uu = across(red[turn][0], waves, Add{});
+      wu = across(red[turn][1], waves, Add{});
+      r = 1.0f / sqrtf(uu / (float)P.K + P.eps);
+      back = r * r * (wu / (float)P.K);
+    }
+    for (int c = g; c < n; c += TPR) {
+      float a[8], b[8], d[8], gain[8], da[8], db[8];
+      v4f dg[2];
+      load(c, a, b, d);
+      if (P.gain) {
+        gain8(P.gain, P.gain_f32, c, gain);
+        dg[0] = sums[c], dg[1] = sums[n + c];
+      }
+      if (OP == ROW_NORM && P.dH) {
+        Vec8<F32> dh;
+        dh.load((const char*)P.dH + t * P.lddh * es, c);
+        dh.to(db);
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        float slope;
+        const float f = act<OP>(a[j], &slope);
+        float du = d[j];
+        if (P.gain) {
+          const float u = two ? f * b[j] : f;
+          dg[j >> 2][j & 3] += d[j] * (u * r);
+          du = r * (d[j] * gain[j] - u * back);
+        }
+        if (OP == ROW_NORM) {
+          da[j] = P.dH ? du + db[j] : du;
+        } else {
+          da[j] = (two ? du * b[j] : du) * slope;
+          db[j] = du * f;
+        }
+      }
+      if (P.gain) sums[c] = dg[0], sums[n + c] = dg[1];
+      Vec8<F32> o;
+      o.from(da);
+      o.store((char*)P.dA + t * P.ldda * es, c);
+      if (two) {
+        o.from(db);
+        o.store((char*)P.dB + t * P.lddb * es, c);
+      }
+    }
+  }
+  if (!P.gain) return;
+  v4f* out = (v4f*)(P.part + (int64_t)blockIdx.x * P.K);
+  for (int c = g; c < n; c += TPR) out[2 * c] = sums[c], out[2 * c + 1] = sums[n + c];
+}
+
 constexpr int64_t GRID_MAX = 1 << 20;                // blocks; rows beyond are taken in further rounds
 
 template <bool F32, RowOp OP, int CH, int MAXT>
@@ -389,7 +562,9 @@ void pick_fwd(const char* name, const FwdArgs& P, hipStream_t st) {
   const int n = P.K / 8;
   if (n <= 512) run_fwd<F32, OP, 1, 512>(name, P, st);
   else if (n <= 1024) run_fwd<F32, OP, 2, 512>(name, P, st);
-  else if (n > 2048) run_fwd<F32, OP, 4, 1024>(name, P, st);
+  else if (n > 2048)
+    SBN_LAUNCH(name, (kept_forward_wide_kernel<F32, OP>), dim3((unsigned)(P.T < GRID_MAX ? P.T : GRID_MAX)),
+               dim3((unsigned)threads_for(n, 4)), 0, st, P);
   else if constexpr (OP == ROW_NORM) run_fwd<F32, OP, 2, 1024>(name, P, st);
   else if (n <= 1536) run_fwd<F32, OP, 3, 512>(name, P, st);
   else run_fwd<F32, OP, 4, 512>(name, P, st);
@@ -399,36 +574,51 @@ void pick_fwd(const char* name, const FwdArgs& P, hipStream_t st) {
 // many as are on the machine at once (16 waves of a unit, one block of more than 8), but
 // at least 8 rows a block where that leaves one a unit, since a block's partial costs as
 // much traffic as two rows in 16 bits.
-int bwd_chunks(int n) { return n <= 512 ? 1 : n <= 2048 ? 2 : 4; }
+int bwd_chunks(int n) { return n <= 1024 ? 1 : n <= 1536 ? 2 : 4; }   // above 2048: of 1024 threads, in rounds
 int bwd_blocks(int64_t T, int64_t K) {
-  const int waves = threads_for((int)(K / 8), bwd_chunks((int)(K / 8))) / 64, most = 256 * (16 / waves);
+  const int n = (int)(K / 8), waves = n > 2048 ? 16 : threads_for(n, bwd_chunks(n)) / 64, most = 256 * (16 / waves);
   int64_t g = T / 8 < 256 ? 256 : T / 8;
   if (g > most) g = most;
   return (int)(g < T ? g : T);
 }
 
-template <bool F32, RowOp OP, int CH, int MAXT, bool AHEAD>
+template <bool F32, RowOp OP, int CH, int MAXT>
 void run_bwd(const char* name, const BwdArgs& P, hipStream_t st) {
   const int64_t blocks = P.gain ? bwd_blocks(P.T, P.K) : P.T < GRID_MAX ? P.T : GRID_MAX;
-  SBN_LAUNCH(name, (kept_backward_kernel<F32, OP, CH, MAXT, AHEAD>), dim3((unsigned)blocks),
+  SBN_LAUNCH(name, (kept_backward_kernel<F32, OP, CH, MAXT>), dim3((unsigned)blocks),
              dim3((unsigned)threads_for(P.K / 8, CH)), 0, st, P);
 }
 template <bool F32, RowOp OP>
-void pick_bwd(const char* name, const BwdArgs& P, hipStream_t st) {
+hipError_t run_bwd_wide(const char* name, const BwdArgs& P, hipStream_t st) {
+  static OncePerDevice once;
+  int device = 0;
+  hipError_t e = hipGetDevice(&device);
+  if (e == hipSuccess)
+    e = once(device, [] {
+      return hipFuncSetAttribute((const void*)kept_backward_wide_kernel<F32, OP>,
+                                 hipFuncAttributeMaxDynamicSharedMemorySize, SBN_RMSNORM_MAX_K * (int)sizeof(float));
+    });
+  if (e != hipSuccess) return e;
+  const int64_t blocks = P.gain ? bwd_blocks(P.T, P.K) : P.T < GRID_MAX ? P.T : GRID_MAX;
+  SBN_LAUNCH(name, (kept_backward_wide_kernel<F32, OP>), dim3((unsigned)blocks), dim3(1024),
+             P.gain ? (size_t)P.K * sizeof(float) : 0, st, P);
+  return hipGetLastError();
+}
+template <bool F32, RowOp OP>
+hipError_t pick_bwd(const char* name, const BwdArgs& P, hipStream_t st) {
   const int n = P.K / 8;
-  if (n <= 512) run_bwd<F32, OP, 1, 512, true>(name, P, st);
-  else if (n <= 1024) run_bwd<F32, OP, 2, 512, true>(name, P, st);
-  else if (n <= 1536) run_bwd<F32, OP, 2, 768, true>(name, P, st);
-  else if (n <= 2048) run_bwd<F32, OP, 2, 1024, false>(name, P, st);
-  else run_bwd<F32, OP, 4, 1024, false>(name, P, st);
+  if (n <= 512) run_bwd<F32, OP, 1, 512>(name, P, st);
+  else if (n <= 1024) run_bwd<F32, OP, 1, 1024>(name, P, st);
+  else if (n <= 1536) run_bwd<F32, OP, 2, 768>(name, P, st);
+  else if (n <= 2048) run_bwd<F32, OP, 4, 512>(name, P, st);
+  else return run_bwd_wide<F32, OP>(name, P, st);
+  return hipGetLastError();
 }
 
 template <RowOp OP>
 hipError_t backward(const char* name, const BwdArgs& P, bool f32, float* dgain, hipStream_t st) {
   if (P.T > 0) {
-    if (f32) pick_bwd<true, OP>(name, P, st);
-    else pick_bwd<false, OP>(name, P, st);
-    const hipError_t e = hipGetLastError();
+    const hipError_t e = f32 ? pick_bwd<true, OP>(name, P, st) : pick_bwd<false, OP>(name, P, st);
     if (e != hipSuccess) return e;
   }
   return dgain ? launch_norm_dgain(P.part, bwd_blocks(P.T, P.K), P.K, dgain, st) : hipSuccess;
