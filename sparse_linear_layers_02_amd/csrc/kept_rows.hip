@@ -227,10 +227,10 @@ __global__ __launch_bounds__(MAXT) void kept_forward_kernel(FwdArgs P) {
   }
 }
 
-// Rows of more than 2048 chunks, which do not fit the registers: read twice, the second
-// time from the cache, chunk by chunk (holding four chunks a thread spilled up to half of
-// them: 4096 x 20480, gated, normed and kept, 289 us).  The same threads and order of sums
-// as the plain norm's.
+// Rows that do not fit the registers: read twice, the second time from the cache, chunk
+// by chunk.  (Holding four chunks a thread spilled up to half of them: 4096 x 20480, gated,
+// normed and kept, 289 us; so 154.)  The norm's threads and order of sums are the plain
+// norm's.
 template <bool F32, RowOp OP>
 __global__ __launch_bounds__(1024) void kept_forward_wide_kernel(FwdArgs P) {
   __shared__ float red[2][2][16];
@@ -556,18 +556,18 @@ void run_fwd(const char* name, const FwdArgs& P, hipStream_t st) {
 // The norm goes by the plain norm's threads, so that its sums have the same order and its
 // scales the same bits.  The activation takes up to 512 threads and more chunks, of which
 // two blocks are on a unit (8192 x 11008, gated, normed and kept: 160 us; 704 threads, one
-// block: 193).
+// block: 193), and above 1536 chunks reads twice (4096 x 16384: 123 us; four chunks held:
+// 143), with 512 threads (256 / 512 / 768 / 1024: 128 / 123 / 124 / 123; 4096 x 20480 163 / 154
+// / 156 / 154).  How many depends on K alone, so a row gives the same bits in any batch.
 template <bool F32, RowOp OP>
 void pick_fwd(const char* name, const FwdArgs& P, hipStream_t st) {
   const int n = P.K / 8;
   if (n <= 512) run_fwd<F32, OP, 1, 512>(name, P, st);
   else if (n <= 1024) run_fwd<F32, OP, 2, 512>(name, P, st);
-  else if (n > 2048)
+  else if (n <= (OP == ROW_NORM ? 2048 : 1536)) run_fwd<F32, OP, OP == ROW_NORM ? 2 : 3, OP == ROW_NORM ? 1024 : 512>(name, P, st);
+  else
     SBN_LAUNCH(name, (kept_forward_wide_kernel<F32, OP>), dim3((unsigned)(P.T < GRID_MAX ? P.T : GRID_MAX)),
-               dim3((unsigned)threads_for(n, 4)), 0, st, P);
-  else if constexpr (OP == ROW_NORM) run_fwd<F32, OP, 2, 1024>(name, P, st);
-  else if (n <= 1536) run_fwd<F32, OP, 3, 512>(name, P, st);
-  else run_fwd<F32, OP, 4, 512>(name, P, st);
+               dim3((unsigned)(OP == ROW_NORM ? threads_for(n, 4) : 512)), 0, st, P);
 }
 
 // Threads of a gradient's block, and blocks with a row of partial sums of dgain each: as
