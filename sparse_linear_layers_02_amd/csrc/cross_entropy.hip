@@ -44,8 +44,8 @@ constexpr int CUS = 256;
 
 // PAIR: D in two bf16 numbers; OUT, ADD: C in bf16 or float32, ADD on top of Cin.
 // SCORE, POLICY: the statistics and D of log probabilities with entropies; TOPS: and
-// the two largest logits of each tops_of(MI).
-enum Epi { EPI_STATS, EPI_SCORE, EPI_SCORE_TOPS, EPI_GRAD, EPI_GRAD_PAIR, EPI_POLICY, EPI_POLICY_PAIR, EPI_OUT16, EPI_OUT32,
+// the two largest logits of each tops_of(MI), TOPS8: of each 8.
+enum Epi { EPI_STATS, EPI_SCORE, EPI_SCORE_TOPS, EPI_SCORE_TOPS8, EPI_GRAD, EPI_GRAD_PAIR, EPI_POLICY, EPI_POLICY_PAIR, EPI_OUT16, EPI_OUT32,
            EPI_ADD32 };
 
 struct GemmArgs {
@@ -268,7 +268,7 @@ __global__ __launch_bounds__(64 * WA * WB, 1) void ce_gemm_kernel(GemmArgs P) {
   constexpr int LPH = LA + LB;
   constexpr bool POLICY = EPI == EPI_POLICY || EPI == EPI_POLICY_PAIR, PAIR = EPI == EPI_GRAD_PAIR || EPI == EPI_POLICY_PAIR;
   constexpr bool GRAD = EPI == EPI_GRAD || PAIR || POLICY;
-  constexpr bool TOPS = EPI == EPI_SCORE_TOPS, SCORE = EPI == EPI_SCORE || TOPS, STATS = EPI == EPI_STATS || SCORE;
+  constexpr bool TOPS8 = EPI == EPI_SCORE_TOPS8, TOPS = EPI == EPI_SCORE_TOPS || TOPS8, SCORE = EPI == EPI_SCORE || TOPS, STATS = EPI == EPI_STATS || SCORE;
   constexpr int AHEAD = RING / 2;
   extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
   static_assert(RING >= 5 && RING % 2 == 1 && (RING - 3) * LPH < 64, "a stage, the next one and a half in flight");
@@ -535,8 +535,12 @@ __global__ __launch_bounds__(64 * WA * WB, 1) void ce_gemm_kernel(GemmArgs P) {
               second = __builtin_amdgcn_fmed3f(first, second, key);
               first = fmaxf(first, key);
             }
+            if (TOPS8 && i % 2 == 1) {
+              if (t < P.nB) P.tops[(int64_t)t * P.ldt + (group * 4 + g16) * (MI / 2) + i / 2] = make_float2(first, second);
+              first = second = -3.0e38f;
+            }
           }
-          if (LANES > 1) {                           // in both, so that the first stays the larger
+          if (LANES > 1 && !TOPS8) {                 // in both, so that the first stays the larger
             first = __uint_as_float(__float_as_uint(first) | lane_bits);
             second = __uint_as_float(__float_as_uint(second) | lane_bits);
             const auto f = __builtin_amdgcn_permlane16_swap(__float_as_uint(first), __float_as_uint(first), false, false);
@@ -545,7 +549,7 @@ __global__ __launch_bounds__(64 * WA * WB, 1) void ce_gemm_kernel(GemmArgs P) {
             second = fmaxf(fminf(f0, f1), fmaxf(__uint_as_float(s[0]), __uint_as_float(s[1])));
             first = fmaxf(f0, f1);
           }
-          if (t < P.nB && (g16 & (LANES - 1)) == 0)
+          if (t < P.nB && (g16 & (LANES - 1)) == 0 && !TOPS8)
             P.tops[(int64_t)t * P.ldt + (group * 4 + g16) / LANES] = make_float2(first, second);
         }
         float m = -INFINITY;
@@ -964,26 +968,27 @@ hipError_t launch_ce(const uint16_t* X, int64_t ldx, const uint16_t* W, int64_t 
 }
 
 // Of a token's tops: the fragments of 16 entries that a wave holds, and the sets.
-LogitTops logit_tops(int64_t T, int64_t V, int64_t K) {
+LogitTops logit_tops(int64_t T, int64_t V, int64_t K, int top) {
   const Tile t = stats_tile(T, V, K);
   const int mi_log2 = t == WIDE ? 3 : t == SQUARE ? 2 : 1;
-  const int of_log2 = tops_of(1 << mi_log2) == 32 ? 5 : 4;
+  const int of_log2 = V < int64_t(4096) * top ? 3 : tops_of(1 << mi_log2) == 32 ? 5 : 4;
   return {mi_log2, of_log2, (int)((stats_groups(T, V, K) << (4 + mi_log2)) >> of_log2)};
 }
 
 hipError_t launch_logits(const uint16_t* X, int64_t ldx, const uint16_t* W, int64_t ldw, const void* tokens, bool tokens64,
                          int64_t T, int64_t V, int64_t K, float scale, float* target, float2* stats, float* mean,
-                         float2* tops, hipStream_t st) {
+                         float2* tops, const LogitTops& sets, hipStream_t st) {
   GemmArgs P{};
   P.A = W, P.lda = ldw, P.nA = P.mA = (int)V;
   P.B = X, P.ldb = ldx, P.nB = P.mB = (int)T;
   P.steps = (int)(K / BK), P.splits = 1;
   P.labels = tokens, P.labels64 = tokens64, P.V = (int)V;
   P.target = target, P.stats = stats, P.mean = mean, P.tops = tops;
-  P.ldt = logit_tops(T, V, K).groups;
+  P.ldt = sets.groups;
   P.scale = scale, P.none = -1e30f / (scale * LOG2E);
   const Tile t = stats_tile(T, V, K);
-  return tops ? gemm<EPI_SCORE_TOPS>(SCORES, t, P, st) : gemm<EPI_SCORE>(SCORES, t, P, st);
+  if (!tops) return gemm<EPI_SCORE>(SCORES, t, P, st);
+  return sets.of_log2 == 3 ? gemm<EPI_SCORE_TOPS8>(SCORES, t, P, st) : gemm<EPI_SCORE_TOPS>(SCORES, t, P, st);
 }
 int64_t logit_groups(int64_t T, int64_t V, int64_t K) { return stats_groups(T, V, K); }
 

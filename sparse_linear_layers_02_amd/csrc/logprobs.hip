@@ -276,7 +276,7 @@ __global__ __launch_bounds__(NT, NT == 256 ? 6 : 4) void logprob_top_kernel(RowA
             if (at < 0) {
               v = single[e + i];
             } else {                                 // of a set whose first alone came before, without it
-              const int g = whole[at >> sets.of_log2], p = at & ((1 << sets.of_log2) - 1);
+              const int g = whole[at >> sets.of_log2], p = sets.place(g, at & ((1 << sets.of_log2) - 1));
               const float f = row[g].x;
               v = f >= over && p == (int)(__float_as_uint(f) & (TOPS_MOST - 1)) ? -1 : sets.entry(g, p);
             }
@@ -348,7 +348,7 @@ Plan plan(int64_t T, int64_t V, int64_t K, int top) {
   L.target = take((size_t)T * sizeof(float));
   L.stats = take(n * sizeof(float2));
   L.mean = take(n * sizeof(float));
-  L.tops = take(top ? (size_t)T * logit_tops(T, V, K).groups * sizeof(float2) : 0);
+  L.tops = take(top ? (size_t)T * logit_tops(T, V, K, top).groups * sizeof(float2) : 0);
   L.total = o;
   return L;
 }
@@ -367,10 +367,11 @@ hipError_t launch_logprobs(const uint16_t* X, int64_t ldx, const uint16_t* W, in
   uint8_t* w = (uint8_t*)ws;
   float *target = (float*)(w + L.target), *mean = (float*)(w + L.mean);
   float2 *stats = (float2*)(w + L.stats), *tops = top ? (float2*)(w + L.tops) : nullptr;
-  const hipError_t e = launch_logits(X, ldx, W, ldw, tokens, tokens64, T, V, K, scale, target, stats, mean, tops, st);
+  const LogitTops sets = logit_tops(T, V, K, top);
+  const hipError_t e = launch_logits(X, ldx, W, ldw, tokens, tokens64, T, V, K, scale, target, stats, mean, tops, sets, st);
   if (e != hipSuccess) return e;
   const RowArgs R{stats, mean, target, tokens, tokens64, (int)logit_groups(T, V, K), (int)T, (int)V, logp, entropy, lse, X, W,
-                  ldx, ldw, (int)K, top, logit_tops(T, V, K), tops, scale, top_ids, top_logp};
+                  ldx, ldw, (int)K, top, sets, tops, scale, top_ids, top_logp};
   if (T <= FEW_TOKENS) {
     SBN_LAUNCH("logprob_rows", (logprob_top_kernel<1024, true>), dim3((unsigned)T), dim3(1024), 0, st, R);
     return hipGetLastError();

@@ -14,27 +14,36 @@ namespace sbn {
 // sums (logits before their scale), the first's place in its last 5 bits.  A set is
 // what one lane holds of a column; of lanes that hold 8, two.  (Few tokens: sets of 8
 // are 64 KB to read for each at 65536 entries, and of 32 twice as often one with two
-// candidates, all of which are then computed.)
+// candidates, all of which are then computed.)  Below 4096 entries for each alternative
+// asked for, where two in a set are common, sets are of 8, parts of a lane's.  (Logits /
+// alternatives, us, with them and without: 20 of 32001 entries, 1024 tokens, K = 4096 218 +
+// 77, 203 + 126; 8 of 20000, 600 tokens, 2560 69 + 23, 69 + 45; 64 of 8000, 2000 tokens, 512
+// 27 + 147, 26 + 317; 20 of 32001, 37 tokens, 4096 61 + 27, 61 + 25.)
 constexpr int TOPS_MOST = 32;
 constexpr int tops_of(int mi) { return 4 * mi >= 16 ? 4 * mi : 16; }
 struct LogitTops {
   int mi_log2;                         // a lane's 4 mi entries are 4 of each of mi fragments of 16
   int of_log2;                         // entries of a set
   int groups;                          // sets, of V rounded up to whole tiles
+  // the place of set g's q-th entry: among its lane's where that holds several sets, else in the set
+  __host__ __device__ int place(int g, int q) const {
+    const int sets = 2 + mi_log2 - of_log2;                      // log2 of a lane's sets
+    return sets > 0 ? ((g & ((1 << sets) - 1)) << of_log2) + q : q;
+  }
   // the vocabulary entry at place p of set g
   __host__ __device__ int entry(int g, int p) const {
-    const int per = 2 + mi_log2;                                 // log2 of a lane's
-    const int lane = (g << (of_log2 - per)) + (p >> per);        // counted through waves, 4 a column
+    const int per = 2 + mi_log2, lanes = of_log2 - per;          // log2 of a lane's entries and a set's lanes
+    const int lane = lanes >= 0 ? (g << lanes) + (p >> per) : g >> -lanes;   // counted through waves, 4 a column
     p &= (1 << per) - 1;
     return ((lane >> 2) << (4 + mi_log2)) + ((p >> 2) << 4) + ((lane & 3) << 2) + (p & 3);
   }
 };
 static_assert(tops_of(8) == TOPS_MOST && TOPS_MOST == 32, "5 bits");
-LogitTops logit_tops(int64_t T, int64_t V, int64_t K);
+LogitTops logit_tops(int64_t T, int64_t V, int64_t K, int top);
 int64_t logit_groups(int64_t T, int64_t V, int64_t K);
 hipError_t launch_logits(const uint16_t* X, int64_t ldx, const uint16_t* W, int64_t ldw, const void* tokens, bool tokens64,
                          int64_t T, int64_t V, int64_t K, float scale, float* target, float2* stats, float* mean,
-                         float2* tops, hipStream_t st);
+                         float2* tops, const LogitTops& sets, hipStream_t st);
 
 // ----------------------------------------------------------------- logprobs.hip
 size_t logprobs_ws_bytes(int64_t T, int64_t V, int64_t K, int top);

@@ -70,7 +70,7 @@ def test_backward(L):
 def test_workspaces():
     wsb = sbn.sbn_token_logprobs_workspace_bytes
     T, V, K = 8192, 262144, 4096
-    assert wsb(T, V, K) < T * V * 2 / 16 and wsb(T, V, K, 64) < T * V * 2 / 4 and wsb(T, V, K, 1) == wsb(T, V, K, 64)
+    assert wsb(T, V, K) < T * V * 2 / 16 and wsb(T, V, K, 64) < T * V * 2 / 4 and wsb(T, 1000, K, 64) < T * 1000 * 2
     assert wsb(T, V, K, 0, True) == sbn.sbn_cross_entropy_workspace_bytes(T, V, K, True)
     assert wsb(0, V, K, 8) == 0 and wsb(0, V, K, 0, True) == 0
     with pytest.raises(sbn.SbnError):
