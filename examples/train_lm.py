@@ -4,7 +4,12 @@ and 8-bit output -> sparse ternary layer -> squared ReLU -> sparse ternary layer
 -> RMS norm -> cross entropy of the head, the gradients of all of them, and one
 AdamW step over all tensors, whose bf16 weights the next step's pack reads.
 
-    python examples/train_lm.py [--steps N] [--bits 32|8] [--seed S]
+    python examples/train_lm.py [--steps N] [--bits 32|8] [--keep 16|8] [--entropy C] [--seed S]
+
+--keep 8: what the blocks keep for the backward pass (the residual stream in front of
+each norm, the activation's input) is kept as 8-bit checkpoints, written by the norm and
+the activation themselves.  --entropy C: the step is that of log probabilities with C
+times the entropy as a bonus, instead of the loss's.
 
 The text repeats a random successor table, so the loss falls from log(vocabulary)
 towards 0 if, and only if, the gradients are right.  Prints the loss and, at the
@@ -28,7 +33,8 @@ V, K, R, BLOCKS, T, N, M = 1000, 256, 512, 2, 1024, 2, 4
 class Model:
     """bf16 weights, float32 gains, and the AdamW state of all of them."""
 
-    def __init__(self, bits: int, seed: int):
+    def __init__(self, bits: int, seed: int, keep: int = 16, entropy: float = 0.0):
+        self.keep, self.entropy = keep, entropy
         g = torch.Generator(device="cuda").manual_seed(seed)
         w = lambda *s: (torch.randn(*s, generator=g, device="cuda") / math.sqrt(s[-1])).bfloat16()  # noqa: E731
         self.emb, self.head = w(V, K) * 4, w(V, K)
@@ -56,7 +62,14 @@ class Model:
     def forward(self, tokens):
         """Hidden states before the head, and what the backward needs."""
         h, x, kept = self.emb[tokens], None, []
-        for b in range(BLOCKS):
+        for b in range(BLOCKS if self.keep == 8 else 0):
+            Xq, s_x, h, kh = sbn.sbn_rmsnorm_quant_keep(h if x is None else x, self.gains[b],
+                                                        residual=None if x is None else h, H=None if x is None else h)
+            a, pa = self._layer(self.up[b], Xq, s_x)
+            Aq, s_a, ka, _ = sbn.sbn_activation_quant(a, act=sbn.SBN_RELU2, gain=self.gains[BLOCKS + 1 + b])
+            x, pb = self._layer(self.down[b], Aq, s_a)
+            kept.append((Xq, s_x, kh, pa, Aq, s_a, ka, pb))
+        for b in range(0 if self.keep == 8 else BLOCKS):
             Xq, s_x, h, rs = sbn.sbn_rmsnorm_quant(h if x is None else x, self.gains[b], residual=None if x is None else h)
             a, pa = self._layer(self.up[b], Xq, s_x)
             act = torch.relu(a).square()
@@ -68,12 +81,25 @@ class Model:
 
     def train_step(self, tokens, targets, lr):
         y, (kept, h, rs) = self.forward(tokens)
-        loss, lse = sbn.sbn_cross_entropy(y, self.head, targets)
         (wt, gw), (gt, gg) = self.tables
         d = torch.full((y.shape[0],), 1.0 / y.shape[0], device="cuda")
-        dy, _ = sbn.sbn_cross_entropy_backward(y, self.head, targets, lse, d, dwdt=sbn.SBN_F32, dW=gw[1])
+        if self.entropy:
+            logp, H, lse, _, _ = sbn.sbn_token_logprobs(y, self.head, targets)
+            loss = -logp
+            dy, _ = sbn.sbn_token_logprobs_backward(y, self.head, targets, lse, H, -d, -self.entropy * d,
+                                                    dwdt=sbn.SBN_F32, dW=gw[1])
+        else:
+            loss, lse = sbn.sbn_cross_entropy(y, self.head, targets)
+            dy, _ = sbn.sbn_cross_entropy_backward(y, self.head, targets, lse, d, dwdt=sbn.SBN_F32, dW=gw[1])
         dh, _ = sbn.sbn_rmsnorm_backward(dy, h, self.gains[BLOCKS], rs, dgain=gg[BLOCKS])
-        for b in reversed(range(BLOCKS)):
+        for b in reversed(range(BLOCKS if self.keep == 8 else 0)):
+            Xq, s_x, kh, pa, Aq, s_a, ka, pb = kept[b]
+            dact, _ = sbn.sbn_backward(dh, Aq, s_a, *pb, N, M, dxdt=sbn.SBN_BF16, dW=gw[2 + BLOCKS + b])
+            da, _, _ = sbn.sbn_activation_backward(dact, ka, act=sbn.SBN_RELU2, gain=self.gains[BLOCKS + 1 + b], dA=dact,
+                                                   dgain=gg[BLOCKS + 1 + b])
+            dx, _ = sbn.sbn_backward(da, Xq, s_x, *pa, N, M, dxdt=sbn.SBN_BF16, dW=gw[2 + b])
+            dh, _ = sbn.sbn_rmsnorm_backward_kept(dx, kh, self.gains[b], dH=dh, dX=dx, dgain=gg[b])
+        for b in reversed(range(0 if self.keep == 8 else BLOCKS)):
             Xq, s_x, h, rs, a, pa, Aq, s_a, act, ra, pb = kept[b]
             dact, _ = sbn.sbn_backward(dh, Aq, s_a, *pb, N, M, dxdt=sbn.SBN_BF16, dW=gw[2 + BLOCKS + b])
             dact, _ = sbn.sbn_rmsnorm_backward(dact, act, self.gains[BLOCKS + 1 + b], ra, dgain=gg[BLOCKS + 1 + b])
@@ -92,11 +118,13 @@ def main(argv=None):
     ap = argparse.ArgumentParser(description=__doc__.split("\n\n")[0])
     ap.add_argument("--steps", type=int, default=60)
     ap.add_argument("--bits", type=int, choices=(32, 8), default=32)
+    ap.add_argument("--keep", type=int, choices=(16, 8), default=16)
+    ap.add_argument("--entropy", type=float, default=0.0)
     ap.add_argument("--seed", type=int, default=0)
     a = ap.parse_args(argv)
     g = torch.Generator(device="cuda").manual_seed(a.seed)
     after = torch.randperm(V, generator=g, device="cuda")
-    model, losses = Model(a.bits, a.seed), []
+    model, losses = Model(a.bits, a.seed, a.keep, a.entropy), []
     for i in range(a.steps):
         tokens = torch.randint(0, V, (T,), generator=g, device="cuda")
         losses.append(model.train_step(tokens, after[tokens], 3e-3))
