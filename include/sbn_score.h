@@ -46,7 +46,7 @@ extern "C" {
  *   top     0 .. min(V, SBN_LOGPROBS_MAX_TOP); with 0 top_ids and top_logp may be NULL
  *   top_ids [T x top] int64, top_logp [T x top] float, contiguous        (out)
  *   ws      sbn_token_logprobs_workspace_bytes(T, V, K, top) bytes, no initialisation
- * 2^-20 <= scale <= 2^20; |l| < 2^96.  Limits of T, V and K as for sbn_cross_entropy
+ * 2^-20 <= scale <= 2^20; |l| < 2^30.  Limits of T, V and K as for sbn_cross_entropy
  * (T = 0: nothing to do).
  */
 #define SBN_LOGPROBS_MAX_TOP 64

@@ -110,11 +110,23 @@ __device__ inline float max_dloss(const float* dloss, const void* labels, bool i
 // The same of log probabilities and entropies; a token without a target has its entropy alone
 __device__ inline float max_policy(const float* dlogp, const float* dentropy, const void* labels, bool is64, int V, int T,
                                    int first, int step) {
+  constexpr int AHEAD = 8;                           // loads in flight
   float m = 0.0f;
-  for (int t = first; t < T; t += step) {
-    const int64_t y = dlogp && labels ? label_at(labels, is64, t) : -1;
-    const float g = y >= 0 && y < V ? dlogp[t] : 0.0f;
-    m = fmaxf(m, fmaxf(fabsf(g), dentropy ? fabsf(dentropy[t]) : 0.0f));
+  for (int t0 = first; t0 < T; t0 += step * AHEAD) {
+    float g[AHEAD], h[AHEAD];
+    int64_t y[AHEAD];
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k) {
+      const int t = t0 + step * k < T ? t0 + step * k : t0;
+      g[k] = h[k] = 0.0f, y[k] = -1;
+      if (dlogp) g[k] = dlogp[t], y[k] = label_at(labels, is64, t);
+      if (dentropy) h[k] = dentropy[t];
+    }
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k) {
+      if (y[k] >= 0 && y[k] < V) m = fmaxf(m, fabsf(g[k]));
+      m = fmaxf(m, fabsf(h[k]));
+    }
   }
   return wave_all(m, Max{});
 }
@@ -609,11 +621,16 @@ __global__ __launch_bounds__(64 * WA * WB, 1) void ce_gemm_kernel(GemmArgs P) {
         const bool live = t < P.nB;
         const int64_t y = live && (!POLICY || P.labels) ? label_at(P.labels, P.labels64, t) : -1;
         kept[j] = y >= 0 && y < P.V ? ~0u : 0u;
-        g[j] = kept[j] && (!POLICY || P.dloss) ? P.dloss[t] * ginv : 0.0f, ls[j] = live ? P.lse[t] * LOG2E : 0.0f;
-        if (POLICY) {
-          const float h = live && P.dentropy ? P.dentropy[t] * ginv : 0.0f;
-          c0[j] = -(g[j] + (h != 0.0f ? h * P.entropy[t] : 0.0f)), c1[j] = -LN2 * h;
+        ls[j] = live ? P.lse[t] * LOG2E : 0.0f;
+        if (POLICY) {                                // loads that do not wait for each other
+          float dl = 0.0f, h = 0.0f, ent = 0.0f;
+          if (live && P.dloss) dl = P.dloss[t];
+          if (live && P.dentropy) h = P.dentropy[t] * ginv, ent = P.entropy[t];
+          g[j] = kept[j] ? dl * ginv : 0.0f;
+          c0[j] = -(g[j] + (h != 0.0f ? h * ent : 0.0f)), c1[j] = -LN2 * h;
           used[j] = g[j] != 0.0f || h != 0.0f ? ~0u : 0u;
+        } else {
+          g[j] = kept[j] ? P.dloss[t] * ginv : 0.0f;
         }
         want[j] = kept[j] ? (int)y - P.v0 - aw - l4 : -1;
       }

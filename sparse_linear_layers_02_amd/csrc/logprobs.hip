@@ -246,15 +246,25 @@ __global__ __launch_bounds__(NT, NT == 256 ? 6 : 4) void logprob_top_kernel(RowA
         __syncthreads();
         const int stop = pieces ? (n - b < NT ? n : b + NT) : n;
 #pragma unroll 1
-        for (int g = b + tid; g < stop; g += NT) {   // a set's candidates into the queues
-          const float2 f = row[g];
-          if (f.x < bound || f.y >= over) continue;  // none, or all of them before
-          if (f.y >= bound) {
-            const uint32_t at = atomicAdd(&wholes, 1u);
-            if (at < QUEUE) whole[at] = g;
-          } else if (f.x < over) {
-            const uint32_t at = atomicAdd(&singles, 1u);
-            if (at < QUEUE) single[at] = sets.entry(g, (int)(__float_as_uint(f.x) & (TOPS_MOST - 1)));
+        for (int g0 = b + tid; g0 < stop; g0 += 4 * NT) {   // a set's candidates into the queues
+          float2 fs[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            fs[k] = make_float2(-INFINITY, -INFINITY);
+            if (g0 + k * NT < stop) fs[k] = row[g0 + k * NT];
+          }
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float2 f = fs[k];
+            const int g = g0 + k * NT;
+            if (g >= stop || f.x < bound || f.y >= over) continue;   // none, or all of them before
+            if (f.y >= bound) {
+              const uint32_t at = atomicAdd(&wholes, 1u);
+              if (at < QUEUE) whole[at] = g;
+            } else if (f.x < over) {
+              const uint32_t at = atomicAdd(&singles, 1u);
+              if (at < QUEUE) single[at] = sets.entry(g, (int)(__float_as_uint(f.x) & (TOPS_MOST - 1)));
+            }
           }
         }
         __syncthreads();
