@@ -64,8 +64,8 @@ sbn_status sbn_token_logprobs(const uint16_t* X, int64_t ldx, const uint16_t* W,
  *   dX = scale * D * W       dW = scale * D^T * X       (float32 sums)
  * Where tokens[t] is outside [0, V) dlogp[t] counts as 0, whatever it holds; where
  * both are 0 the row gives nothing, whatever lse and entropy hold (its row of X has
- * to be finite).  D is held in bf16, or in two bf16 numbers for a gradient of type
- * SBN_F32_FINE, as by sbn_cross_entropy_backward.
+ * to be finite).  D is held in bf16, as by sbn_cross_entropy_backward, or in two bf16
+ * numbers for a gradient of type SBN_F32_FINE and, for any type, of up to 128 tokens.
  *
  *   dlogp, dentropy  [T] float; either NULL for zeros.  tokens NULL: dlogp is NULL.
  *                    entropy may be NULL with dentropy.

@@ -41,12 +41,20 @@ constexpr float NONE = -1.0e38f * LOG2E;            // the (scaled) maximum of n
 constexpr int64_t D_ELEMS = int64_t(1) << 28;
 constexpr int GMAX_WAVE = 1024;                     // tokens whose largest |dloss| a wave finds in two rounds of loads
 constexpr int CUS = 256;
+// Log probabilities' gradients take D in two bf16 numbers up to so many tokens: most of
+// a row of dW (and of dX) is then of few products, whose rounding of D no others average
+// (at worst 2^-8 of the row; of 8 tokens, 32001 entries, K = 2560, in bf16 0.0024 of the
+// gradients' norm, with two 0.0016, what rounding them leaves).  It takes 16 to 24% longer
+// (8 tokens 112 -> 130 us, 128 138 -> 168), of 256 45%.
+constexpr int PAIR_TOKENS = 128;
 
-// PAIR: D in two bf16 numbers; OUT, ADD: C in bf16 or float32, ADD on top of Cin.
+// PAIR: D in two bf16 numbers; OUT, ADD: C in bf16 or float32, ADD on top of Cin;
+// TWIN: the sum of two products, with B and a second B, stage by stage.  (One on top of
+// the other, 128 tokens of 50001 entries, K = 4096, with D in two numbers took 939 us, so 542.)
 // SCORE, POLICY: the statistics and D of log probabilities with entropies; TOPS: and
 // the two largest logits of each tops_of(MI), TOPS8: of each 8.
 enum Epi { EPI_STATS, EPI_SCORE, EPI_SCORE_TOPS, EPI_SCORE_TOPS8, EPI_GRAD, EPI_GRAD_PAIR, EPI_POLICY, EPI_POLICY_PAIR, EPI_OUT16, EPI_OUT32,
-           EPI_ADD32 };
+           EPI_TWIN16, EPI_TWIN32, EPI_ADD32 };
 
 struct GemmArgs {
   const uint16_t *A, *B;               // rows of lda, ldb
@@ -74,7 +82,8 @@ struct GemmArgs {
   const float *entropy, *dentropy;     // dloss: of the log probabilities; either gradient may be NULL
   uint16_t* D;                         // [tpad][ldd], ldd a multiple of 256; 0 past the tokens and past nA
   int64_t ldd;
-  int64_t dlow;                        // EPI_GRAD_PAIR: elements from D to what its rounding left
+  int64_t dlow;                        // PAIR: elements from D to what its rounding left
+  int64_t twin;                        // EPI_TWIN: bytes from B to the second one; 0 for others
   int tpad;                            // a multiple of 64
   // EPI_OUT: C [nB][ldc], A outputs along the row
   void* C;
@@ -281,6 +290,7 @@ __global__ __launch_bounds__(64 * WA * WB, 1) void ce_gemm_kernel(GemmArgs P) {
   constexpr bool POLICY = EPI == EPI_POLICY || EPI == EPI_POLICY_PAIR, PAIR = EPI == EPI_GRAD_PAIR || EPI == EPI_POLICY_PAIR;
   constexpr bool GRAD = EPI == EPI_GRAD || PAIR || POLICY;
   constexpr bool TOPS8 = EPI == EPI_SCORE_TOPS8, TOPS = EPI == EPI_SCORE_TOPS || TOPS8, SCORE = EPI == EPI_SCORE || TOPS, STATS = EPI == EPI_STATS || SCORE;
+  constexpr bool TWIN = EPI == EPI_TWIN16 || EPI == EPI_TWIN32;
   constexpr int AHEAD = RING / 2;
   extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
   static_assert(RING >= 5 && RING % 2 == 1 && (RING - 3) * LPH < 64, "a stage, the next one and a half in flight");
@@ -303,6 +313,7 @@ __global__ __launch_bounds__(64 * WA * WB, 1) void ce_gemm_kernel(GemmArgs P) {
     const int more = P.steps - each * P.splits;      // the first `more` parts have one stage more
     t.s_lo = t.part * each + (t.part < more ? t.part : more);
     t.nsteps = each + (t.part < more ? 1 : 0);
+    if (TWIN) t.nsteps *= 2;
     return t;
   };
 
@@ -340,6 +351,13 @@ __global__ __launch_bounds__(64 * WA * WB, 1) void ce_gemm_kernel(GemmArgs P) {
   auto next_stage = [&]() {                          // past the last item: its last stage again
     if (lleft > 1) {
       --lleft;
+      if (TWIN) {                                    // a stage of B, then the same one of the second B
+        if (lleft & 1) {
+          gB += P.twin;
+          return;
+        }
+        gB -= P.twin;
+      }
       k0 += BK;
       gA += TRA ? P.lda * (2 * BK) : 2 * BK;
       gB += TRB ? P.ldb * (2 * BK) : 2 * BK;
@@ -702,7 +720,7 @@ __global__ __launch_bounds__(64 * WA * WB, 1) void ce_gemm_kernel(GemmArgs P) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) c[h][e] = x[e] * gmax;
           }
-          if (EPI != EPI_OUT16) {
+          if (EPI != EPI_OUT16 && EPI != EPI_TWIN16) {
             float* to = (float*)P.C + row + 16 * i + l4;
             *(v4f*)to = *(const v4f*)c[0], *(v4f*)(to + 16) = *(const v4f*)c[1];
           } else {
@@ -940,12 +958,13 @@ template <bool TRB>
 hipError_t product(Names& names, Tile tile, GemmArgs P, bool c_f32, float* part, hipStream_t st) {
   if (P.splits == 1) {
     if (TRB && P.Cin) return gemm<EPI_ADD32, true, TRB>(names, tile, P, st);
+    if (P.twin) return c_f32 ? gemm<EPI_TWIN32, true, TRB>(names, tile, P, st) : gemm<EPI_TWIN16, true, TRB>(names, tile, P, st);
     return c_f32 ? gemm<EPI_OUT32, true, TRB>(names, tile, P, st) : gemm<EPI_OUT16, true, TRB>(names, tile, P, st);
   }
   GemmArgs Q = P;                                    // the parts' sums side by side
   Q.C = part, Q.ldc = P.nA, Q.part_stride = (int64_t)P.nB * P.nA;
   Q.Cin = nullptr, Q.gmax = nullptr;
-  const hipError_t e = gemm<EPI_OUT32, true, TRB>(names, tile, Q, st);
+  const hipError_t e = P.twin ? gemm<EPI_TWIN32, true, TRB>(names, tile, Q, st) : gemm<EPI_OUT32, true, TRB>(names, tile, Q, st);
   if (e != hipSuccess) return e;
   SBN_LAUNCH("ce_sum", ce_sum_kernel, dim3((unsigned)grid_for((int64_t)P.nB * (P.nA / 4))), dim3(256), 0, st, part,
              P.splits, (int64_t)P.nB, P.nA, P.Cin, P.ldcin, P.gmax, P.C, c_f32, P.ldc);
@@ -1009,13 +1028,16 @@ hipError_t launch_logits(const uint16_t* X, int64_t ldx, const uint16_t* W, int6
 }
 int64_t logit_groups(int64_t T, int64_t V, int64_t K) { return stats_groups(T, V, K); }
 
+bool policy_pair(int64_t T) { return T <= PAIR_TOKENS; }
 size_t ce_bwd_ws_bytes(int64_t T, int64_t V, int64_t K, bool pair) { return ce_plan(T, V, K, pair).total; }
 
 hipError_t launch_ce_backward(const uint16_t* X, int64_t ldx, const uint16_t* W, int64_t ldw, const HeadGrad& H, int64_t T,
                               int64_t V, int64_t K, void* dX, sbn_dtype dxdt, int64_t lddx, void* dW, sbn_dtype dwdt,
                               int64_t lddw, void* ws, hipStream_t st) {
   const bool dx_f32 = dxdt != SBN_BF16, dw_f32 = dwdt != SBN_BF16;
-  const bool dx_pair = dX && dxdt == SBN_F32_FINE, dw_pair = dW && dwdt == SBN_F32_FINE, pair = dx_pair || dw_pair;
+  // a second product, added to the first one's, or one of both numbers
+  const bool dx_pair = dX && dxdt == SBN_F32_FINE, dw_pair = dW && dwdt == SBN_F32_FINE, few = H.policy && T <= PAIR_TOKENS,
+             pair = dx_pair || dw_pair || few;
   const CePlan L = ce_plan(T, V, K, pair);
   uint8_t* w = (uint8_t*)ws;
   uint16_t* D = (uint16_t*)(w + L.d);
@@ -1047,25 +1069,27 @@ hipError_t launch_ce_backward(const uint16_t* X, int64_t ldx, const uint16_t* W,
     if (H.policy) e = pair ? gemm<EPI_POLICY_PAIR>(DPOLICY, tile, G, st) : gemm<EPI_POLICY>(DPOLICY, tile, G, st);
     else e = pair ? gemm<EPI_GRAD_PAIR>(DLOGITS, tile, G, st) : gemm<EPI_GRAD>(DLOGITS, tile, G, st);
     if (e != hipSuccess) return e;
-    for (int low = 0; dX && low <= (int)dx_pair; ++low) {
+    for (int low = 0; dX && low <= (int)(dx_pair && !H.policy); ++low) {
       GemmArgs P{};
       P.A = W + v0 * ldw, P.lda = ldw, P.nA = P.mA = (int)K, P.kA = (int)nv;
       P.B = D + low * dlow, P.ldb = L.piece, P.nB = P.mB = (int)T;
       P.steps = (int)(vpad / BK), P.splits = L.x.splits <= P.steps ? L.x.splits : P.steps;
-      const bool last = i + 1 == L.pieces && low == (int)dx_pair;
+      const bool last = i + 1 == L.pieces && low == (int)(dx_pair && !H.policy);
+      P.twin = H.policy && (few || dx_pair) ? 2 * dlow : 0;
       P.Cin = i > 0 || low > 0 ? acc : nullptr, P.ldcin = K;
       P.gmax = last ? factor : nullptr;
       P.C = last ? dX : acc, P.ldc = last ? lddx : K;
       if ((e = product<false>(DX, L.x.tile, P, last ? dx_f32 : true, part, st)) != hipSuccess) return e;
     }
-    for (int low = 0; dW && low <= (int)dw_pair; ++low) {
+    for (int low = 0; dW && low <= (int)(dw_pair && !H.policy); ++low) {
       GemmArgs P{};
       P.A = X, P.lda = ldx, P.nA = P.mA = (int)K, P.kA = (int)T;
       P.B = D + low * dlow, P.ldb = L.piece, P.nB = (int)nv, P.mB = (int)vpad, P.kB = (int)L.tpad;
       P.steps = (int)(L.tpad / BK), P.splits = L.w.splits;
       P.C = (uint8_t*)dW + v0 * lddw * (dw_f32 ? 4 : 2), P.ldc = lddw;
       P.Cin = low > 0 ? (const float*)P.C : nullptr, P.ldcin = lddw;
-      P.gmax = low == (int)dw_pair ? factor : nullptr;
+      P.twin = H.policy && (few || dw_pair) ? 2 * dlow : 0;
+      P.gmax = low == (int)(dw_pair && !H.policy) ? factor : nullptr;
       if ((e = product<true>(DW, L.w.tile, P, dw_f32, part, st)) != hipSuccess) return e;
     }
   }

@@ -109,7 +109,8 @@ sbn_status sbn_token_logprobs_backward(const uint16_t* X, int64_t ldx, const uin
   SBN_ELEM_ALIGNED(dlogp, 4);
   SBN_ELEM_ALIGNED(dentropy, 4);
   SBN_ALIGNED(ws);
-  const size_t need = ce_bwd_ws_bytes(T, V, K, (dX && dxdt == SBN_F32_FINE) || (dW && dwdt == SBN_F32_FINE));
+  const bool pair = policy_pair(T) || (dX && dxdt == SBN_F32_FINE) || (dW && dwdt == SBN_F32_FINE);
+  const size_t need = ce_bwd_ws_bytes(T, V, K, pair);
   if (ws_bytes < need) return fail(SBN_ERR_WORKSPACE, "%s: workspace %zu bytes, need %zu", fn, ws_bytes, need);
   if (!dX && !dW) return ok();
   if (dW) SBN_NOT_IN_PLACE(dX, X);                   // which dW's product reads after dX's last

@@ -12,7 +12,7 @@ Bounds, with u = 2^-24 and b = 2^-8, each a worst case (l: scaled logits):
   top      ids: those of 64-bit sums; values: lse's and 2 u of their own
   D        with s = sum of the errors of l, of lse and 6 u (1 + |l| + |lse|):
            p s (|dlogp| + |dH| (|log p| + |H| + 1)) + p |dH| (entropy's) + 8 u p (|dlogp| + |dH|
-           (|log p| + |H|)) + b |D| + 2 u |dlogp|; in two bf16 numbers 2^-16 for b
+           (|log p| + |H|)) + b |D| + 2 u |dlogp|; in two bf16 numbers, as up to 128 tokens, 2^-16 for b
   dX       scale (sum_v D's |w| + (V + 16) u sum_v |D w|), + b |dX| for bf16; dW the same over t
 """
 from __future__ import annotations
@@ -100,7 +100,7 @@ def check_forward(got, r, y, top):
 
 SHAPES = [(1, 1, 64), (1, 1000, 64), (2, 63, 128), (17, 64, 64), (64, 65, 192), (65, 129, 64), (130, 257, 320),
           (1, 513, 2560), (33, 1999, 128), (257, 300, 64), (300, 2500, 256), (1021, 777, 192), (64, 9001, 64),
-          (2100, 4700, 64), (4100, 4097, 128), (3, 30011, 64)]
+          (2100, 4700, 64), (4100, 4097, 128), (3, 30011, 64), (128, 1500, 192), (129, 1500, 192)]
 
 
 @pytest.mark.parametrize("T,V,K", SHAPES)
@@ -108,7 +108,7 @@ def test_forward_and_gradients(T, V, K):
     import torch
     scale = (1.0, 0.75, 1.3)[(T + V) % 3]
     X, W, y, dl, dh = problem(T, V, K, 1000 * T + V, ignored=0.2 if T > 1 else 0.0)
-    r = reference(X, W, y, scale, dl, dh)
+    r = reference(X, W, y, scale, dl, dh, fine=T <= 128)
     for top in sorted({0, 1, min(V, 7), min(V, 64)}):
         check_forward(sbn.sbn_token_logprobs(X, W, y, scale=scale, top=top), r, y, top)
     logp, H, lse, _, _ = a = sbn.sbn_token_logprobs(X, W, y, scale=scale)
@@ -139,6 +139,11 @@ def test_fine_gradients(T, V, K):
     dX, dW = sbn.sbn_token_logprobs_backward(X, W, y, lse, H, dl, dh, scale=1.3, dxdt=two, dwdt=two)
     close(dX, r["dX"], r["bX"], "dX")
     close(dW, r["dW"], r["bW"], "dW")
+    x2, w2 = sbn.sbn_token_logprobs_backward(X, W, y, lse, H, dl, dh, scale=1.3, dxdt=two)      # one of them alone
+    x3, w3 = sbn.sbn_token_logprobs_backward(X, W, y, lse, H, dl, dh, scale=1.3, dwdt=two)
+    assert (x2 == dX).all() and (w3 == dW).all()
+    one = sbn.sbn_token_logprobs_backward(X, W, y, lse, H, dl, dh, scale=1.3)
+    assert (x3 == one[0]).all() and (w2 == one[1]).all()
 
 
 def test_one_gradient_alone():
@@ -302,15 +307,17 @@ def test_tiles(shape, tile):
         assert (g.double() - ref).norm() <= 2.0 ** -7 * ref.norm(), what
 
 
-def test_several_pieces_of_the_vocabulary():
+@pytest.mark.parametrize("T,V,dxdt,pieces", [(4096, 70001, sbn.SBN_F32, 2), (4096, 70001, sbn.SBN_F32_FINE, 3),
+                                             (100, 1100003, sbn.SBN_F32, 2)])
+def test_several_pieces_of_the_vocabulary(T, V, dxdt, pieces):
     import torch
-    T, V, K = 4096, 70001, 64
+    K = 64
     X, W, y, dl, dh = problem(T, V, K, 7)
-    r = reference(X, W, y, 0.75, dl, dh)
+    r = reference(X, W, y, 0.75, dl, dh, fine=T <= 128)
     logp, H, lse, _, _ = sbn.sbn_token_logprobs(X, W, y, scale=0.75)
-    f = dict(scale=0.75, dxdt=sbn.SBN_F32)
+    f = dict(scale=0.75, dxdt=dxdt)
     (dX, dW), ran = launches(lambda: sbn.sbn_token_logprobs_backward(X, W, y, lse, H, dl, dh, **f))
-    assert sum(n for k, n in ran.items() if k.startswith("logprob_dlogits")) == 2
+    assert sum(n for k, n in ran.items() if k.startswith("logprob_dlogits")) == pieces
     close(dX, r["dX"], r["bX"], "dX")
     close(dW, r["dW"], r["bW"] + B * r["dW"].abs(), "dW")
     again = sbn.sbn_token_logprobs_backward(X, W, y, lse, H, dl, dh, **f)
