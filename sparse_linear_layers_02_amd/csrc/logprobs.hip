@@ -331,7 +331,7 @@ __global__ __launch_bounds__(NT, NT == 256 ? 6 : 4) void logprob_top_kernel(RowA
       const double least = value[top - 1];
       const double margin = 2.0 * ((double)(P.K + 64) * 0x1p-24 * (double)__uint_as_float(largest) + 0x1p-17 * fabs(least));
       if (bound == -INFINITY || !((double)bound + margin > least)) break;
-      over = bound, bound = __double2float_rd(least - margin);
+      over = bound, bound = round < 14 ? __double2float_rd(least - margin) : -INFINITY;   // everything, in the end
       __syncthreads();                               // value and largest are read by all
     }
     for (int i = tid; i < top; i += NT) {

@@ -24,6 +24,7 @@ import pytest
 
 import sparse_linear_layers_02_amd as sbn
 from test_gpu_graphs import replay_matches
+from test_gpu_head_tiles import launches
 from test_gpu_rmsnorm import B, U, close, get, put, reference, rnd, codes_of
 from gpu_util import dev, host
 
@@ -402,6 +403,43 @@ def test_many_elements():
     for k in (ka, e):
         assert torch.equal(k.codes[-last:], kt.codes) and torch.equal(k.scales[-last:], kt.scales)
     assert torch.equal(y[-last:], sbn.sbn_keep8_decode(kt, dt=sbn.SBN_BF16))
+
+
+@pytest.mark.parametrize("gain", [True, False])
+def test_many_short_rows(gain):
+    """More rows than a grid has blocks (2^20): the last ones as in a call of their own."""
+    import torch
+    T, K, last = 2 ** 20 + 77, 40, 100
+    g = torch.Generator(device="cuda").manual_seed(2)
+    a, b = (torch.randn(T, K, generator=g, device="cuda", dtype=torch.bfloat16) for _ in range(2))
+    w = torch.linspace(0.5, 1.5, K, device="cuda") if gain else None
+
+    def work(a, b):
+        Xq, s_x, ka, kb = sbn.sbn_activation_quant(a, b, act=sbn.SBN_SILU, gain=w)
+        dA, dB, _ = sbn.sbn_activation_backward(b, ka, kb, act=sbn.SBN_SILU, gain=w)
+        out = [Xq, s_x, *ka, *kb, dA, dB]
+        if gain:
+            Xn, s_n, H, kh = sbn.sbn_rmsnorm_quant_keep(a, w, residual=b)
+            out += [Xn, s_n, H, *kh, sbn.sbn_rmsnorm_backward_kept(b, kh, w, dH=a)[0]]
+        return out
+
+    for x, y in zip(work(a, b), work(a[-last:].contiguous(), b[-last:].contiguous())):
+        assert torch.equal(x[-last:], y)
+
+
+def test_more_threads_than_a_launch_takes():
+    """Checkpoints of so many short rows that they are taken in two launches."""
+    import torch
+    T, K, last = 2 ** 27 + 9, 8, 3 * 2 ** 20                        # 16 threads a row
+    x = torch.empty((T, K), dtype=torch.bfloat16, device="cuda")
+    for t in range(0, T, 2 ** 25):
+        n = min(2 ** 25, T - t)
+        x[t: t + n] = (torch.arange(t, t + n, device="cuda") % 8191 - 4000)[:, None] * torch.arange(1, K + 1, device="cuda")
+    kept, launched = launches(lambda: sbn.sbn_keep8_encode(x))
+    assert launched["keep8_encode"] == 2
+    tail = sbn.sbn_keep8_encode(x[-last:].contiguous())
+    assert torch.equal(kept.codes[-last:], tail.codes) and torch.equal(kept.scales[-last:], tail.scales)
+    assert torch.equal(sbn.sbn_keep8_decode(kept, dt=sbn.SBN_BF16)[-last:], sbn.sbn_keep8_decode(tail, dt=sbn.SBN_BF16))
 
 
 def test_finite_check(monkeypatch):

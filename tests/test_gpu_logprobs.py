@@ -402,6 +402,53 @@ def test_streams_at_once():
             assert all(torch.equal(p, q) for p, q in zip(a, b))
 
 
+def test_threads_at_once():
+    """Two threads of calls, on streams of their own and both on one."""
+    import threading
+
+    import torch
+    ins = [problem(200 + 70 * i, 3000, 128, 50 + i) for i in range(2)]
+
+    def work(X, W, y, dl, dh):
+        logp, H, lse, ids, tlp = sbn.sbn_token_logprobs(X, W, y, top=4)
+        return (logp, H, lse, ids, tlp, *sbn.sbn_token_logprobs_backward(X, W, y, lse, H, dl, dh))
+
+    ref = [work(*a) for a in ins]
+    torch.cuda.synchronize()
+    one = torch.cuda.Stream()
+    for streams in ([torch.cuda.Stream(), torch.cuda.Stream()], [one, one]):
+        got = [[], []]
+
+        def run(i):
+            with torch.cuda.stream(streams[i]):
+                got[i] += [work(*ins[i]) for _ in range(20)]
+
+        threads = [threading.Thread(target=run, args=(i,)) for i in range(2)]
+        for t in threads:
+            t.start()
+        for t in threads:
+            t.join()
+        torch.cuda.synchronize()
+        for a, r in zip(got, ref):
+            assert len(a) == 20 and all(torch.equal(p, q) for out in a for p, q in zip(out, r))
+
+
+@pytest.mark.parametrize("T,top", [(5, 3), (5, 64), (300, 3), (300, 20)])
+def test_rows_that_are_not_finite_stay_alone(T, top):
+    """Outside the contract: the call ends, its ids are of the vocabulary, and the other rows have their values."""
+    import torch
+    V, K = 2100, 64
+    X, W, y, _, _ = problem(T, V, K, 60, ignored=0.0)
+    ref = sbn.sbn_token_logprobs(X, W, y, top=top)
+    bad = X.clone()
+    bad[1, 5], bad[3, 7] = float("nan"), float("inf")
+    got = sbn.sbn_token_logprobs(bad, W, y, top=top)
+    rest = torch.tensor([t not in (1, 3) for t in range(T)], device="cuda")
+    assert all(torch.equal(a[rest], b[rest]) for a, b in zip(got, ref))
+    assert ((got[3] >= 0) & (got[3] < V)).all()
+    assert got[0][1].isnan() and got[2][1].isnan()
+
+
 def test_a_batch_of_a_large_vocabulary():
     """The alternatives' pairs past 2^31 bytes: the last rows as in a call of their own."""
     import torch
