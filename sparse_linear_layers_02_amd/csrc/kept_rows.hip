@@ -99,26 +99,32 @@ __global__ __launch_bounds__(256) void keep8_decode_kernel(const int8_t* __restr
 // ---------------------------------------------------------------- the functions
 enum RowOp { ROW_NORM, ROW_RELU2, ROW_SILU };        // ROW_NORM: u = x
 
-// f(a) and, if asked, f'(a)
+// 1 / (1 + exp(-a)), the exponential by the base-2 instruction, with what the exponent's
+// rounding left and the constant's: within 3 units of 2^-24; where it is Inf, 0
+__device__ inline float sigmoid(float a) {
+  constexpr float L = -1.44269502f, LOW = -1.925963033e-8f;
+  const float z = a * L, low = fmaf(a, LOW, fmaf(a, L, -z));
+  const float e = __builtin_amdgcn_exp2f(z) * fmaf(low, 0.6931471806f, 1.0f);
+  return __builtin_amdgcn_rcpf(1.0f + e);
+}
+// f(a), given ROW_SILU's sigmoid g, and, if asked, f'(a)
 template <RowOp OP>
-__device__ inline float act(float a, float* slope = nullptr) {
+__device__ inline float act(float a, float g, float* slope = nullptr) {
   if (OP == ROW_RELU2) {
     const float r = fmaxf(a, 0.0f);
     if (slope) *slope = 2.0f * r;
     return r * r;
   }
   if (OP == ROW_SILU) {
-    // exp(-a) by the base-2 instruction, with what the exponent's rounding left and the
-    // constant's: within 3 units of 2^-24; where it is Inf, g is 0
-    constexpr float L = -1.44269502f, LOW = -1.925963033e-8f;
-    const float z = a * L, low = fmaf(a, LOW, fmaf(a, L, -z));
-    const float e = __builtin_amdgcn_exp2f(z) * fmaf(low, 0.6931471806f, 1.0f);
-    const float g = __builtin_amdgcn_rcpf(1.0f + e);
     if (slope) *slope = g * (1.0f + a * (1.0f - g));
     return a * g;
   }
   if (slope) *slope = 1.0f;
   return a;
+}
+template <RowOp OP>
+__device__ inline float act(float a, float* slope = nullptr) {
+  return act<OP>(a, OP == ROW_SILU ? sigmoid(a) : 0.0f, slope);
 }
 
 // sums or maxima of a row's waves, from LDS `red` of its own; all threads call it
@@ -356,30 +362,41 @@ struct KeptRow {
   }
 };
 
-// A row is loaded while the one before it is worked on.
-template <bool F32, RowOp OP, int CH, int MAXT>
+// A row is loaded while the one before it is worked on.  Without a gain a block has a
+// row, unless there are more than GRID_MAX: nothing is summed over rows, and no wave
+// waits for another (8192 x 11008 bf16, ROW_SILU, gated: 129 us, 5.6 TB/s; as many
+// blocks as fit at once, rows ahead: 151).  Normed, ROW_RELU2 143 to 152 us, 4.8 to 5.1 TB/s;
+// ROW_SILU 192, by its exponentials.  ROW_SILU's sigmoids are kept from
+// the sums to the gradients, up to two chunks a thread (8192 x 11008 bf16, gated and
+// normed 221 -> 195 us; with four, float32 rows spilled: 182 -> 276).
+template <bool F32, RowOp OP, int CH, int MAXT, bool GAIN>
 __global__ __launch_bounds__(MAXT) void kept_backward_kernel(BwdArgs P) {
   __shared__ float red[2][2][MAXT / 64];
   const int g = threadIdx.x, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
   const int n = P.K / 8, es = F32 ? 4 : 2, TPR = blockDim.x, nb = (n + LANES - 1) / LANES;
+  // true wherever GAIN is, but asked: with it known the schedule of ROW_RELU2's bf16 rows takes 5 to 10% longer
+  const bool normed = GAIN && P.gain;
   float dg[CH][8], kept_gain[CH][8];
 #pragma unroll
   for (int i = 0; i < CH; ++i)
 #pragma unroll
     for (int j = 0; j < 8; ++j) dg[i][j] = 0.0f;
-  if (P.gain) {
+  if (normed) {
 #pragma unroll
     for (int i = 0; i < CH; ++i)
       if (g + TPR * i < n) gain8(P.gain, P.gain_f32, g + TPR * i, kept_gain[i]);
   }
+  constexpr bool KEEP = GAIN && OP == ROW_SILU && CH <= 2;
+  float sig[KEEP ? CH : 1][8];
   int turn = 0;
   KeptRow<F32, OP, CH> row, next;
   next.load(P, blockIdx.x, nb);
   for (int64_t t = blockIdx.x; t < P.T; t += gridDim.x, turn ^= 1) {
     row = next;
-    next.load(P, t + gridDim.x < P.T ? t + gridDim.x : t, nb);
+    if (GAIN) next.load(P, t + gridDim.x < P.T ? t + gridDim.x : t, nb);
+    else if (t + gridDim.x < P.T) next.load(P, t + gridDim.x, nb);
     float r = 1.0f, back = 0.0f;                     // back: r^2 mean(w u)
-    if (P.gain) {
+    if (normed) {
       float uu = 0.0f, wu = 0.0f;
 #pragma unroll
       for (int i = 0; i < CH; ++i) {
@@ -391,7 +408,8 @@ __global__ __launch_bounds__(MAXT) void kept_backward_kernel(BwdArgs P) {
           row.dy[i].to(w);
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
-            float u = act<OP>(a[j]);
+            if (KEEP) sig[i][j] = sigmoid(a[j]);
+            float u = KEEP ? act<OP>(a[j], sig[i][j]) : act<OP>(a[j]);
             if (OP != ROW_NORM && P.kB) u *= b[j];
             uu += u * u;
             wu += w[j] * gain[j] * u;
@@ -421,9 +439,9 @@ __global__ __launch_bounds__(MAXT) void kept_backward_kernel(BwdArgs P) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           float slope;
-          const float f = act<OP>(a[j], &slope);
+          const float f = KEEP ? act<OP>(a[j], sig[i][j], &slope) : act<OP>(a[j], &slope);
           float du = d[j];
-          if (P.gain) {
+          if (normed) {
             const float u = OP != ROW_NORM && P.kB ? f * b[j] : f;
             dg[i][j] += d[j] * (u * r);
             du = r * (d[j] * gain[j] - u * back);
@@ -445,7 +463,7 @@ __global__ __launch_bounds__(MAXT) void kept_backward_kernel(BwdArgs P) {
       }
     }
   }
-  if (!P.gain) return;
+  if (!normed) return;
   float* out = P.part + (int64_t)blockIdx.x * P.K;
 #pragma unroll
   for (int i = 0; i < CH; ++i) {
@@ -584,9 +602,12 @@ int bwd_blocks(int64_t T, int64_t K) {
 
 template <bool F32, RowOp OP, int CH, int MAXT>
 void run_bwd(const char* name, const BwdArgs& P, hipStream_t st) {
-  const int64_t blocks = P.gain ? bwd_blocks(P.T, P.K) : P.T < GRID_MAX ? P.T : GRID_MAX;
-  SBN_LAUNCH(name, (kept_backward_kernel<F32, OP, CH, MAXT>), dim3((unsigned)blocks),
-             dim3((unsigned)threads_for(P.K / 8, CH)), 0, st, P);
+  const dim3 threads((unsigned)threads_for(P.K / 8, CH));
+  if (OP == ROW_NORM || P.gain)
+    SBN_LAUNCH(name, (kept_backward_kernel<F32, OP, CH, MAXT, true>), dim3((unsigned)bwd_blocks(P.T, P.K)), threads, 0, st, P);
+  else
+    SBN_LAUNCH(name, (kept_backward_kernel<F32, OP, CH, MAXT, OP == ROW_NORM>),
+               dim3((unsigned)(P.T < GRID_MAX ? P.T : GRID_MAX)), threads, 0, st, P);
 }
 template <bool F32, RowOp OP>
 hipError_t run_bwd_wide(const char* name, const BwdArgs& P, hipStream_t st) {
