@@ -7,10 +7,15 @@
 // 2^(m - M) (q + (m - M) s).  Both terms of the entropy are of its own size, so a
 // distribution that is nearly certain loses nothing to a difference.
 //
-// Alternatives: of every 32 or 16 logits, the two largest are kept in float32.  The k-th largest of any partition's maxima is no larger than the k-th
-// largest logit, so a row's candidates are the firsts above such a bound, and, where
-// a second is above it as well, all of them.  Candidates' sums are formed again, in 64 bits,
-// and ordered by them.
+// Alternatives: of every 32, 16 or 8 logits, the two largest are kept in float32.  The
+// k-th largest of any partition's maxima is no larger than the k-th largest logit, so a
+// row's candidates are the firsts above such a bound, and, where a second is above it as
+// well, all of its set.  Candidates' sums are formed again, in 64 bits, and ordered by them.
+//
+// Bound by dependent reads: of one token (50001 entries, K = 2560, 8 alternatives) 14 us,
+// 2.5 of them the join, 2 the bound, 2 the scan, 4 the sums of K, 1 their order; of 37
+// tokens (32001, 4096, 20 alternatives) 24.  Of 4096 tokens (65536, 2560, 8) 92 to 104 us
+// for 67 MB of sets and 330 MB of rows of W, and 9 the join.
 #include "score_internal.h"
 
 namespace sbn {
@@ -163,8 +168,9 @@ __device__ inline float reached_by(const float* slot, int k) {
 // places in a queue, whose order does not matter: candidates are ordered by (sum,
 // index) in the end.  The code is kept short, without unrolling: one token's block
 // fetches each line of it for the first time.
-// Many tokens: 5 loads ahead in 84 registers, 6 blocks a unit (4096 tokens of 65536
-// entries, K = 2560, 8 alternatives: 104 us; 8 ahead, 4 blocks: 113; 3, 8: 113).
+// Many tokens: 5 loads ahead in 84 registers (4 of them spilled, outside the sums), 6
+// blocks a unit (4096 tokens of 65536 entries, K = 2560, 8 alternatives: 101 us; 5 blocks
+// without spills 102; 4 ahead 120; 6 ahead, 4 or 5 blocks 107; 3, 8 blocks: 113).
 template <int NT, bool JOIN>
 __global__ __launch_bounds__(NT, NT == 256 ? 6 : 4) void logprob_top_kernel(RowArgs P) {
   constexpr int WAVES = NT / 64, SLOTS = 256, QUEUE = 1024, BATCH = 256, MOST = SBN_LOGPROBS_MAX_TOP;

@@ -10,7 +10,7 @@ namespace sbn {
 // Statistics come in logit_groups() groups of entries, [group][T]: (maximum, sum of
 // exponentials) and the sum of exponential times exponent, exponents times log2 e and
 // less the maximum.  `target` [T]: the token's logit.  tops (or NULL): per token
-// logit_tops().groups pairs of the largest and second largest of a set of 32 or 16
+// logit_tops().groups pairs of the largest and second largest of a set of 32, 16 or 8
 // sums (logits before their scale), the first's place in its last 5 bits.  A set is
 // what one lane holds of a column; of lanes that hold 8, two.  (Few tokens: sets of 8
 // are 64 KB to read for each at 65536 entries, and of 32 twice as often one with two
