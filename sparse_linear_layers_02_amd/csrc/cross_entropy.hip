@@ -49,8 +49,8 @@ constexpr int CUS = 256;
 // Log probabilities' gradients take D in two bf16 numbers up to so many tokens: most of
 // a row of dW (and of dX) is then of few products, whose rounding of D no others average
 // (at worst 2^-8 of the row; of 8 tokens, 32001 entries, K = 2560, in bf16 0.0024 of the
-// gradients' norm, with two 0.0016, what rounding them leaves).  It takes 16 to 24% longer
-// (8 tokens 112 -> 130 us, 128 138 -> 168), of 256 45%.
+// gradients' norm, with two 0.0016, what rounding them leaves).  It takes 4 to 24% longer
+// (8 tokens 112 -> 116 us, 128 138 -> 168), of 256 45%.
 constexpr int PAIR_TOKENS = 128;
 
 // PAIR: D in two bf16 numbers; OUT, ADD: C in bf16 or float32, ADD on top of Cin;
@@ -815,7 +815,15 @@ __global__ __launch_bounds__(256) void ce_sum_kernel(const float* __restrict__ p
   const int64_t n = rows * (cols / 4);
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
     v4f c = ((const v4f*)part)[i];
-    for (int p = 1; p < splits; ++p) c += ((const v4f*)part)[p * n + i];
+    int p = 1;
+    for (; p + 8 <= splits; p += 8) {                // 8 loads in flight
+      v4f x[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) x[k] = ((const v4f*)part)[(p + k) * n + i];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) c += x[k];
+    }
+    for (; p < splits; ++p) c += ((const v4f*)part)[p * n + i];
     const int64_t r = i / (cols / 4), a = (i - r * (cols / 4)) * 4;
     if (Cin) c += *(const v4f*)(Cin + r * ldcin + a);
     c *= scale;
@@ -889,7 +897,7 @@ hipError_t gemm(Names& names, Tile tile, GemmArgs& P, hipStream_t st) {
 int64_t tiles_of(Tile t, int64_t a, int64_t b) { return cdiv(a, SHAPE[t].a) * cdiv(b, SHAPE[t].b); }
 
 // The tile shape of a product and the parts its contraction is split into
-// (splittable: 1 .. 16), by their estimated time in stages of a wide tile (1.45 us):
+// (splittable: 1 .. `most`), by their estimated time in stages of a wide tile (1.45 us):
 //   sum of rounds (stages x stage + start, with parts + 1 or 2), with parts + 2 + (2 parts + 1) a b 6.1e-7
 // A compute unit runs one wide block or two of the others.  stage is that of a
 // round that fills the machine; where at most one block of two runs on each
@@ -905,7 +913,7 @@ struct Choice {
   Tile tile;
   int splits;
 };
-Choice pick(int64_t a, int64_t b, int64_t steps, bool splittable) {
+Choice pick(int64_t a, int64_t b, int64_t steps, bool splittable, int most = 16) {
   const double STAGE[] = {1.0, 0.7, splittable ? 0.54 : 0.44}, ALONE[] = {1.0, 0.33, splittable ? 0.27 : 0.22};
   constexpr double START[] = {6.0, 5.0, 4.0}, PARTS[] = {2.0, 1.0, 1.0};
   Choice best{WIDE, 1};
@@ -913,7 +921,7 @@ Choice pick(int64_t a, int64_t b, int64_t steps, bool splittable) {
   for (const Tile t : {WIDE, SQUARE, FLAT}) {
     const int slots = t == WIDE ? CUS : 2 * CUS;
     const int64_t n = tiles_of(t, a, b);
-    for (int s = 1; s <= (splittable ? 16 : 1) && (s == 1 || steps / s >= 16); ++s) {
+    for (int s = 1; s <= (splittable ? most : 1) && (s == 1 || steps / s >= 16); s += s < 16 ? 1 : s / 4) {
       const int64_t full = n * s / slots, rest = n * s % slots;
       double stage = (double)full * STAGE[t];
       if (rest) stage += rest > CUS ? STAGE[t] : ALONE[t] * (t == WIDE ? 0.75 + 0.25 * (double)rest / CUS : 1.0);
@@ -933,8 +941,8 @@ struct CePlan {
   size_t gmax, d, acc, part, total;
 };
 
-// pair: D in two bf16 numbers, for SBN_F32_FINE
-CePlan ce_plan(int64_t T, int64_t V, int64_t K, bool pair) {
+// pair: D in two bf16 numbers; twin_x, twin_w: both in one product, of twice the stages
+CePlan ce_plan(int64_t T, int64_t V, int64_t K, bool pair, bool twin_x = false, bool twin_w = false) {
   CePlan L;
   L.tpad = round_up(T, 64);
   int64_t most = D_ELEMS / (pair ? 2 : 1) / L.tpad / 256 * 256;
@@ -943,8 +951,10 @@ CePlan ce_plan(int64_t T, int64_t V, int64_t K, bool pair) {
   L.pieces = cdiv(vpad, most);
   L.piece = round_up(cdiv(vpad, L.pieces), 256);
   L.pieces = cdiv(V, L.piece);
-  L.x = pick(K, T, L.piece / BK, true);
-  L.w = pick(K, L.piece, L.tpad / BK, true);
+  // few tokens leave few tiles, and two numbers twice the stages: more parts (dX and their sum, 8 tokens
+  // of 32001 entries, K = 2560: 42 + 5 -> 32 + 4.5 us; 2 of 47758, K = 320: 41 + 6 -> 14.5 + 5.7)
+  L.x = pick(K, T, L.piece / BK * (twin_x ? 2 : 1), true, twin_x && T <= PAIR_TOKENS ? 64 : 16);
+  L.w = pick(K, L.piece, L.tpad / BK * (twin_w ? 2 : 1), true);
   size_t o = 0;
   auto take = [&](size_t bytes) {
     const size_t at = o;
@@ -1036,8 +1046,16 @@ hipError_t launch_logits(const uint16_t* X, int64_t ldx, const uint16_t* W, int6
 }
 int64_t logit_groups(int64_t T, int64_t V, int64_t K) { return stats_groups(T, V, K); }
 
-bool policy_pair(int64_t T) { return T <= PAIR_TOKENS; }
 size_t ce_bwd_ws_bytes(int64_t T, int64_t V, int64_t K, bool pair) { return ce_plan(T, V, K, pair).total; }
+namespace {
+CePlan policy_plan(int64_t T, int64_t V, int64_t K, bool fine_x, bool fine_w) {
+  const bool few = T <= PAIR_TOKENS;
+  return ce_plan(T, V, K, few || fine_x || fine_w, few || fine_x, few || fine_w);
+}
+}  // namespace
+size_t policy_bwd_ws_bytes(int64_t T, int64_t V, int64_t K, bool fine_x, bool fine_w) {
+  return policy_plan(T, V, K, fine_x, fine_w).total;
+}
 
 hipError_t launch_ce_backward(const uint16_t* X, int64_t ldx, const uint16_t* W, int64_t ldw, const HeadGrad& H, int64_t T,
                               int64_t V, int64_t K, void* dX, sbn_dtype dxdt, int64_t lddx, void* dW, sbn_dtype dwdt,
@@ -1046,7 +1064,7 @@ hipError_t launch_ce_backward(const uint16_t* X, int64_t ldx, const uint16_t* W,
   // a second product, added to the first one's, or one of both numbers
   const bool dx_pair = dX && dxdt == SBN_F32_FINE, dw_pair = dW && dwdt == SBN_F32_FINE, few = H.policy && T <= PAIR_TOKENS,
              pair = dx_pair || dw_pair || few;
-  const CePlan L = ce_plan(T, V, K, pair);
+  const CePlan L = H.policy ? policy_plan(T, V, K, dx_pair, dw_pair) : ce_plan(T, V, K, pair);
   uint8_t* w = (uint8_t*)ws;
   uint16_t* D = (uint16_t*)(w + L.d);
   float *acc = (float*)(w + L.acc), *part = (float*)(w + L.part), *gmax = (float*)(w + L.gmax);

@@ -77,8 +77,11 @@ sbn_status sbn_token_logprobs_backward_workspace_bytes(int64_t T, int64_t V, int
   const char* fn = "sbn_token_logprobs_backward_workspace_bytes";
   SBN_NONNULL(bytes);
   SBN_TRY(check_ce_shape(fn, T, V, K));
-  const size_t one = T > 0 ? ce_bwd_ws_bytes(T, V, K, false) : 0, two = T > 0 ? ce_bwd_ws_bytes(T, V, K, true) : 0;
-  *bytes = one > two ? one : two;
+  *bytes = 0;
+  for (int fine = 0; fine < (T > 0 ? 4 : 0); ++fine) {
+    const size_t b = policy_bwd_ws_bytes(T, V, K, fine & 1, fine & 2);
+    if (b > *bytes) *bytes = b;
+  }
   return ok();
 }
 
@@ -109,8 +112,7 @@ sbn_status sbn_token_logprobs_backward(const uint16_t* X, int64_t ldx, const uin
   SBN_ELEM_ALIGNED(dlogp, 4);
   SBN_ELEM_ALIGNED(dentropy, 4);
   SBN_ALIGNED(ws);
-  const bool pair = policy_pair(T) || (dX && dxdt == SBN_F32_FINE) || (dW && dwdt == SBN_F32_FINE);
-  const size_t need = ce_bwd_ws_bytes(T, V, K, pair);
+  const size_t need = policy_bwd_ws_bytes(T, V, K, dX && dxdt == SBN_F32_FINE, dW && dwdt == SBN_F32_FINE);
   if (ws_bytes < need) return fail(SBN_ERR_WORKSPACE, "%s: workspace %zu bytes, need %zu", fn, ws_bytes, need);
   if (!dX && !dW) return ok();
   if (dW) SBN_NOT_IN_PLACE(dX, X);                   // which dW's product reads after dX's last
