@@ -53,12 +53,6 @@ class Kept8(NamedTuple):
     scales: object
 
 
-def _new_kept(T: int, K: int, device) -> Kept8:
-    torch = _torch()
-    return Kept8(torch.empty((T, K), dtype=torch.int8, device=device),
-                 torch.empty((T, -(-K // SBN_KEEP_BLOCK)), dtype=torch.float32, device=device))
-
-
 def _kept(kept, name: str, shape, device, fn: str):
     """`kept` is a checkpoint of a matrix of `shape` (None: of any) on `device`."""
     torch = _torch()
@@ -78,6 +72,16 @@ def _kept(kept, name: str, shape, device, fn: str):
     if not (codes.is_contiguous() and scales.is_contiguous()):
         raise SbnError(fn, 2, f"{name} must be contiguous")
     return codes, scales
+
+
+def _kept_out(kept, name: str, like, fn: str):
+    """A checkpoint of `like` to write: `kept`, checked, or a new one."""
+    if kept is not None:
+        return _kept(kept, name, like.shape, like.device, fn)
+    T, K = like.shape
+    torch = _torch()
+    return (like.new_empty((T, K), dtype=torch.int8),
+            like.new_empty((T, -(-K // SBN_KEEP_BLOCK)), dtype=torch.float32))
 
 
 def _codes_out(Xq, s_x, like, fn):
@@ -105,9 +109,7 @@ def sbn_keep8_encode(X, *, kept=None, stream=None):
     _matrix(X, "X", fn)
     dt = _dtype(X, "X", fn)
     T, K = X.shape
-    if kept is None:
-        kept = _new_kept(T, K, X.device)
-    codes, scales = _kept(kept, "kept", X.shape, X.device, fn)
+    codes, scales = _kept_out(kept, "kept", X, fn)
     _check(fn, _so().sbn_keep8_encode(X.data_ptr(), _ld(X) if T else K, dt, T, K, codes.data_ptr(), scales.data_ptr(),
                                       _raw_stream(X.device)))
     return Kept8(codes, scales)
@@ -158,9 +160,7 @@ def sbn_rmsnorm_quant_keep(X, gain, *, residual=None, eps: float = 1e-6, H=None,
     elif H is not None:
         raise SbnError(fn, 2, "H is written only with a residual (without one, h is X)")
     Xq, s_x = _codes_out(Xq, s_x, X, fn)
-    if kept is None:
-        kept = _new_kept(T, K, X.device)
-    codes, scales = _kept(kept, "kept", X.shape, X.device, fn)
+    codes, scales = _kept_out(kept, "kept", X, fn)
     if T:
         _check(fn, _so().sbn_rmsnorm_quant_keep(
             X.data_ptr(), _ld(X), _addr(residual), 0 if residual is None else _ld(residual), dt, gain.data_ptr(), gdt, T,
@@ -237,9 +237,9 @@ def sbn_activation_quant(A, B=None, *, act: int, gain=None, eps: float = 1e-6, k
     none = (None, None)
     ka = kb = none
     if keep:
-        ka = _kept(kept_A if kept_A is not None else _new_kept(T, K, A.device), "kept_A", A.shape, A.device, fn)
+        ka = _kept_out(kept_A, "kept_A", A, fn)
         if B is not None:
-            kb = _kept(kept_B if kept_B is not None else _new_kept(T, K, A.device), "kept_B", A.shape, A.device, fn)
+            kb = _kept_out(kept_B, "kept_B", A, fn)
     if (kept_A is not None and ka is none) or (kept_B is not None and kb is none):
         raise SbnError(fn, 2, "a checkpoint to write that the call does not keep")
     if T:
