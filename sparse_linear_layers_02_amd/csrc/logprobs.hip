@@ -106,38 +106,70 @@ __global__ __launch_bounds__(1024) void logprob_join_kernel(RowArgs P, int first
 }
 
 // ---------------------------------------------------------------- top alternatives
-// sum_k x w in 64 bits and sum_k |x w|, of a wave; W's loads of 512 AHEAD entries at once
-template <int AHEAD>
-__device__ inline double exact_sum(const uint16_t* x, const uint16_t* w, int K, float& size) {
+template <int N>
+struct Int {
+  static constexpr int value = N;
+};
+template <int CTRL>
+__device__ inline double row_moved(double x) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, x);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_mov_dpp((int)(uint32_t)b, CTRL, 0xf, 0xf, true);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_mov_dpp((int)(uint32_t)(b >> 32), CTRL, 0xf, 0xf, true);
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+// the sum of a wave's, as wave_all
+__device__ inline double wave_sum(double x) {
+  x += row_moved<0xB1>(x);
+  x += row_moved<0x4E>(x);
+  x += row_moved<0x141>(x);
+  x += row_moved<0x140>(x);
+  auto halves = [](auto lo, auto hi) {
+    return __builtin_bit_cast(double, (uint64_t)hi[0] << 32 | lo[0]) + __builtin_bit_cast(double, (uint64_t)hi[1] << 32 | lo[1]);
+  };
+  uint64_t b = __builtin_bit_cast(uint64_t, x);
+  x = halves(__builtin_amdgcn_permlane16_swap((uint32_t)b, (uint32_t)b, false, false),
+             __builtin_amdgcn_permlane16_swap((uint32_t)(b >> 32), (uint32_t)(b >> 32), false, false));
+  b = __builtin_bit_cast(uint64_t, x);
+  return halves(__builtin_amdgcn_permlane32_swap((uint32_t)b, (uint32_t)b, false, false),
+                __builtin_amdgcn_permlane32_swap((uint32_t)(b >> 32), (uint32_t)(b >> 32), false, false));
+}
+
+// sum_k x w in 64 bits and sum_k |x w| of ROWS rows w, of a wave; loads of 512 AHEAD entries of each at once
+template <int AHEAD, int ROWS>
+__device__ inline void exact_sums(const uint16_t* x, const uint16_t* const (&w)[ROWS], int K, double (&sum)[ROWS],
+                                  float (&size)[ROWS]) {
   const int lane = threadIdx.x & 63, n = K / 8;
-  double s0 = 0.0, s1 = 0.0;
-  float a = 0.0f;
+  double s0[ROWS], s1[ROWS];
+  float a[ROWS];
+#pragma unroll
+  for (int r = 0; r < ROWS; ++r) s0[r] = s1[r] = 0.0, a[r] = 0.0f;
 #pragma unroll 1
   for (int c0 = lane; c0 < n; c0 += 64 * AHEAD) {
-    v4i wv[AHEAD];
+    v4i wv[ROWS][AHEAD];
 #pragma unroll
-    for (int k = 0; k < AHEAD; ++k) {
-      wv[k] = (v4i){0, 0, 0, 0};
-      if (c0 + 64 * k < n) wv[k] = ((const v4i*)w)[c0 + 64 * k];
-    }
+    for (int k = 0; k < AHEAD; ++k)
+#pragma unroll
+      for (int r = 0; r < ROWS; ++r) {
+        wv[r][k] = (v4i){0, 0, 0, 0};
+        if (c0 + 64 * k < n) wv[r][k] = ((const v4i*)w[r])[c0 + 64 * k];
+      }
 #pragma unroll
     for (int k = 0; k < AHEAD; ++k) {
       const v4i xv = ((const v4i*)x)[c0 + 64 * k < n ? c0 + 64 * k : c0];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {                  // products of bf16 are exact in float32
-        const float lo = __uint_as_float((uint32_t)xv[j] << 16) * __uint_as_float((uint32_t)wv[k][j] << 16);
-        const float hi = __uint_as_float(xv[j] & 0xFFFF0000u) * __uint_as_float(wv[k][j] & 0xFFFF0000u);
-        s0 += (double)lo;
-        s1 += (double)hi;
-        a += fabsf(lo) + fabsf(hi);
-      }
+      for (int r = 0; r < ROWS; ++r)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {                // products of bf16 are exact in float32
+          const float lo = __uint_as_float((uint32_t)xv[j] << 16) * __uint_as_float((uint32_t)wv[r][k][j] << 16);
+          const float hi = __uint_as_float(xv[j] & 0xFFFF0000u) * __uint_as_float(wv[r][k][j] & 0xFFFF0000u);
+          s0[r] += (double)lo;
+          s1[r] += (double)hi;
+          a[r] += fabsf(lo) + fabsf(hi);
+        }
     }
   }
-  double s = s0 + s1;
 #pragma unroll
-  for (int d = 32; d >= 1; d >>= 1) s += __shfl_xor(s, d);
-  size = wave_all(a, Add{});
-  return s;
+  for (int r = 0; r < ROWS; ++r) sum[r] = wave_sum(s0[r] + s1[r]), size[r] = wave_all(a[r], Add{});
 }
 
 // A float that at least k of 256 reach (-Inf if fewer than k are above it), within 2^-11 of
@@ -168,9 +200,12 @@ __device__ inline float reached_by(const float* slot, int k) {
 // places in a queue, whose order does not matter: candidates are ordered by (sum,
 // index) in the end.  The code is kept short, without unrolling: one token's block
 // fetches each line of it for the first time.
-// Many tokens: 5 loads ahead in 84 registers (4 of them spilled, outside the sums), 6
-// blocks a unit (4096 tokens of 65536 entries, K = 2560, 8 alternatives: 101 us; 5 blocks
-// without spills 102; 4 ahead 120; 6 ahead, 4 or 5 blocks 107; 3, 8 blocks: 113).
+// Many tokens: a wave sums two rows at once, 2 loads of each ahead, 6 blocks a unit (4096
+// tokens of 65536 entries, K = 2560, 8 alternatives 101 us; 600 of 50000, 4096, 8 46; 2051
+// of 26574, 3776, 20 97; one row, 5 ahead 101, 57, 110; 7 and 8 blocks 111, 48, 106 and 115,
+// 50, 110).  Few: one row, 8 ahead, or, where waves have more than one and 4 ahead are a
+// whole row, two (10 tokens of 2062 entries, K = 256, 32 alternatives 27 -> 21 us; with two
+// for K = 4096, 20 of 32001, 37 tokens 25 -> 27).
 template <int NT, bool JOIN>
 __global__ __launch_bounds__(NT, NT == 256 ? 6 : 4) void logprob_top_kernel(RowArgs P) {
   constexpr int WAVES = NT / 64, SLOTS = 256, QUEUE = 1024, BATCH = 256, MOST = SBN_LOGPROBS_MAX_TOP;
@@ -285,28 +320,45 @@ __global__ __launch_bounds__(NT, NT == 256 ? 6 : 4) void logprob_top_kernel(RowA
 #pragma unroll 1
         for (int e = 0; e < entries; e += BATCH) {   // a batch of entries into the best so far
           const int count = entries - e < BATCH ? entries - e : BATCH;
+          // the sums of rows `i0` on, every WAVES-th, of ROWS of them at a time
+          auto sums = [&](auto rows, auto ahead) {
+            constexpr int ROWS = decltype(rows)::value, AHEAD = decltype(ahead)::value;
 #pragma unroll 1
-          for (int i = wave; i < count; i += WAVES) {
-            const int at = e + i - (int)ns;
-            int v;
-            if (at < 0) {
-              v = single[e + i];
-            } else {                                 // of a set whose first alone came before, without it
-              const int g = whole[at >> sets.of_log2], p = sets.place(g, at & ((1 << sets.of_log2) - 1));
-              const float f = row[g].x;
-              v = f >= over && p == (int)(__float_as_uint(f) & (TOPS_MOST - 1)) ? -1 : sets.entry(g, p);
+            for (int i0 = wave; i0 < count; i0 += WAVES * ROWS) {
+              const uint16_t* w[ROWS];
+              int v[ROWS];
+#pragma unroll
+              for (int r = 0; r < ROWS; ++r) {
+                const int i = i0 + r * WAVES, at = e + i - (int)ns;
+                int entry = -1;                      // none
+                if (i < count && at < 0) {
+                  entry = single[e + i];
+                } else if (i < count) {              // of a set whose first alone came before, without it
+                  const int g = whole[at >> sets.of_log2], p = sets.place(g, at & ((1 << sets.of_log2) - 1));
+                  const float f = row[g].x;
+                  if (!(f >= over && p == (int)(__float_as_uint(f) & (TOPS_MOST - 1)))) entry = sets.entry(g, p);
+                }
+                entry = __builtin_amdgcn_readfirstlane(entry);
+                v[r] = (uint32_t)entry < (uint32_t)P.V ? entry : -1;   // and not past the vocabulary
+                w[r] = P.W + (int64_t)(v[r] >= 0 ? v[r] : 0) * P.ldw;
+              }
+              double sum[ROWS];
+              float size[ROWS];
+              exact_sums<AHEAD, ROWS>(x, w, P.K, sum, size);
+#pragma unroll
+              for (int r = 0; r < ROWS; ++r) {
+                const int i = have + i0 + r * WAVES;
+                if (lane == 0 && i < have + count) {
+                  value[i] = v[r] >= 0 && sum[r] == sum[r] ? sum[r] : -INFINITY;   // NaN (outside the contract): an order all the same
+                  index[i] = v[r] >= 0 ? v[r] : 0x7FFFFFFF;
+                  if (v[r] >= 0) atomicMax(&largest, __float_as_uint(size[r]));
+                }
+              }
             }
-            v = __builtin_amdgcn_readfirstlane(v);
-            const bool real = (uint32_t)v < (uint32_t)P.V;   // and not past the vocabulary
-            float size = 0.0f;
-            double sum = -INFINITY;
-            if (real) sum = exact_sum<JOIN ? 8 : 5>(x, P.W + (int64_t)v * P.ldw, P.K, size);
-            if (!(sum == sum)) sum = -INFINITY;      // NaN (outside the contract): an order all the same
-            if (lane == 0) {
-              value[have + i] = sum, index[have + i] = real ? v : 0x7FFFFFFF;
-              atomicMax(&largest, __float_as_uint(size));
-            }
-          }
+          };
+          if (!JOIN) sums(Int<2>{}, Int<2>{});
+          else if (count > WAVES && P.K <= 4 * 512) sums(Int<2>{}, Int<4>{});
+          else sums(Int<1>{}, Int<8>{});
           __syncthreads();
           constexpr int EACH = (MOST + BATCH + NT - 1) / NT;
           double sum[EACH];
