@@ -14,8 +14,8 @@
 //
 // Bound by dependent reads: of one token (50001 entries, K = 2560, 8 alternatives) 14 us,
 // 2.5 of them the join, 2 the bound, 2 the scan, 4 the sums of K, 1 their order; of 37
-// tokens (32001, 4096, 20 alternatives) 24.  Of 4096 tokens (65536, 2560, 8) 92 to 104 us
-// for 67 MB of sets and 330 MB of rows of W, and 9 the join.
+// tokens (32001, 4096, 20 alternatives) 24.  Of 4096 tokens (65536, 2560, 8) 91 to 98 us
+// for 67 MB of sets and 300 MB of rows of W, and 9 the join.
 #include "score_internal.h"
 
 namespace sbn {
@@ -200,14 +200,15 @@ __device__ inline float reached_by(const float* slot, int k) {
 // places in a queue, whose order does not matter: candidates are ordered by (sum,
 // index) in the end.  The code is kept short, without unrolling: one token's block
 // fetches each line of it for the first time.
-// Many tokens: a wave sums two rows at once, 2 loads of each ahead, 6 blocks a unit (4096
-// tokens of 65536 entries, K = 2560, 8 alternatives 101 us; 600 of 50000, 4096, 8 46; 2051
-// of 26574, 3776, 20 97; one row, 5 ahead 101, 57, 110; 7 and 8 blocks 111, 48, 106 and 115,
-// 50, 110).  Few: one row, 8 ahead, or, where waves have more than one and 4 ahead are a
-// whole row, two (10 tokens of 2062 entries, K = 256, 32 alternatives 27 -> 21 us; with two
-// for K = 4096, 20 of 32001, 37 tokens 25 -> 27).
+// Many tokens: a wave sums three rows at once, 2 loads of each ahead, 5 blocks a unit:
+// 4096 tokens of 65536 entries, K = 2560, 8 alternatives 91 us; 600 of 50000, 4096, 8 41;
+// 2051 of 26574, 3776, 20 88; 2641 of 1158, 1024, 5 27 (two rows 99, 44, 89, 24; four 104,
+// 41, 100, 30; two with 3 ahead 99, 46, 92, 26; one row, 5 ahead, 6 blocks 101, 57, 110, 31;
+// two rows, 7 blocks 111, 48, 106, 27).  Few: one row, 8 ahead, or, where waves have more
+// than one and 4 ahead are a whole row, two (10 tokens of 2062 entries, K = 256, 32
+// alternatives 27 -> 21 us; with two for K = 4096, 20 of 32001, 37 tokens 25 -> 27).
 template <int NT, bool JOIN>
-__global__ __launch_bounds__(NT, NT == 256 ? 6 : 4) void logprob_top_kernel(RowArgs P) {
+__global__ __launch_bounds__(NT, NT == 256 ? 5 : 4) void logprob_top_kernel(RowArgs P) {
   constexpr int WAVES = NT / 64, SLOTS = 256, QUEUE = 1024, BATCH = 256, MOST = SBN_LOGPROBS_MAX_TOP;
   constexpr int HELD = 4;
   static_assert(NT % SLOTS == 0 && NT <= QUEUE, "threads");
@@ -356,7 +357,7 @@ __global__ __launch_bounds__(NT, NT == 256 ? 6 : 4) void logprob_top_kernel(RowA
               }
             }
           };
-          if (!JOIN) sums(Int<2>{}, Int<2>{});
+          if (!JOIN) sums(Int<3>{}, Int<2>{});
           else if (count > WAVES && P.K <= 4 * 512) sums(Int<2>{}, Int<4>{});
           else sums(Int<1>{}, Int<8>{});
           __syncthreads();
