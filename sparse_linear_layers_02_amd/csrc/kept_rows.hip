@@ -109,6 +109,7 @@ enum RowOp { ROW_NORM, ROW_RELU2, ROW_SILU };        // ROW_NORM: u = x
 // rounding left and the constant's: within 3 units of 2^-24; where it is Inf, 0
 __device__ inline float sigmoid(float a) {
   constexpr float L = -1.44269502f, LOW = -1.925963033e-8f;
+  a = fminf(a, 256.0f);                              // of more the product overflows, and 0 Inf is no exponential
   const float z = a * L, low = fmaf(a, LOW, fmaf(a, L, -z));
   const float e = __builtin_amdgcn_exp2f(z) * fmaf(low, 0.6931471806f, 1.0f);
   return __builtin_amdgcn_rcpf(1.0f + e);

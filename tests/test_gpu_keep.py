@@ -239,6 +239,26 @@ def test_activation(T, K, f32, act, gated, norm):
 
 
 @pytest.mark.parametrize("f32", [False, True])
+def test_sigmoid_of_extremes(f32):
+    """Rows of one value each, up to the largest, where u stays finite.  A sigmoid g below 2^-126
+    has no full mantissa (or is 0), an error of at most 2^-126: of f = a g |a| 2^-126, of f' = g (1 + a (1 - g)),
+    with 0 <= 1 - g <= 1, (1 + |a|) 2^-126.  From a = -128 on g < 2^-184, so both are 0 in float32."""
+    vals = np.array([0.0, 1e-30, -1e-30, 1.0, -1.0, 17.0, -17.0, 60.0, -60.0, 88.5, -88.5, 89.0, -89.0, 127.0, -127.0, 200.5, -200.5, 1e4,
+                     -1e4, 1e30, -1e30, 2.3e38, -2.3e38, 3e38, -3e38], dtype=np.float32)
+    a, av = put(np.repeat(vals[:, None], 40, 1), f32)
+    Xq, s_x, ka, _ = sbn.sbn_activation_quant(a, act=sbn.SBN_SILU)
+    u = act64(av.astype(np.float64), sbn.SBN_SILU)[0]
+    m = np.maximum(np.abs(u).max(1), float(TINY))
+    tiny = 2.0 ** -126 * (1 + np.minimum(np.abs(av.astype(np.float64)), 128))
+    close(host(s_x), m / 127, 60 * U * m / 127 + tiny[:, 0] / 127 + 2.0 ** -149, "s_x")
+    assert (np.abs(host(Xq) * host(s_x)[:, None].astype(np.float64) - u) <= (m * (0.5 / 127 + 60 * U))[:, None] + tiny).all()
+    f, slope, bs = act64(host(sbn.sbn_keep8_decode(ka)).astype(np.float64), sbn.SBN_SILU)
+    dy, dyv = put(np.full(av.shape, 0.5, dtype=np.float32), f32)
+    dA, _, _ = sbn.sbn_activation_backward(dy, ka, act=sbn.SBN_SILU)
+    close(get(dA, f32), 0.5 * slope, U * 0.5 * bs + 20 * U * np.abs(slope) + (0 if f32 else B) * np.abs(slope) + tiny, "dA")
+
+
+@pytest.mark.parametrize("f32", [False, True])
 def test_halves_of_one_matrix_in_place(f32):
     """A and B as halves of one product's output, dA in dY's place, outputs given, columns beside them untouched."""
     import torch
