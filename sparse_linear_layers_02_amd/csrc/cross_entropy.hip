@@ -847,16 +847,16 @@ int grid_for(int64_t items) {
 
 // ---------------------------------------------------------------- tile shapes
 // wide: 256 x 256, one block per compute unit; square: 128 x 128; flat: 128 A
-// rows x 64 B rows, for few tokens or few tiles.
-enum Tile { WIDE, SQUARE, FLAT };
+// rows x 64 B rows, for few tokens or few tiles; slim: 64 x 64.
+enum Tile { WIDE, SQUARE, FLAT, SLIM };
 struct TileShape {
   int a, b;
 };
-constexpr TileShape SHAPE[] = {{256, 256}, {128, 128}, {128, 64}};
+constexpr TileShape SHAPE[] = {{256, 256}, {128, 128}, {128, 64}, {64, 64}};
 
 // a product's launches, named by what they compute and their tile shape
-using Names = const char* const[3];
-#define SBN_TILE_NAMES(what) {what "_wide", what "_square", what "_flat"}
+using Names = const char* const[4];
+#define SBN_TILE_NAMES(what) {what "_wide", what "_square", what "_flat", what "_slim"}
 constexpr Names LOGITS = SBN_TILE_NAMES("ce_logits"), DLOGITS = SBN_TILE_NAMES("ce_dlogits"),
                 DX = SBN_TILE_NAMES("ce_dx"), DW = SBN_TILE_NAMES("ce_dw"), SCORES = SBN_TILE_NAMES("logprob_logits"),
                 DPOLICY = SBN_TILE_NAMES("logprob_dlogits");
@@ -890,6 +890,9 @@ hipError_t gemm(Names& names, Tile tile, GemmArgs& P, hipStream_t st) {
   switch (tile) {
     case WIDE: return run_gemm<2, 4, 8, 4, 5, EPI, TRA, TRB>(name, P, st);
     case SQUARE: return run_gemm<2, 2, 4, 4, 5, EPI, TRA, TRB>(name, P, st);
+    case SLIM:
+      if constexpr (EPI == EPI_SCORE || EPI == EPI_SCORE_TOPS || EPI == EPI_SCORE_TOPS8 || EPI == EPI_POLICY || EPI == EPI_POLICY_PAIR)
+        return run_gemm<2, 2, 2, 2, 5, EPI, TRA, TRB>(name, P, st);
     default: return run_gemm<4, 1, 2, 4, 5, EPI, TRA, TRB>(name, P, st);
   }
 }
@@ -990,9 +993,17 @@ hipError_t product(Names& names, Tile tile, GemmArgs P, bool c_f32, float* part,
 }
 
 Tile stats_tile(int64_t T, int64_t V, int64_t K) { return pick(V, T, K / BK, false).tile; }
-int64_t stats_groups(int64_t T, int64_t V, int64_t K) {
+int64_t groups_of(Tile t, int64_t V) { return cdiv(V, SHAPE[t].a) * (t == FLAT ? 4 : 2); }
+int64_t stats_groups(int64_t T, int64_t V, int64_t K) { return groups_of(stats_tile(T, V, K), V); }
+
+// Of log probabilities' logits and their D: where flat tiles are at most one a unit, twice as
+// many of half the entries (us: 37 tokens of 32001 entries, K = 4096, 59.6 -> 57.5, D of K =
+// 2560 32.5 -> 29.3; 17 of 3953, 1792 15.6 -> 13.3 and 17.8 -> 13.0; 126 of 1315, 3456 25.7 -> 22.7
+// and 27.2 -> 18.8; where there are more than units, 1 of 50001, 2560 49.9 -> 52.3).  The loss
+// keeps its tiles, and so its sums' order.
+Tile score_tile(int64_t T, int64_t V, int64_t K) {
   const Tile t = stats_tile(T, V, K);
-  return cdiv(V, SHAPE[t].a) * (t == FLAT ? 4 : 2);
+  return t == FLAT && tiles_of(FLAT, V, T) <= CUS ? SLIM : t;
 }
 
 }  // namespace
@@ -1023,10 +1034,10 @@ hipError_t launch_ce(const uint16_t* X, int64_t ldx, const uint16_t* W, int64_t 
 
 // Of a token's tops: the fragments of 16 entries that a wave holds, and the sets.
 LogitTops logit_tops(int64_t T, int64_t V, int64_t K, int top) {
-  const Tile t = stats_tile(T, V, K);
+  const Tile t = score_tile(T, V, K);
   const int mi_log2 = t == WIDE ? 3 : t == SQUARE ? 2 : 1;
   const int of_log2 = V < int64_t(4096) * top ? 3 : tops_of(1 << mi_log2) == 32 ? 5 : 4;
-  return {mi_log2, of_log2, (int)((stats_groups(T, V, K) << (4 + mi_log2)) >> of_log2)};
+  return {mi_log2, of_log2, (int)((groups_of(t, V) << (4 + mi_log2)) >> of_log2)};
 }
 
 hipError_t launch_logits(const uint16_t* X, int64_t ldx, const uint16_t* W, int64_t ldw, const void* tokens, bool tokens64,
@@ -1040,11 +1051,11 @@ hipError_t launch_logits(const uint16_t* X, int64_t ldx, const uint16_t* W, int6
   P.target = target, P.stats = stats, P.mean = mean, P.tops = tops;
   P.ldt = sets.groups;
   P.scale = scale, P.none = -1e30f / (scale * LOG2E);
-  const Tile t = stats_tile(T, V, K);
+  const Tile t = score_tile(T, V, K);
   if (!tops) return gemm<EPI_SCORE>(SCORES, t, P, st);
   return sets.of_log2 == 3 ? gemm<EPI_SCORE_TOPS8>(SCORES, t, P, st) : gemm<EPI_SCORE_TOPS>(SCORES, t, P, st);
 }
-int64_t logit_groups(int64_t T, int64_t V, int64_t K) { return stats_groups(T, V, K); }
+int64_t logit_groups(int64_t T, int64_t V, int64_t K) { return groups_of(score_tile(T, V, K), V); }
 
 size_t ce_bwd_ws_bytes(int64_t T, int64_t V, int64_t K, bool pair) { return ce_plan(T, V, K, pair).total; }
 namespace {
@@ -1091,7 +1102,7 @@ hipError_t launch_ce_backward(const uint16_t* X, int64_t ldx, const uint16_t* W,
     G.lse = H.lse, G.dloss = H.dloss, G.gmax = gmax;
     G.scale = H.scale, G.entropy = H.entropy, G.dentropy = H.dentropy;
     G.D = D, G.ldd = L.piece, G.dlow = dlow, G.tpad = (int)L.tpad;
-    const Tile tile = pick(nv, T, G.steps, false).tile;
+    const Tile tile = H.policy ? score_tile(T, nv, K) : stats_tile(T, nv, K);
     if (H.policy) e = pair ? gemm<EPI_POLICY_PAIR>(DPOLICY, tile, G, st) : gemm<EPI_POLICY>(DPOLICY, tile, G, st);
     else e = pair ? gemm<EPI_GRAD_PAIR>(DLOGITS, tile, G, st) : gemm<EPI_GRAD>(DLOGITS, tile, G, st);
     if (e != hipSuccess) return e;

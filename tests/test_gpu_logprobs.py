@@ -289,7 +289,8 @@ def rows(T, top):
 
 # tokens, entries, K: the tiles of the logits and of D
 @pytest.mark.parametrize("shape,tile", [((8100, 7000, 4096), "wide"), ((1285, 3664, 3136), "square"), ((65, 17007, 2112), "square"),
-                                        ((16, 1796, 2112), "flat"), ((5000, 300, 320), "flat")])
+                                        ((16, 1796, 2112), "slim"), ((40, 32700, 320), "slim"), ((5000, 300, 320), "slim"),
+                                        ((16, 33000, 2112), "flat"), ((5500, 300, 320), "flat")])
 def test_tiles(shape, tile):
     T, V, K = shape
     X, W, y, dl, dh = problem(T, V, K, T + V + K)
