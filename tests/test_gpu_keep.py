@@ -259,10 +259,10 @@ def test_sigmoid_of_extremes(f32):
 
 
 @pytest.mark.parametrize("f32", [False, True])
-def test_halves_of_one_matrix_in_place(f32):
+@pytest.mark.parametrize("T,K", [(37, 520), (1100, 520), (300, 9000), (300, 14344), (37, 16400)])
+def test_halves_of_one_matrix_in_place(T, K, f32):
     """A and B as halves of one product's output, dA in dY's place, outputs given, columns beside them untouched."""
     import torch
-    T, K = 37, 520
     both, _ = put(np.concatenate([rows(1, T, K), rnd(2, T, K)], 1), f32)
     A, Bm = both[:, :K], both[:, K:]
     g = dev(1 + 0.2 * rnd(3, K))

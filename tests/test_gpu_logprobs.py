@@ -197,6 +197,20 @@ def test_strides_and_given_outputs(T, V, K):
     assert (bx[:, K:] == 3.0).all() and (bw[:, K:] == 5.0).all(), "columns past the rows"
 
 
+@pytest.mark.parametrize("T,V,K", [(70, 300, 64), (300, 2500, 256), (65400, 9500, 64)])
+def test_gradients_in_place_of_inputs(T, V, K):
+    import torch
+    X, W, y, dl, dh = problem(T, V, K, 19, ldx=K + 8, ldw=K + 16)
+    _, H, lse, _, _ = sbn.sbn_token_logprobs(X, W, y)
+    dX, dW = sbn.sbn_token_logprobs_backward(X, W, y, lse, H, dl, dh)
+    W2 = torch.empty((V, K + 16), dtype=torch.bfloat16, device="cuda")[:, :K]
+    W2.copy_(W)
+    a, b = sbn.sbn_token_logprobs_backward(X, W2, y, lse, H, dl, dh, dW=W2)
+    assert b is W2 and torch.equal(a, dX) and torch.equal(W2, dW)
+    a, _ = sbn.sbn_token_logprobs_backward(X, W, y, lse, H, dl, dh, dX=X, need_dW=False)
+    assert a is X and torch.equal(X, dX)
+
+
 def test_tokens_out_of_range():
     import torch
     T, V, K = 70, 200, 64
