@@ -815,15 +815,15 @@ __global__ __launch_bounds__(256) void ce_sum_kernel(const float* __restrict__ p
   const int64_t n = rows * (cols / 4);
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
     v4f c = ((const v4f*)part)[i];
-    int p = 1;
-    for (; p + 8 <= splits; p += 8) {                // 8 loads in flight
+    for (int p = 1; p < splits; p += 8) {            // 8 loads in flight
       v4f x[8];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) x[k] = ((const v4f*)part)[(p + k) * n + i];
+      for (int k = 0; k < 8; ++k)
+        if (p + k < splits) x[k] = ((const v4f*)part)[(p + k) * n + i];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) c += x[k];
+      for (int k = 0; k < 8; ++k)
+        if (p + k < splits) c += x[k];
     }
-    for (; p < splits; ++p) c += ((const v4f*)part)[p * n + i];
     const int64_t r = i / (cols / 4), a = (i - r * (cols / 4)) * 4;
     if (Cin) c += *(const v4f*)(Cin + r * ldcin + a);
     c *= scale;
