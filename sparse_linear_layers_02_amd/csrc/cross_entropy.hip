@@ -1036,7 +1036,8 @@ hipError_t launch_ce(const uint16_t* X, int64_t ldx, const uint16_t* W, int64_t 
 LogitTops logit_tops(int64_t T, int64_t V, int64_t K, int top) {
   const Tile t = score_tile(T, V, K);
   const int mi_log2 = t == WIDE ? 3 : t == SQUARE ? 2 : 1;
-  const int of_log2 = V < int64_t(4096) * top ? 3 : tops_of(1 << mi_log2) == 32 ? 5 : 4;
+  const int64_t near = top + 3, rows_spared = near * near * K * (T * V < int64_t(1) << 26 ? 2048 : 1024);
+  const int of_log2 = rows_spared > V * V ? 3 : tops_of(1 << mi_log2) == 32 ? 5 : 4;
   return {mi_log2, of_log2, (int)((groups_of(t, V) << (4 + mi_log2)) >> of_log2)};
 }
 

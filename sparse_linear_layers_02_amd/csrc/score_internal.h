@@ -14,11 +14,15 @@ namespace sbn {
 // sums (logits before their scale), the first's place in its last 5 bits.  A set is
 // what one lane holds of a column; of lanes that hold 8, two.  (Few tokens: sets of 8
 // are 64 KB to read for each at 65536 entries, and of 32 twice as often one with two
-// candidates, all of which are then computed.)  Below 4096 entries for each alternative
-// asked for, where two in a set are common, sets are of 8, parts of a lane's.  (Logits /
-// alternatives, us, with them and without: 20 of 32001 entries, 1024 tokens, K = 4096 218 +
-// 77, 203 + 126; 8 of 20000, 600 tokens, 2560 69 + 23, 69 + 45; 64 of 8000, 2000 tokens, 512
-// 27 + 147, 26 + 317; 20 of 32001, 37 tokens, 4096 61 + 27, 61 + 25.)
+// candidates, all of which are then computed.)  Where two in a set are common, sets are of
+// 8, parts of a lane's: of about c = top + 3 candidates 512 c^2 / V rows of W are computed for
+// their neighbours' sake, with sets of 8 a sixteenth of that, and V bytes a token are written
+// and read twice instead of V / 4, which costs least while the caches hold them.  (Logits +
+// alternatives, us, with sets of 8 and without: 20 of 32001 entries, 1024 tokens, K = 4096 222 +
+// 60, 204 + 96; the same, 8192 tokens 1573 + 330, 1566 + 367; 6 of 20000, 600, 2560 67 + 20, 66
+// + 31; 64 of 8000, 2000, 512 27 + 78, 25 + 320; 20 of 32001, 37, 4096 61 + 25, 61 + 28; and
+// where they are not taken 32 of 65536, 4096, 2560 1034 + 218, 974 + 211; 8 of 32001, 4096, 2560
+// 517 + 89, 495 + 77; 8 of 16000, 8192, 1024 242 + 81, 232 + 85.)
 constexpr int TOPS_MOST = 32;
 constexpr int tops_of(int mi) { return 4 * mi >= 16 ? 4 * mi : 16; }
 struct LogitTops {
