@@ -36,12 +36,14 @@ extern "C" {
  * -100, marks a row without one; its distribution is there all the same.
  *
  * The order of the alternatives is that of sums in 64 bits: float32 sums only
- * choose who is compared, with a margin of their worst error (K 2^-24 of
- * sum_k |X W| as found among the largest, both sides), so rows of W whose logits
- * agree to float32's precision are still told apart.
+ * choose who is compared, with a margin of their worst error (K 2^-23 |X[t]| |W[v]|, the
+ * norms' product being no less than sum_k |X W|, with the largest |W[v]| of a group of 32 to 128
+ * entries), so rows of W whose logits agree to float32's precision, and rows of any
+ * size whose large parts cancel, are still told apart.
  * Every logit within that margin of the last alternative is summed again: a row
  * whose logits are all equal takes as long as 64-bit sums of all of them (4096 rows
- * of 65536 equal logits, K = 2560: 0.2 s; rows of X that are zero, such as padding, none).
+ * of 65536 equal logits, K = 2560: 0.2 s; rows of X that are zero, such as padding, none),
+ * and a row of W far larger than the others costs the sums of its group.
  *
  *   X [T x K], W [V x K] bf16, row strides ldx, ldw     as sbn_cross_entropy
  *   tokens  [T] int64 (token_bytes = 8) or int32 (4); or NULL with logp NULL

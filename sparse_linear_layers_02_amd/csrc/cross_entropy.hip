@@ -84,6 +84,7 @@ struct GemmArgs {
   float* mean;                         // beside stats: sum of exponential times scaled exponent
   float2* tops;                        // [nB][ldt] the two largest sums of each set, the first's place in its last bits
   int64_t ldt;
+  float* norms;                        // beside tops: [groups][WB] no less than the largest |row of A| of a group's fragments i, i % WB alike
   const float *entropy, *dentropy;     // dloss: of the log probabilities; either gradient may be NULL
   uint16_t* D;                         // [tpad][ldd], ldd a multiple of 256; 0 past the tokens and past nA
   int64_t ldd;
@@ -456,6 +457,17 @@ __global__ __launch_bounds__(64 * WA * WB, 1) void ce_gemm_kernel(GemmArgs P) {
   };
   // taken in snake order: each product shares an operand with the one before (0.3% of a training step)
   auto multiply = [&](int i, int j, int sub) { mfma_acc(acc[i][j], i < MI - 1 ? fa[i] : fl[sub], fb[sub][j]); };
+  // TOPS: norms of A's rows, the same in all of a token's tiles and in the waves of one `wa`: the first tile's
+  // waves take MI / WB of the fragments each, and read them again.  (Taken from the fragments of the products,
+  // they cost 100 to 200 spilled registers.)
+  float squares[MI / WB] = {};
+  bool norms = false;
+  auto square = [&](int p0, int p1) {
+    const uint8_t* half = smem + (wa >= WA / 2 ? p1 : p0) * HALF;
+#pragma unroll
+    for (int k = 0; k < 2 * MI / WB; ++k)
+      squares[k / 2] = add_squares(fragment(HA{}, half, wa % (WA / 2) * MI + wb * (MI / WB) + k / 2, k % 2), squares[k / 2]);
+  };
   auto wrap = [](int p) { return p >= RING ? p - RING : p; };
 
   // Stages are numbered through all items of the block; half stage u (of stage
@@ -480,6 +492,7 @@ __global__ __launch_bounds__(64 * WA * WB, 1) void ce_gemm_kernel(GemmArgs P) {
   }
   const float ginv = gmax >= 0x1p-126f ? 1.0f / gmax : 0.0f;   // smaller ones have no quotient: gradients 0
   Item it = item(blockIdx.x, P);
+  if (TOPS) norms = it.b0 == 0;
   start_item(it, P);
 #pragma unroll
   for (int n = 0; n < AHEAD; ++n) {
@@ -499,6 +512,7 @@ __global__ __launch_bounds__(64 * WA * WB, 1) void ce_gemm_kernel(GemmArgs P) {
   for (int w = blockIdx.x;; w += (int)gridDim.x) {
     for (int left = it.nsteps; left > 0; --left) {
       const int p1 = wrap(p0 + 1), n0 = wrap(p0 + 2), n1 = wrap(p0 + 3), free0 = wrap(p0 + RING - 1);
+      if (TOPS && norms) square(p0, p1);
       lds_reads_done();                              // before new reads, which the first products need not wait for
 #pragma unroll
       for (int i = 0; i < MI; ++i) {
@@ -540,6 +554,16 @@ __global__ __launch_bounds__(64 * WA * WB, 1) void ce_gemm_kernel(GemmArgs P) {
       const float factor = SCORE ? P.scale * LOG2E : LOG2E;
       const bool ragged = aw + MI * 16 > P.nA;
       const int group = it.a0 / (MI * 16) + wa;
+      if constexpr (TOPS) {
+        if (norms) {
+          float most = 0.0f;
+#pragma unroll
+          for (int i = 0; i < MI / WB; ++i) most = fmaxf(most, rows_all(squares[i], Add{})), squares[i] = 0.0f;
+          // a lane's K / 8 sums of two squares, up to three roundings each: under 2^-6 for K <= 2^18; and what was taken for 0
+          most = row16_all(most, Max{}) * (1.0f + 0x1p-6f) + (float)(P.steps * BK) * 0x1p-124f;
+          if (lane == 0) P.norms[group * WB + wb] = sqrtf(most);
+        }
+      }
       int wants[MJ];
 #pragma unroll
       for (int j = 0; j < MJ; ++j) {                 // all loads before the first store: they would wait for it
@@ -739,6 +763,7 @@ __global__ __launch_bounds__(64 * WA * WB, 1) void ce_gemm_kernel(GemmArgs P) {
     }
     if (w + (int)gridDim.x >= work) break;
     it = item(w + (int)gridDim.x, P);
+    if (TOPS) norms = it.b0 == 0;
     start_sums(it, P);
   }
   wait_vmcnt<0>();                                   // no load into LDS outlives the block
@@ -888,7 +913,7 @@ hipError_t gemm(Names& names, Tile tile, GemmArgs& P, hipStream_t st) {
   P.tilesB = (int)cdiv(P.nB, SHAPE[tile].b);
   const char* name = names[tile];
   switch (tile) {
-    case WIDE: return run_gemm<2, 4, 8, 4, 5, EPI, TRA, TRB>(name, P, st);
+    case WIDE: return run_gemm<2, 4, 8, 4, 5, EPI, TRA, TRB>(name, P, st);   // WB as in logit_norms()
     case SQUARE: return run_gemm<2, 2, 4, 4, 5, EPI, TRA, TRB>(name, P, st);
     case SLIM:
       if constexpr (EPI == EPI_SCORE || EPI == EPI_SCORE_TOPS || EPI == EPI_SCORE_TOPS8 || EPI == EPI_POLICY || EPI == EPI_POLICY_PAIR)
@@ -1043,18 +1068,22 @@ LogitTops logit_tops(int64_t T, int64_t V, int64_t K, int top) {
 
 hipError_t launch_logits(const uint16_t* X, int64_t ldx, const uint16_t* W, int64_t ldw, const void* tokens, bool tokens64,
                          int64_t T, int64_t V, int64_t K, float scale, float* target, float2* stats, float* mean,
-                         float2* tops, const LogitTops& sets, hipStream_t st) {
+                         float2* tops, float* norms, const LogitTops& sets, hipStream_t st) {
   GemmArgs P{};
   P.A = W, P.lda = ldw, P.nA = P.mA = (int)V;
   P.B = X, P.ldb = ldx, P.nB = P.mB = (int)T;
   P.steps = (int)(K / BK), P.splits = 1;
   P.labels = tokens, P.labels64 = tokens64, P.V = (int)V;
-  P.target = target, P.stats = stats, P.mean = mean, P.tops = tops;
+  P.target = target, P.stats = stats, P.mean = mean, P.tops = tops, P.norms = norms;
   P.ldt = sets.groups;
   P.scale = scale, P.none = -1e30f / (scale * LOG2E);
   const Tile t = score_tile(T, V, K);
   if (!tops) return gemm<EPI_SCORE>(SCORES, t, P, st);
   return sets.of_log2 == 3 ? gemm<EPI_SCORE_TOPS8>(SCORES, t, P, st) : gemm<EPI_SCORE_TOPS>(SCORES, t, P, st);
+}
+int logit_norms(int64_t T, int64_t V, int64_t K) {
+  const Tile t = score_tile(T, V, K);
+  return t == WIDE ? 4 : t == FLAT ? 1 : 2;
 }
 int64_t logit_groups(int64_t T, int64_t V, int64_t K) { return groups_of(score_tile(T, V, K), V); }
 

@@ -11,6 +11,11 @@
 // k-th largest of any partition's maxima is no larger than the k-th largest logit, so a
 // row's candidates are the firsts above such a bound, and, where a second is above it as
 // well, all of its set.  Candidates' sums are formed again, in 64 bits, and ordered by them.
+// A sum of K products in float32, in any order, is off by at most K 2^-24 sum |x w| <= K 2^-24
+// |x| |w| (twice that if the hardware cuts off instead of rounding), and the product leaves the largest |w|
+// of each of its groups of rows.  Sets that hold an entry which with that margin reaches the
+// last alternative, and which no one has summed, are candidates of a second round, and then
+// none is left.
 //
 // Bound by dependent reads: of one token (50001 entries, K = 2560, 8 alternatives) 14 us,
 // 2.5 of them the join, 2 the bound, 2 the scan, 4 the sums of K, 1 their order; of 37
@@ -50,6 +55,9 @@ struct RowArgs {
   int K, top;
   LogitTops sets;
   const float2* tops;
+  const float* norms;                  // `each` of a group
+  int each;
+  float* most;                         // the largest of norms; unused where a block joins its own token's statistics
   float scale;
   int64_t* ids;
   float* top_logp;
@@ -90,6 +98,19 @@ __device__ inline Stat join_groups(const RowArgs& P, int64_t t, int first, int s
 // triples are joined in a tree.
 __global__ __launch_bounds__(1024) void logprob_join_kernel(RowArgs P, int first) {
   __shared__ float sm[3][64][17];
+  if (P.top && first + blockIdx.x * 16 >= P.T) {     // one block past the tokens, beside the others
+    float m = 0.0f;
+#pragma unroll 4
+    for (int g = threadIdx.x; g < P.groups * P.each; g += 1024) m = fmaxf(m, P.norms[g]);
+    m = wave_all(m, Max{});
+    if ((threadIdx.x & 63) == 0) sm[0][0][threadIdx.x >> 6] = m;
+    __syncthreads();
+    if (threadIdx.x < 16) {
+      m = row16_all(sm[0][0][threadIdx.x], Max{});
+      if (threadIdx.x == 0) *P.most = m;
+    }
+    return;
+  }
   const int tl = threadIdx.x & 15, part = threadIdx.x >> 4;
   const int t = first + blockIdx.x * 16 + tl;
   Stat a{NONE, 0.0f, 0.0f};
@@ -134,15 +155,13 @@ __device__ inline double wave_sum(double x) {
                 __builtin_amdgcn_permlane32_swap((uint32_t)(b >> 32), (uint32_t)(b >> 32), false, false));
 }
 
-// sum_k x w in 64 bits and sum_k |x w| of ROWS rows w, of a wave; loads of 512 AHEAD entries of each at once
+// sum_k x w in 64 bits of ROWS rows w, of a wave; loads of 512 AHEAD entries of each at once
 template <int AHEAD, int ROWS>
-__device__ inline void exact_sums(const uint16_t* x, const uint16_t* const (&w)[ROWS], int K, double (&sum)[ROWS],
-                                  float (&size)[ROWS]) {
+__device__ inline void exact_sums(const uint16_t* x, const uint16_t* const (&w)[ROWS], int K, double (&sum)[ROWS]) {
   const int lane = threadIdx.x & 63, n = K / 8;
   double s0[ROWS], s1[ROWS];
-  float a[ROWS];
 #pragma unroll
-  for (int r = 0; r < ROWS; ++r) s0[r] = s1[r] = 0.0, a[r] = 0.0f;
+  for (int r = 0; r < ROWS; ++r) s0[r] = s1[r] = 0.0;
 #pragma unroll 1
   for (int c0 = lane; c0 < n; c0 += 64 * AHEAD) {
     v4i wv[ROWS][AHEAD];
@@ -164,12 +183,11 @@ __device__ inline void exact_sums(const uint16_t* x, const uint16_t* const (&w)[
           const float hi = __uint_as_float(xv[j] & 0xFFFF0000u) * __uint_as_float(wv[r][k][j] & 0xFFFF0000u);
           s0[r] += (double)lo;
           s1[r] += (double)hi;
-          a[r] += fabsf(lo) + fabsf(hi);
         }
     }
   }
 #pragma unroll
-  for (int r = 0; r < ROWS; ++r) sum[r] = wave_sum(s0[r] + s1[r]), size[r] = wave_all(a[r], Add{});
+  for (int r = 0; r < ROWS; ++r) sum[r] = wave_sum(s0[r] + s1[r]);
 }
 
 // A float that at least k of 256 reach (-Inf if fewer than k are above it), within 2^-11 of
@@ -204,7 +222,7 @@ __device__ inline float reached_by(const float* slot, int k) {
 // 4096 tokens of 65536 entries, K = 2560, 8 alternatives 91 us; 600 of 50000, 4096, 8 41;
 // 2051 of 26574, 3776, 20 88; 2641 of 1158, 1024, 5 27 (two rows 99, 44, 89, 24; four 104,
 // 41, 100, 30; two with 3 ahead 99, 46, 92, 26; one row, 5 ahead, 6 blocks 101, 57, 110, 31;
-// two rows, 7 blocks 111, 48, 106, 27).  Few: one row, 8 ahead, or, where waves have more
+// two rows, 7 blocks 111, 48, 106, 27; with the margin by norms 91, 40, 100, 26).  Few: one row, 8 ahead, or, where waves have more
 // than one and 4 ahead are a whole row, two (10 tokens of 2062 entries, K = 256, 32
 // alternatives 27 -> 21 us; with two for K = 4096, 20 of 32001, 37 tokens 25 -> 27).
 template <int NT, bool JOIN>
@@ -215,7 +233,8 @@ __global__ __launch_bounds__(NT, NT == 256 ? 5 : 4) void logprob_top_kernel(RowA
   __shared__ __attribute__((aligned(16))) float slot[NT];
   __shared__ float log_sum;
   __shared__ Stat stat[WAVES];
-  __shared__ uint32_t singles, wholes, largest;      // queued entries, queued sets, bits of the largest sum |x w|
+  __shared__ uint32_t singles, wholes;               // queued entries, queued sets
+  __shared__ float x_squares[WAVES], w_norm[WAVES];
   __shared__ int single[QUEUE], whole[QUEUE];
   __shared__ double value[MOST + BATCH];             // the best so far in order, then a batch
   __shared__ int index[MOST + BATCH];
@@ -229,7 +248,11 @@ __global__ __launch_bounds__(NT, NT == 256 ? 5 : 4) void logprob_top_kernel(RowA
     float firsts[HELD];                              // loaded before the statistics are waited for
 #pragma unroll
     for (int k = 0; k < HELD; ++k) firsts[k] = top && tid + k * NT < n ? row[tid + k * NT].x : -INFINITY;
+    float w_most = 0.0f;
     if (JOIN) {
+      if (top)
+#pragma unroll 2
+        for (int g = tid; g < P.groups * P.each; g += NT) w_most = fmaxf(w_most, P.norms[g]);
       Stat a = join_groups<2>(P, t, tid, NT);
       auto over_lanes = [&](int d) {
 #pragma unroll 1
@@ -251,18 +274,25 @@ __global__ __launch_bounds__(NT, NT == 256 ? 5 : 4) void logprob_top_kernel(RowA
       log_sum = P.lse[t];
     }
     // a bound that at least top + 2 firsts reach, if there are as many: the places past
-    // the top itself leave room for the margin below, which then rarely asks for more
+    // the top itself leave room for the margin below, which then asks for a second round less
+    // often (more than two: at best 1 us of 25 less, at worst 30 of 90 more)
     float m = firsts[0];
 #pragma unroll
     for (int k = 1; k < HELD; ++k) m = fmaxf(m, firsts[k]);
 #pragma unroll 4
     for (int g = tid + HELD * NT; g < n; g += NT) m = fmaxf(m, row[g].x);
     bool any = false;
+    float xx = 0.0f;
 #pragma unroll 1
     for (int c = tid; c < P.K / 8; c += NT) {
       const v4i v = ((const v4i*)x)[c];
       any |= ((v[0] | v[1] | v[2] | v[3]) & 0x7FFF7FFF) != 0;
+      xx = add_squares(__builtin_bit_cast(v8bf, v), xx);
     }
+    xx = wave_all(xx, Add{});
+    if (JOIN) w_most = wave_all(w_most, Max{});
+    else w_most = *P.most;
+    if (lane == 0) x_squares[wave] = xx, w_norm[wave] = w_most;
     slot[tid] = m;
     if (!__syncthreads_or(any)) {                    // a row of zeros (padding): all logits are equal, the first ones win
       for (int i = tid; i < top; i += NT) P.ids[(int64_t)t * top + i] = i, P.top_logp[(int64_t)t * top + i] = -log_sum;
@@ -277,11 +307,12 @@ __global__ __launch_bounds__(NT, NT == 256 ? 5 : 4) void logprob_top_kernel(RowA
       if (tid < SLOTS) slot[tid] = m;
       __syncthreads();
     }
-    // candidates are those from bound to over
-    float bound = reached_by(slot, top + 2), over = INFINITY;
+    const float bound = reached_by(slot, top + 2);
+    float reach = 0.0f, least = 0.0f;                // second round: a margin's share of x, and the last alternative
     int have = 0;
-    if (tid == 0) largest = 0;
-    for (int round = 0; round < 16; ++round) {       // hardly ever a third
+#pragma unroll 1
+    for (int round = 0; round < 2; ++round) {
+      const float over = round ? bound : INFINITY;   // from here on entries alone, or with their sets, were summed
       bool pieces = false;                           // as many equal logits that the queues do not hold all sets'
       for (int b = 0; b < n;) {
         if (tid == 0) singles = wholes = 0;
@@ -299,11 +330,20 @@ __global__ __launch_bounds__(NT, NT == 256 ? 5 : 4) void logprob_top_kernel(RowA
           for (int k = 0; k < 4; ++k) {
             const float2 f = fs[k];
             const int g = g0 + k * NT;
-            if (g >= stop || f.x < bound || f.y >= over) continue;   // none, or all of them before
-            if (f.y >= bound) {
+            if (g >= stop) continue;
+            bool all = f.y >= bound, one = f.x >= bound;
+            if (round) {                             // 2^-16: the last bits, which hold the place, and roundings here
+              const float* norms = P.norms + sets.group(g) * P.each;
+              float norm = norms[0];
+              for (int k = 1; k < P.each; ++k) norm = fmaxf(norm, norms[k]);
+              const float margin = reach * norm;
+              auto may = [&](float key) { return !(key >= over) && !(key + fabsf(key) * 0x1p-16f + margin < least); };
+              all = may(f.y), one = may(f.x);
+            }
+            if (all) {
               const uint32_t at = atomicAdd(&wholes, 1u);
               if (at < QUEUE) whole[at] = g;
-            } else if (f.x < over) {
+            } else if (one) {
               const uint32_t at = atomicAdd(&singles, 1u);
               if (at < QUEUE) single[at] = sets.entry(g, (int)(__float_as_uint(f.x) & (TOPS_MOST - 1)));
             }
@@ -344,15 +384,13 @@ __global__ __launch_bounds__(NT, NT == 256 ? 5 : 4) void logprob_top_kernel(RowA
                 w[r] = P.W + (int64_t)(v[r] >= 0 ? v[r] : 0) * P.ldw;
               }
               double sum[ROWS];
-              float size[ROWS];
-              exact_sums<AHEAD, ROWS>(x, w, P.K, sum, size);
+              exact_sums<AHEAD, ROWS>(x, w, P.K, sum);
 #pragma unroll
               for (int r = 0; r < ROWS; ++r) {
                 const int i = have + i0 + r * WAVES;
                 if (lane == 0 && i < have + count) {
                   value[i] = v[r] >= 0 && sum[r] == sum[r] ? sum[r] : -INFINITY;   // NaN (outside the contract): an order all the same
                   index[i] = v[r] >= 0 ? v[r] : 0x7FFFFFFF;
-                  if (v[r] >= 0) atomicMax(&largest, __float_as_uint(size[r]));
                 }
               }
             }
@@ -384,14 +422,16 @@ __global__ __launch_bounds__(NT, NT == 256 ? 5 : 4) void logprob_top_kernel(RowA
           __syncthreads();
         }
       }
-      // A logit that was left out is below `bound` in float32, so in 64 bits below it and a margin of
-      // both sums' errors and of the last bits that hold its place.
-      if (have < top) break;                         // NaN again
-      const double least = value[top - 1];
-      const double margin = 2.0 * ((double)(P.K + 64) * 0x1p-24 * (double)__uint_as_float(largest) + 0x1p-17 * fabs(least));
-      if (bound == -INFINITY || !((double)bound + margin > least)) break;
-      over = bound, bound = round < 14 ? __double2float_rd(least - margin) : -INFINITY;   // everything, in the end
-      __syncthreads();                               // value and largest are read by all
+      if (round || have < top || bound == -INFINITY) break;   // fewer than top: NaN again
+      // A logit that was left out is below bound in float32, so in 64 bits below it and its margin
+      float squares = 0.0f, most = 0.0f;
+#pragma unroll
+      for (int w = 0; w < WAVES; ++w) squares += x_squares[w], most = fmaxf(most, w_norm[w]);
+      // x squared as the rows of W; 2^-23 and K + 64 leave room for the roundings here
+      reach = (float)(P.K + 64) * 0x1p-23f * (1.0f + 0x1p-6f) * sqrtf(squares * (1.0f + 0x1p-6f) + (float)P.K * 0x1p-124f);
+      least = __double2float_rd(value[top - 1]);
+      if (bound + fabsf(bound) * 0x1p-16f + reach * most < least) break;
+      __syncthreads();                               // value is read by all
     }
     for (int i = tid; i < top; i += NT) {
       const bool found = i < have && (uint32_t)index[i] < (uint32_t)P.V;   // always, of finite logits
@@ -403,10 +443,10 @@ __global__ __launch_bounds__(NT, NT == 256 ? 5 : 4) void logprob_top_kernel(RowA
 }
 
 struct Plan {
-  size_t target, stats, mean, tops, total;
+  size_t target, stats, mean, tops, norms, total;
 };
 Plan plan(int64_t T, int64_t V, int64_t K, int top) {
-  const size_t n = (size_t)logit_groups(T, V, K) * T;
+  const size_t groups = (size_t)logit_groups(T, V, K), n = groups * T;
   Plan L;
   size_t o = 0;
   auto take = [&](size_t bytes) {
@@ -418,6 +458,7 @@ Plan plan(int64_t T, int64_t V, int64_t K, int top) {
   L.stats = take(n * sizeof(float2));
   L.mean = take(n * sizeof(float));
   L.tops = take(top ? (size_t)T * logit_tops(T, V, K, top).groups * sizeof(float2) : 0);
+  L.norms = take(top ? (groups * logit_norms(T, V, K) + 1) * sizeof(float) : 0);
   L.total = o;
   return L;
 }
@@ -436,19 +477,22 @@ hipError_t launch_logprobs(const uint16_t* X, int64_t ldx, const uint16_t* W, in
   uint8_t* w = (uint8_t*)ws;
   float *target = (float*)(w + L.target), *mean = (float*)(w + L.mean);
   float2 *stats = (float2*)(w + L.stats), *tops = top ? (float2*)(w + L.tops) : nullptr;
+  float* norms = top ? (float*)(w + L.norms) : nullptr;        // and after them the largest
   const LogitTops sets = logit_tops(T, V, K, top);
-  const hipError_t e = launch_logits(X, ldx, W, ldw, tokens, tokens64, T, V, K, scale, target, stats, mean, tops, sets, st);
+  const hipError_t e = launch_logits(X, ldx, W, ldw, tokens, tokens64, T, V, K, scale, target, stats, mean, tops, norms, sets, st);
   if (e != hipSuccess) return e;
-  const RowArgs R{stats, mean, target, tokens, tokens64, (int)logit_groups(T, V, K), (int)T, (int)V, logp, entropy, lse, X, W,
-                  ldx, ldw, (int)K, top, sets, tops, scale, top_ids, top_logp};
+  const int groups = (int)logit_groups(T, V, K), each = logit_norms(T, V, K);
+  const RowArgs R{stats, mean, target, tokens, tokens64, groups, (int)T, (int)V, logp, entropy, lse, X, W,
+                  ldx, ldw, (int)K, top, sets, tops, norms, each, top ? norms + groups * each : nullptr, scale, top_ids, top_logp};
   if (T <= FEW_TOKENS) {
     SBN_LAUNCH("logprob_rows", (logprob_top_kernel<1024, true>), dim3((unsigned)T), dim3(1024), 0, st, R);
     return hipGetLastError();
   }
   constexpr int64_t JOIN_TOKENS = 1 << 24;           // of a launch: fewer than 2^32 threads
-  for (int64_t t = 0; t < T; t += JOIN_TOKENS)
-    SBN_LAUNCH("logprob_join", logprob_join_kernel, dim3((unsigned)cdiv(T - t < JOIN_TOKENS ? T - t : JOIN_TOKENS, 16)),
-               dim3(1024), 0, st, R, (int)t);
+  for (int64_t t = 0; t < T; t += JOIN_TOKENS) {
+    const int64_t rest = T - t, blocks = rest > JOIN_TOKENS ? JOIN_TOKENS / 16 : cdiv(rest, 16) + (top > 0);
+    SBN_LAUNCH("logprob_join", logprob_join_kernel, dim3((unsigned)blocks), dim3(1024), 0, st, R, (int)t);
+  }
   if (top)
     SBN_LAUNCH("logprob_top", (logprob_top_kernel<256, false>), dim3((unsigned)(T < (1 << 20) ? T : (1 << 20))), dim3(256), 0,
                st, R);

@@ -12,7 +12,8 @@ namespace sbn {
 // less the maximum.  `target` [T]: the token's logit.  tops (or NULL): per token
 // logit_tops().groups pairs of the largest and second largest of a set of 32, 16 or 8
 // sums (logits before their scale), the first's place in its last 5 bits.  A set is
-// what one lane holds of a column; of lanes that hold 8, two.  (Few tokens: sets of 8
+// what one lane holds of a column; of lanes that hold 8, two.  With tops, norms: per group
+// logit_norms() numbers, the largest of which is no less than the norm of any of its rows of W.  (Few tokens: sets of 8
 // are 64 KB to read for each at 65536 entries, and of 32 twice as often one with two
 // candidates, all of which are then computed.)  Where two in a set are common, sets are of
 // 8, parts of a lane's: of about c = top + 3 candidates 512 c^2 / V rows of W are computed for
@@ -29,6 +30,8 @@ struct LogitTops {
   int mi_log2;                         // a lane's 4 mi entries are 4 of each of mi fragments of 16
   int of_log2;                         // entries of a set
   int groups;                          // sets, of V rounded up to whole tiles
+  // the logits' group (of those that have statistics) that set g is of
+  __host__ __device__ int group(int g) const { return g >> (4 + mi_log2 - of_log2); }
   // the place of set g's q-th entry: among its lane's where that holds several sets, else in the set
   __host__ __device__ int place(int g, int q) const {
     const int sets = 2 + mi_log2 - of_log2;                      // log2 of a lane's sets
@@ -45,9 +48,10 @@ struct LogitTops {
 static_assert(tops_of(8) == TOPS_MOST && TOPS_MOST == 32, "5 bits");
 LogitTops logit_tops(int64_t T, int64_t V, int64_t K, int top);
 int64_t logit_groups(int64_t T, int64_t V, int64_t K);
+int logit_norms(int64_t T, int64_t V, int64_t K);
 hipError_t launch_logits(const uint16_t* X, int64_t ldx, const uint16_t* W, int64_t ldw, const void* tokens, bool tokens64,
                          int64_t T, int64_t V, int64_t K, float scale, float* target, float2* stats, float* mean,
-                         float2* tops, const LogitTops& sets, hipStream_t st);
+                         float2* tops, float* norms, const LogitTops& sets, hipStream_t st);
 
 // ----------------------------------------------------------------- logprobs.hip
 size_t logprobs_ws_bytes(int64_t T, int64_t V, int64_t K, int top);

@@ -48,6 +48,17 @@ template <class Op>
 __device__ inline float wave_all(float x, Op op) {
   return rows_all(row16_all(x, op), op);
 }
+// sum + the squares of 8 bf16 values, by an instruction that rounds up to three times for
+// two of them and may take what is under 2^-126 for 0
+__device__ inline float add_squares(v8bf x, float sum) {
+  typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
+#pragma unroll
+  for (int j = 0; j < 8; j += 2) {
+    const v2bf two = {x[j], x[j + 1]};
+    sum = __builtin_amdgcn_fdot2_f32_bf16(two, two, sum, false);
+  }
+  return sum;
+}
 #endif
 
 // ----------------------------------------------------------------- RMS norm (T >= 1)
