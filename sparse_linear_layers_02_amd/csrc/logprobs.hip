@@ -367,20 +367,23 @@ __global__ __launch_bounds__(NT, NT == 256 ? 5 : 4) void logprob_top_kernel(RowA
 #pragma unroll 1
             for (int i0 = wave; i0 < count; i0 += WAVES * ROWS) {
               const uint16_t* w[ROWS];
-              int v[ROWS];
+              int v[ROWS], place[ROWS];
 #pragma unroll
               for (int r = 0; r < ROWS; ++r) {
                 const int i = i0 + r * WAVES, at = e + i - (int)ns;
-                int entry = -1;                      // none
+                int entry = 0;
+                bool none = i >= count;
                 if (i < count && at < 0) {
                   entry = single[e + i];
                 } else if (i < count) {              // of a set whose first alone came before, without it
                   const int g = whole[at >> sets.of_log2], p = sets.place(g, at & ((1 << sets.of_log2) - 1));
                   const float f = row[g].x;
-                  if (!(f >= over && p == (int)(__float_as_uint(f) & (TOPS_MOST - 1)))) entry = sets.entry(g, p);
+                  none = f >= over && p == (int)(__float_as_uint(f) & (TOPS_MOST - 1));
+                  entry = sets.entry(g, p);
                 }
-                entry = __builtin_amdgcn_readfirstlane(entry);
-                v[r] = (uint32_t)entry < (uint32_t)P.V ? entry : -1;   // and not past the vocabulary
+                place[r] = __builtin_amdgcn_readfirstlane(entry);
+                none |= (uint32_t)entry >= (uint32_t)P.V;   // past the vocabulary
+                v[r] = __builtin_amdgcn_readfirstlane(none ? -1 : entry);
                 w[r] = P.W + (int64_t)(v[r] >= 0 ? v[r] : 0) * P.ldw;
               }
               double sum[ROWS];
@@ -390,7 +393,7 @@ __global__ __launch_bounds__(NT, NT == 256 ? 5 : 4) void logprob_top_kernel(RowA
                 const int i = have + i0 + r * WAVES;
                 if (lane == 0 && i < have + count) {
                   value[i] = v[r] >= 0 && sum[r] == sum[r] ? sum[r] : -INFINITY;   // NaN (outside the contract): an order all the same
-                  index[i] = v[r] >= 0 ? v[r] : 0x7FFFFFFF;
+                  index[i] = place[r];               // of none too: equal ones would leave places of the order empty
                 }
               }
             }

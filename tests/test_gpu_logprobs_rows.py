@@ -70,3 +70,15 @@ def test_one_row_far_larger_than_all_others():
         r = reference(X, W, y)
         ids = sbn.sbn_token_logprobs(X, W, y, top=10)[3]
         assert torch.equal(ids, torch.sort(r["z"], dim=1, descending=True, stable=True).indices[:, :10])
+
+
+@pytest.mark.parametrize("V", [257, 260, 300, 511, 513])
+def test_vocabularies_that_leave_most_of_a_tile_empty(V):
+    """Whole tiles of 256 entries: sets of which all or a part is past the vocabulary are among the candidates."""
+    import torch
+    T, K = 70000, 64
+    X, W, y, _, _ = problem(T, V, K, V)
+    z = reference(X, W, y)["z"]
+    got, ran = launches(lambda: sbn.sbn_token_logprobs(X, W, y, top=64))
+    assert ran["logprob_logits_wide"] == 1
+    assert torch.equal(got[3], torch.sort(z, dim=1, descending=True, stable=True).indices[:, :64])
