@@ -35,6 +35,10 @@ extern "C" {
  * scale is the inverse of a sampling temperature.  A token outside [0, V), such as
  * -100, marks a row without one; its distribution is there all the same.
  *
+ * logp and top_logp are at most 0 and entropy at least 0, and near 0 they keep float32's
+ * relative precision: they are formed from differences to the row's largest logit, not from
+ * lse.  (The logits themselves are float32 sums, and those of top_logp 64-bit ones.)
+ *
  * The order of the alternatives is that of sums in 64 bits: float32 sums only
  * choose who is compared, with a margin of their worst error (K 2^-23 |X[t]| |W[v]|, the
  * norms' product being no less than sum_k |X W|, with the largest |W[v]| of a group of 32 to 128

@@ -74,8 +74,8 @@ struct GemmArgs {
   bool labels64;
   int v0;                              // vocabulary entry of A row 0
   int V;
-  float2* stats;                       // [2-wave column groups][nB]: maximum (times log2 e), sum
-  float* target;                       // [nB] logit of the label
+  float2* stats;                       // [2-wave column groups][nB]: maximum (times log2 e), sum; EPI_SCORE: maximum, sum without it
+  float* target;                       // [nB] sum of the label's entry
   const float *lse, *dloss;
   float* gmax;                         // max |dloss|; EPI_GRAD divides by it, EPI_OUT multiplies
   // EPI_SCORE, EPI_POLICY: logits are scale times the sums
@@ -635,29 +635,35 @@ __global__ __launch_bounds__(64 * WA * WB, 1) void ce_gemm_kernel(GemmArgs P) {
 #pragma unroll
             for (int e = 0; e < 4; ++e)
               if (at == 16 * i + e) hit = c[i][e];
-          if (has) P.target[t] = SCORE ? hit * P.scale : hit;
+          if (has) P.target[t] = hit;
         }
 #pragma unroll
         for (int i = 0; i < MI; ++i)
 #pragma unroll
           for (int e = 0; e < 4; ++e) m = fmaxf(m, c[i][e]);
         m = rows_all(m, Max{});
-        const float top = fmaxf(m * factor, NONE);   // a group past the vocabulary has no logits
-        float sum = 0.0f, mean = 0.0f;
+        // a group past the vocabulary has no logits
+        const float top = SCORE ? fmaxf(m, P.none) : fmaxf(m * factor, NONE);
+        float sum = 0.0f, rest = 0.0f, mean = 0.0f;
 #pragma unroll
         for (int i = 0; i < MI; ++i)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float d = c[i][e] * factor - top, x = __builtin_amdgcn_exp2f(d);
+            const float d = SCORE ? (c[i][e] - top) * factor : c[i][e] * factor - top, x = __builtin_amdgcn_exp2f(d);
             sum += x;
-            if (SCORE) mean += x * d;
+            // without the largest itself, whose 1 would take the last bits of small ones
+            if (SCORE) rest += __builtin_amdgcn_fractf(x), mean += x * d;
           }
         sum = rows_all(sum, Add{});
-        if (SCORE) mean = rows_all(mean, Add{});
-        const bool empty = SCORE && aw >= P.nA;      // `none` less its own rounding is nothing to sum
+        if (SCORE) rest = rows_all(rest, Add{}), mean = rows_all(mean, Add{});
         if (lane < 16 && t < P.nB) {
-          P.stats[(int64_t)group * P.nB + t] = empty ? make_float2(NONE, 0.0f) : make_float2(top, sum);
-          if (SCORE) P.mean[(int64_t)group * P.nB + t] = empty ? 0.0f : mean;
+          float2 stat = make_float2(top, sum);
+          if (SCORE) {
+            stat.y = rest + (rintf(sum - rest) - 1.0f);   // of several that are as large, all but one
+            if (aw >= P.nA) stat.y = -1.0f, mean = 0.0f;
+            P.mean[(int64_t)group * P.nB + t] = mean;
+          }
+          P.stats[(int64_t)group * P.nB + t] = stat;
         }
       }
     } else if (GRAD) {
@@ -1076,7 +1082,7 @@ hipError_t launch_logits(const uint16_t* X, int64_t ldx, const uint16_t* W, int6
   P.labels = tokens, P.labels64 = tokens64, P.V = (int)V;
   P.target = target, P.stats = stats, P.mean = mean, P.tops = tops, P.norms = norms;
   P.ldt = sets.groups;
-  P.scale = scale, P.none = -1e30f / (scale * LOG2E);
+  P.scale = scale, P.none = logit_none(scale);
   const Tile t = score_tile(T, V, K);
   if (!tops) return gemm<EPI_SCORE>(SCORES, t, P, st);
   return sets.of_log2 == 3 ? gemm<EPI_SCORE_TOPS8>(SCORES, t, P, st) : gemm<EPI_SCORE_TOPS>(SCORES, t, P, st);

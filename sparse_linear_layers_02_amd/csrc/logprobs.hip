@@ -1,11 +1,15 @@
 // Log probabilities of given tokens, entropies and top alternatives, from what the
 // head's product leaves of each group of logits while they are in registers.
 //
-//   with exponents z = l log2 e, a group's maximum m, s = sum 2^(z - m), q = sum 2^(z - m) (z - m):
-//   lse = ln 2 m + ln s;  logp = l_y - lse;  entropy = lse - sum p l = ln s - ln 2 q / s
-// Groups join as (m, s, q): relative to the larger maximum M, s 2^(m - M) and
-// 2^(m - M) (q + (m - M) s).  Both terms of the entropy are of its own size, so a
-// distribution that is nearly certain loses nothing to a difference.
+//   with a group's largest logit m, exponents z = (l - m) log2 e, r = sum 2^z without that of m
+//   itself, q = sum 2^z z:
+//   lse = m + ln(1 + r);  logp = l_y - m - ln(1 + r);  entropy = lse - sum p l = ln(1 + r) - ln 2 q / (1 + r)
+// Groups join as (m, r, q): to those of the larger m come 2^d (1 + r) and 2^d (q + d (1 + r)), d the
+// other's m less the larger one, times log2 e.  No term is larger than what it goes into, so
+// distributions that are nearly certain lose nothing to a difference: log probabilities and entropies
+// near 0 keep their relative precision, and none is on its wrong side.
+// The alternatives' sums are in 64 bits, m in 32: theirs are taken from the 64-bit sum of
+// the entry that m is of.
 //
 // Alternatives: of every 32, 16 or 8 logits, the two largest are kept in float32.  The
 // k-th largest of any partition's maxima is no larger than the k-th largest logit, so a
@@ -27,19 +31,18 @@ namespace sbn {
 namespace {
 
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
-constexpr float NONE = -1.0e38f * LOG2E;             // the maximum of no logits
 
 __device__ inline int64_t token_at(const void* tokens, bool is64, int64_t t) {
   return is64 ? ((const int64_t*)tokens)[t] : (int64_t)((const int32_t*)tokens)[t];
 }
 
 struct Stat {
-  float m, s, q;
+  float m, r, q;                       // m before the logits' scale
 };
-__device__ inline Stat join(Stat a, Stat b) {
-  const float top = fmaxf(a.m, b.m), da = a.m - top, db = b.m - top;
-  const float ea = __builtin_amdgcn_exp2f(da), eb = __builtin_amdgcn_exp2f(db);
-  return {top, a.s * ea + b.s * eb, ea * (a.q + da * a.s) + eb * (b.q + db * b.s)};
+__device__ inline Stat join(Stat a, Stat b, float factor) {
+  const Stat hi = a.m >= b.m ? a : b, lo = a.m >= b.m ? b : a;
+  const float d = (lo.m - hi.m) * factor, e = __builtin_amdgcn_exp2f(d), s = 1.0f + lo.r;
+  return {hi.m, hi.r + e * s, hi.q + e * (lo.q + d * s)};
 }
 
 struct RowArgs {
@@ -48,6 +51,8 @@ struct RowArgs {
   const void* tokens;
   bool tokens64;
   int groups, T, V;
+  float factor, none;                  // scale log2 e; the maximum of no logits
+  float2* rows;                        // [T] m and ln(1 + r), for the alternatives
   float *logp, *entropy, *lse;
   // alternatives
   const uint16_t *X, *W;
@@ -63,21 +68,22 @@ struct RowArgs {
   float* top_logp;
 };
 
-// a token's outputs from all its logits' statistics; returns lse
-__device__ inline float finish(const RowArgs& P, int64_t t, Stat a) {
-  const float ln = logf(a.s), l = a.m * LN2 + ln;
-  P.lse[t] = l;
-  if (P.entropy) P.entropy[t] = ln - (a.q / a.s) * LN2;
+// a token's outputs from all its logits' statistics; returns m and ln(1 + r)
+__device__ inline float2 finish(const RowArgs& P, int64_t t, Stat a) {
+  const float ln = log1pf(a.r);
+  P.lse[t] = a.m * P.scale + ln;
+  if (P.entropy) P.entropy[t] = ln - (a.q / (1.0f + a.r)) * LN2;
   if (P.logp) {
     const int64_t y = token_at(P.tokens, P.tokens64, t);
-    P.logp[t] = y >= 0 && y < P.V ? P.target[t] - l : 0.0f;
+    P.logp[t] = y >= 0 && y < P.V ? (P.target[t] - a.m) * P.scale - ln : 0.0f;
   }
-  return l;
+  return make_float2(a.m, ln);
 }
 // every `step`-th group from `first` on, AHEAD loads in flight
 template <int AHEAD>
 __device__ inline Stat join_groups(const RowArgs& P, int64_t t, int first, int step) {
-  Stat a{NONE, 0.0f, 0.0f};
+  const Stat none{P.none, -1.0f, 0.0f};
+  Stat a = none;
   for (int g = first; g < P.groups; g += step * AHEAD) {
     Stat x[AHEAD];
 #pragma unroll
@@ -86,10 +92,10 @@ __device__ inline Stat join_groups(const RowArgs& P, int64_t t, int first, int s
       const int64_t at = (int64_t)(in ? g + step * k : g) * P.T + t;
       const float2 ms = P.stats[at];
       const float q = P.mean[at];
-      x[k] = in ? Stat{ms.x, ms.y, q} : Stat{NONE, 0.0f, 0.0f};
+      x[k] = in ? Stat{ms.x, ms.y, q} : none;
     }
 #pragma unroll
-    for (int k = 0; k < AHEAD; ++k) a = join(a, x[k]);
+    for (int k = 0; k < AHEAD; ++k) a = join(a, x[k], P.factor);
   }
   return a;
 }
@@ -113,17 +119,20 @@ __global__ __launch_bounds__(1024) void logprob_join_kernel(RowArgs P, int first
   }
   const int tl = threadIdx.x & 15, part = threadIdx.x >> 4;
   const int t = first + blockIdx.x * 16 + tl;
-  Stat a{NONE, 0.0f, 0.0f};
+  Stat a{P.none, -1.0f, 0.0f};
   if (t < P.T) a = join_groups<4>(P, t, part, 64);
-  auto put = [&](Stat x) { sm[0][part][tl] = x.m, sm[1][part][tl] = x.s, sm[2][part][tl] = x.q; };
+  auto put = [&](Stat x) { sm[0][part][tl] = x.m, sm[1][part][tl] = x.r, sm[2][part][tl] = x.q; };
   put(a);
   __syncthreads();
 #pragma unroll
   for (int d = 32; d >= 1; d >>= 1) {
-    if (part < d) put(a = join(a, Stat{sm[0][part + d][tl], sm[1][part + d][tl], sm[2][part + d][tl]}));
+    if (part < d) put(a = join(a, Stat{sm[0][part + d][tl], sm[1][part + d][tl], sm[2][part + d][tl]}, P.factor));
     __syncthreads();
   }
-  if (part == 0 && t < P.T) finish(P, t, a);
+  if (part == 0 && t < P.T) {
+    const float2 row = finish(P, t, a);
+    if (P.top) P.rows[t] = row;
+  }
 }
 
 // ---------------------------------------------------------------- top alternatives
@@ -192,12 +201,13 @@ __device__ inline void exact_sums(const uint16_t* x, const uint16_t* const (&w)[
 
 // A float that at least k of 256 reach (-Inf if fewer than k are above it), within 2^-11 of
 // the k-th largest: the leading bits of the order-preserving integers, one at a time,
-// as long as k are no smaller.  Each wave for itself.  (Counting for each of the 256
+// as long as k are no smaller; and the largest.  Each wave for itself.  (Counting for each of the 256
 // how many are larger took 12.5 us of one token's 23.)
-__device__ inline float reached_by(const float* slot, int k) {
+__device__ inline float reached_by(const float* slot, int k, float& most) {
   constexpr uint32_t LEAST = 0x00800000u;            // the integers of -Inf and below
   const v4f o = *(const v4f*)(slot + 4 * (threadIdx.x & 63));
   uint32_t key[4], found = 0;
+  most = wave_all(fmaxf(fmaxf(o[0], o[1]), fmaxf(o[2], o[3])), Max{});
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     const uint32_t u = __float_as_uint(o[e]);
@@ -231,7 +241,8 @@ __global__ __launch_bounds__(NT, NT == 256 ? 5 : 4) void logprob_top_kernel(RowA
   constexpr int HELD = 4;
   static_assert(NT % SLOTS == 0 && NT <= QUEUE, "threads");
   __shared__ __attribute__((aligned(16))) float slot[NT];
-  __shared__ float log_sum;
+  __shared__ float2 largest;                         // m and ln(1 + r)
+  __shared__ int leader;                             // the entry that m is of
   __shared__ Stat stat[WAVES];
   __shared__ uint32_t singles, wholes;               // queued entries, queued sets
   __shared__ float x_squares[WAVES], w_norm[WAVES];
@@ -256,7 +267,7 @@ __global__ __launch_bounds__(NT, NT == 256 ? 5 : 4) void logprob_top_kernel(RowA
       Stat a = join_groups<2>(P, t, tid, NT);
       auto over_lanes = [&](int d) {
 #pragma unroll 1
-        for (; d >= 1; d >>= 1) a = join(a, Stat{__shfl_xor(a.m, d), __shfl_xor(a.s, d), __shfl_xor(a.q, d)});
+        for (; d >= 1; d >>= 1) a = join(a, Stat{__shfl_xor(a.m, d), __shfl_xor(a.r, d), __shfl_xor(a.q, d)}, P.factor);
       };
       over_lanes(32);
       if (lane == 0) stat[wave] = a;
@@ -264,14 +275,14 @@ __global__ __launch_bounds__(NT, NT == 256 ? 5 : 4) void logprob_top_kernel(RowA
       if (wave == 0) {
         a = stat[lane & (WAVES - 1)];
         over_lanes(WAVES / 2);
-        if (tid == 0) log_sum = finish(P, t, a);
+        if (tid == 0) largest = finish(P, t, a);
       }
       if (!top) {
         __syncthreads();
         continue;
       }
     } else if (tid == 0) {
-      log_sum = P.lse[t];
+      largest = P.rows[t];
     }
     // a bound that at least top + 2 firsts reach, if there are as many: the places past
     // the top itself leave room for the margin below, which then asks for a second round less
@@ -295,7 +306,7 @@ __global__ __launch_bounds__(NT, NT == 256 ? 5 : 4) void logprob_top_kernel(RowA
     if (lane == 0) x_squares[wave] = xx, w_norm[wave] = w_most;
     slot[tid] = m;
     if (!__syncthreads_or(any)) {                    // a row of zeros (padding): all logits are equal, the first ones win
-      for (int i = tid; i < top; i += NT) P.ids[(int64_t)t * top + i] = i, P.top_logp[(int64_t)t * top + i] = -log_sum;
+      for (int i = tid; i < top; i += NT) P.ids[(int64_t)t * top + i] = i, P.top_logp[(int64_t)t * top + i] = -largest.y;
       __syncthreads();
       continue;
     }
@@ -307,7 +318,9 @@ __global__ __launch_bounds__(NT, NT == 256 ? 5 : 4) void logprob_top_kernel(RowA
       if (tid < SLOTS) slot[tid] = m;
       __syncthreads();
     }
-    const float bound = reached_by(slot, top + 2);
+    float most_likely;
+    const float bound = reached_by(slot, top + 2, most_likely);
+    if (tid == 0) leader = 0x7FFFFFFF;
     float reach = 0.0f, least = 0.0f;                // second round: a margin's share of x, and the last alternative
     int have = 0;
 #pragma unroll 1
@@ -332,6 +345,7 @@ __global__ __launch_bounds__(NT, NT == 256 ? 5 : 4) void logprob_top_kernel(RowA
             const int g = g0 + k * NT;
             if (g >= stop) continue;
             bool all = f.y >= bound, one = f.x >= bound;
+            if (!round && f.x == most_likely) atomicMin(&leader, sets.entry(g, (int)(__float_as_uint(f.x) & (TOPS_MOST - 1))));
             if (round) {                             // 2^-16: the last bits, which hold the place, and roundings here
               const float* norms = P.norms + sets.group(g) * P.each;
               float norm = norms[0];
@@ -436,17 +450,22 @@ __global__ __launch_bounds__(NT, NT == 256 ? 5 : 4) void logprob_top_kernel(RowA
       if (bound + fabsf(bound) * 0x1p-16f + reach * most < least) break;
       __syncthreads();                               // value is read by all
     }
+    // m's 64-bit sum, if it is an alternative; if not (its 32 bits are as far off), m itself
+    double from = largest.x;
+    for (int i = 0; i < have; ++i)
+      if (index[i] == leader) from = value[i];
     for (int i = tid; i < top; i += NT) {
       const bool found = i < have && (uint32_t)index[i] < (uint32_t)P.V;   // always, of finite logits
+      const float logp = (float)((double)P.scale * (value[i] - from) - (double)largest.y);
       P.ids[(int64_t)t * top + i] = found ? index[i] : 0;
-      P.top_logp[(int64_t)t * top + i] = found ? (float)((double)P.scale * value[i] - (double)log_sum) : NAN;
+      P.top_logp[(int64_t)t * top + i] = found ? logp > 0.0f ? 0.0f : logp : NAN;
     }
     __syncthreads();
   }
 }
 
 struct Plan {
-  size_t target, stats, mean, tops, norms, total;
+  size_t target, stats, mean, tops, norms, rows, total;
 };
 Plan plan(int64_t T, int64_t V, int64_t K, int top) {
   const size_t groups = (size_t)logit_groups(T, V, K), n = groups * T;
@@ -462,6 +481,7 @@ Plan plan(int64_t T, int64_t V, int64_t K, int top) {
   L.mean = take(n * sizeof(float));
   L.tops = take(top ? (size_t)T * logit_tops(T, V, K, top).groups * sizeof(float2) : 0);
   L.norms = take(top ? (groups * logit_norms(T, V, K) + 1) * sizeof(float) : 0);
+  L.rows = take(top ? (size_t)T * sizeof(float2) : 0);
   L.total = o;
   return L;
 }
@@ -485,7 +505,8 @@ hipError_t launch_logprobs(const uint16_t* X, int64_t ldx, const uint16_t* W, in
   const hipError_t e = launch_logits(X, ldx, W, ldw, tokens, tokens64, T, V, K, scale, target, stats, mean, tops, norms, sets, st);
   if (e != hipSuccess) return e;
   const int groups = (int)logit_groups(T, V, K), each = logit_norms(T, V, K);
-  const RowArgs R{stats, mean, target, tokens, tokens64, groups, (int)T, (int)V, logp, entropy, lse, X, W,
+  const RowArgs R{stats, mean, target, tokens, tokens64, groups, (int)T, (int)V,
+                  scale * LOG2E, logit_none(scale), (float2*)(w + L.rows), logp, entropy, lse, X, W,
                   ldx, ldw, (int)K, top, sets, tops, norms, each, top ? norms + groups * each : nullptr, scale, top_ids, top_logp};
   if (T <= FEW_TOKENS) {
     SBN_LAUNCH("logprob_rows", (logprob_top_kernel<1024, true>), dim3((unsigned)T), dim3(1024), 0, st, R);

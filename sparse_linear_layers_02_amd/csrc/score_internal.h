@@ -7,9 +7,10 @@
 namespace sbn {
 
 // ----------------------------------------------------------------- the logits' statistics (cross_entropy.hip)
-// Statistics come in logit_groups() groups of entries, [group][T]: (maximum, sum of
-// exponentials) and the sum of exponential times exponent, exponents times log2 e and
-// less the maximum.  `target` [T]: the token's logit.  tops (or NULL): per token
+// Statistics come in logit_groups() groups of entries, [group][T]: the maximum of the sums
+// x w (logits before their scale) and the sum of exponentials, one of the maximum left out (-1 of
+// no entries), and the sum of exponential times exponent, exponents times scale log2 e and
+// less the maximum's.  `target` [T]: the token's sum.  tops (or NULL): per token
 // logit_tops().groups pairs of the largest and second largest of a set of 32, 16 or 8
 // sums (logits before their scale), the first's place in its last 5 bits.  A set is
 // what one lane holds of a column; of lanes that hold 8, two.  With tops, norms: per group
@@ -24,6 +25,8 @@ namespace sbn {
 // + 31; 64 of 8000, 2000, 512 27 + 78, 25 + 320; 20 of 32001, 37, 4096 61 + 25, 61 + 28; and
 // where they are not taken 32 of 65536, 4096, 2560 1034 + 218, 974 + 211; 8 of 32001, 4096, 2560
 // 517 + 89, 495 + 77; 8 of 16000, 8192, 1024 242 + 81, 232 + 85.)
+// the sum that stands for no entry: -1e30 as an exponent
+inline float logit_none(float scale) { return -1e30f / (scale * 1.4426950408889634f); }
 constexpr int TOPS_MOST = 32;
 constexpr int tops_of(int mi) { return 4 * mi >= 16 ? 4 * mi : 16; }
 struct LogitTops {
