@@ -54,7 +54,9 @@ extern "C" {
  *   logp, lse [T] float; entropy [T] float or NULL                       (out)
  *   top     0 .. min(V, SBN_LOGPROBS_MAX_TOP); with 0 top_ids and top_logp may be NULL
  *   top_ids [T x top] int64, top_logp [T x top] float, contiguous        (out)
- *   ws      sbn_token_logprobs_workspace_bytes(T, V, K, top) bytes, no initialisation
+ *   ws      sbn_token_logprobs_workspace_bytes(T, V, K, top) bytes, no initialisation:
+ *           V / 10 to 3 V / 8 bytes a token, with alternatives V / 4 to V more, as far as 4 GiB
+ *           (512 MiB for V more); of more tokens it is used for one part after the other
  * 2^-20 <= scale <= 2^20; |l| < 2^30.  Limits of T, V and K as for sbn_cross_entropy
  * (T = 0: nothing to do).
  */

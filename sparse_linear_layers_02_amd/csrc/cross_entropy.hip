@@ -1073,7 +1073,7 @@ LogitTops logit_tops(int64_t T, int64_t V, int64_t K, int top) {
 }
 
 hipError_t launch_logits(const uint16_t* X, int64_t ldx, const uint16_t* W, int64_t ldw, const void* tokens, bool tokens64,
-                         int64_t T, int64_t V, int64_t K, float scale, float* target, float2* stats, float* mean,
+                         int64_t T, int64_t all, int64_t V, int64_t K, float scale, float* target, float2* stats, float* mean,
                          float2* tops, float* norms, const LogitTops& sets, hipStream_t st) {
   GemmArgs P{};
   P.A = W, P.lda = ldw, P.nA = P.mA = (int)V;
@@ -1083,7 +1083,7 @@ hipError_t launch_logits(const uint16_t* X, int64_t ldx, const uint16_t* W, int6
   P.target = target, P.stats = stats, P.mean = mean, P.tops = tops, P.norms = norms;
   P.ldt = sets.groups;
   P.scale = scale, P.none = logit_none(scale);
-  const Tile t = score_tile(T, V, K);
+  const Tile t = score_tile(all, V, K);
   if (!tops) return gemm<EPI_SCORE>(SCORES, t, P, st);
   return sets.of_log2 == 3 ? gemm<EPI_SCORE_TOPS8>(SCORES, t, P, st) : gemm<EPI_SCORE_TOPS>(SCORES, t, P, st);
 }

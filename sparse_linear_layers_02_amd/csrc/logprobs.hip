@@ -464,24 +464,38 @@ __global__ __launch_bounds__(NT, NT == 256 ? 5 : 4) void logprob_top_kernel(RowA
   }
 }
 
+// Tokens are taken in parts whose statistics and sets' pairs stay below so many bytes, of
+// 64 tokens at least; pairs of sets of 8, V bytes a token, in parts as were measured.  (What it
+// takes: W is read once more for each part, of thousands of tokens.)
+constexpr int64_t PART_BYTES = int64_t(1) << 32, PAIRS8_BYTES = int64_t(1) << 29;
+
 struct Plan {
+  int64_t part;                                      // tokens of all parts but the last
   size_t target, stats, mean, tops, norms, rows, total;
 };
 Plan plan(int64_t T, int64_t V, int64_t K, int top) {
-  const size_t groups = (size_t)logit_groups(T, V, K), n = groups * T;
+  const size_t groups = (size_t)logit_groups(T, V, K);
+  const LogitTops sets = logit_tops(T, V, K, top);
+  const int64_t pairs = top ? (int64_t)sets.groups * (int64_t)sizeof(float2) : 0;
+  int64_t most = PART_BYTES / ((int64_t)groups * 12 + pairs);
+  if (top && sets.of_log2 == 3 && most > PAIRS8_BYTES / pairs) most = PAIRS8_BYTES / pairs;
+  const int64_t unit = most >= 256 ? 256 : 64;       // tiles' tokens
+  most = most < unit ? unit : most / unit * unit;
   Plan L;
+  L.part = T <= most ? T : round_up(cdiv(T, cdiv(T, most)), unit);
+  const size_t n = groups * L.part;
   size_t o = 0;
   auto take = [&](size_t bytes) {
     const size_t at = o;
     o += align256(bytes);
     return at;
   };
-  L.target = take((size_t)T * sizeof(float));
+  L.target = take((size_t)L.part * sizeof(float));
   L.stats = take(n * sizeof(float2));
   L.mean = take(n * sizeof(float));
-  L.tops = take(top ? (size_t)T * logit_tops(T, V, K, top).groups * sizeof(float2) : 0);
+  L.tops = take((size_t)L.part * pairs);
   L.norms = take(top ? (groups * logit_norms(T, V, K) + 1) * sizeof(float) : 0);
-  L.rows = take(top ? (size_t)T * sizeof(float2) : 0);
+  L.rows = take(top ? (size_t)L.part * sizeof(float2) : 0);
   L.total = o;
   return L;
 }
@@ -502,24 +516,31 @@ hipError_t launch_logprobs(const uint16_t* X, int64_t ldx, const uint16_t* W, in
   float2 *stats = (float2*)(w + L.stats), *tops = top ? (float2*)(w + L.tops) : nullptr;
   float* norms = top ? (float*)(w + L.norms) : nullptr;        // and after them the largest
   const LogitTops sets = logit_tops(T, V, K, top);
-  const hipError_t e = launch_logits(X, ldx, W, ldw, tokens, tokens64, T, V, K, scale, target, stats, mean, tops, norms, sets, st);
-  if (e != hipSuccess) return e;
   const int groups = (int)logit_groups(T, V, K), each = logit_norms(T, V, K);
-  const RowArgs R{stats, mean, target, tokens, tokens64, groups, (int)T, (int)V,
-                  scale * LOG2E, logit_none(scale), (float2*)(w + L.rows), logp, entropy, lse, X, W,
-                  ldx, ldw, (int)K, top, sets, tops, norms, each, top ? norms + groups * each : nullptr, scale, top_ids, top_logp};
-  if (T <= FEW_TOKENS) {
-    SBN_LAUNCH("logprob_rows", (logprob_top_kernel<1024, true>), dim3((unsigned)T), dim3(1024), 0, st, R);
-    return hipGetLastError();
+  for (int64_t t0 = 0; t0 < T; t0 += L.part) {
+    const int64_t n = T - t0 < L.part ? T - t0 : L.part;
+    const uint16_t* x = X + t0 * ldx;
+    const void* y = tokens ? (const uint8_t*)tokens + t0 * (tokens64 ? 8 : 4) : nullptr;
+    const hipError_t e = launch_logits(x, ldx, W, ldw, y, tokens64, n, T, V, K, scale, target, stats, mean, tops, norms, sets, st);
+    if (e != hipSuccess) return e;
+    const RowArgs R{stats, mean, target, y, tokens64, groups, (int)n, (int)V,
+                    scale * LOG2E, logit_none(scale), (float2*)(w + L.rows), logp ? logp + t0 : nullptr,
+                    entropy ? entropy + t0 : nullptr, lse + t0, x, W, ldx, ldw, (int)K, top, sets, tops, norms, each,
+                    top ? norms + groups * each : nullptr, scale, top ? top_ids + t0 * top : nullptr,
+                    top ? top_logp + t0 * top : nullptr};
+    if (T <= FEW_TOKENS) {
+      SBN_LAUNCH("logprob_rows", (logprob_top_kernel<1024, true>), dim3((unsigned)n), dim3(1024), 0, st, R);
+      continue;
+    }
+    constexpr int64_t JOIN_TOKENS = 1 << 24;         // of a launch: fewer than 2^32 threads
+    for (int64_t t = 0; t < n; t += JOIN_TOKENS) {
+      const int64_t rest = n - t, blocks = rest > JOIN_TOKENS ? JOIN_TOKENS / 16 : cdiv(rest, 16) + (top > 0);
+      SBN_LAUNCH("logprob_join", logprob_join_kernel, dim3((unsigned)blocks), dim3(1024), 0, st, R, (int)t);
+    }
+    if (top)
+      SBN_LAUNCH("logprob_top", (logprob_top_kernel<256, false>), dim3((unsigned)(n < (1 << 20) ? n : (1 << 20))), dim3(256), 0,
+                 st, R);
   }
-  constexpr int64_t JOIN_TOKENS = 1 << 24;           // of a launch: fewer than 2^32 threads
-  for (int64_t t = 0; t < T; t += JOIN_TOKENS) {
-    const int64_t rest = T - t, blocks = rest > JOIN_TOKENS ? JOIN_TOKENS / 16 : cdiv(rest, 16) + (top > 0);
-    SBN_LAUNCH("logprob_join", logprob_join_kernel, dim3((unsigned)blocks), dim3(1024), 0, st, R, (int)t);
-  }
-  if (top)
-    SBN_LAUNCH("logprob_top", (logprob_top_kernel<256, false>), dim3((unsigned)(T < (1 << 20) ? T : (1 << 20))), dim3(256), 0,
-               st, R);
   return hipGetLastError();
 }
 

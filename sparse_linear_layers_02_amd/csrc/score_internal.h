@@ -52,8 +52,9 @@ static_assert(tops_of(8) == TOPS_MOST && TOPS_MOST == 32, "5 bits");
 LogitTops logit_tops(int64_t T, int64_t V, int64_t K, int top);
 int64_t logit_groups(int64_t T, int64_t V, int64_t K);
 int logit_norms(int64_t T, int64_t V, int64_t K);
+// T tokens of `all`, for which logit_tops(), logit_groups() and logit_norms() are asked
 hipError_t launch_logits(const uint16_t* X, int64_t ldx, const uint16_t* W, int64_t ldw, const void* tokens, bool tokens64,
-                         int64_t T, int64_t V, int64_t K, float scale, float* target, float2* stats, float* mean,
+                         int64_t T, int64_t all, int64_t V, int64_t K, float scale, float* target, float2* stats, float* mean,
                          float2* tops, float* norms, const LogitTops& sets, hipStream_t st);
 
 // ----------------------------------------------------------------- logprobs.hip
