@@ -41,7 +41,7 @@ extern "C" {
  *
  * SBN_KEEP_BLOCK neighbours of a row (the last block of a row may be shorter)
  * share one float32 scale s = a / 127, a the block's largest magnitude, 0 if that
- * is under 2^-100.  A code q in [-127, 127] stands for q * s:
+ * is under 2^-100, and no more than what 127 times is finite.  A code q in [-127, 127] stands for q * s:
  *   q = rint((127 * x) / a)     round half to even, all in float32 (127 x without
  *                               overflow); 0 where s = 0
  * so a value is off by at most a / 254.  A NaN or Inf in a block becomes its

@@ -25,6 +25,7 @@ namespace {
 
 constexpr int LANES = SBN_KEEP_BLOCK / 8;            // threads of a checkpoint's block
 static_assert(LANES == 16, "a block is one row of lanes");
+constexpr float LARGEST_SCALE = 0x1.020406p121f;     // the next one's 127-fold rounds to Inf, and so may a / 127's
 
 template <int CTRL>
 __device__ inline uint32_t row_move_bits(uint32_t x) {
@@ -53,7 +54,8 @@ __device__ inline void keep_chunk(const float* v, bool live, int64_t t, int c, i
   const float rcp = none ? 0.0f : __builtin_amdgcn_rcpf(a * (1.0f / 127.0f));
   if (live) {
     *(uint2*)(codes + t * K + 8 * c) = BF16 ? codes8_bf16(v, rcp) : codes8(v, rcp, a);
-    if ((c & (LANES - 1)) == 0) scales[t * nb + c / LANES] = none ? 0.0f : a / 127.0f + (a - a);   // Inf - Inf: NaN
+    if ((c & (LANES - 1)) == 0)                      // Inf - Inf: NaN
+      scales[t * nb + c / LANES] = none ? 0.0f : fminf(a / 127.0f, LARGEST_SCALE) + (a - a);
   }
 }
 
