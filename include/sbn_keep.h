@@ -108,7 +108,8 @@ sbn_status sbn_rmsnorm_backward_kept(const void* dY, int64_t lddy, const void* d
  *   codes_a, scales_a, codes_b, scales_b   the checkpoints of A and of B: all of them
  *             NULL (inference); or all there, without B those of A
  * |u| has to stay finite, and with a gain a row's sum of u^2 below 2^128; squares of
- * |u| < 2^-75 count as 0 there.
+ * |u| < 2^-75 count as 0 there.  eps >= 0 and finite; with eps = 0 a row of u that counts as
+ * zeros, such as relu^2 of a row without positive values, has no norm (s_x is Inf, its gradients NaN).
  */
 typedef enum { SBN_RELU2 = 0, SBN_SILU = 1 } sbn_act;
 
