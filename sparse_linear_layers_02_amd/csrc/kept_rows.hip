@@ -485,7 +485,7 @@ __global__ __launch_bounds__(MAXT) void kept_backward_kernel(BwdArgs P) {
   }
 }
 
-// Rows of more than 2048 chunks: read twice, and dgain's sums in LDS.
+// Rows of more than 2048 chunks (float32 ones of the norm: 1536): read twice, and dgain's sums in LDS.
 template <bool F32, RowOp OP>
 __global__ __launch_bounds__(1024) void kept_backward_wide_kernel(BwdArgs P) {
   __shared__ float red[2][2][16];
@@ -636,12 +636,18 @@ hipError_t run_bwd_wide(const char* name, const BwdArgs& P, hipStream_t st) {
              P.gain ? (size_t)P.K * sizeof(float) : 0, st, P);
   return hipGetLastError();
 }
+// Above 1536 chunks float32 rows of the norm are read twice: held, 24 of their registers
+// were spilled (600 x 14344: 28 us, held 38; 4096 x 14344 201 and 202).  Those of the activation are held
+// all the same, with 2 (relu^2) and 8 (SiLU) spilled where there is a gain (4096 x 14344: 170 and 203 us,
+// 5.0 and 4.2 TB/s; read twice 218 and 227; 600 x 14344 32 and 41, 34 and 37), and so are bf16 ones, which
+// do not spill (norm 82, read twice 112).
 template <bool F32, RowOp OP>
 hipError_t pick_bwd(const char* name, const BwdArgs& P, hipStream_t st) {
   const int n = P.K / 8;
   if (n <= 512) run_bwd<F32, OP, 1, 512>(name, P, st);
   else if (n <= 1024) run_bwd<F32, OP, 1, 1024>(name, P, st);
   else if (n <= 1536) run_bwd<F32, OP, 2, 768>(name, P, st);
+  else if constexpr (F32 && OP == ROW_NORM) return run_bwd_wide<F32, OP>(name, P, st);
   else if (n <= 2048) run_bwd<F32, OP, 4, 512>(name, P, st);
   else return run_bwd_wide<F32, OP>(name, P, st);
   return hipGetLastError();
