@@ -644,27 +644,33 @@ __global__ __launch_bounds__(64 * WA * WB, 1) void ce_gemm_kernel(GemmArgs P) {
         m = rows_all(m, Max{});
         // a group past the vocabulary has no logits
         const float top = SCORE ? fmaxf(m, P.none) : fmaxf(m * factor, NONE);
-        float sum = 0.0f, rest = 0.0f, mean = 0.0f;
+        float sum = 0.0f, mean = 0.0f;
 #pragma unroll
         for (int i = 0; i < MI; ++i)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const float d = SCORE ? (c[i][e] - top) * factor : c[i][e] * factor - top, x = __builtin_amdgcn_exp2f(d);
             sum += x;
-            // without the largest itself, whose 1 would take the last bits of small ones
-            if (SCORE) rest += __builtin_amdgcn_fractf(x), mean += x * d;
+            if (SCORE) mean += x * d, c[i][e] = x;
           }
         sum = rows_all(sum, Add{});
-        if (SCORE) rest = rows_all(rest, Add{}), mean = rows_all(mean, Add{});
-        if (lane < 16 && t < P.nB) {
-          float2 stat = make_float2(top, sum);
-          if (SCORE) {
-            stat.y = rest + (rintf(sum - rest) - 1.0f);   // of several that are as large, all but one
-            if (aw >= P.nA) stat.y = -1.0f, mean = 0.0f;
-            P.mean[(int64_t)group * P.nB + t] = mean;
+        if (SCORE) {
+          mean = rows_all(mean, Add{});
+          float rest = sum - 1.0f;                   // without the largest itself
+          if (__any(sum < 1.25f)) {                  // whose 1 took the last bits of the others
+            float small = 0.0f;
+#pragma unroll
+            for (int i = 0; i < MI; ++i)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) small += __builtin_amdgcn_fractf(c[i][e]);
+            small = rows_all(small, Add{});
+            rest = small + (rintf(sum - small) - 1.0f);   // of several that are as large, all but one
           }
-          P.stats[(int64_t)group * P.nB + t] = stat;
+          if (aw >= P.nA) rest = -1.0f, mean = 0.0f;
+          if (lane < 16 && t < P.nB) P.mean[(int64_t)group * P.nB + t] = mean;
+          sum = rest;
         }
+        if (lane < 16 && t < P.nB) P.stats[(int64_t)group * P.nB + t] = make_float2(top, sum);
       }
     } else if (GRAD) {
       const float factor = POLICY ? P.scale * LOG2E : LOG2E;

@@ -450,15 +450,19 @@ __global__ __launch_bounds__(NT, NT == 256 ? 5 : 4) void logprob_top_kernel(RowA
       if (bound + fabsf(bound) * 0x1p-16f + reach * most < least) break;
       __syncthreads();                               // value is read by all
     }
-    // m's 64-bit sum, if it is an alternative; if not (its 32 bits are as far off), m itself
-    double from = largest.x;
-    for (int i = 0; i < have; ++i)
-      if (index[i] == leader) from = value[i];
-    for (int i = tid; i < top; i += NT) {
-      const bool found = i < have && (uint32_t)index[i] < (uint32_t)P.V;   // always, of finite logits
-      const float logp = (float)((double)P.scale * (value[i] - from) - (double)largest.y);
-      P.ids[(int64_t)t * top + i] = found ? index[i] : 0;
-      P.top_logp[(int64_t)t * top + i] = found ? logp > 0.0f ? 0.0f : logp : NAN;
+    static_assert(MOST <= 64, "a wave");
+    if (wave == 0) {
+      const double sum = lane < have ? value[lane] : 0.0;
+      const int id = lane < have ? index[lane] : -1;
+      // m's 64-bit sum, if it is an alternative; if not (its 32 bits are as far off), m itself
+      const uint64_t its = __ballot(id == leader);
+      const double from = its ? __shfl(sum, __builtin_ctzll(its)) : (double)largest.x;
+      const bool found = (uint32_t)id < (uint32_t)P.V;   // always, of finite logits
+      const float logp = (float)((double)P.scale * (sum - from) - (double)largest.y);
+      if (lane < top) {
+        P.ids[(int64_t)t * top + lane] = found ? id : 0;
+        P.top_logp[(int64_t)t * top + lane] = found ? logp > 0.0f ? 0.0f : logp : NAN;
+      }
     }
     __syncthreads();
   }
