@@ -259,11 +259,11 @@ __global__ __launch_bounds__(NT, NT == 256 ? 5 : 4) void logprob_top_kernel(RowA
     float firsts[HELD];                              // loaded before the statistics are waited for
 #pragma unroll
     for (int k = 0; k < HELD; ++k) firsts[k] = top && tid + k * NT < n ? row[tid + k * NT].x : -INFINITY;
-    float w_most = 0.0f;
+    const int norms = top && JOIN ? P.groups * P.each : 0;
+    float w_norms[2];                                // as firsts
+#pragma unroll
+    for (int k = 0; k < 2; ++k) w_norms[k] = tid + k * NT < norms ? P.norms[tid + k * NT] : 0.0f;
     if (JOIN) {
-      if (top)
-#pragma unroll 2
-        for (int g = tid; g < P.groups * P.each; g += NT) w_most = fmaxf(w_most, P.norms[g]);
       Stat a = join_groups<2>(P, t, tid, NT);
       auto over_lanes = [&](int d) {
 #pragma unroll 1
@@ -300,6 +300,8 @@ __global__ __launch_bounds__(NT, NT == 256 ? 5 : 4) void logprob_top_kernel(RowA
       any |= ((v[0] | v[1] | v[2] | v[3]) & 0x7FFF7FFF) != 0;
       xx = add_squares(__builtin_bit_cast(v8bf, v), xx);
     }
+    float w_most = fmaxf(w_norms[0], w_norms[1]);
+    for (int g = tid + 2 * NT; g < norms; g += NT) w_most = fmaxf(w_most, P.norms[g]);
     xx = wave_all(xx, Add{});
     if (JOIN) w_most = wave_all(w_most, Max{});
     else w_most = *P.most;
