@@ -657,14 +657,15 @@ __global__ __launch_bounds__(64 * WA * WB, 1) void ce_gemm_kernel(GemmArgs P) {
         if (SCORE) {
           mean = rows_all(mean, Add{});
           float rest = sum - 1.0f;                   // without the largest itself
-          if (__any(sum < 1.25f)) {                  // whose 1 took the last bits of the others
+          const bool near = sum < 1.25f;             // whose 1 took the last bits of the others
+          if (__any(near)) {
             float small = 0.0f;
 #pragma unroll
             for (int i = 0; i < MI; ++i)
 #pragma unroll
               for (int e = 0; e < 4; ++e) small += __builtin_amdgcn_fractf(c[i][e]);
             small = rows_all(small, Add{});
-            rest = small + (rintf(sum - small) - 1.0f);   // of several that are as large, all but one
+            if (near) rest = small + (rintf(sum - small) - 1.0f);   // of several that are as large, all but one
           }
           if (aw >= P.nA) rest = -1.0f, mean = 0.0f;
           if (lane < 16 && t < P.nB) P.mean[(int64_t)group * P.nB + t] = mean;

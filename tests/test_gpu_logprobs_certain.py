@@ -90,3 +90,19 @@ def test_never_above_zero(T):
     for scale in (0.5, 1.0, 64.0):
         logp, H, _, _, tlp = sbn.sbn_token_logprobs(X, W, first, scale=scale, top=9)
         assert (logp <= 0).all() and (H >= 0).all() and (tlp <= 0).all()
+
+
+@pytest.mark.parametrize("T", [9, 300, 1100])
+def test_a_certain_row_changes_no_other(T):
+    """How a row's sums are formed goes by that row alone."""
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(T)
+    V = 9000
+    X = torch.randn(T, 256, generator=g, device="cuda").bfloat16()
+    W = (torch.randn(V, 256, generator=g, device="cuda") * 0.05).bfloat16()
+    y = torch.randint(0, V, (T,), generator=g, device="cuda")
+    a = sbn.sbn_token_logprobs(X, W, y, top=5)
+    X[3::7] *= 64                                    # nearly certain
+    b = sbn.sbn_token_logprobs(X, W, y, top=5)
+    rest = torch.arange(T, device="cuda") % 7 != 3
+    assert all(torch.equal(p[rest], q[rest]) for p, q in zip(a, b))
