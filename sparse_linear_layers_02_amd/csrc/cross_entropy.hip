@@ -284,10 +284,10 @@ struct HalfStage {
 // the entries 1.61, 1.53 and 1.64 ms (1.37, 1.44, 1.34; the library's halves of dX
 // and dW 1.61 and 1.87); up to 8% more on cards of lower clocks.  No LDS bank
 // conflicts; 6.4 GB fetched from beyond L2 in the forward.  At 17 tokens (FLAT) bound by reading W: a head of 50001 x
-// 2560, 256 MB, in 50 us, 5.1 TB/s.  Log probabilities: the entropies' sums take 0 to 1%
-// of the statistics' time, the largest logits 2 to 3% more (4096 tokens, 65536 entries, K =
-// 2560: 1020, 1050 us; the plain statistics and the library's bare product 1026 each on that
-// card), D with entropies 0 to 2% of D's.
+// 2560, 256 MB, in 50 us, 5.1 TB/s.  Log probabilities: the entropies' sums take 1.5%
+// of the statistics' time, the largest logits and the norms 3% more (4096 tokens, 65536 entries, K =
+// 2560: 952, 966 and 992 us; the library's bare product 963 on that card), D with entropies 0 to
+// 2% of D's.
 template <int WA, int WB, int MI, int MJ, int RING, int EPI, bool TRA, bool TRB>
 __global__ __launch_bounds__(64 * WA * WB, 1) void ce_gemm_kernel(GemmArgs P) {
   constexpr int TA = WA * MI * 16, TB = WB * MJ * 16, NW = WA * WB;

@@ -21,10 +21,14 @@
 // last alternative, and which no one has summed, are candidates of a second round, and then
 // none is left.
 //
-// Bound by dependent reads: of one token (50001 entries, K = 2560, 8 alternatives) 14 us,
+// Bound by dependent reads: of one token (50001 entries, K = 2560, 8 alternatives) 15 to 16 us,
 // 2.5 of them the join, 2 the bound, 2 the scan, 4 the sums of K, 1 their order; of 37
-// tokens (32001, 4096, 20 alternatives) 24.  Of 4096 tokens (65536, 2560, 8) 91 to 98 us
-// for 67 MB of sets and 300 MB of rows of W, and 9 the join.
+// tokens (32001, 4096, 20 alternatives) 25 to 27.  Of 4096 tokens (65536, 2560, 8) 90 to 100 us
+// for 67 MB of sets and 300 MB of rows of W, and 9 the join.  Second rounds, which margins by
+// norms ask for more often than one from the candidates' sums |x w| would: 20 alternatives of 1024
+// tokens (32001, 4096) 59 -> 68 us, of 2051 (26574, 3776) 88 -> 101; 64 of 2000 (8000, 512) 77 -> 70,
+// without those sums.  One row of W 50 times as large as the others, 4096 tokens as above: 117 us, with a
+// margin for all rows alike 199; 1000 times: 350, 113000.
 #include "score_internal.h"
 
 namespace sbn {
@@ -229,12 +233,12 @@ __device__ inline float reached_by(const float* slot, int k, float& most) {
 // index) in the end.  The code is kept short, without unrolling: one token's block
 // fetches each line of it for the first time.
 // Many tokens: a wave sums three rows at once, 2 loads of each ahead, 5 blocks a unit:
-// 4096 tokens of 65536 entries, K = 2560, 8 alternatives 91 us; 600 of 50000, 4096, 8 41;
-// 2051 of 26574, 3776, 20 88; 2641 of 1158, 1024, 5 27 (two rows 99, 44, 89, 24; four 104,
-// 41, 100, 30; two with 3 ahead 99, 46, 92, 26; one row, 5 ahead, 6 blocks 101, 57, 110, 31;
-// two rows, 7 blocks 111, 48, 106, 27; with the margin by norms 91, 40, 100, 26).  Few: one row, 8 ahead, or, where waves have more
-// than one and 4 ahead are a whole row, two (10 tokens of 2062 entries, K = 256, 32
-// alternatives 27 -> 21 us; with two for K = 4096, 20 of 32001, 37 tokens 25 -> 27).
+// 4096 tokens of 65536 entries, K = 2560, 8 alternatives 90 us; 600 of 50000, 4096, 8 40;
+// 2051 of 26574, 3776, 20 101; 2641 of 1158, 1024, 5 27 (without second rounds 91, 41, 88, 27,
+// and so measured two rows 99, 44, 89, 24; four 104, 41, 100, 30; two with 3 ahead 99, 46, 92, 26;
+// one row, 5 ahead, 6 blocks 101, 57, 110, 31; two rows, 7 blocks 111, 48, 106, 27).  Few: one row, 8
+// ahead, or, where waves have more than one and 4 ahead are a whole row, two (10 tokens of 2062
+// entries, K = 256, 32 alternatives 27 -> 21 us; with two for K = 4096, 20 of 32001, 37 tokens 25 -> 27).
 template <int NT, bool JOIN>
 __global__ __launch_bounds__(NT, NT == 256 ? 5 : 4) void logprob_top_kernel(RowArgs P) {
   constexpr int WAVES = NT / 64, SLOTS = 256, QUEUE = 1024, BATCH = 256, MOST = SBN_LOGPROBS_MAX_TOP;

@@ -20,11 +20,11 @@ namespace sbn {
 // 8, parts of a lane's: of about c = top + 3 candidates 512 c^2 / V rows of W are computed for
 // their neighbours' sake, with sets of 8 a sixteenth of that, and V bytes a token are written
 // and read twice instead of V / 4, which costs least while the caches hold them.  (Logits +
-// alternatives, us, with sets of 8 and without: 20 of 32001 entries, 1024 tokens, K = 4096 222 +
-// 60, 204 + 96; the same, 8192 tokens 1573 + 330, 1566 + 367; 6 of 20000, 600, 2560 67 + 20, 66
-// + 31; 64 of 8000, 2000, 512 27 + 78, 25 + 320; 20 of 32001, 37, 4096 61 + 25, 61 + 28; and
-// where they are not taken 32 of 65536, 4096, 2560 1034 + 218, 974 + 211; 8 of 32001, 4096, 2560
-// 517 + 89, 495 + 77; 8 of 16000, 8192, 1024 242 + 81, 232 + 85.)
+// alternatives, us, with sets of 8 and without: 20 of 32001 entries, 1024 tokens, K = 4096 215 +
+// 68, 206 + 92; the same, 8192 tokens 1521 + 365, 1513 + 372; 6 of 20000, 600, 2560 68 + 25, 67
+// + 29; 64 of 8000, 2000, 512 27 + 70, 27 + 284; 20 of 32001, 37, 4096 58 + 27, 62 + 28; and
+// where they are not taken 32 of 65536, 4096, 2560 1022 + 239, 990 + 207; 8 of 32001, 4096, 2560
+// 507 + 97, 500 + 75; 8 of 16000, 8192, 1024 238 + 87, 233 + 84.)
 // the sum that stands for no entry: -1e30 as an exponent
 inline float logit_none(float scale) { return -1e30f / (scale * 1.4426950408889634f); }
 constexpr int TOPS_MOST = 32;
