@@ -43,7 +43,8 @@ extern "C" {
  * choose who is compared, with a margin of their worst error (K 2^-23 |X[t]| |W[v]|, the
  * norms' product being no less than sum_k |X W|, with the largest |W[v]| of a group of 32 to 128
  * entries), so rows of W whose logits agree to float32's precision, and rows of any
- * size whose large parts cancel, are still told apart.
+ * size whose large parts cancel, are still told apart.  (Products |X W| below 2^-134, which
+ * float32 does not hold exactly, count as rounded to multiples of 2^-149.)
  * Every logit within that margin of the last alternative is summed again: a row
  * whose logits are all equal takes as long as 64-bit sums of all of them (4096 rows
  * of 65536 equal logits, K = 2560: 0.2 s; rows of X that are zero, such as padding, none),

@@ -33,3 +33,20 @@ def test_more_tokens_than_blocks(top):
     got = sbn.sbn_token_logprobs(X, W, y, top=top)
     for rows in (slice(0, 40), slice(2 ** 20 - 20, 2 ** 20 + 20), slice(T - 40, T)):
         check_forward([None if t is None else t[rows] for t in got], reference(X[rows], W, y[rows]), y[rows], top)
+
+
+@pytest.mark.parametrize("T", [5, 300])
+@pytest.mark.parametrize("power", [-60, -66, -70, -74])
+def test_sums_that_float32_hardly_holds(T, power):
+    """Products and sums below 2^-126: whatever the matrix instructions make of them, the order is that of the 64-bit
+    sums of products that are rounded as float32 rounds below its range."""
+    import torch
+    V, K = 3000, 128
+    X, W, y, _, _ = problem(T, V, K, 7, scale=1.0)
+    X, W = X * 2.0 ** power, W * 2.0 ** power
+    assert (X != 0).any(1).all() and (W != 0).any()
+    for top in (1, 30):
+        got = sbn.sbn_token_logprobs(X, W, y, top=top)
+        sums = torch.stack([(x.float() * W.float()).double().sum(1) for x in X])
+        assert torch.equal(got[3], torch.sort(sums, dim=1, descending=True, stable=True).indices[:, :top])
+        check_forward([*got[:3], None, None], reference(X, W, y), y, 0)
